@@ -25,6 +25,11 @@ LIB_PATH = os.path.join(_HERE, "libgs.so")
 GS_OK, GS_ERR_INVALID_ARG, GS_ERR_CAPACITY, GS_ERR_HIP = 0, 1, 2, 3
 GS_OP_PREPROCESS, GS_OP_BIN_SORT, GS_OP_LOSS, GS_OP_SPARSE_ADAM, GS_OP_RASTER = 0, 1, 2, 3, 4
 GS_OP_VIEW_OVERLAP, GS_OP_PACK, GS_OP_DENSIFY, GS_OP_PREPROCESS_VIEWS = 5, 6, 7, 8
+GS_OP_LAYER_NORM_BWD = 9
+GS_TYPE_BF16, GS_TYPE_F16, GS_TYPE_F32 = 0, 1, 2
+GS_ACT_NONE, GS_ACT_RELU, GS_ACT_SILU, GS_ACT_GELU = 0, 1, 2, 3
+GS_MAX_NET_DIM = 65536
+GS_MAX_NET_GROUPS = 1024
 GS_PROJ_WORDS = 16
 GS_GRAD2D_WORDS = 12
 GS_MAX_FUSED_VIEWS = 16
@@ -42,7 +47,8 @@ EXPORTS = ["gs_status_string", "gs_last_error", "gs_version", "gs_workspace_size
            "gs_bin_sort", "gs_bin_sort_async", "gs_render_fwd", "gs_loss", "gs_render_bwd", "gs_project_bwd",
            "gs_sparse_adam", "gs_project_bwd_adam", "gs_visible_list", "gs_view_overlap", "gs_view_priority",
            "gs_tile_partition", "gs_pack_records", "gs_unpack_grads", "gs_densify_stats", "gs_densify",
-           "gs_sparse_adam_noalloc", "gs_preprocess_views"]
+           "gs_sparse_adam_noalloc", "gs_preprocess_views", "gs_layer_norm_fwd", "gs_layer_norm_bwd", "gs_linear_fwd",
+           "gs_linear_workspace_size", "gs_linear_bwd", "gs_grouped_linear_fwd", "gs_grouped_linear_bwd"]
 GS_NOALLOC_SCRATCH_BYTES = 256 * 1024
 GS_NOALLOC_MAX_N = (GS_NOALLOC_SCRATCH_BYTES // 4 - 1) * 4096
 
@@ -106,6 +112,18 @@ def lib():
     L.gs_densify_stats.argtypes = [_P, _P, _P, _i64, _P, _P, _P]
     L.gs_densify.argtypes = [_P, _P, _P, _i64, _i64, _P, _P, _P, _f32, _f32, _f32, _f32, _P, _P, _P, _i64, _P, _P,
                              _sz, _P]
+    L.gs_layer_norm_fwd.argtypes = [_P, _i64, _P, _P, _i64, _i32, _f32, _i32, _P, _i64, _P, _P, _P]
+    L.gs_layer_norm_bwd.argtypes = [_P, _i64, _P, _i64, _P, _P, _P, _P, _i64, _i64, _i32, _i32, _P, _i64, _P, _P,
+                                    _P, _sz, _P]
+    L.gs_linear_fwd.argtypes = [_P, _i64, _P, _i64, _P, _P, _i64, _i64, _i32, _i32, _i32, _i32, _P, _i64, _P, _i64,
+                                _P]
+    L.gs_linear_workspace_size.argtypes = [_i64, _i32, _i32, _i32, _i32, _i32, C.POINTER(_sz)]
+    L.gs_linear_bwd.argtypes = [_P, _i64, _P, _i64, _P, _i64, _P, _i64, _i64, _i32, _i32, _i32, _i32, _P, _i64, _P,
+                                _i32, _P, _P, _sz, _P]
+    L.gs_grouped_linear_fwd.argtypes = [_P, _i64, _P, _i64, _P, _P, _i32, _P, _i64, _i64, _i32, _i32, _i32, _i32, _P,
+                                        _i64, _P, _i64, _P]
+    L.gs_grouped_linear_bwd.argtypes = [_P, _i64, _P, _i64, _P, _i32, _P, _i64, _P, _i64, _i64, _i32, _i32, _i32,
+                                        _i32, _P, _i64, _P, _i32, _P, _P, _sz, _P]
     for name in EXPORTS[3:]:
         getattr(L, name).restype = C.c_int
     _handle = L
@@ -1000,3 +1018,7 @@ def from_workload(work, device="cuda", **kw) -> TrainStep:
     """TrainStep for a ``synth.Workload``."""
     return TrainStep(work.params, work.cameras, work.targets, work.w_l1, work.w_ssim, work.lr, work.beta1,
                      work.beta2, work.eps, device=device, **kw)
+
+
+from .network import (gs_grouped_linear_bwd, gs_grouped_linear_fwd, gs_layer_norm_bwd, gs_layer_norm_fwd,  # noqa: E402
+                      gs_linear_bwd, gs_linear_fwd, gs_linear_workspace_size)

@@ -3,6 +3,7 @@
 // work is enqueued, so a GS_ERR_INVALID_ARG call has launched nothing.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -17,6 +18,12 @@ static_assert(GS_MAX_PREPROCESS_VIEWS == gs::kMaxPreprocessViews, "preprocess vi
 static_assert(GS_MAX_COUPLED_VIEWS == gs::kMaxCoupledViews, "coupled view limit");
 static_assert(GS_MAX_TILE_BLOCKS == gs::kMaxTileBlocks, "tile block limit");
 static_assert(GS_MAX_PARTITION_TILES == gs::kMaxPartitionTiles, "partition tile limit");
+static_assert(GS_TYPE_BF16 == gs::kTypeBF16 && GS_TYPE_F16 == gs::kTypeF16 && GS_TYPE_F32 == gs::kTypeF32,
+              "storage types");
+static_assert(GS_ACT_NONE == gs::kActNone && GS_ACT_RELU == gs::kActRelu && GS_ACT_SILU == gs::kActSilu &&
+                  GS_ACT_GELU == gs::kActGelu,
+              "activations");
+static_assert(GS_MAX_NET_DIM == gs::kMaxNetDim && GS_MAX_NET_GROUPS == gs::kMaxNetGroups, "network limits");
 
 namespace {
 
@@ -114,6 +121,81 @@ gs::SsimWindow make_window() {
 
 size_t adam_ws_bytes(int64_t n) { return gs::compact_ws_bytes(n); }
 
+// --- network operators ---------------------------------------------------------
+
+gs_status check_net_sizes(int64_t rows, int32_t type) {
+  REQUIRE(type >= GS_TYPE_BF16 && type <= GS_TYPE_F32, "type = %d unknown", int(type));
+  REQUIRE(rows >= 0 && rows < (int64_t(1) << 31), "rows = %lld out of range", (long long)rows);
+  return GS_OK;
+}
+
+// A row-major matrix argument (rows > 0).
+gs_status check_matrix(const char* name, const void* p, int64_t ld, int32_t width, size_t elem) {
+  REQUIRE(p != nullptr, "%s is NULL", name);
+  REQUIRE(aligned(p, elem), "%s not aligned to its elements", name);
+  REQUIRE(ld >= width && ld < (int64_t(1) << 31), "%s: leading dimension %lld for width %d", name, (long long)ld,
+          int(width));
+  return GS_OK;
+}
+
+gs_status check_vector(const char* name, const void* p) {
+  REQUIRE(aligned(p, 4), "%s not 4-byte aligned", name);
+  return GS_OK;
+}
+
+gs_status check_linear(const gs::LinearArgs& a, int64_t rows, int32_t type) {
+  CHECK(check_net_sizes(rows, type));
+  REQUIRE(a.in >= 1 && a.in <= GS_MAX_NET_DIM, "in = %d out of range", int(a.in));
+  REQUIRE(a.out >= 1 && a.out <= GS_MAX_NET_DIM, "out = %d out of range", int(a.out));
+  REQUIRE(a.act >= GS_ACT_NONE && a.act <= GS_ACT_GELU, "act = %d unknown", int(a.act));
+  REQUIRE(a.groups >= 0 && a.groups <= GS_MAX_NET_GROUPS, "num_groups = %d out of range", int(a.groups));
+  REQUIRE(gs::linear_fits(rows, a.in, a.out, a.groups), "rows = %lld, in = %d, out = %d pass a launch grid",
+          (long long)rows, int(a.in), int(a.out));
+  if (a.groups > 0)
+    REQUIRE(a.offsets != nullptr && aligned(a.offsets, 8), "offsets NULL or not 8-byte aligned");
+  return GS_OK;
+}
+
+gs_status linear_fwd(gs::LinearArgs a, int64_t rows, int32_t type, void* stream, const char* where) {
+  CHECK(check_linear(a, rows, type));
+  if (rows == 0) return ok();
+  const size_t elem = gs::type_bytes(type);
+  CHECK(check_matrix("x", a.x, a.ldx, a.in, elem));
+  CHECK(check_matrix("w", a.w, a.ldw, a.in, elem));
+  CHECK(check_matrix("y", a.y, a.ldy, a.out, elem));
+  CHECK(check_vector("bias", a.bias));
+  if (a.residual != nullptr) CHECK(check_matrix("residual", a.residual, a.ldr, a.out, elem));
+  if (a.z != nullptr) CHECK(check_matrix("z", a.z, a.ldz, a.out, elem));
+  a.rows = int32_t(rows);
+  return hip_status(gs::launch_linear_fwd(type, a, static_cast<hipStream_t>(stream)), where);
+}
+
+gs_status linear_bwd(gs::LinearArgs a, int64_t rows, int32_t type, int32_t dw_type, void* ws, size_t ws_bytes,
+                     void* stream, const char* where) {
+  CHECK(check_linear(a, rows, type));
+  const size_t elem = gs::type_bytes(type);
+  if (rows > 0) {
+    CHECK(check_matrix("dy", a.dy, a.lddy, a.out, elem));
+    if (a.act != GS_ACT_NONE) CHECK(check_matrix("z", a.z, a.ldz, a.out, elem));
+    if (a.dw != nullptr) CHECK(check_matrix("x", a.x, a.ldx, a.in, elem));
+    if (a.dx != nullptr) {
+      CHECK(check_matrix("w", a.w, a.ldw, a.in, elem));
+      CHECK(check_matrix("dx", a.dx, a.lddx, a.in, elem));
+    }
+  }
+  if (a.dw != nullptr) {
+    REQUIRE(dw_type == type || dw_type == GS_TYPE_F32, "dw_type = %d is neither type nor GS_TYPE_F32", int(dw_type));
+    REQUIRE(aligned(a.dw, gs::type_bytes(dw_type)), "dw not aligned to its elements");
+  }
+  CHECK(check_vector("db", a.db));
+  REQUIRE(ws != nullptr && aligned(ws, 256), "workspace NULL or not 256-byte aligned");
+  const size_t need = gs::linear_bwd_ws_bytes(type, rows, a.in, a.out, a.groups, a.act);
+  REQUIRE(ws_bytes >= need, "workspace_bytes = %zu < %zu needed", ws_bytes, need);
+  a.rows = int32_t(rows);
+  a.dw_f32 = dw_type == GS_TYPE_F32;
+  return hip_status(gs::launch_linear_bwd(type, a, ws, static_cast<hipStream_t>(stream)), where);
+}
+
 }  // namespace
 
 // The scratch of gs_sparse_adam_noalloc.  In host code `scratch` names a
@@ -196,6 +278,11 @@ gs_status gs_workspace_size(gs_op op, int64_t n, int32_t width, int32_t height, 
       REQUIRE(n >= 0 && n < (int64_t(1) << 31), "n = %lld out of range", (long long)n);
       REQUIRE(width >= 1 && width <= GS_MAX_PREPROCESS_VIEWS, "num_views = %d out of range", width);
       *bytes = gs::preprocess_views_ws_bytes(n, width);
+      return ok();
+    case GS_OP_LAYER_NORM_BWD:
+      REQUIRE(n >= 0 && n < (int64_t(1) << 31), "rows = %lld out of range", (long long)n);
+      REQUIRE(width >= 1 && width <= GS_MAX_NET_DIM, "width = %d out of range", width);
+      *bytes = gs::layer_norm_ws_bytes(n, width);
       return ok();
     case GS_OP_DENSIFY:
       REQUIRE(n >= 0 && n < (int64_t(1) << 30), "n = %lld out of range", (long long)n);
@@ -653,6 +740,188 @@ gs_status gs_densify(const float* params, const float* m, const float* v, int64_
                                        log_scale_threshold, logit_threshold, log_shrink, out_params, out_m, out_v,
                                        ld_out, out_n, workspace, static_cast<hipStream_t>(stream)),
                     "gs_densify");
+}
+
+gs_status gs_layer_norm_fwd(const void* x, int64_t ldx, const float* gamma, const float* beta, int64_t rows,
+                            int32_t width, float eps, int32_t type, void* y, int64_t ldy, float* mean, float* rstd,
+                            void* stream) {
+  CHECK(check_net_sizes(rows, type));
+  REQUIRE(width >= 1 && width <= GS_MAX_NET_DIM, "width = %d out of range", int(width));
+  REQUIRE(std::isfinite(eps) && eps >= 0.0f, "eps negative or not finite");
+  if (rows == 0) return ok();
+  const size_t elem = gs::type_bytes(type);
+  CHECK(check_matrix("x", x, ldx, width, elem));
+  CHECK(check_matrix("y", y, ldy, width, elem));
+  CHECK(check_vector("gamma", gamma));
+  CHECK(check_vector("beta", beta));
+  CHECK(check_vector("mean", mean));
+  CHECK(check_vector("rstd", rstd));
+  gs::NormArgs a{};
+  a.x = x;
+  a.ldx = ldx;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.rows = int32_t(rows);
+  a.width = width;
+  a.eps = eps;
+  a.y = y;
+  a.ldy = ldy;
+  a.mean = mean;
+  a.rstd = rstd;
+  return hip_status(gs::launch_layer_norm_fwd(type, a, static_cast<hipStream_t>(stream)), "gs_layer_norm_fwd");
+}
+
+gs_status gs_layer_norm_bwd(const void* x, int64_t ldx, const void* dy, int64_t lddy, const float* gamma,
+                            const float* mean, const float* rstd, const void* dres, int64_t lddres, int64_t rows,
+                            int32_t width, int32_t type, void* dx, int64_t lddx, float* dgamma, float* dbeta,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  CHECK(check_net_sizes(rows, type));
+  REQUIRE(width >= 1 && width <= GS_MAX_NET_DIM, "width = %d out of range", int(width));
+  const size_t elem = gs::type_bytes(type);
+  if (rows > 0) {
+    CHECK(check_matrix("x", x, ldx, width, elem));
+    CHECK(check_matrix("dy", dy, lddy, width, elem));
+    REQUIRE(mean != nullptr && rstd != nullptr, "mean / rstd NULL");
+    CHECK(check_vector("mean", mean));
+    CHECK(check_vector("rstd", rstd));
+    CHECK(check_vector("gamma", gamma));
+    if (dres != nullptr) CHECK(check_matrix("dres", dres, lddres, width, elem));
+    if (dx != nullptr) CHECK(check_matrix("dx", dx, lddx, width, elem));
+  }
+  CHECK(check_vector("dgamma", dgamma));
+  CHECK(check_vector("dbeta", dbeta));
+  REQUIRE(workspace != nullptr && aligned(workspace, 256), "workspace NULL or not 256-byte aligned");
+  const size_t need = gs::layer_norm_ws_bytes(rows, width);
+  REQUIRE(workspace_bytes >= need, "workspace_bytes = %zu < %zu needed", workspace_bytes, need);
+  gs::NormArgs a{};
+  a.x = x;
+  a.ldx = ldx;
+  a.dy = dy;
+  a.lddy = lddy;
+  a.dres = dres;
+  a.lddres = lddres;
+  a.gamma = gamma;
+  a.mean = const_cast<float*>(mean);
+  a.rstd = const_cast<float*>(rstd);
+  a.rows = int32_t(rows);
+  a.width = width;
+  a.dx = dx;
+  a.lddx = lddx;
+  a.dgamma = dgamma;
+  a.dbeta = dbeta;
+  return hip_status(gs::launch_layer_norm_bwd(type, a, workspace, static_cast<hipStream_t>(stream)),
+                    "gs_layer_norm_bwd");
+}
+
+gs_status gs_linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, const float* bias,
+                        const void* residual, int64_t ldr, int64_t rows, int32_t in, int32_t out, int32_t type,
+                        int32_t act, void* y, int64_t ldy, void* z, int64_t ldz, void* stream) {
+  gs::LinearArgs a{};
+  a.x = x;
+  a.ldx = ldx;
+  a.w = w;
+  a.ldw = ldw;
+  a.bias = bias;
+  a.residual = residual;
+  a.ldr = ldr;
+  a.in = in;
+  a.out = out;
+  a.act = act;
+  a.y = y;
+  a.ldy = ldy;
+  a.z = z;
+  a.ldz = ldz;
+  return linear_fwd(a, rows, type, stream, "gs_linear_fwd");
+}
+
+gs_status gs_linear_workspace_size(int64_t rows, int32_t in, int32_t out, int32_t num_groups, int32_t type,
+                                   int32_t act, size_t* bytes) {
+  REQUIRE(bytes != nullptr, "bytes is NULL");
+  *bytes = 0;
+  gs::LinearArgs a{};
+  a.in = in;
+  a.out = out;
+  a.act = act;
+  CHECK(check_linear(a, rows, type));
+  REQUIRE(num_groups >= 0 && num_groups <= GS_MAX_NET_GROUPS, "num_groups = %d out of range", int(num_groups));
+  REQUIRE(gs::linear_fits(rows, in, out, num_groups), "sizes pass a launch grid");
+  *bytes = std::max<size_t>(256, gs::linear_bwd_ws_bytes(type, rows, in, out, num_groups, act));
+  return ok();
+}
+
+gs_status gs_linear_bwd(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* z, int64_t ldz,
+                        const void* dy, int64_t lddy, int64_t rows, int32_t in, int32_t out, int32_t type,
+                        int32_t act, void* dx, int64_t lddx, void* dw, int32_t dw_type, float* db, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  gs::LinearArgs a{};
+  a.x = x;
+  a.ldx = ldx;
+  a.w = w;
+  a.ldw = ldw;
+  a.z = const_cast<void*>(z);
+  a.ldz = ldz;
+  a.dy = dy;
+  a.lddy = lddy;
+  a.in = in;
+  a.out = out;
+  a.act = act;
+  a.dx = dx;
+  a.lddx = lddx;
+  a.dw = dw;
+  a.db = db;
+  return linear_bwd(a, rows, type, dw_type, workspace, workspace_bytes, stream, "gs_linear_bwd");
+}
+
+gs_status gs_grouped_linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, const float* bias,
+                                const int64_t* offsets, int32_t num_groups, const void* residual, int64_t ldr,
+                                int64_t rows, int32_t in, int32_t out, int32_t type, int32_t act, void* y,
+                                int64_t ldy, void* z, int64_t ldz, void* stream) {
+  REQUIRE(num_groups >= 1, "num_groups = %d out of range", int(num_groups));
+  gs::LinearArgs a{};
+  a.x = x;
+  a.ldx = ldx;
+  a.w = w;
+  a.ldw = ldw;
+  a.bias = bias;
+  a.offsets = offsets;
+  a.groups = num_groups;
+  a.residual = residual;
+  a.ldr = ldr;
+  a.in = in;
+  a.out = out;
+  a.act = act;
+  a.y = y;
+  a.ldy = ldy;
+  a.z = z;
+  a.ldz = ldz;
+  return linear_fwd(a, rows, type, stream, "gs_grouped_linear_fwd");
+}
+
+gs_status gs_grouped_linear_bwd(const void* x, int64_t ldx, const void* w, int64_t ldw, const int64_t* offsets,
+                                int32_t num_groups, const void* z, int64_t ldz, const void* dy, int64_t lddy,
+                                int64_t rows, int32_t in, int32_t out, int32_t type, int32_t act, void* dx,
+                                int64_t lddx, void* dw, int32_t dw_type, float* db, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  REQUIRE(num_groups >= 1, "num_groups = %d out of range", int(num_groups));
+  gs::LinearArgs a{};
+  a.x = x;
+  a.ldx = ldx;
+  a.w = w;
+  a.ldw = ldw;
+  a.offsets = offsets;
+  a.groups = num_groups;
+  a.z = const_cast<void*>(z);
+  a.ldz = ldz;
+  a.dy = dy;
+  a.lddy = lddy;
+  a.in = in;
+  a.out = out;
+  a.act = act;
+  a.dx = dx;
+  a.lddx = lddx;
+  a.dw = dw;
+  a.db = db;
+  return linear_bwd(a, rows, type, dw_type, workspace, workspace_bytes, stream, "gs_grouped_linear_bwd");
 }
 
 }  // extern "C"

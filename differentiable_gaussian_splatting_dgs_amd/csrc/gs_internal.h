@@ -165,4 +165,56 @@ hipError_t launch_densify(const float* params, const float* m, const float* v, i
                           float log_scale_threshold, float logit_threshold, float log_shrink, float* out_params,
                           float* out_m, float* out_v, int64_t ld_out, int64_t* out_n, void* ws, hipStream_t st);
 
+// --- network operators (layer_norm.hip, linear_*.hip) --------------------------
+// storage types and activations, as gs_type and gs_act number them
+constexpr int kTypeBF16 = 0, kTypeF16 = 1, kTypeF32 = 2;
+constexpr int kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3;
+constexpr int32_t kMaxNetDim = 65536;     // widths of a layer or norm
+constexpr int32_t kMaxNetGroups = 1024;
+inline size_t type_bytes(int type) { return type == kTypeF32 ? 4 : 2; }
+
+struct NormArgs {
+  const void* x;
+  const void* dy;      // backward only, as are dres, dx, dgamma, dbeta
+  const void* dres;    // or NULL
+  const float* gamma;  // or NULL: 1
+  const float* beta;   // or NULL: 0
+  float* mean;         // read by the backward pass
+  float* rstd;
+  void* y;
+  void* dx;
+  float* dgamma;       // or NULL
+  float* dbeta;        // or NULL
+  int64_t ldx, lddy, lddres, ldy, lddx;
+  int32_t rows, width;
+  float eps;
+};
+size_t layer_norm_ws_bytes(int64_t rows, int32_t width);
+hipError_t launch_layer_norm_fwd(int type, const NormArgs& a, hipStream_t st);
+hipError_t launch_layer_norm_bwd(int type, const NormArgs& a, void* ws, hipStream_t st);
+
+// The linear layer over rows, or (groups > 0) over the ragged row groups
+// whose bounds offsets[0 .. groups] hold on the device.
+struct LinearArgs {
+  const void* x;         // [rows][ldx]
+  const void* w;         // [groups or 1][out][ldw]
+  const float* bias;     // [groups or 1][out] or NULL
+  const void* residual;  // [rows][ldr] or NULL
+  void* y;
+  void* z;               // forward: written if not NULL; backward: read if act is not none
+  const void* dy;        // backward only, as are dx, dw, db
+  void* dx;              // or NULL
+  void* dw;              // or NULL
+  float* db;             // or NULL
+  const int64_t* offsets;
+  int64_t ldx, ldw, ldr, ldy, ldz, lddy, lddx;
+  int32_t rows, in, out, groups, act;
+  int32_t dw_f32;        // dw is fp32 whatever the storage type
+};
+// 0 where a launch grid would pass what the hardware takes
+bool linear_fits(int64_t rows, int32_t in, int32_t out, int32_t groups);
+size_t linear_bwd_ws_bytes(int type, int64_t rows, int32_t in, int32_t out, int32_t groups, int act);
+hipError_t launch_linear_fwd(int type, const LinearArgs& a, hipStream_t st);
+hipError_t launch_linear_bwd(int type, const LinearArgs& a, void* ws, hipStream_t st);
+
 }  // namespace gs

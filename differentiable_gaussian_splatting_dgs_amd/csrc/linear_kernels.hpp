@@ -1,0 +1,555 @@
+// The linear layer's kernels, included by linear_bf16.hip, linear_f16.hip and
+// linear_f32.hip (one storage type each, so that they build side by side).
+//
+//   forward    z = x w^T + bias, y = act(z) + residual
+//   backward   dz = dy act'(z); dx = dz w; dw = dz^T x; db = sum of dz's rows
+//
+// One tiled product C[m][n] = sum_k A(m, k) B(n, k) serves the three:
+//   kFwd  m = rows, n = out, k = in    A = x  (k along memory), B = w (k along memory)
+//   kDx   m = rows, n = in,  k = out   A = dz (k along memory), B = w (n along memory)
+//   kDw   m = out,  n = in,  k = rows  A = dz (m along memory), B = x (n along memory)
+#pragma once
+
+#include <algorithm>
+
+#include "net_common.hpp"
+
+namespace gs {
+namespace net {
+namespace {
+
+enum Mode { kFwd = 0, kDx = 1, kDw = 2 };
+
+struct ProductArgs {
+  const void* a;
+  const void* b;
+  int64_t lda, ldb, b_group;      // b_group: elements from one group's weights to the next
+  const int64_t* offsets;
+  int32_t rows, groups;           // groups == 0: one group of all rows
+  int32_t m, n, k;                // the fixed extents (kFwd, kDx: m unused; kDw: k unused)
+  int32_t unit;                   // kDw: rows of a stretch; else the tile height
+  int32_t tiles_n, tiles;         // tiles across, tiles in all (kDw: tiles of one stretch)
+  // epilogue
+  const float* bias;
+  const void* residual;
+  void* out;
+  void* z;
+  float* part;                    // kDw: partial products, one [m][n] plane per stretch
+  int64_t ldr, ldo, ldz;
+  int32_t act, out_f32;
+};
+
+// --- matrix instructions ------------------------------------------------------------
+
+// A fragment is 16 bytes of one row along k: lane l holds row l % 16 and
+// k-chunk l / 16 of a 16 x (64 bytes) block.  16-bit types: one 16x16x32
+// instruction; fp32: four 16x16x4, component c of every lane's chunk in the
+// c-th (the same order of k on both sides, so the sum is the same).
+// D: lane l holds rows 4 (l / 16) .. + 3 of column l % 16.
+template <typename T>
+struct Frag;
+template <>
+struct Frag<bf16> {
+  typedef __bf16 V __attribute__((ext_vector_type(8)));
+  static __device__ __forceinline__ f32x4 mma(V a, V b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+};
+template <>
+struct Frag<f16> {
+  typedef _Float16 V __attribute__((ext_vector_type(8)));
+  static __device__ __forceinline__ f32x4 mma(V a, V b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
+};
+template <>
+struct Frag<float> {
+  typedef float V __attribute__((ext_vector_type(4)));
+  static __device__ __forceinline__ f32x4 mma(V a, V b, f32x4 c) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
+    return c;
+  }
+};
+
+// --- tiles in LDS ---------------------------------------------------------------------
+
+// A k step is 128 bytes of k: 64 16-bit or 32 fp32 values.  Two layouts of a
+// D-row operand, both of D * 128 bytes:
+//   along k    [D][128 bytes]: 8 chunks a row, chunk c of row r at c ^ (r % 8),
+//              so that the 16 rows a fragment reads spread over all banks
+//   across k   [k][D]: read back transposed, 16-bit types with the LDS
+//              transpose read (4 x 16 blocks), fp32 value by value; the
+//              chunks of row k are permuted in pairs (16-bit) or fours
+//              (fp32) by the bits of k that a wave's read spans
+template <typename T>
+constexpr int kStep = int(128 / sizeof(T));
+
+template <typename T, int D>
+__device__ __forceinline__ int across_swizzle(int k) {
+  constexpr int chunks = D / kChunk<T>;
+  if constexpr (sizeof(T) == 2)
+    return (2 * ((k & 3) | ((k >> 1) & 4))) & (chunks - 1);
+  else
+    return (((k >> 2) & 3) << 2) & (chunks - 1);
+}
+
+// Byte offset of chunk c of row r.
+template <typename T, int D, bool ACROSS>
+__device__ __forceinline__ int tile_at(int r, int c) {
+  if constexpr (ACROSS)
+    return (r * (D / kChunk<T>) + (c ^ across_swizzle<T, D>(r))) * 16;
+  else
+    return (r * 8 + (c ^ (r & 7))) * 16;
+}
+
+typedef __attribute__((address_space(3))) char lds_char;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+// The fragment of rows d0 .. d0 + 15, k chunk group kk (64 bytes of k).
+template <typename T, int D, bool ACROSS>
+__device__ __forceinline__ typename Frag<T>::V read_frag(const char* tile, int d0, int kk, int lane) {
+  using V = typename Frag<T>::V;
+  const int i = lane & 15, g = lane >> 4;
+  if constexpr (!ACROSS) {
+    return *reinterpret_cast<const V*>(tile + tile_at<T, D, false>(d0 + i, 4 * kk + g));
+  } else if constexpr (sizeof(T) == 2) {
+    // lane i of a quarter wave reads 4 values of row k + i / 4 at column
+    // 4 (i % 4); the read hands it column i of the four rows
+    s16x8 v;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = 32 * kk + 8 * g + 4 * h + (i >> 2);
+      const char* p = tile + tile_at<T, D, true>(k, (d0 >> 3) + ((i & 3) >> 1)) + (i & 1) * 8;
+      const s16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p));
+      v[4 * h] = u[0];
+      v[4 * h + 1] = u[1];
+      v[4 * h + 2] = u[2];
+      v[4 * h + 3] = u[3];
+    }
+    return __builtin_bit_cast(V, v);
+  } else {
+    V v;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int k = 16 * kk + 4 * g + c;
+      v[c] = *reinterpret_cast<const float*>(tile + tile_at<T, D, true>(k, (d0 + i) >> 2) + ((d0 + i) & 3) * 4);
+    }
+    return v;
+  }
+}
+
+// Global -> registers -> LDS for one operand, at any alignment.  `row` and
+// `col` extents are what is left of the operand from the tile's corner: rows
+// and columns past them read as 0.
+template <typename T, int D, bool ACROSS, int THREADS>
+struct Stage {
+  static constexpr int kPer = D * 8 / THREADS;
+  static constexpr int kAcross = ACROSS ? D / kChunk<T> : 8;   // chunks of a tile row
+  Chunk<T> c[kPer];
+  __device__ __forceinline__ void load(const T* __restrict__ p, int64_t ld, int rows, int cols, int tid) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int id = j * THREADS + tid, r = id / kAcross, at = (id % kAcross) * kChunk<T>;
+      const int n = r < rows ? cols - at : 0;
+      c[j] = load_chunk_n(p + r * ld + at, n < 0 ? 0 : n);
+    }
+  }
+  __device__ __forceinline__ void store(char* tile, int tid) const {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int id = j * THREADS + tid;
+      *reinterpret_cast<Chunk<T>*>(tile + tile_at<T, D, ACROSS>(id / kAcross, id % kAcross)) = c[j];
+    }
+  }
+};
+
+// --- epilogue -----------------------------------------------------------------------------
+
+// Eight values of one output row from column `col`, `n` of them real.
+template <typename T>
+__device__ __forceinline__ void emit(const ProductArgs& p, const float* __restrict__ bias, int64_t row, int col, int n,
+                                     float (&v)[8], float* __restrict__ plane) {
+  if (plane != nullptr) {   // partial product
+    float* o = plane + row * p.n + col;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      Chunk<float> c;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c.v[i] = v[4 * h + i];
+      if (n > 4 * h) store_chunk_n(o + 4 * h, c, n - 4 * h);
+    }
+    return;
+  }
+  if (bias != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) v[i] += bias[col + i];
+  }
+  constexpr int K = kChunk<T>;
+#pragma unroll
+  for (int h = 0; h < 8 / K; ++h) {
+    if (n <= K * h) break;
+    Chunk<T> c;
+    if (p.z != nullptr) {
+#pragma unroll
+      for (int i = 0; i < K; ++i) c.v[i] = T(v[K * h + i]);
+      store_chunk_n(static_cast<T*>(p.z) + row * p.ldz + col + K * h, c, n - K * h);
+    }
+    if (p.act != kActNone) {
+#pragma unroll
+      for (int i = 0; i < K; ++i) v[K * h + i] = act_apply<T>(v[K * h + i], p.act);
+    }
+    if (p.residual != nullptr) {
+      c = load_chunk_n(static_cast<const T*>(p.residual) + row * p.ldr + col + K * h, n - K * h);
+#pragma unroll
+      for (int i = 0; i < K; ++i) v[K * h + i] += float(c.v[i]);
+    }
+    if (p.out_f32) {
+      float* o = static_cast<float*>(p.out) + row * p.ldo + col + K * h;
+#pragma unroll
+      for (int i = 0; i < K; ++i)
+        if (K * h + i < n) o[i] = v[K * h + i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < K; ++i) c.v[i] = T(v[K * h + i]);
+      store_chunk_n(static_cast<T*>(p.out) + row * p.ldo + col + K * h, c, n - K * h);
+    }
+  }
+}
+
+// --- the product ------------------------------------------------------------------------------
+
+// BM x BN outputs a workgroup, WM x WN waves.  The n side is the first
+// operand of the matrix instruction, so that a lane's four results are
+// neighbours along n; each wave then turns 16 rows at a time through LDS
+// into whole chunks of output rows.
+template <typename T, Mode MODE, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void k_product(ProductArgs p) {
+  constexpr int THREADS = 64 * WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
+  constexpr bool A_ACROSS = MODE == kDw, B_ACROSS = MODE != kFwd;
+  constexpr int kPatch = TN + 4;   // floats of a patch row: 4 more keep its 16-byte writes off each other's banks
+  constexpr int kTiles = (BM + BN) * 128, kPatches = WM * WN * 16 * kPatch * 4;
+  __shared__ __align__(16) char lds[kTiles > kPatches ? kTiles : kPatches];
+  char* const ta = lds;
+  char* const tb = lds + BM * 128;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
+
+  // Which tile.  kFwd, kDx: the height index picks group and rows; kDw: the
+  // stretch does, and the tile inside the plane is apart from it.
+  const int stretch = MODE == kDw ? int(blockIdx.x) / p.tiles : int(blockIdx.x) / p.tiles_n;
+  const int within = MODE == kDw ? int(blockIdx.x) % p.tiles : int(blockIdx.x) % p.tiles_n;
+  const Span s = find_span(p.offsets, p.groups, p.rows, p.unit, stretch);
+  if (s.e < 0) return;
+  const int m0 = MODE == kDw ? within / p.tiles_n * BM : 0;
+  const int n0 = (MODE == kDw ? within % p.tiles_n : within) * BN;
+  const int m_left = MODE == kDw ? p.m - m0 : s.row1 - s.row0, n_left = p.n - n0;
+  const int k_all = MODE == kDw ? s.row1 - s.row0 : p.k;
+  const T* a = static_cast<const T*>(p.a) + int64_t(s.row0) * p.lda + m0;
+  const T* b = static_cast<const T*>(p.b);
+  if constexpr (MODE == kFwd) b += int64_t(s.e) * p.b_group + int64_t(n0) * p.ldb;
+  if constexpr (MODE == kDx) b += int64_t(s.e) * p.b_group + n0;
+  if constexpr (MODE == kDw) b += int64_t(s.row0) * p.ldb + n0;
+  const int64_t step_a = A_ACROSS ? kStep<T> * p.lda : kStep<T>, step_b = B_ACROSS ? kStep<T> * p.ldb : kStep<T>;
+
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  Stage<T, BM, A_ACROSS, THREADS> sa;
+  Stage<T, BN, B_ACROSS, THREADS> sb;
+  sa.load(a, p.lda, A_ACROSS ? k_all : m_left, A_ACROSS ? m_left : k_all, tid);
+  sb.load(b, p.ldb, B_ACROSS ? k_all : n_left, B_ACROSS ? n_left : k_all, tid);
+  for (int k0 = 0; k0 < k_all; k0 += kStep<T>) {
+    sa.store(ta, tid);
+    sb.store(tb, tid);
+    __syncthreads();
+    const int left = k_all - k0 - kStep<T>;
+    if (left > 0) {   // the next step's loads fly while this one is multiplied
+      a += step_a;
+      b += step_b;
+      sa.load(a, p.lda, A_ACROSS ? left : m_left, A_ACROSS ? m_left : left, tid);
+      sb.load(b, p.ldb, B_ACROSS ? left : n_left, B_ACROSS ? n_left : left, tid);
+    }
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      typename Frag<T>::V fa[FM], fb[FN];
+#pragma unroll
+      for (int i = 0; i < FM; ++i) fa[i] = read_frag<T, BM, A_ACROSS>(ta, wm * TM + 16 * i, kk, lane);
+#pragma unroll
+      for (int j = 0; j < FN; ++j) fb[j] = read_frag<T, BN, B_ACROSS>(tb, wn * TN + 16 * j, kk, lane);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = Frag<T>::mma(fb[j], fa[i], acc[i][j]);
+    }
+    __syncthreads();
+  }
+
+  const float* bias = nullptr;
+  float* plane = nullptr;
+  int64_t row0 = MODE == kDw ? m0 : s.row0;
+  if (MODE == kFwd && p.bias != nullptr) bias = p.bias + int64_t(s.e) * p.n;
+  ProductArgs q = p;
+  if constexpr (MODE == kDw) {
+    if (p.part != nullptr && s.slots > 1)
+      plane = p.part + int64_t(stretch) * p.m * p.n;
+    else
+      q.out = p.out_f32 ? static_cast<void*>(static_cast<float*>(p.out) + int64_t(s.e) * p.m * p.ldo)
+                        : static_cast<void*>(static_cast<T*>(p.out) + int64_t(s.e) * p.m * p.ldo);
+  }
+  float* patch = reinterpret_cast<float*>(lds) + wave * 16 * kPatch;
+  constexpr int kAcross = TN / 8, kRows = 64 / kAcross;   // lanes of an output row, rows a pass
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      *reinterpret_cast<f32x4*>(patch + (lane & 15) * kPatch + 16 * j + 4 * (lane >> 4)) = acc[i][j];
+    wave_sync();
+#pragma unroll
+    for (int r = lane / kAcross; r < 16; r += kRows) {
+      const int m = wm * TM + 16 * i + r, col = wn * TN + (lane % kAcross) * 8;
+      float v[8];
+      const f32x4 lo = *reinterpret_cast<const f32x4*>(patch + r * kPatch + (lane % kAcross) * 8);
+      const f32x4 hi = *reinterpret_cast<const f32x4*>(patch + r * kPatch + (lane % kAcross) * 8 + 4);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        v[c] = lo[c];
+        v[4 + c] = hi[c];
+      }
+      if (m < m_left && col < n_left) emit<T>(q, bias, row0 + m, n0 + col, std::min(8, n_left - col), v, plane);
+    }
+    wave_sync();
+  }
+}
+
+// --- dz and db ----------------------------------------------------------------------------------
+
+// dz = dy act'(z) rounded into the storage type (what the matrix
+// instructions take; db is summed from the unrounded values), and one
+// partial row of db per stretch of rows: part[slot][out].  Without an
+// activation dz is dy itself and only the sums are made.
+template <typename T>
+__global__ __launch_bounds__(256) void k_act_grad(const T* __restrict__ dy, int64_t lddy, const T* __restrict__ z,
+                                                  int64_t ldz, T* __restrict__ dz, int64_t lddz,
+                                                  const int64_t* __restrict__ offsets, int32_t groups, int32_t rows,
+                                                  int32_t unit, int32_t out, int act, int lanes,
+                                                  float* __restrict__ part) {
+  constexpr int K = kChunk<T>;
+  __shared__ float s[256][K + 1];
+  const Span sp = find_span(offsets, groups, rows, unit, blockIdx.x);
+  if (sp.e < 0) return;
+  const int cl = threadIdx.x % lanes, rl = threadIdx.x / lanes, col = (blockIdx.y * lanes + cl) * K;
+  const int n = std::min(K, std::max(0, out - col));
+  float sum[K];
+#pragma unroll
+  for (int i = 0; i < K; ++i) sum[i] = 0.0f;
+  if (n > 0)
+#pragma unroll 2
+    for (int r = sp.row0 + rl; r < sp.row1; r += 256 / lanes) {
+      const Chunk<T> c = load_chunk_n(dy + int64_t(r) * lddy + col, n);
+      float v[K];
+#pragma unroll
+      for (int i = 0; i < K; ++i) v[i] = float(c.v[i]);
+      if (dz != nullptr) {
+        const Chunk<T> zc = load_chunk_n(z + int64_t(r) * ldz + col, n);
+        Chunk<T> o;
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+          v[i] *= act_slope<T>(float(zc.v[i]), act);
+          o.v[i] = T(v[i]);
+        }
+        store_chunk(dz + int64_t(r) * lddz + col, o);   // lddz is whole chunks: the padding is written too
+      }
+#pragma unroll
+      for (int i = 0; i < K; ++i) sum[i] += v[i];
+    }
+  if (part == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < K; ++i) s[threadIdx.x][i] = sum[i];
+  __syncthreads();
+  for (int step = 128; step >= lanes; step >>= 1) {
+    if (int(threadIdx.x) < step)
+#pragma unroll
+      for (int i = 0; i < K; ++i) s[threadIdx.x][i] += s[threadIdx.x + step][i];
+    __syncthreads();
+  }
+  if (rl == 0)
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+      if (i < n) part[int64_t(blockIdx.x) * out + col + i] = s[threadIdx.x][i];
+}
+
+// Sums a group's planes of `size` values, in order.  Groups of one plane
+// were written by the product itself where `whole` says so; empty ones are 0.
+template <typename O>
+__global__ __launch_bounds__(256) void k_join(const float* __restrict__ part, const int64_t* __restrict__ offsets,
+                                              int32_t groups, int32_t rows, int32_t unit, int64_t size, bool whole,
+                                              O* __restrict__ out) {
+  const Span s = group_span(offsets, groups, rows, unit, blockIdx.y);
+  if (whole && s.slots == 1) return;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < size; i += int64_t(gridDim.x) * 256) {
+    float v = 0.0f;
+#pragma unroll 8
+    for (int t = 0; t < s.slots; ++t) v += part[(int64_t(s.slot0) + t) * size + i];
+    out[int64_t(blockIdx.y) * size + i] = O(v);
+  }
+}
+
+// --- launch ----------------------------------------------------------------------------------------
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// Stretches of at most `unit` rows that `rows` rows in `groups` groups can make.
+inline int64_t max_slots(int64_t rows, int32_t groups, int64_t unit) {
+  if (groups == 0) return ceil_div(rows, unit);
+  return rows / unit + std::min<int64_t>(groups, rows);
+}
+
+template <typename T, Mode MODE, int BM, int BN, int WM, int WN>
+void go_product(ProductArgs p, hipStream_t st) {
+  p.tiles_n = int32_t(ceil_div(p.n, BN));
+  int64_t grid;
+  if (MODE == kDw) {
+    p.tiles = int32_t(ceil_div(p.m, BM)) * p.tiles_n;
+    grid = max_slots(p.rows, p.groups, p.unit) * p.tiles;
+  } else {
+    p.unit = BM;
+    p.tiles = p.tiles_n;
+    grid = max_slots(p.rows, p.groups, BM) * p.tiles_n;
+  }
+  k_product<T, MODE, BM, BN, WM, WN><<<int(grid), 64 * WM * WN, 0, st>>>(p);
+}
+
+template <typename T, Mode MODE>
+void run_rows(const ProductArgs& p, hipStream_t st) {
+  const int64_t big = max_slots(p.rows, p.groups, 128) * ceil_div(p.n, 128);
+  if (big >= 256)
+    go_product<T, MODE, 128, 128, 2, 2>(p, st);
+  else
+    go_product<T, MODE, 64, 64, 2, 2>(p, st);
+}
+
+// Rows of a stretch of db: enough workgroups to fill the chip.
+inline int32_t db_unit(int64_t rows, int32_t out, int chunk) {
+  const int64_t across = ceil_div(out, 64 * chunk);
+  return int32_t(std::max<int64_t>(64, ceil_div(ceil_div(rows * across, 2048), 64) * 64));
+}
+// Rows of a stretch of dw.
+inline int32_t dw_unit(int64_t rows, int32_t in, int32_t out) {
+  const int64_t tiles = ceil_div(out, 128) * ceil_div(in, 128);
+  return int32_t(std::max<int64_t>(256, ceil_div(ceil_div(rows * tiles, 768), 64) * 64));
+}
+inline int64_t dz_ld(int32_t out, int chunk) { return ceil_div(out, chunk) * chunk; }
+
+struct BwdSpace {
+  size_t dz, db, dw, total;
+};
+template <typename T>
+BwdSpace bwd_space(int64_t rows, int32_t in, int32_t out, int32_t groups, int act) {
+  BwdSpace s;
+  s.dz = act == kActNone ? 0 : align_up(size_t(rows) * dz_ld(out, kChunk<T>) * sizeof(T), 256);
+  s.db = align_up(size_t(max_slots(rows, groups, db_unit(rows, out, kChunk<T>))) * out * 4, 256);
+  s.dw = align_up(size_t(max_slots(rows, groups, dw_unit(rows, in, out))) * out * in * 4, 256);
+  s.total = s.dz + s.db + s.dw;
+  return s;
+}
+
+template <typename T>
+hipError_t linear_fwd(const LinearArgs& a, hipStream_t st) {
+  ProductArgs p{};
+  p.a = a.x;
+  p.lda = a.ldx;
+  p.b = a.w;
+  p.ldb = a.ldw;
+  p.b_group = int64_t(a.out) * a.ldw;
+  p.offsets = a.offsets;
+  p.rows = a.rows;
+  p.groups = a.groups;
+  p.n = a.out;
+  p.k = a.in;
+  p.bias = a.bias;
+  p.residual = a.residual;
+  p.ldr = a.ldr;
+  p.out = a.y;
+  p.ldo = a.ldy;
+  p.z = a.z;
+  p.ldz = a.ldz;
+  p.act = a.act;
+  run_rows<T, kFwd>(p, st);
+  return hipGetLastError();
+}
+
+template <typename O>
+void join(const float* part, const LinearArgs& a, int32_t unit, int64_t size, bool whole, O* out, hipStream_t st) {
+  const int64_t blocks = std::min<int64_t>(ceil_div(size, 256), 4096);
+  k_join<O><<<dim3(int(blocks), std::max(1, a.groups)), 256, 0, st>>>(part, a.offsets, a.groups, a.rows, unit, size,
+                                                                     whole, out);
+}
+
+template <typename T>
+hipError_t linear_bwd(const LinearArgs& a, char* ws, hipStream_t st) {
+  const BwdSpace space = bwd_space<T>(a.rows, a.in, a.out, a.groups, a.act);
+  T* dz = reinterpret_cast<T*>(ws);
+  float* db_part = reinterpret_cast<float*>(ws + space.dz);
+  float* dw_part = reinterpret_cast<float*>(ws + space.dz + space.db);
+  const int32_t unit_b = db_unit(a.rows, a.out, kChunk<T>), unit_w = dw_unit(a.rows, a.in, a.out);
+  const bool slope = a.act != kActNone;
+  const T* g = slope ? dz : static_cast<const T*>(a.dy);
+  const int64_t ldg = slope ? dz_ld(a.out, kChunk<T>) : a.lddy;
+  if (a.rows > 0 && (slope || a.db != nullptr)) {
+    int lanes = 1;
+    while (lanes < 64 && lanes * kChunk<T> < a.out) lanes *= 2;
+    const dim3 grid(int(max_slots(a.rows, a.groups, unit_b)), int(ceil_div(a.out, lanes * kChunk<T>)));
+    k_act_grad<T><<<grid, 256, 0, st>>>(static_cast<const T*>(a.dy), a.lddy, static_cast<const T*>(a.z), a.ldz,
+                                        slope ? dz : nullptr, ldg, a.offsets, a.groups, a.rows, unit_b, a.out, a.act,
+                                        lanes, a.db != nullptr ? db_part : nullptr);
+  }
+  if (a.db != nullptr) join<float>(db_part, a, unit_b, a.out, false, a.db, st);
+  ProductArgs p{};
+  p.a = g;
+  p.lda = ldg;
+  p.offsets = a.offsets;
+  p.rows = a.rows;
+  p.groups = a.groups;
+  if (a.dx != nullptr && a.rows > 0) {
+    ProductArgs q = p;
+    q.b = a.w;
+    q.ldb = a.ldw;
+    q.b_group = int64_t(a.out) * a.ldw;
+    q.n = a.in;
+    q.k = a.out;
+    q.out = a.dx;
+    q.ldo = a.lddx;
+    run_rows<T, kDx>(q, st);
+  }
+  if (a.dw != nullptr) {
+    ProductArgs q = p;
+    q.b = a.x;
+    q.ldb = a.ldx;
+    q.m = a.out;
+    q.n = a.in;
+    q.unit = unit_w;
+    q.out = a.dw;
+    q.out_f32 = a.dw_f32;
+    q.ldo = a.in;
+    q.part = dw_part;
+    if (a.rows > 0) {
+      go_product<T, kDw, 128, 128, 2, 2>(q, st);
+    }
+    const int64_t size = int64_t(a.out) * a.in;
+    if (a.dw_f32)
+      join<float>(dw_part, a, unit_w, size, true, static_cast<float*>(a.dw), st);
+    else
+      join<T>(dw_part, a, unit_w, size, true, static_cast<T*>(a.dw), st);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace net
+}  // namespace gs

@@ -111,8 +111,29 @@ typedef enum gs_op {
   GS_OP_VIEW_OVERLAP = 5,
   GS_OP_PACK = 6,
   GS_OP_DENSIFY = 7,
-  GS_OP_PREPROCESS_VIEWS = 8
+  GS_OP_PREPROCESS_VIEWS = 8,
+  GS_OP_LAYER_NORM_BWD = 9
 } gs_op;
+
+/* Storage types of the network operators (gs_layer_norm_*, gs_linear_*,
+ * gs_grouped_linear_*); every sum, statistic and epilogue is fp32. */
+typedef enum gs_type {
+  GS_TYPE_BF16 = 0,
+  GS_TYPE_F16 = 1,
+  GS_TYPE_F32 = 2
+} gs_type;
+
+/* Activations: v; max(v, 0); v / (1 + e^-v); v (1 + erf(v / sqrt 2)) / 2 */
+typedef enum gs_act {
+  GS_ACT_NONE = 0,
+  GS_ACT_RELU = 1,
+  GS_ACT_SILU = 2,
+  GS_ACT_GELU = 3
+} gs_act;
+
+/* widest layer or norm, and most groups, of the network operators */
+#define GS_MAX_NET_DIM 65536
+#define GS_MAX_NET_GROUPS 1024
 
 /* Static description of a status code (never NULL). */
 const char* gs_status_string(int status);
@@ -131,6 +152,8 @@ int gs_version(void);
  *   GS_OP_PACK        n, width = num_blocks
  *   GS_OP_DENSIFY     n
  *   GS_OP_PREPROCESS_VIEWS n, width = num_views
+ *   GS_OP_LAYER_NORM_BWD n = rows, width
+ * (gs_linear_bwd and gs_grouped_linear_bwd: gs_linear_workspace_size.)
  * Unused arguments are ignored.  The workspace is caller-owned device
  * memory, 256-byte aligned; its contents need no initialisation and are
  * scratch between calls. */
@@ -634,6 +657,119 @@ gs_status gs_densify(const float* params, const float* m, const float* v, int64_
                      float log_scale_threshold, float logit_threshold, float log_shrink, float* out_params,
                      float* out_m, float* out_v, int64_t ld_out, int64_t* out_n, void* workspace,
                      size_t workspace_bytes, void* stream);
+
+/* ---- network operators ------------------------------------------------------
+ * The layers of a network that decodes a Gaussian's parameters from learned
+ * features: a norm, a linear layer, and a linear layer whose weights go by
+ * group (one head per block of the scene; group bounds like gs_pack_records'
+ * send_offsets).  The pages hold no such operator: these are
+ * additions of this library.
+ *
+ * Matrices are row-major with a leading dimension in elements (>= the row's
+ * width; any value, any element alignment: 16-byte aligned rows are the
+ * fastest).  Storage is `type` (gs_type); bias, gamma, beta, the statistics
+ * and db are fp32.  All calls are asynchronous on `stream`, allocate
+ * nothing, use no atomics (the same call gives the same bits) and may be
+ * captured into a graph.  rows = 0 is valid: gradients of weights are then
+ * 0 and nothing else is written.  Outputs may not overlap inputs, except
+ * that y may be residual itself (same pointer, same leading dimension).
+ * NaN and infinity pass through as in the formulas; relu'(NaN) is 0. */
+
+/* Layer norm of each row: mean, variance (of the whole row, biased),
+ * rstd = 1 / sqrt(variance + eps), y = gamma (x - mean) rstd + beta.
+ *   x            device, [rows][ldx]
+ *   gamma, beta  device, [width] fp32, or NULL for 1 and 0
+ *   y            device out, [rows][ldy]
+ *   mean, rstd   device out, [rows] fp32, or NULL
+ * Errors: GS_ERR_INVALID_ARG for an unknown type, rows outside [0, 2^31),
+ * width outside [1, GS_MAX_NET_DIM], a leading dimension below width, eps
+ * negative or not finite, a NULL or misaligned array. */
+gs_status gs_layer_norm_fwd(const void* x, int64_t ldx, const float* gamma, const float* beta, int64_t rows,
+                            int32_t width, float eps, int32_t type, void* y, int64_t ldy, float* mean, float* rstd,
+                            void* stream);
+
+/* Its backward pass: xh = (x - mean) rstd, g = dy gamma,
+ * dx = rstd (g - mean(g) - xh mean(g xh)) + dres,
+ * dgamma = sum over rows of dy xh, dbeta = sum over rows of dy.
+ *   dy           device, [rows][lddy]
+ *   mean, rstd   device, as the forward pass wrote them
+ *   dres         device, [rows][lddres] added into dx (the gradient that
+ *                reaches x past the norm, as a residual connection's), or NULL
+ *   dx           device out, [rows][lddx], or NULL
+ *   dgamma, dbeta  device out, [width] fp32, or NULL
+ *   workspace    device, >= gs_workspace_size(GS_OP_LAYER_NORM_BWD, rows,
+ *                width) bytes, 256-byte aligned
+ * Errors: as the forward pass, and a workspace that is too small. */
+gs_status gs_layer_norm_bwd(const void* x, int64_t ldx, const void* dy, int64_t lddy, const float* gamma,
+                            const float* mean, const float* rstd, const void* dres, int64_t lddres, int64_t rows,
+                            int32_t width, int32_t type, void* dx, int64_t lddx, float* dgamma, float* dbeta,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Linear layer with its epilogue: z = x w^T + bias, y = act(z) + residual.
+ *   x            device, [rows][ldx], width in
+ *   w            device, [out][ldw], width in
+ *   bias         device, [out] fp32, or NULL
+ *   residual     device, [rows][ldr], width out, or NULL
+ *   y            device out, [rows][ldy], width out
+ *   z            device out, [rows][ldz], width out: the value before the
+ *                activation, for the backward pass, or NULL
+ * Errors: GS_ERR_INVALID_ARG for an unknown type or activation, rows
+ * outside [0, 2^31), in or out outside [1, GS_MAX_NET_DIM], a leading
+ * dimension below its width, sizes past a launch grid, a NULL or misaligned
+ * array. */
+gs_status gs_linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, const float* bias,
+                        const void* residual, int64_t ldr, int64_t rows, int32_t in, int32_t out, int32_t type,
+                        int32_t act, void* y, int64_t ldy, void* z, int64_t ldz, void* stream);
+
+/* Workspace bytes of gs_linear_bwd (num_groups 0) and
+ * gs_grouped_linear_bwd (host, no device work). */
+gs_status gs_linear_workspace_size(int64_t rows, int32_t in, int32_t out, int32_t num_groups, int32_t type,
+                                   int32_t act, size_t* bytes);
+
+/* Its backward pass: dz = dy act'(z), dx = dz w, dw = dz^T x, db = sum over
+ * rows of dz.  (The residual's gradient is dy itself.)
+ *   z            device, [rows][ldz], as the forward pass wrote it; not read
+ *                (may be NULL) for GS_ACT_NONE
+ *   dy           device, [rows][lddy], width out
+ *   dx           device out, [rows][lddx], width in, or NULL
+ *   dw           device out, [out][in] without padding, of type dw_type
+ *                (`type` or GS_TYPE_F32), or NULL
+ *   db           device out, [out] fp32, or NULL
+ *   workspace    device, >= gs_linear_workspace_size(...) bytes, 256-byte
+ *                aligned
+ * Errors: as the forward pass, a dw_type that is neither, and a workspace
+ * that is too small. */
+gs_status gs_linear_bwd(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* z, int64_t ldz,
+                        const void* dy, int64_t lddy, int64_t rows, int32_t in, int32_t out, int32_t type,
+                        int32_t act, void* dx, int64_t lddx, void* dw, int32_t dw_type, float* db, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* The linear layer with weights by group: rows offsets[e] ..
+ * offsets[e + 1] - 1 use w[e] and bias[e].
+ *   w            device, [num_groups][out][ldw]
+ *   bias         device, [num_groups][out] fp32, or NULL
+ *   offsets      device, [num_groups + 1] int64, ascending; read on the
+ *                device.  Bounds outside [0, rows] are clamped and a bound
+ *                below one before it counts as that one, so any contents
+ *                are safe.  Rows in no group (before offsets[0], from
+ *                offsets[num_groups] on) are not written.
+ * Errors: as gs_linear_fwd, and num_groups outside [1, GS_MAX_NET_GROUPS]
+ * or offsets NULL or misaligned. */
+gs_status gs_grouped_linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, const float* bias,
+                                const int64_t* offsets, int32_t num_groups, const void* residual, int64_t ldr,
+                                int64_t rows, int32_t in, int32_t out, int32_t type, int32_t act, void* y,
+                                int64_t ldy, void* z, int64_t ldz, void* stream);
+
+/* Its backward pass: dw[e] and db[e] over the rows of group e (0 for an
+ * empty group); dx of rows in no group is not written.
+ *   dw           device out, [num_groups][out][in] without padding
+ *   db           device out, [num_groups][out] fp32
+ * The rest and the errors: as gs_linear_bwd and gs_grouped_linear_fwd. */
+gs_status gs_grouped_linear_bwd(const void* x, int64_t ldx, const void* w, int64_t ldw, const int64_t* offsets,
+                                int32_t num_groups, const void* z, int64_t ldz, const void* dy, int64_t lddy,
+                                int64_t rows, int32_t in, int32_t out, int32_t type, int32_t act, void* dx,
+                                int64_t lddx, void* dw, int32_t dw_type, float* db, void* workspace,
+                                size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
