@@ -11,6 +11,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 
 #include "net_common.hpp"
 
@@ -166,6 +167,53 @@ struct Stage {
   }
 };
 
+// Global -> LDS without registers, for operands of whole aligned chunks: the
+// buffer load writes lane i's 16 bytes at 16 i of the wave's kilobyte, so the
+// permutation of the chunks is done on the addresses.  Rows past the end
+// lie past the buffer's size and read as 0; across k, columns past the end
+// hold whatever follows in the row (their results are never stored).
+template <typename T, int D, bool ACROSS, int THREADS>
+struct Direct {
+  static constexpr int kPer = D * 8 / THREADS;
+  static constexpr int kAcross = ACROSS ? D / kChunk<T> : 8;
+  static_assert(ACROSS || (THREADS / 8) % 8 == 0, "one chunk for all of a thread's rows");
+  uint32_t off[kPer];
+  int chunk;   // along k: the chunk of the row this thread fetches
+  __device__ __forceinline__ void init(int64_t ld, int tid) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int id = j * THREADS + tid, r = id / kAcross;
+      const int c = (id % kAcross) ^ (ACROSS ? across_swizzle<T, D>(r) : (r & 7));
+      off[j] = uint32_t(r) * uint32_t(ld * sizeof(T)) + uint32_t(c) * 16u;
+      if (j == 0) chunk = c;
+    }
+  }
+  // `rows`, `cols`: the operand's extent from p on (both > 0), cols in whole
+  // chunks along k.
+  __device__ __forceinline__ void load(const T* p, int64_t ld, int rows, int cols, char* tile, int wave) const {
+#ifdef __HIP_DEVICE_COMPILE__   // the host pass does not know the buffer builtins
+    constexpr int most_rows = ACROSS ? kStep<T> : D, most_cols = ACROSS ? D : kStep<T>;
+    const int r = rows < most_rows ? rows : most_rows, c = cols < most_cols ? cols : most_cols;
+    // whole chunks: an aligned chunk that holds a value of the row lies inside its padding
+    const int whole = (c + kChunk<T> - 1) / kChunk<T> * kChunk<T>;
+    const uint32_t bytes = uint32_t(((r - 1) * ld + whole) * int64_t(sizeof(T)));
+    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(p), 0, bytes, 0x00020000);
+    const bool past = !ACROSS && chunk * kChunk<T> >= cols;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rsrc, (__attribute__((address_space(3))) void*)(tile + j * THREADS * 16 + wave * 1024), 16,
+          past ? 0xfffffff0u : off[j], 0, 0, 0);
+#endif
+  }
+};
+
+// Every wave's loads into LDS have landed and its reads of LDS are done,
+// then the workgroup meets.
+__device__ __forceinline__ void tile_barrier() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 // --- epilogue -----------------------------------------------------------------------------
 
 // Eight values of one output row from column `col`, `n` of them real.
@@ -222,26 +270,52 @@ __device__ __forceinline__ void emit(const ProductArgs& p, const float* __restri
 
 // --- the product ------------------------------------------------------------------------------
 
+// Consecutive workgroups go round the 8 XCDs, each with an L2 of its own:
+// hand every XCD one contiguous share of the tiles instead.
+__device__ __forceinline__ int xcd_tile(int id, int n) {
+  const int x = id & 7, share = n >> 3, more = n & 7;
+  return x * share + std::min(x, more) + (id >> 3);
+}
+
+// What one wave does with a k step in LDS.
+template <typename T, int BM, int BN, bool A_ACROSS, bool B_ACROSS, int FM, int FN>
+__device__ __forceinline__ void multiply_step(const char* ta, const char* tb, int am, int bn, int lane,
+                                              f32x4 (&acc)[FM][FN]) {
+#pragma unroll
+  for (int kk = 0; kk < 2; ++kk) {
+    typename Frag<T>::V fa[FM], fb[FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) fa[i] = read_frag<T, BM, A_ACROSS>(ta, am + 16 * i, kk, lane);
+#pragma unroll
+    for (int j = 0; j < FN; ++j) fb[j] = read_frag<T, BN, B_ACROSS>(tb, bn + 16 * j, kk, lane);
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] = Frag<T>::mma(fb[j], fa[i], acc[i][j]);
+  }
+}
+
 // BM x BN outputs a workgroup, WM x WN waves.  The n side is the first
 // operand of the matrix instruction, so that a lane's four results are
 // neighbours along n; each wave then turns 16 rows at a time through LDS
-// into whole chunks of output rows.
-template <typename T, Mode MODE, int BM, int BN, int WM, int WN>
+// into whole chunks of output rows.  DIRECT: both operands in whole aligned
+// chunks, loaded straight into one of two LDS stages while the other is
+// multiplied; else through registers, at any alignment.
+template <typename T, Mode MODE, int BM, int BN, int WM, int WN, bool DIRECT>
 __global__ __launch_bounds__(64 * WM * WN) void k_product(ProductArgs p) {
   constexpr int THREADS = 64 * WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
   constexpr bool A_ACROSS = MODE == kDw, B_ACROSS = MODE != kFwd;
   constexpr int kPatch = TN + 4;   // floats of a patch row: 4 more keep its 16-byte writes off each other's banks
-  constexpr int kTiles = (BM + BN) * 128, kPatches = WM * WN * 16 * kPatch * 4;
-  __shared__ __align__(16) char lds[kTiles > kPatches ? kTiles : kPatches];
-  char* const ta = lds;
-  char* const tb = lds + BM * 128;
+  constexpr int kTiles = (BM + BN) * 128;
+  extern __shared__ __align__(16) char lds[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
 
   // Which tile.  kFwd, kDx: the height index picks group and rows; kDw: the
   // stretch does, and the tile inside the plane is apart from it.
-  const int stretch = MODE == kDw ? int(blockIdx.x) / p.tiles : int(blockIdx.x) / p.tiles_n;
-  const int within = MODE == kDw ? int(blockIdx.x) % p.tiles : int(blockIdx.x) % p.tiles_n;
+  const int tile = xcd_tile(blockIdx.x, gridDim.x);
+  const int stretch = MODE == kDw ? tile / p.tiles : tile / p.tiles_n;
+  const int within = MODE == kDw ? tile % p.tiles : tile % p.tiles_n;
   const Span s = find_span(p.offsets, p.groups, p.rows, p.unit, stretch);
   if (s.e < 0) return;
   const int m0 = MODE == kDw ? within / p.tiles_n * BM : 0;
@@ -261,34 +335,50 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product(ProductArgs p) {
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  Stage<T, BM, A_ACROSS, THREADS> sa;
-  Stage<T, BN, B_ACROSS, THREADS> sb;
-  sa.load(a, p.lda, A_ACROSS ? k_all : m_left, A_ACROSS ? m_left : k_all, tid);
-  sb.load(b, p.ldb, B_ACROSS ? k_all : n_left, B_ACROSS ? n_left : k_all, tid);
-  for (int k0 = 0; k0 < k_all; k0 += kStep<T>) {
-    sa.store(ta, tid);
-    sb.store(tb, tid);
-    __syncthreads();
-    const int left = k_all - k0 - kStep<T>;
-    if (left > 0) {   // the next step's loads fly while this one is multiplied
-      a += step_a;
-      b += step_b;
-      sa.load(a, p.lda, A_ACROSS ? left : m_left, A_ACROSS ? m_left : left, tid);
-      sb.load(b, p.ldb, B_ACROSS ? left : n_left, B_ACROSS ? n_left : left, tid);
+  if constexpr (DIRECT) {
+    Direct<T, BM, A_ACROSS, THREADS> da;
+    Direct<T, BN, B_ACROSS, THREADS> db;
+    da.init(p.lda, tid);
+    db.init(p.ldb, tid);
+    da.load(a, p.lda, A_ACROSS ? k_all : m_left, A_ACROSS ? m_left : k_all, lds, wave);
+    db.load(b, p.ldb, B_ACROSS ? k_all : n_left, B_ACROSS ? n_left : k_all, lds + BM * 128, wave);
+    int stage = 0;
+    for (int left = k_all; left > 0; left -= kStep<T>) {
+      tile_barrier();
+      const int next = left - kStep<T>;
+      if (next > 0) {
+        a += step_a;
+        b += step_b;
+        char* t = lds + (stage ^ 1) * kTiles;
+        da.load(a, p.lda, A_ACROSS ? next : m_left, A_ACROSS ? m_left : next, t, wave);
+        db.load(b, p.ldb, B_ACROSS ? next : n_left, B_ACROSS ? n_left : next, t + BM * 128, wave);
+      }
+      const char* t = lds + stage * kTiles;
+      multiply_step<T, BM, BN, A_ACROSS, B_ACROSS, FM, FN>(t, t + BM * 128, wm * TM, wn * TN, lane, acc);
+      stage ^= 1;
     }
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      typename Frag<T>::V fa[FM], fb[FN];
-#pragma unroll
-      for (int i = 0; i < FM; ++i) fa[i] = read_frag<T, BM, A_ACROSS>(ta, wm * TM + 16 * i, kk, lane);
-#pragma unroll
-      for (int j = 0; j < FN; ++j) fb[j] = read_frag<T, BN, B_ACROSS>(tb, wn * TN + 16 * j, kk, lane);
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = Frag<T>::mma(fb[j], fa[i], acc[i][j]);
+    tile_barrier();
+  } else {
+    char* const ta = lds;
+    char* const tb = lds + BM * 128;
+    Stage<T, BM, A_ACROSS, THREADS> sa;
+    Stage<T, BN, B_ACROSS, THREADS> sb;
+    sa.load(a, p.lda, A_ACROSS ? k_all : m_left, A_ACROSS ? m_left : k_all, tid);
+    sb.load(b, p.ldb, B_ACROSS ? k_all : n_left, B_ACROSS ? n_left : k_all, tid);
+    for (int k0 = 0; k0 < k_all; k0 += kStep<T>) {
+      sa.store(ta, tid);
+      sb.store(tb, tid);
+      __syncthreads();
+      const int left = k_all - k0 - kStep<T>;
+      if (left > 0) {   // the next step's loads fly while this one is multiplied
+        a += step_a;
+        b += step_b;
+        sa.load(a, p.lda, A_ACROSS ? left : m_left, A_ACROSS ? m_left : left, tid);
+        sb.load(b, p.ldb, B_ACROSS ? left : n_left, B_ACROSS ? n_left : left, tid);
+      }
+      multiply_step<T, BM, BN, A_ACROSS, B_ACROSS, FM, FN>(ta, tb, wm * TM, wn * TN, lane, acc);
+      __syncthreads();
     }
-    __syncthreads();
   }
 
   const float* bias = nullptr;
@@ -410,6 +500,37 @@ inline int64_t max_slots(int64_t rows, int32_t groups, int64_t unit) {
   return rows / unit + std::min<int64_t>(groups, rows);
 }
 
+// Both operands in whole 16-byte chunks, near enough for 32-bit offsets.
+template <typename T>
+bool direct_ok(const ProductArgs& p, Mode mode) {
+  const auto whole = [](const void* q, int64_t ld) {
+    return (reinterpret_cast<uintptr_t>(q) & 15u) == 0 && ld % kChunk<T> == 0 && ld <= (1 << 20);
+  };
+  return whole(p.a, p.lda) && whole(p.b, p.ldb) && (mode == kDw || p.k % kChunk<T> == 0);
+}
+
+template <typename T, Mode MODE, int BM, int BN, int WM, int WN, bool DIRECT>
+void go_tile(const ProductArgs& p, int64_t grid, hipStream_t st) {
+  constexpr int tiles = (BM + BN) * 128, patches = WM * WN * 16 * (BN / WN + 4) * 4;
+  constexpr int most = std::max(2 * tiles, patches);
+  if constexpr (most > 65536) {
+    // more LDS than a launch gets unasked; once per device
+    static std::atomic<uint64_t> asked{0};
+    int dev = 0;
+    (void)hipGetDevice(&dev);
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if ((asked.load(std::memory_order_relaxed) & bit) == 0) {
+      (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&k_product<T, MODE, BM, BN, WM, WN, DIRECT>),
+                                hipFuncAttributeMaxDynamicSharedMemorySize, most);
+      asked.fetch_or(bit, std::memory_order_relaxed);
+    }
+  }
+  // one k step needs one stage, and leaves LDS for more workgroups
+  const int steps = MODE == kDw ? 2 : (p.k > kStep<T> ? 2 : 1);
+  const int lds = std::max(patches, tiles * (DIRECT ? steps : 1));
+  k_product<T, MODE, BM, BN, WM, WN, DIRECT><<<int(grid), 64 * WM * WN, lds, st>>>(p);
+}
+
 template <typename T, Mode MODE, int BM, int BN, int WM, int WN>
 void go_product(ProductArgs p, hipStream_t st) {
   p.tiles_n = int32_t(ceil_div(p.n, BN));
@@ -422,13 +543,19 @@ void go_product(ProductArgs p, hipStream_t st) {
     p.tiles = p.tiles_n;
     grid = max_slots(p.rows, p.groups, BM) * p.tiles_n;
   }
-  k_product<T, MODE, BM, BN, WM, WN><<<int(grid), 64 * WM * WN, 0, st>>>(p);
+  if (direct_ok<T>(p, MODE))
+    go_tile<T, MODE, BM, BN, WM, WN, true>(p, grid, st);
+  else if constexpr (BM <= 128 && BN <= 128)
+    go_tile<T, MODE, BM, BN, WM, WN, false>(p, grid, st);
 }
 
 template <typename T, Mode MODE>
 void run_rows(const ProductArgs& p, hipStream_t st) {
+  const int64_t large = max_slots(p.rows, p.groups, 256) * ceil_div(p.n, 256);
   const int64_t big = max_slots(p.rows, p.groups, 128) * ceil_div(p.n, 128);
-  if (big >= 256)
+  if (large >= 256 && p.k >= 512 && direct_ok<T>(p, MODE))
+    go_product<T, MODE, 256, 256, 2, 4>(p, st);
+  else if (big >= 256)
     go_product<T, MODE, 128, 128, 2, 2>(p, st);
   else
     go_product<T, MODE, 64, 64, 2, 2>(p, st);
