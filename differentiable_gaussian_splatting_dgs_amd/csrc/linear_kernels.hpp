@@ -216,55 +216,38 @@ __device__ __forceinline__ void tile_barrier() {
 
 // --- epilogue -----------------------------------------------------------------------------
 
-// Eight values of one output row from column `col`, `n` of them real.
+// Eight values of an output row, as chunks of storage.
 template <typename T>
-__device__ __forceinline__ void emit(const ProductArgs& p, const float* __restrict__ bias, int64_t row, int col, int n,
-                                     float (&v)[8], float* __restrict__ plane) {
-  if (plane != nullptr) {   // partial product
-    float* o = plane + row * p.n + col;
+struct Eight {
+  static constexpr int kParts = 8 / kChunk<T>;
+  Chunk<T> c[kParts];
+  __device__ __forceinline__ float get(int i) const { return float(c[i / kChunk<T>].v[i % kChunk<T>]); }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      Chunk<float> c;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) c.v[i] = v[4 * h + i];
-      if (n > 4 * h) store_chunk_n(o + 4 * h, c, n - 4 * h);
-    }
-    return;
+    for (int i = 0; i < 8; ++i) c[i / kChunk<T>].v[i % kChunk<T>] = T(v[i]);
   }
-  if (bias != nullptr) {
+  // n values at p (n < 8 in the last columns only)
+  __device__ __forceinline__ void load(const T* __restrict__ p, int n) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) v[i] += bias[col + i];
+    for (int h = 0; h < kParts; ++h) c[h] = load_chunk_n(p + h * kChunk<T>, n - h * kChunk<T>);
   }
-  constexpr int K = kChunk<T>;
+  __device__ __forceinline__ void store(T* __restrict__ p, int n) const {
 #pragma unroll
-  for (int h = 0; h < 8 / K; ++h) {
-    if (n <= K * h) break;
-    Chunk<T> c;
-    if (p.z != nullptr) {
+    for (int h = 0; h < kParts; ++h) store_chunk_n(p + h * kChunk<T>, c[h], n - h * kChunk<T>);
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void act_eight(float (&v)[8], int act) {   // act is uniform: one branch for the eight
+  if (act == kActRelu) {
 #pragma unroll
-      for (int i = 0; i < K; ++i) c.v[i] = T(v[K * h + i]);
-      store_chunk_n(static_cast<T*>(p.z) + row * p.ldz + col + K * h, c, n - K * h);
-    }
-    if (p.act != kActNone) {
+    for (int i = 0; i < 8; ++i) v[i] = act_apply<T>(v[i], kActRelu);
+  } else if (act == kActSilu) {
 #pragma unroll
-      for (int i = 0; i < K; ++i) v[K * h + i] = act_apply<T>(v[K * h + i], p.act);
-    }
-    if (p.residual != nullptr) {
-      c = load_chunk_n(static_cast<const T*>(p.residual) + row * p.ldr + col + K * h, n - K * h);
+    for (int i = 0; i < 8; ++i) v[i] = act_apply<T>(v[i], kActSilu);
+  } else if (act == kActGelu) {
 #pragma unroll
-      for (int i = 0; i < K; ++i) v[K * h + i] += float(c.v[i]);
-    }
-    if (p.out_f32) {
-      float* o = static_cast<float*>(p.out) + row * p.ldo + col + K * h;
-#pragma unroll
-      for (int i = 0; i < K; ++i)
-        if (K * h + i < n) o[i] = v[K * h + i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < K; ++i) c.v[i] = T(v[K * h + i]);
-      store_chunk_n(static_cast<T*>(p.out) + row * p.ldo + col + K * h, c, n - K * h);
-    }
+    for (int i = 0; i < 8; ++i) v[i] = act_apply<T>(v[i], kActGelu);
   }
 }
 
@@ -381,40 +364,84 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product(ProductArgs p) {
     }
   }
 
-  const float* bias = nullptr;
+  // Epilogue: 16 rows at a time through the wave's patch.  A lane has the
+  // same eight columns in every pass, so their bias stays in registers; the
+  // residual's chunks are all asked for before the first is needed.
+  constexpr int kAcross = TN / 8, kRows = 64 / kAcross, kPasses = 16 / kRows;   // lanes of a row, rows a pass
+  constexpr int kBatch = std::min(FM, 16 / (kPasses * Eight<T>::kParts));       // fragments whose residual is in flight
+  const int col = wn * TN + (lane % kAcross) * 8, n = std::min(8, n_left - col);
+  const int64_t row0 = MODE == kDw ? m0 : s.row0;
   float* plane = nullptr;
-  int64_t row0 = MODE == kDw ? m0 : s.row0;
-  if (MODE == kFwd && p.bias != nullptr) bias = p.bias + int64_t(s.e) * p.n;
-  ProductArgs q = p;
+  void* out = p.out;
   if constexpr (MODE == kDw) {
     if (p.part != nullptr && s.slots > 1)
       plane = p.part + int64_t(stretch) * p.m * p.n;
     else
-      q.out = p.out_f32 ? static_cast<void*>(static_cast<float*>(p.out) + int64_t(s.e) * p.m * p.ldo)
-                        : static_cast<void*>(static_cast<T*>(p.out) + int64_t(s.e) * p.m * p.ldo);
+      out = p.out_f32 ? static_cast<void*>(static_cast<float*>(p.out) + int64_t(s.e) * p.m * p.ldo)
+                      : static_cast<void*>(static_cast<T*>(p.out) + int64_t(s.e) * p.m * p.ldo);
+  }
+  float bias[8];
+  if constexpr (MODE == kFwd) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) bias[i] = p.bias != nullptr && i < n ? p.bias[int64_t(s.e) * p.n + n0 + col + i] : 0.0f;
   }
   float* patch = reinterpret_cast<float*>(lds) + wave * 16 * kPatch;
-  constexpr int kAcross = TN / 8, kRows = 64 / kAcross;   // lanes of an output row, rows a pass
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
+  for (int i0 = 0; i0 < FM; i0 += kBatch) {
+    Eight<T> res[kBatch * kPasses];
+    if (MODE == kFwd && p.residual != nullptr) {
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
-      *reinterpret_cast<f32x4*>(patch + (lane & 15) * kPatch + 16 * j + 4 * (lane >> 4)) = acc[i][j];
-    wave_sync();
-#pragma unroll
-    for (int r = lane / kAcross; r < 16; r += kRows) {
-      const int m = wm * TM + 16 * i + r, col = wn * TN + (lane % kAcross) * 8;
-      float v[8];
-      const f32x4 lo = *reinterpret_cast<const f32x4*>(patch + r * kPatch + (lane % kAcross) * 8);
-      const f32x4 hi = *reinterpret_cast<const f32x4*>(patch + r * kPatch + (lane % kAcross) * 8 + 4);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        v[c] = lo[c];
-        v[4 + c] = hi[c];
+      for (int q = 0; q < kBatch * kPasses; ++q) {
+        const int m = wm * TM + 16 * (i0 + q / kPasses) + (q % kPasses) * kRows + lane / kAcross;
+        res[q].load(static_cast<const T*>(p.residual) + (row0 + m) * p.ldr + n0 + col, m < m_left ? n : 0);
       }
-      if (m < m_left && col < n_left) emit<T>(q, bias, row0 + m, n0 + col, std::min(8, n_left - col), v, plane);
     }
-    wave_sync();
+#pragma unroll
+    for (int i = i0; i < i0 + kBatch; ++i) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        *reinterpret_cast<f32x4*>(patch + (lane & 15) * kPatch + 16 * j + 4 * (lane >> 4)) = acc[i][j];
+      wave_sync();
+#pragma unroll
+      for (int q = 0; q < kPasses; ++q) {
+        const int r = q * kRows + lane / kAcross, m = wm * TM + 16 * i + r;
+        float v[8];
+        const f32x4 lo = *reinterpret_cast<const f32x4*>(patch + r * kPatch + (lane % kAcross) * 8);
+        const f32x4 hi = *reinterpret_cast<const f32x4*>(patch + r * kPatch + (lane % kAcross) * 8 + 4);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          v[c] = lo[c];
+          v[4 + c] = hi[c];
+        }
+        if (m >= m_left || n <= 0) continue;
+        const int64_t row = row0 + m;
+        if (MODE == kDw && (plane != nullptr || p.out_f32)) {
+          Eight<float> o;
+          o.set(v);
+          o.store(plane != nullptr ? plane + row * p.n + n0 + col : static_cast<float*>(out) + row * p.ldo + n0 + col,
+                  n);
+          continue;
+        }
+        Eight<T> o;
+        if constexpr (MODE == kFwd) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) v[c] += bias[c];
+          if (p.z != nullptr) {
+            o.set(v);
+            o.store(static_cast<T*>(p.z) + row * p.ldz + n0 + col, n);
+          }
+          act_eight<T>(v, p.act);
+          if (p.residual != nullptr) {
+            const Eight<T>& x = res[(i - i0) * kPasses + q];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) v[c] += x.get(c);
+          }
+        }
+        o.set(v);
+        o.store(static_cast<T*>(out) + row * p.ldo + n0 + col, n);
+      }
+      wave_sync();
+    }
   }
 }
 
