@@ -12,6 +12,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "net_common.hpp"
 
@@ -445,6 +446,228 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product(ProductArgs p) {
   }
 }
 
+// --- the product over many rows of a short k ---------------------------------------
+
+// For k of at most four steps: the weights are a constant of the kernel, not
+// an operand to stream.  Each of 8 waves keeps the fragments of its 32 output
+// columns in registers (KS * 16 of them) and the workgroup walks its share of
+// the row tiles, 16 KB of rows a tile, three LDS stages deep, so that rows are
+// read from HBM once and loads are always in flight.  Every tile issues the
+// same number of memory instructions (buffer loads and stores, whose rows
+// past the end are dropped by the buffer's size), which lets the wait for a
+// stage count them instead of draining the stores of the tile before.
+// 128 / KS rows a tile, WM x WN = 8 waves of 128 / KS / WM x 32 outputs.
+// Bound by HBM: 1,000,000 rows, bf16: 256 -> 256 213 us, 4.8 TB/s (340 us with
+// 128 x 128 tiles, whose loads stop for the epilogue); 64 -> 256 with gelu
+// and z 270 us, 4.3 TB/s (324 us).
+
+template <int N>
+__device__ __forceinline__ void rows_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N < 63 ? N : 63) : "memory");   // the counter holds 6 bits
+}
+
+#ifdef __HIP_DEVICE_COMPILE__   // the host pass does not know the buffer builtins
+// A wave-uniform address range for buffer instructions.
+template <typename T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(T* p, int64_t ld, int rows, int cols) {
+  const uint32_t bytes = rows > 0 ? uint32_t(((rows - 1) * ld + cols) * int64_t(sizeof(T))) : 0u;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<std::remove_const_t<T>*>(p), 0, bytes, 0x00020000);
+}
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+template <typename T>
+__device__ __forceinline__ void buffer_store_eight(__amdgpu_buffer_rsrc_t r, const Eight<T>& e, uint32_t off) {
+#pragma unroll
+  for (int h = 0; h < Eight<T>::kParts; ++h)
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, e.c[h]), r, off + 16u * h, 0, 0);
+}
+template <typename T>
+__device__ __forceinline__ void buffer_load_eight(__amdgpu_buffer_rsrc_t r, Eight<T>& e, uint32_t off) {
+#pragma unroll
+  for (int h = 0; h < Eight<T>::kParts; ++h)
+    e.c[h] = __builtin_bit_cast(Chunk<T>, __builtin_amdgcn_raw_buffer_load_b128(r, off + 16u * h, 0, 0));
+}
+#endif
+
+template <typename T, Mode MODE, int KS, int WM, int WN>
+__global__ __launch_bounds__(512, 4) void k_rows(ProductArgs p, int shares) {
+#ifdef __HIP_DEVICE_COMPILE__
+  constexpr int BM = 128 / KS, TM = BM / WM, FM = TM / 16, FB = std::min(FM, 4), FN = 2, BN = WN * 32;
+  static_assert(WM * WN == 8 && TM >= 16, "8 waves of 32 columns");
+  constexpr int kStage = 16384, kStages = 3, kPatch = 36;
+  constexpr int kLoads = 2;                                  // loads of a stage a thread: 1024 chunks over 512
+  constexpr int kPlane = FM * Eight<T>::kParts;              // memory instructions of one output or residual plane
+  __shared__ __align__(16) char lds[kStages * kStage + 8 * 16 * kPatch * 4];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
+  float* patch = reinterpret_cast<float*>(lds + kStages * kStage) + wave * 16 * kPatch;
+
+  // the share of row tiles and the column tile
+  const int id = xcd_tile(blockIdx.x, gridDim.x), n0 = id % p.tiles_n * BN, share = id / p.tiles_n;
+  const int64_t total = total_slots(p.offsets, p.groups, p.rows, BM);
+  const int t0 = int(total * share / shares), t1 = int(total * (share + 1) / shares);
+  if (t0 >= t1) return;
+  const int n_left = p.n - n0;
+
+  // chunk this thread fetches: 8 chunks of a row and step, row by row, step by step
+  uint32_t off[kLoads];
+  bool in_k[kLoads];
+#pragma unroll
+  for (int j = 0; j < kLoads; ++j) {
+    const int at = j * 512 + tid, step = at / (BM * 8), r = at / 8 % BM, c = (at & 7) ^ (r & 7);
+    off[j] = uint32_t(r) * uint32_t(p.lda * sizeof(T)) + uint32_t(step * 128 + c * 16);
+    in_k[j] = (step * 8 + c) * kChunk<T> < p.k;
+    if (!in_k[j]) off[j] = 0xfffffff0u;
+  }
+  const auto fetch = [&](const Span& s, int stage) {
+    const __amdgpu_buffer_rsrc_t r = buffer_of(static_cast<const T*>(p.a) + int64_t(s.row0) * p.lda, p.lda,
+                                               s.e < 0 ? 0 : s.row1 - s.row0, p.k);
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          r, (__attribute__((address_space(3))) void*)(lds + stage * kStage + j * 8192 + wave * 1024), 16, off[j], 0, 0,
+          0);
+  };
+
+  // the tile after `s`, inside its group or in the next one
+  const auto after = [&](const Span& s, int t) {
+    if (t >= t1) return Span{-1, 0, 0, 0, 0, 0};
+    if (p.groups > 0 && t >= s.slot0 + s.slots) return find_span(p.offsets, p.groups, p.rows, BM, t);
+    Span q = s;
+    q.row0 = s.row0 + BM;
+    q.row1 = std::min(s.end, q.row0 + BM);
+    return q;
+  };
+  Span now = find_span(p.offsets, p.groups, p.rows, BM, t0), next = after(now, t0 + 1);
+  fetch(now, 0);
+  fetch(next, 1);
+
+  typename Frag<T>::V fw[KS * 2][FN];
+  float bias[8];
+  const int col = wn * 32 + (lane & 3) * 8;                  // of this lane in the epilogue
+  const bool live = col < n_left;                            // n_left is whole chunks of 8
+  int group = -1, stage = 0;
+  const int planes = 1 + (p.z != nullptr) + (p.residual != nullptr);
+
+  for (int t = t0; t < t1; ++t) {
+    // after this stage's loads come: the next stage's, and the last two
+    // tiles' epilogues (less of both at the start)
+    if (t - t0 < 2)
+      rows_barrier<kLoads>();
+    else if (planes == 1)
+      rows_barrier<kLoads + 2 * kPlane>();
+    else if (planes == 2)
+      rows_barrier<kLoads + 4 * kPlane>();
+    else
+      rows_barrier<kLoads + 6 * kPlane>();
+    const Span later = after(next, t + 2);
+    fetch(later, stage == 0 ? 2 : stage - 1);
+    asm volatile("" ::: "memory");   // the counted order: these loads, then the epilogue
+
+    if (now.e != group) {
+      group = now.e;
+      const T* w = static_cast<const T*>(p.b) + int64_t(group) * p.b_group;
+      int ln = lane;
+      asm volatile("" : "+v"(ln));   // addresses are made here, not kept through the loop
+#pragma unroll
+      for (int kk = 0; kk < KS * 2; ++kk)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          const int n = n0 + wn * 32 + 16 * j + (ln & 15), k = (4 * kk + (ln >> 4)) * kChunk<T>;
+          Chunk<T> c;
+          if constexpr (MODE == kFwd) {   // k is whole chunks: all of one or none
+            c = load_chunk(w + int64_t(std::min(n, p.n - 1)) * p.ldb + (k < p.k ? k : 0));
+#pragma unroll
+            for (int i = 0; i < kChunk<T>; ++i) c.v[i] = n < p.n && k < p.k ? c.v[i] : T(0.0f);
+          } else {
+            const T* q = w + std::min(n, p.n - 1) + int64_t(k < p.k ? k : 0) * p.ldb;
+#pragma unroll
+            for (int i = 0; i < kChunk<T>; ++i) c.v[i] = q[i * p.ldb];
+#pragma unroll
+            for (int i = 0; i < kChunk<T>; ++i) c.v[i] = n < p.n && k < p.k ? c.v[i] : T(0.0f);
+          }
+          fw[kk][j] = __builtin_bit_cast(typename Frag<T>::V, c);
+          if (MODE == kDx) __builtin_amdgcn_sched_barrier(0);   // a fragment's values at a time: no spills
+        }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        bias[i] = MODE == kFwd && p.bias != nullptr && live ? p.bias[int64_t(group) * p.n + n0 + col + i] : 0.0f;
+    }
+
+    const int rows = now.row1 - now.row0, m0 = wm * TM + (lane >> 2);
+    const bool add = MODE == kFwd && p.residual != nullptr;
+    const auto rr = buffer_of(static_cast<const T*>(p.residual) + int64_t(now.row0) * p.ldr + n0, p.ldr, rows, n_left);
+    const auto ro = buffer_of(static_cast<T*>(p.out) + int64_t(now.row0) * p.ldo + n0, p.ldo, rows, n_left);
+    const auto rz = buffer_of(static_cast<T*>(p.z) + int64_t(now.row0) * p.ldz + n0, p.ldz, rows, n_left);
+    const auto at = [&](int i, int64_t ld) {   // byte offset of this lane's eight values in rows 16 i ..
+      return live ? uint32_t(m0 + 16 * i) * uint32_t(ld * sizeof(T)) + uint32_t(col * sizeof(T)) : 0xffffff00u;
+    };
+    const char* tile = lds + stage * kStage;
+    Eight<T> res;
+    if (add) buffer_load_eight(rr, res, at(0, p.ldr));
+#pragma unroll
+    for (int i0 = 0; i0 < FM; i0 += FB) {
+      f32x4 acc[FB][FN];
+#pragma unroll
+      for (int i = 0; i < FB; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int kk = 0; kk < KS * 2; ++kk) {
+        typename Frag<T>::V fa[FB];
+#pragma unroll
+        for (int i = 0; i < FB; ++i)
+          fa[i] = read_frag<T, BM, false>(tile + (kk >> 1) * BM * 128, wm * TM + 16 * (i0 + i), kk & 1, lane);
+#pragma unroll
+        for (int i = 0; i < FB; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j) acc[i][j] = Frag<T>::mma(fw[kk][j], fa[i], acc[i][j]);
+      }
+#pragma unroll
+      for (int i = 0; i < FB; ++i) {
+        Eight<T> ahead;
+        if (add && i0 + i + 1 < FM) buffer_load_eight(rr, ahead, at(i0 + i + 1, p.ldr));
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          *reinterpret_cast<f32x4*>(patch + (lane & 15) * kPatch + 16 * j + 4 * (lane >> 4)) = acc[i][j];
+        wave_sync();
+        const f32x4 lo = *reinterpret_cast<const f32x4*>(patch + (lane >> 2) * kPatch + (lane & 3) * 8);
+        const f32x4 hi = *reinterpret_cast<const f32x4*>(patch + (lane >> 2) * kPatch + (lane & 3) * 8 + 4);
+        float v[8];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          v[c] = lo[c];
+          v[4 + c] = hi[c];
+        }
+        Eight<T> o;
+        if constexpr (MODE == kFwd) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) v[c] += bias[c];
+          if (p.z != nullptr) {
+            o.set(v);
+            buffer_store_eight(rz, o, at(i0 + i, p.ldz));
+          }
+          act_eight<T>(v, p.act);
+          if (add) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) v[c] += res.get(c);
+            res = ahead;
+          }
+        }
+        o.set(v);
+        buffer_store_eight(ro, o, at(i0 + i, p.ldo));
+        wave_sync();
+      }
+    }
+    now = next;
+    next = later;
+    stage = stage == 2 ? 0 : stage + 1;
+  }
+  rows_barrier<0>();   // no load into LDS outlives the workgroup
+#endif
+}
+
 // --- dz and db ----------------------------------------------------------------------------------
 
 // dz = dy act'(z) rounded into the storage type (what the matrix
@@ -576,8 +799,44 @@ void go_product(ProductArgs p, hipStream_t st) {
     go_tile<T, MODE, BM, BN, WM, WN, false>(p, grid, st);
 }
 
+// k_rows: a short k, whole chunks everywhere, and rows enough that every
+// workgroup walks several tiles for each time it fetches its weights: by
+// measurement (bf16, gelu, this kernel against 128 x 128 tiles) 64 -> 256
+// at 65,536 rows 17 us against 19, 128 -> 128 at 65,536 rows 15 against 12 and
+// at 262,144 rows 32 against 39, 256 -> 256 at 65,536 rows 26 against 25 and at
+// 262,144 rows 71 against 86.
+template <typename T, Mode MODE>
+bool rows_ok(const ProductArgs& p) {
+  const auto whole = [](const void* q, int64_t ld) {
+    return (reinterpret_cast<uintptr_t>(q) & 15u) == 0 && ld % kChunk<T> == 0 && ld <= (1 << 20);
+  };
+  return direct_ok<T>(p, MODE) && p.k <= 4 * kStep<T> && p.n % 8 == 0 && whole(p.out, p.ldo) &&
+         (p.z == nullptr || whole(p.z, p.ldz)) && (p.residual == nullptr || whole(p.residual, p.ldr)) &&
+         p.rows >= 32768 * ceil_div(p.k, kStep<T>);
+}
+
+template <typename T, Mode MODE, int KS, int WM, int WN>
+void go_rows(ProductArgs p, hipStream_t st) {
+  constexpr int BM = 128 / KS;
+  p.tiles_n = int32_t(ceil_div(p.n, WN * 32));
+  const int64_t most = max_slots(p.rows, p.groups, BM);
+  const int shares = int(std::min<int64_t>(most, std::max(1, 512 / p.tiles_n)));   // two workgroups a CU
+  k_rows<T, MODE, KS, WM, WN><<<shares * p.tiles_n, 512, 0, st>>>(p, shares);
+}
+
 template <typename T, Mode MODE>
 void run_rows(const ProductArgs& p, hipStream_t st) {
+  if (rows_ok<T, MODE>(p)) {
+    const int steps = int(ceil_div(p.k, kStep<T>));
+    if (steps > 2) return p.n <= 128 ? go_rows<T, MODE, 4, 2, 4>(p, st) : go_rows<T, MODE, 4, 1, 8>(p, st);
+    if (steps == 2)
+      return p.n <= 64    ? go_rows<T, MODE, 2, 4, 2>(p, st)
+             : p.n <= 128 ? go_rows<T, MODE, 2, 2, 4>(p, st)
+                          : go_rows<T, MODE, 2, 1, 8>(p, st);
+    return p.n <= 64    ? go_rows<T, MODE, 1, 4, 2>(p, st)
+           : p.n <= 128 ? go_rows<T, MODE, 1, 2, 4>(p, st)
+                        : go_rows<T, MODE, 1, 1, 8>(p, st);
+  }
   const int64_t large = max_slots(p.rows, p.groups, 256) * ceil_div(p.n, 256);
   const int64_t big = max_slots(p.rows, p.groups, 128) * ceil_div(p.n, 128);
   if (large >= 256 && p.k >= 512 && direct_ok<T>(p, MODE))

@@ -135,6 +135,7 @@ __device__ __forceinline__ float act_slope(float v, int act) {
 struct Span {
   int32_t e, row0, row1;      // group, rows
   int32_t slot0, slots;       // the group's first slot and how many it has
+  int32_t end;                // the group's last row + 1
 };
 
 __device__ __forceinline__ int32_t clamp_row(int64_t v, int32_t rows) {
@@ -180,7 +181,7 @@ __device__ __forceinline__ Span find_span(const int64_t* __restrict__ offsets, i
   if (groups == 0) {
     const int64_t r0 = int64_t(t) * unit;
     const int64_t r1 = r0 + unit < rows ? r0 + unit : rows;
-    return Span{r0 < rows ? 0 : -1, int32_t(r0), int32_t(r1), 0, int32_t((uint32_t(rows) + unit - 1) / unit)};
+    return Span{r0 < rows ? 0 : -1, int32_t(r0), int32_t(r1), 0, int32_t((uint32_t(rows) + unit - 1) / unit), rows};
   }
   int32_t carry = clamp_row(offsets[0], rows), base = 0;
   for (int32_t e0 = 0; e0 < groups; e0 += 64) {
@@ -191,15 +192,28 @@ __device__ __forceinline__ Span find_span(const int64_t* __restrict__ offsets, i
     const int l = __builtin_ctzll(m);
     const int32_t s0 = __builtin_amdgcn_readlane(first, l), h0 = __builtin_amdgcn_readlane(hi, l);
     const int32_t r0 = __builtin_amdgcn_readlane(lo, l) + int32_t(uint32_t(t - s0) * unit);
-    return Span{e0 + l, r0, uint32_t(h0 - r0) < unit ? h0 : r0 + int32_t(unit), s0, __builtin_amdgcn_readlane(n, l)};
+    return Span{e0 + l, r0, uint32_t(h0 - r0) < unit ? h0 : r0 + int32_t(unit), s0, __builtin_amdgcn_readlane(n, l),
+                h0};
   }
-  return Span{-1, 0, 0, 0, 0};
+  return Span{-1, 0, 0, 0, 0, 0};
+}
+
+// Slots of all groups.
+__device__ __forceinline__ int32_t total_slots(const int64_t* __restrict__ offsets, int32_t groups, int32_t rows,
+                                               uint32_t unit) {
+  if (groups == 0) return int32_t((uint32_t(rows) + unit - 1) / unit);
+  int32_t carry = clamp_row(offsets[0], rows), base = 0;
+  for (int32_t e0 = 0; e0 < groups; e0 += 64) {
+    int32_t lo, hi, first, n;
+    group_block(offsets, groups, rows, unit, e0, carry, base, lo, hi, first, n);
+  }
+  return base;
 }
 
 // All rows and the slots of group e.
 __device__ __forceinline__ Span group_span(const int64_t* __restrict__ offsets, int32_t groups, int32_t rows,
                                            uint32_t unit, int32_t e) {
-  if (groups == 0) return Span{0, 0, rows, 0, int32_t((uint32_t(rows) + unit - 1) / unit)};
+  if (groups == 0) return Span{0, 0, rows, 0, int32_t((uint32_t(rows) + unit - 1) / unit), rows};
   int32_t carry = clamp_row(offsets[0], rows), base = 0;
   for (int32_t e0 = 0;; e0 += 64) {
     int32_t lo, hi, first, n;
@@ -207,7 +221,8 @@ __device__ __forceinline__ Span group_span(const int64_t* __restrict__ offsets, 
     if (e >= e0 + 64) continue;
     const int l = e - e0;
     return Span{e, __builtin_amdgcn_readlane(lo, l), __builtin_amdgcn_readlane(hi, l),
-                __builtin_amdgcn_readlane(first, l), __builtin_amdgcn_readlane(n, l)};
+                __builtin_amdgcn_readlane(first, l), __builtin_amdgcn_readlane(n, l),
+                __builtin_amdgcn_readlane(hi, l)};
   }
 }
 

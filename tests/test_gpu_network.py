@@ -312,8 +312,13 @@ LINEAR_SHAPES = [(1, 1, 1), (2, 3, 5), (7, 64, 64), (1, 256, 130), (19, 59, 48),
                  (130, 72, 59), (257, 200, 320), (600, 48, 264), (33, 1031, 40), (16, 512, 1024)]
 
 
+# rows enough for the kernels that keep their weights, at every width of theirs
+MANY_ROWS = [(20000, 40, 136), (9000, 264, 520), (33001, 64, 64), (66001, 128, 128), (132001, 256, 256),
+             (33000, 24, 256), (66000, 96, 120), (100003, 184, 512), (132001, 192, 48), (33000, 56, 104), (66000, 72, 264)]
+
+
 @pytest.mark.parametrize("name", TYPES)
-@pytest.mark.parametrize("rows,inner,out", LINEAR_SHAPES + [(20000, 40, 136), (9000, 264, 520)])
+@pytest.mark.parametrize("rows,inner,out", LINEAR_SHAPES + MANY_ROWS)
 def test_linear_forward(gs, name, rows, inner, out):
     gen, t = _gen(rows + 7 * inner + 13 * out), _dtype(name)
     x, w = _rand(gen, rows, inner, dtype=t), _rand(gen, out, inner, scale=2 * inner ** -0.5, dtype=t)
@@ -341,7 +346,7 @@ def test_linear_activations(gs, name, act):
 
 
 @pytest.mark.parametrize("name", TYPES)
-@pytest.mark.parametrize("rows,inner,out", LINEAR_SHAPES + [(20000, 40, 136), (9000, 264, 256), (5000, 256, 250)])
+@pytest.mark.parametrize("rows,inner,out", LINEAR_SHAPES + MANY_ROWS + [(5000, 256, 250)])
 def test_linear_backward(gs, name, rows, inner, out):
     gen, t = _gen(rows + 17 * inner + 13 * out), _dtype(name)
     x, w = _rand(gen, rows, inner, dtype=t), _rand(gen, out, inner, scale=2 * inner ** -0.5, dtype=t)
@@ -491,6 +496,19 @@ def test_grouped_linear_many_groups(gs, name):
     dy, z = _rand(gen, rows, 88, dtype=t), _rand(gen, rows, 88, dtype=t)
     _linear_fwd_check(gs, x, w, bias, "relu", None, offsets)
     _linear_bwd_check(gs, x, w, dy, z, "gelu", offsets)
+
+
+@pytest.mark.parametrize("name", TYPES)
+@pytest.mark.parametrize("inner,out", [(64, 256), (256, 64), (120, 136)])
+def test_grouped_linear_many_rows(gs, name, inner, out):
+    gen, t = _gen(79), _dtype(name)
+    offsets = [3, 50000, 50000, 50001, 90000, 90040, 90040, 132000]
+    rows = 132050
+    x, w = _rand(gen, rows, inner, dtype=t), _rand(gen, 7, out, inner, scale=0.2, dtype=t)
+    bias, residual = _rand(gen, 7, out), _rand(gen, rows, out, dtype=t)
+    dy, z = _rand(gen, rows, out, dtype=t), _rand(gen, rows, out, dtype=t)
+    _linear_fwd_check(gs, x, w, bias, "gelu", residual, offsets)
+    _linear_bwd_check(gs, x, w, dy, z, "silu", offsets)
 
 
 def test_grouped_linear_any_offsets_are_safe(gs):
