@@ -17,10 +17,10 @@ size_t linear_bwd_ws_f32(int64_t rows, int32_t in, int32_t out, int32_t groups, 
 
 bool linear_fits(int64_t rows, int32_t in, int32_t out, int32_t groups) {
   // 256 threads a workgroup and a launch below 2^32 threads; the smallest
-  // tile is 64 x 64, the weight gradient's 128 x 128
+  // tile is 64 x 64
   const int64_t most = int64_t(1) << 24, side = std::max(in, out);
   const int64_t high = rows / 64 + std::max(groups, 1), wide = (side + 63) / 64;
-  const int64_t planes = ((int64_t(in) + 127) / 128) * ((int64_t(out) + 127) / 128);
+  const int64_t planes = ((int64_t(in) + 63) / 64) * ((int64_t(out) + 63) / 64);
   return high * wide < most && (planes + 768) * (std::max(groups, 1) + 1) < most;
 }
 

@@ -36,7 +36,9 @@ struct ProductArgs {
   const void* residual;
   void* out;
   void* z;
-  float* part;                    // kDw: partial products, one [m][n] plane per stretch
+  float* part;                    // kDw: partial products, one plane of `plane` values per stretch: [m][n], then [m] of db
+  float* db;                      // kDw: the sums of a's columns, or NULL
+  int64_t plane;
   int64_t ldr, ldo, ldz;
   int32_t act, out_f32;
 };
@@ -261,10 +263,11 @@ __device__ __forceinline__ int xcd_tile(int id, int n) {
   return x * share + std::min(x, more) + (id >> 3);
 }
 
-// What one wave does with a k step in LDS.
-template <typename T, int BM, int BN, bool A_ACROSS, bool B_ACROSS, int FM, int FN>
+// What one wave does with a k step in LDS.  `sums`: also adds the columns
+// of a (a product with a row of ones: exact, in fp32).
+template <typename T, int BM, int BN, bool A_ACROSS, bool B_ACROSS, int FM, int FN, int FS>
 __device__ __forceinline__ void multiply_step(const char* ta, const char* tb, int am, int bn, int lane,
-                                              f32x4 (&acc)[FM][FN]) {
+                                              f32x4 (&acc)[FM][FN], f32x4 (&sum)[FS], bool sums) {
 #pragma unroll
   for (int kk = 0; kk < 2; ++kk) {
     typename Frag<T>::V fa[FM], fb[FN];
@@ -276,6 +279,15 @@ __device__ __forceinline__ void multiply_step(const char* ta, const char* tb, in
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int j = 0; j < FN; ++j) acc[i][j] = Frag<T>::mma(fb[j], fa[i], acc[i][j]);
+    if constexpr (FS == FM) {
+      if (sums) {
+        typename Frag<T>::V one;
+#pragma unroll
+        for (int c = 0; c < kChunk<T>; ++c) one[c] = T(1.0f);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) sum[i] = Frag<T>::mma(one, fa[i], sum[i]);
+      }
+    }
   }
 }
 
@@ -286,21 +298,21 @@ __device__ __forceinline__ void multiply_step(const char* ta, const char* tb, in
 // chunks, loaded straight into one of two LDS stages while the other is
 // multiplied; else through registers, at any alignment.
 template <typename T, Mode MODE, int BM, int BN, int WM, int WN, bool DIRECT>
-__global__ __launch_bounds__(64 * WM * WN) void k_product(ProductArgs p) {
+__device__ __forceinline__ void product_tile(const ProductArgs& p, int tile, char* lds) {
   constexpr int THREADS = 64 * WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
   constexpr bool A_ACROSS = MODE == kDw, B_ACROSS = MODE != kFwd;
   constexpr int kPatch = TN + 4;   // floats of a patch row: 4 more keep its 16-byte writes off each other's banks
   constexpr int kTiles = (BM + BN) * 128;
-  extern __shared__ __align__(16) char lds[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
 
   // Which tile.  kFwd, kDx: the height index picks group and rows; kDw: the
-  // stretch does, and the tile inside the plane is apart from it.
-  const int tile = xcd_tile(blockIdx.x, gridDim.x);
+  // stretch does (without planes to join, every group is one stretch, and
+  // empty ones store their zeros), the tile inside the plane is apart from it.
   const int stretch = MODE == kDw ? tile / p.tiles : tile / p.tiles_n;
   const int within = MODE == kDw ? tile % p.tiles : tile % p.tiles_n;
-  const Span s = find_span(p.offsets, p.groups, p.rows, p.unit, stretch);
+  const Span s = MODE == kDw && p.part == nullptr ? group_span(p.offsets, p.groups, p.rows, p.unit, stretch)
+                                                  : find_span(p.offsets, p.groups, p.rows, p.unit, stretch);
   if (s.e < 0) return;
   const int m0 = MODE == kDw ? within / p.tiles_n * BM : 0;
   const int n0 = (MODE == kDw ? within % p.tiles_n : within) * BN;
@@ -318,8 +330,14 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product(ProductArgs p) {
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  f32x4 sum[MODE == kDw ? FM : 1];
+#pragma unroll
+  for (f32x4& v : sum) v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const bool sums = MODE == kDw && p.db != nullptr && n0 == 0 && wn == 0;
 
-  if constexpr (DIRECT) {
+  if (MODE == kDw && k_all == 0) {
+    // an empty group's zeros
+  } else if constexpr (DIRECT) {
     Direct<T, BM, A_ACROSS, THREADS> da;
     Direct<T, BN, B_ACROSS, THREADS> db;
     da.init(p.lda, tid);
@@ -338,7 +356,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product(ProductArgs p) {
         db.load(b, p.ldb, B_ACROSS ? next : n_left, B_ACROSS ? n_left : next, t + BM * 128, wave);
       }
       const char* t = lds + stage * kTiles;
-      multiply_step<T, BM, BN, A_ACROSS, B_ACROSS, FM, FN>(t, t + BM * 128, wm * TM, wn * TN, lane, acc);
+      multiply_step<T, BM, BN, A_ACROSS, B_ACROSS, FM, FN>(t, t + BM * 128, wm * TM, wn * TN, lane, acc, sum, sums);
       stage ^= 1;
     }
     tile_barrier();
@@ -360,7 +378,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product(ProductArgs p) {
         sa.load(a, p.lda, A_ACROSS ? left : m_left, A_ACROSS ? m_left : left, tid);
         sb.load(b, p.ldb, B_ACROSS ? left : n_left, B_ACROSS ? n_left : left, tid);
       }
-      multiply_step<T, BM, BN, A_ACROSS, B_ACROSS, FM, FN>(ta, tb, wm * TM, wn * TN, lane, acc);
+      multiply_step<T, BM, BN, A_ACROSS, B_ACROSS, FM, FN>(ta, tb, wm * TM, wn * TN, lane, acc, sum, sums);
       __syncthreads();
     }
   }
@@ -376,10 +394,21 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product(ProductArgs p) {
   void* out = p.out;
   if constexpr (MODE == kDw) {
     if (p.part != nullptr && s.slots > 1)
-      plane = p.part + int64_t(stretch) * p.m * p.n;
+      plane = p.part + int64_t(stretch) * p.plane;
     else
       out = p.out_f32 ? static_cast<void*>(static_cast<float*>(p.out) + int64_t(s.e) * p.m * p.ldo)
                       : static_cast<void*>(static_cast<T*>(p.out) + int64_t(s.e) * p.m * p.ldo);
+  }
+  if constexpr (MODE == kDw) {
+    if (sums && lane < 16) {   // lane m has the sum of column m in every register
+      float* o = plane != nullptr ? plane + int64_t(p.m) * p.n : p.db + int64_t(s.e) * p.m;
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        const int m = wm * TM + 16 * i + lane;
+        if (m < m_left) o[m0 + m] = sum[i][0];
+      }
+    }
+    if (p.out == nullptr) return;   // no rows and db alone: its zeros
   }
   float bias[8];
   if constexpr (MODE == kFwd) {
@@ -444,6 +473,12 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product(ProductArgs p) {
       wave_sync();
     }
   }
+}
+
+template <typename T, Mode MODE, int BM, int BN, int WM, int WN, bool DIRECT>
+__global__ __launch_bounds__(64 * WM * WN) void k_product(ProductArgs p) {
+  extern __shared__ __align__(16) char lds[];
+  product_tile<T, MODE, BM, BN, WM, WN, DIRECT>(p, xcd_tile(blockIdx.x, gridDim.x), lds);
 }
 
 // --- the product over many rows of a short k ---------------------------------------
@@ -671,18 +706,19 @@ __global__ __launch_bounds__(512, 4) void k_rows(ProductArgs p, int shares) {
 // --- dz and db ----------------------------------------------------------------------------------
 
 // dz = dy act'(z) rounded into the storage type (what the matrix
-// instructions take; db is summed from the unrounded values), and one
-// partial row of db per stretch of rows: part[slot][out].  Without an
-// activation dz is dy itself and only the sums are made.
+// instructions take; db is summed from the unrounded values, in fp32; no dz:
+// the sums of dy alone), and one partial row of db per stretch of rows, part[slot][out], or without
+// `part` db itself, one stretch a group.
 template <typename T>
 __global__ __launch_bounds__(256) void k_act_grad(const T* __restrict__ dy, int64_t lddy, const T* __restrict__ z,
                                                   int64_t ldz, T* __restrict__ dz, int64_t lddz,
                                                   const int64_t* __restrict__ offsets, int32_t groups, int32_t rows,
                                                   int32_t unit, int32_t out, int act, int lanes,
-                                                  float* __restrict__ part) {
+                                                  float* __restrict__ part, float* __restrict__ db) {
   constexpr int K = kChunk<T>;
   __shared__ float s[256][K + 1];
-  const Span sp = find_span(offsets, groups, rows, unit, blockIdx.x);
+  const Span sp = part == nullptr ? group_span(offsets, groups, rows, unit, blockIdx.x)
+                                  : find_span(offsets, groups, rows, unit, blockIdx.x);
   if (sp.e < 0) return;
   const int cl = threadIdx.x % lanes, rl = threadIdx.x / lanes, col = (blockIdx.y * lanes + cl) * K;
   const int n = std::min(K, std::max(0, out - col));
@@ -709,7 +745,9 @@ __global__ __launch_bounds__(256) void k_act_grad(const T* __restrict__ dy, int6
 #pragma unroll
       for (int i = 0; i < K; ++i) sum[i] += v[i];
     }
-  if (part == nullptr) return;
+  float* __restrict__ to = part != nullptr ? part + int64_t(blockIdx.x) * out : db != nullptr ? db + int64_t(sp.e) * out
+                                                                                            : nullptr;
+  if (to == nullptr) return;
 #pragma unroll
   for (int i = 0; i < K; ++i) s[threadIdx.x][i] = sum[i];
   __syncthreads();
@@ -722,23 +760,64 @@ __global__ __launch_bounds__(256) void k_act_grad(const T* __restrict__ dy, int6
   if (rl == 0)
 #pragma unroll
     for (int i = 0; i < K; ++i)
-      if (i < n) part[int64_t(blockIdx.x) * out + col + i] = s[threadIdx.x][i];
+      if (i < n) to[col + i] = s[threadIdx.x][i];
 }
 
-// Sums a group's planes of `size` values, in order.  Groups of one plane
-// were written by the product itself where `whole` says so; empty ones are 0.
-template <typename O>
-__global__ __launch_bounds__(256) void k_join(const float* __restrict__ part, const int64_t* __restrict__ offsets,
-                                              int32_t groups, int32_t rows, int32_t unit, int64_t size, bool whole,
-                                              O* __restrict__ out) {
-  const Span s = group_span(offsets, groups, rows, unit, blockIdx.y);
-  if (whole && s.slots == 1) return;
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < size; i += int64_t(gridDim.x) * 256) {
-    float v = 0.0f;
+// Sum over a group's stretches, in order: value i of planes `plane` apart.
+__device__ __forceinline__ float plane_sum(const float* __restrict__ part, int64_t plane, const Span& s, int64_t i) {
+  float v = 0.0f;
 #pragma unroll 8
-    for (int t = 0; t < s.slots; ++t) v += part[(int64_t(s.slot0) + t) * size + i];
-    out[int64_t(blockIdx.y) * size + i] = O(v);
+  for (int t = 0; t < s.slots; ++t) v += part[(int64_t(s.slot0) + t) * plane + i];
+  return v;
+}
+
+// Joins the planes of dw (size values, then m of db).  Groups of one
+// stretch were written by the product itself; empty ones are 0.
+template <typename O>
+__global__ __launch_bounds__(256) void k_join(const float* __restrict__ part, int64_t plane,
+                                              const int64_t* __restrict__ offsets, int32_t groups, int32_t rows,
+                                              int32_t unit, int64_t size, O* __restrict__ out, int32_t m,
+                                              float* __restrict__ db) {
+  const Span s = group_span(offsets, groups, rows, unit, blockIdx.y);
+  if (s.slots == 1) return;
+  const int64_t all = size + (db != nullptr ? m : 0);
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += int64_t(gridDim.x) * 256) {
+    const float v = plane_sum(part, plane, s, i);
+    if (i < size)
+      out[int64_t(blockIdx.y) * size + i] = O(v);
+    else
+      db[int64_t(blockIdx.y) * m + (i - size)] = v;
   }
+}
+
+// db from the partial rows of k_act_grad.
+struct DbJoin {
+  const float* part;
+  float* db;
+  int32_t out, unit, blocks;   // blocks: workgroups of 256 columns a group
+};
+__device__ __forceinline__ void join_db(const DbJoin& j, const ProductArgs& p, int block) {
+  const Span s = group_span(p.offsets, p.groups, p.rows, j.unit, block / j.blocks);
+  const int col = block % j.blocks * 256 + threadIdx.x;
+  if (col < j.out) j.db[int64_t(s.e) * j.out + col] = plane_sum(j.part, j.out, s, col);
+}
+__global__ __launch_bounds__(256) void k_join_db(DbJoin j, ProductArgs p) { join_db(j, p, blockIdx.x); }
+
+// Small problems, whose cost is their launches: dx, dw and what is left of
+// db in one, the workgroups shared out among the three.
+template <typename T, bool DIRECT>
+__global__ __launch_bounds__(256) void k_bwd(ProductArgs x, int x_tiles, ProductArgs w, int w_tiles, DbJoin j) {
+  extern __shared__ __align__(16) char lds[];
+  int b = blockIdx.x;
+  if (b < x_tiles) {
+    product_tile<T, kDx, 64, 64, 2, 2, DIRECT>(x, b, lds);
+    return;
+  }
+  b -= x_tiles;
+  if (b < w_tiles)
+    product_tile<T, kDw, 64, 64, 2, 2, DIRECT>(w, b, lds);
+  else
+    join_db(j, w, b - w_tiles);
 }
 
 // --- launch ----------------------------------------------------------------------------------------
@@ -781,18 +860,22 @@ void go_tile(const ProductArgs& p, int64_t grid, hipStream_t st) {
   k_product<T, MODE, BM, BN, WM, WN, DIRECT><<<int(grid), 64 * WM * WN, lds, st>>>(p);
 }
 
+// Tiles of the product and the shape of its grid.
+template <Mode MODE>
+int64_t lay_out(ProductArgs& p, int bm, int bn) {
+  p.tiles_n = int32_t(ceil_div(p.n, bn));
+  if (MODE == kDw) {
+    p.tiles = int32_t(ceil_div(p.m, bm)) * p.tiles_n;
+    return (p.part != nullptr ? max_slots(p.rows, p.groups, p.unit) : std::max(1, p.groups)) * p.tiles;
+  }
+  p.unit = bm;
+  p.tiles = p.tiles_n;
+  return max_slots(p.rows, p.groups, bm) * p.tiles_n;
+}
+
 template <typename T, Mode MODE, int BM, int BN, int WM, int WN>
 void go_product(ProductArgs p, hipStream_t st) {
-  p.tiles_n = int32_t(ceil_div(p.n, BN));
-  int64_t grid;
-  if (MODE == kDw) {
-    p.tiles = int32_t(ceil_div(p.m, BM)) * p.tiles_n;
-    grid = max_slots(p.rows, p.groups, p.unit) * p.tiles;
-  } else {
-    p.unit = BM;
-    p.tiles = p.tiles_n;
-    grid = max_slots(p.rows, p.groups, BM) * p.tiles_n;
-  }
+  const int64_t grid = lay_out<MODE>(p, BM, BN);
   if (direct_ok<T>(p, MODE))
     go_tile<T, MODE, BM, BN, WM, WN, true>(p, grid, st);
   else if constexpr (BM <= 128 && BN <= 128)
@@ -847,27 +930,35 @@ void run_rows(const ProductArgs& p, hipStream_t st) {
     go_product<T, MODE, 64, 64, 2, 2>(p, st);
 }
 
-// Rows of a stretch of db: enough workgroups to fill the chip.
-inline int32_t db_unit(int64_t rows, int32_t out, int chunk) {
-  const int64_t across = ceil_div(out, 64 * chunk);
-  return int32_t(std::max<int64_t>(64, ceil_div(ceil_div(rows * across, 2048), 64) * 64));
-}
-// Rows of a stretch of dw.
-inline int32_t dw_unit(int64_t rows, int32_t in, int32_t out) {
-  const int64_t tiles = ceil_div(out, 128) * ceil_div(in, 128);
-  return int32_t(std::max<int64_t>(256, ceil_div(ceil_div(rows * tiles, 768), 64) * 64));
-}
-inline int64_t dz_ld(int32_t out, int chunk) { return ceil_div(out, chunk) * chunk; }
-
-struct BwdSpace {
+// How the backward pass is cut: from the sizes alone, so that the workspace
+// can be sized for it.
+struct BwdPlan {
+  bool small;              // dx and dw in one launch of 64 x 64 tiles
+  int32_t unit_b, unit_w;  // rows of a stretch of db (with an activation) and of dw
+  bool part_b, part_w;     // more than one stretch a group: partial sums to join
+  int64_t plane;           // values of a plane of dw
   size_t dz, db, dw, total;
 };
+inline int64_t dz_ld(int32_t out, int chunk) { return ceil_div(out, chunk) * chunk; }
+
 template <typename T>
-BwdSpace bwd_space(int64_t rows, int32_t in, int32_t out, int32_t groups, int act) {
-  BwdSpace s;
+BwdPlan bwd_plan(int64_t rows, int32_t in, int32_t out, int32_t groups, int act) {
+  BwdPlan s;
+  const int64_t slots = max_slots(rows, groups, 128);
+  s.small = slots * ceil_div(in, 128) < 256 && slots * ceil_div(out, 128) < 256;
+  const int64_t side = s.small ? 64 : 128;
+  const int64_t tiles = ceil_div(out, side) * ceil_div(in, side);
+  // stretches so that about 768 workgroups share the rows, 256 rows at least
+  s.unit_w = int32_t(std::max<int64_t>(256, ceil_div(ceil_div(rows * tiles, 768), 64) * 64));
+  s.part_w = rows > s.unit_w;
+  s.plane = ceil_div(int64_t(out) * in + out, 64) * 64;
+  // about 2048 workgroups of the slope's kernel, 64 rows at least
+  const int64_t across = ceil_div(out, 64 * kChunk<T>);
+  s.unit_b = int32_t(std::max<int64_t>(64, ceil_div(ceil_div(rows * across, 2048), 64) * 64));
+  s.part_b = rows > s.unit_b;
   s.dz = act == kActNone ? 0 : align_up(size_t(rows) * dz_ld(out, kChunk<T>) * sizeof(T), 256);
-  s.db = align_up(size_t(max_slots(rows, groups, db_unit(rows, out, kChunk<T>))) * out * 4, 256);
-  s.dw = align_up(size_t(max_slots(rows, groups, dw_unit(rows, in, out))) * out * in * 4, 256);
+  s.db = !s.part_b ? 0 : align_up(size_t(max_slots(rows, groups, s.unit_b)) * out * 4, 256);
+  s.dw = !s.part_w ? 0 : align_up(size_t(max_slots(rows, groups, s.unit_w)) * s.plane * 4, 256);
   s.total = s.dz + s.db + s.dw;
   return s;
 }
@@ -897,68 +988,85 @@ hipError_t linear_fwd(const LinearArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <typename O>
-void join(const float* part, const LinearArgs& a, int32_t unit, int64_t size, bool whole, O* out, hipStream_t st) {
-  const int64_t blocks = std::min<int64_t>(ceil_div(size, 256), 4096);
-  k_join<O><<<dim3(int(blocks), std::max(1, a.groups)), 256, 0, st>>>(part, a.offsets, a.groups, a.rows, unit, size,
-                                                                     whole, out);
-}
-
 template <typename T>
 hipError_t linear_bwd(const LinearArgs& a, char* ws, hipStream_t st) {
-  const BwdSpace space = bwd_space<T>(a.rows, a.in, a.out, a.groups, a.act);
+  const BwdPlan plan = bwd_plan<T>(a.rows, a.in, a.out, a.groups, a.act);
   T* dz = reinterpret_cast<T*>(ws);
-  float* db_part = reinterpret_cast<float*>(ws + space.dz);
-  float* dw_part = reinterpret_cast<float*>(ws + space.dz + space.db);
-  const int32_t unit_b = db_unit(a.rows, a.out, kChunk<T>), unit_w = dw_unit(a.rows, a.in, a.out);
   const bool slope = a.act != kActNone;
-  const T* g = slope ? dz : static_cast<const T*>(a.dy);
-  const int64_t ldg = slope ? dz_ld(a.out, kChunk<T>) : a.lddy;
-  if (a.rows > 0 && (slope || a.db != nullptr)) {
+  const int groups = std::max(1, a.groups);
+  // without rows only the zeros of dw and db are left to write
+  const bool any = a.rows > 0;
+
+  // db comes out of dw's product, but with an activation (or without dw) out
+  // of the slope's pass
+  const bool own_db = slope || a.dw == nullptr;
+  DbJoin j{};
+  if (any && (slope || (own_db && a.db != nullptr))) {
     int lanes = 1;
     while (lanes < 64 && lanes * kChunk<T> < a.out) lanes *= 2;
-    const dim3 grid(int(max_slots(a.rows, a.groups, unit_b)), int(ceil_div(a.out, lanes * kChunk<T>)));
-    k_act_grad<T><<<grid, 256, 0, st>>>(static_cast<const T*>(a.dy), a.lddy, static_cast<const T*>(a.z), a.ldz,
-                                        slope ? dz : nullptr, ldg, a.offsets, a.groups, a.rows, unit_b, a.out, a.act,
-                                        lanes, a.db != nullptr ? db_part : nullptr);
+    const bool parts = a.db != nullptr && plan.part_b;
+    float* part = reinterpret_cast<float*>(ws + plan.dz);
+    // stretches as planned for the partial sums (unread where many rows come
+    // without db); few rows: the groups themselves
+    const bool cut = plan.part_b;
+    k_act_grad<T><<<dim3(int(cut ? max_slots(a.rows, a.groups, plan.unit_b) : groups),
+                         int(ceil_div(a.out, lanes * kChunk<T>))),
+                    256, 0, st>>>(static_cast<const T*>(a.dy), a.lddy, static_cast<const T*>(a.z), a.ldz,
+                                  slope ? dz : nullptr, dz_ld(a.out, kChunk<T>), a.offsets, a.groups, a.rows,
+                                  plan.unit_b, a.out, a.act, lanes, cut ? part : nullptr, a.db);
+    if (parts) j = DbJoin{part, a.db, a.out, plan.unit_b, int32_t(ceil_div(a.out, 256))};
   }
-  if (a.db != nullptr) join<float>(db_part, a, unit_b, a.out, false, a.db, st);
+
   ProductArgs p{};
-  p.a = g;
-  p.lda = ldg;
+  p.a = slope ? dz : a.dy;
+  p.lda = slope ? dz_ld(a.out, kChunk<T>) : a.lddy;
   p.offsets = a.offsets;
   p.rows = a.rows;
   p.groups = a.groups;
-  if (a.dx != nullptr && a.rows > 0) {
-    ProductArgs q = p;
-    q.b = a.w;
-    q.ldb = a.ldw;
-    q.b_group = int64_t(a.out) * a.ldw;
-    q.n = a.in;
-    q.k = a.out;
-    q.out = a.dx;
-    q.ldo = a.lddx;
-    run_rows<T, kDx>(q, st);
-  }
-  if (a.dw != nullptr) {
-    ProductArgs q = p;
-    q.b = a.x;
-    q.ldb = a.ldx;
-    q.m = a.out;
-    q.n = a.in;
-    q.unit = unit_w;
-    q.out = a.dw;
-    q.out_f32 = a.dw_f32;
-    q.ldo = a.in;
-    q.part = dw_part;
-    if (a.rows > 0) {
-      go_product<T, kDw, 128, 128, 2, 2>(q, st);
+  ProductArgs x = p, w = p;
+  x.b = a.w;
+  x.ldb = a.ldw;
+  x.b_group = int64_t(a.out) * a.ldw;
+  x.n = a.in;
+  x.k = a.out;
+  x.out = a.dx;
+  x.ldo = a.lddx;
+  w.b = a.x;
+  w.ldb = a.ldx;
+  w.m = a.out;
+  w.n = a.in;
+  w.unit = plan.unit_w;
+  w.out = a.dw;
+  w.out_f32 = a.dw_f32;
+  w.ldo = a.in;
+  w.part = plan.part_w ? reinterpret_cast<float*>(ws + plan.dz + plan.db) : nullptr;
+  w.plane = plan.plane;
+  w.db = own_db && any ? nullptr : a.db;
+  const bool want_dx = a.dx != nullptr && any, want_dw = a.dw != nullptr || (w.db != nullptr && !any);
+  if (plan.small) {
+    const int64_t x_tiles = want_dx ? lay_out<kDx>(x, 64, 64) : 0, w_tiles = want_dw ? lay_out<kDw>(w, 64, 64) : 0;
+    const int64_t grid = x_tiles + w_tiles + int64_t(j.blocks) * groups;
+    constexpr int tiles = 128 * 128, patches = 4 * 16 * 36 * 4;
+    if (grid > 0) {
+      if ((!want_dx || direct_ok<T>(x, kDx)) && (!want_dw || direct_ok<T>(w, kDw)))
+        k_bwd<T, true><<<int(grid), 256, std::max(2 * tiles, patches), st>>>(x, int(x_tiles), w, int(w_tiles), j);
+      else
+        k_bwd<T, false><<<int(grid), 256, std::max(tiles, patches), st>>>(x, int(x_tiles), w, int(w_tiles), j);
     }
+  } else {
+    if (j.blocks > 0) k_join_db<<<j.blocks * groups, 256, 0, st>>>(j, p);
+    if (want_dx) run_rows<T, kDx>(x, st);
+    if (want_dw) go_product<T, kDw, 128, 128, 2, 2>(w, st);
+  }
+  if (want_dw && w.part != nullptr) {
     const int64_t size = int64_t(a.out) * a.in;
+    const dim3 grid(int(std::min<int64_t>(ceil_div(size + a.out, 256), 4096)), groups);
     if (a.dw_f32)
-      join<float>(dw_part, a, unit_w, size, true, static_cast<float*>(a.dw), st);
+      k_join<float><<<grid, 256, 0, st>>>(w.part, w.plane, a.offsets, a.groups, a.rows, plan.unit_w, size,
+                                          static_cast<float*>(a.dw), a.out, w.db);
     else
-      join<T>(dw_part, a, unit_w, size, true, static_cast<T*>(a.dw), st);
+      k_join<T><<<grid, 256, 0, st>>>(w.part, w.plane, a.offsets, a.groups, a.rows, plan.unit_w, size,
+                                      static_cast<T*>(a.dw), a.out, w.db);
   }
   return hipGetLastError();
 }

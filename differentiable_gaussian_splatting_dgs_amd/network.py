@@ -91,33 +91,27 @@ def _optional(t):
     return None if t is None else t.data_ptr()
 
 
-class _On:
-    """The call's device and stream: tensors made inside belong to the stream."""
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
-    def __init__(self, x, stream):
-        if not x.is_cuda:
-            raise ValueError(f"x is on {x.device}: the kernels need a GPU tensor")
-        self.ctx = None
-        if stream is not None:
-            self.ctx = torch.cuda.stream(stream)
-        elif x.device.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(x.device)
-        self.stream, self.device = stream, x.device
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return (self.stream if self.stream is not None else torch.cuda.current_stream(self.device)).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
-        return False
+def _launch(x, stream, call):
+    """call(stream handle) with the tensors it makes, workspaces among them,
+    belonging to the stream and the device of x."""
+    if not x.is_cuda:
+        raise ValueError(f"x is on {x.device}: the kernels need a GPU tensor")
+    device = x.device.index
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+    if device != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return call(_raw_stream(device))
+    return call(_raw_stream(device))
 
 
 def _workspace(ws, need, like):
     if ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=like.device)
+        return torch.empty(need, dtype=torch.uint8, device=like.device), need
     return ws, ws.numel() * ws.element_size()
 
 
@@ -128,13 +122,19 @@ def gs_layer_norm_fwd(x, gamma=None, beta=None, eps=1e-5, y=None, mean=None, rst
     rows, width = x.shape
     _placed(x, x, "x")
     g, b = _vector(gamma, (width,), x, "gamma"), _vector(beta, (width,), x, "beta")
-    with _On(x, stream) as s:
-        y = torch.empty_like(x, memory_format=torch.contiguous_format) if y is None else y
-        mean = torch.empty(rows, dtype=torch.float32, device=x.device) if mean is None else mean
-        rstd = torch.empty(rows, dtype=torch.float32, device=x.device) if rstd is None else rstd
+
+    def call(s):
+        nonlocal y, mean, rstd
+        if y is None:
+            y = torch.empty(rows, width, dtype=x.dtype, device=x.device)
+        if mean is None:
+            mean = torch.empty(rows, dtype=torch.float32, device=x.device)
+        if rstd is None:
+            rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
         _check(lib().gs_layer_norm_fwd(x.data_ptr(), _ld(x, rows, width), g, b, rows, width, eps, t, y.data_ptr(),
                                        _matrix(y, rows, width, x, "y"), _vector(mean, (rows,), x, "mean"),
                                        _vector(rstd, (rows,), x, "rstd"), s), "gs_layer_norm_fwd")
+    _launch(x, stream, call)
     return y, mean, rstd
 
 
@@ -149,16 +149,22 @@ def gs_layer_norm_bwd(x, dy, gamma, mean, rstd, dres=None, dx=None, dgamma=None,
     ldr = 0 if dres is None else _matrix(dres, rows, width, x, "dres")
     g = _vector(gamma, (width,), x, "gamma")
     m, r = _vector(mean, (rows,), x, "mean"), _vector(rstd, (rows,), x, "rstd")
-    with _On(x, stream) as s:
-        dx = torch.empty_like(x, memory_format=torch.contiguous_format) if dx is None else dx
-        dgamma = torch.empty(width, dtype=torch.float32, device=x.device) if dgamma is None else dgamma
-        dbeta = torch.empty(width, dtype=torch.float32, device=x.device) if dbeta is None else dbeta
+
+    def call(s):
+        nonlocal dx, dgamma, dbeta
+        if dx is None:
+            dx = torch.empty(rows, width, dtype=x.dtype, device=x.device)
+        if dgamma is None:
+            dgamma = torch.empty(width, dtype=torch.float32, device=x.device)
+        if dbeta is None:
+            dbeta = torch.empty(width, dtype=torch.float32, device=x.device)
         ws, nbytes = _workspace(workspace, gs_workspace_size(GS_OP_LAYER_NORM_BWD, rows, width), x)
         _check(lib().gs_layer_norm_bwd(x.data_ptr(), _ld(x, rows, width), dy.data_ptr(), lddy, g, m, r,
                                        _optional(dres), ldr, rows, width, t, dx.data_ptr(),
                                        _matrix(dx, rows, width, x, "dx"), _vector(dgamma, (width,), x, "dgamma"),
                                        _vector(dbeta, (width,), x, "dbeta"), ws.data_ptr(), nbytes, s),
                "gs_layer_norm_bwd")
+    _launch(x, stream, call)
     return dx, dgamma, dbeta
 
 
@@ -170,8 +176,11 @@ def _fwd(x, w, offsets, bias, act, residual, y, z, save_z, stream, where):
     ldw, out = _weights(w, groups, x, inner)
     b = _vector(bias, (groups, out) if groups else (out,), x, "bias")
     ldr = 0 if residual is None else _matrix(residual, rows, out, x, "residual")
-    with _On(x, stream) as s:
-        y = torch.empty(rows, out, dtype=x.dtype, device=x.device) if y is None else y
+
+    def call(s):
+        nonlocal y, z
+        if y is None:
+            y = torch.empty(rows, out, dtype=x.dtype, device=x.device)
         if z is None and save_z:
             z = torch.empty(rows, out, dtype=x.dtype, device=x.device)
         ldz = 0 if z is None else _matrix(z, rows, out, x, "z")
@@ -182,6 +191,7 @@ def _fwd(x, w, offsets, bias, act, residual, y, z, save_z, stream, where):
             _check(lib().gs_grouped_linear_fwd(*head, offsets.data_ptr(), groups, *tail), where)
         else:
             _check(lib().gs_linear_fwd(*head, *tail), where)
+    _launch(x, stream, call)
     return y if z is None else (y, z)
 
 
@@ -216,16 +226,20 @@ def _bwd(x, w, offsets, dy, z, act, dx, dw, db, want_dx, workspace, stream, wher
     if z is None and act != GS_ACT_NONE:
         raise ValueError("the activation's slope needs z, the value before it")
     ldz = 0 if z is None else _matrix(z, rows, out, x, "z")
-    with _On(x, stream) as s:
+    bshape = (groups, out) if groups else (out,)
+
+    def call(s):
+        nonlocal dx, dw, db
         if dx is None and want_dx:
             dx = torch.empty(rows, inner, dtype=x.dtype, device=x.device)
-        dw = torch.empty(w.shape, dtype=w.dtype, device=x.device) if dw is None else dw
-        if dw.shape != w.shape or dw.dtype not in (w.dtype, torch.float32) or not dw.is_contiguous():
+        if dw is None:
+            dw = torch.empty(w.shape, dtype=w.dtype, device=x.device)
+        elif dw.shape != w.shape or dw.dtype not in (w.dtype, torch.float32) or not dw.is_contiguous():
             raise ValueError(f"dw is {dw.dtype} {tuple(dw.shape)}: contiguous {w.dtype} or torch.float32 "
                              f"{tuple(w.shape)} expected")
         _placed(dw, x, "dw")
-        bshape = (groups, out) if groups else (out,)
-        db = torch.empty(bshape, dtype=torch.float32, device=x.device) if db is None else db
+        if db is None:
+            db = torch.empty(bshape, dtype=torch.float32, device=x.device)
         ws, nbytes = _workspace(workspace, gs_linear_workspace_size(rows, inner, out, groups, t, act), x)
         head = (x.data_ptr(), _ld(x, rows, inner), w.data_ptr(), ldw)
         tail = (_optional(z), ldz, dy.data_ptr(), lddy, rows, inner, out, t, act, _optional(dx),
@@ -235,6 +249,7 @@ def _bwd(x, w, offsets, dy, z, act, dx, dw, db, want_dx, workspace, stream, wher
             _check(lib().gs_grouped_linear_bwd(*head, offsets.data_ptr(), groups, *tail), where)
         else:
             _check(lib().gs_linear_bwd(*head, *tail), where)
+    _launch(x, stream, call)
     return dx, dw, db
 
 

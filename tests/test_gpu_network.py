@@ -584,3 +584,44 @@ def test_graph_replays_match_the_eager_calls(gs):
         torch.cuda.synchronize()
         for a, b in zip(outs, _layer(gs, *fresh)):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("rows", [37, 900, 140000])
+@pytest.mark.parametrize("act", ["none", "silu"])
+def test_linear_backward_in_parts(gs, rows, act):
+    """Each of dx, dw and db alone (the others NULL) has the bits it has
+    beside the others; db without dw within fp32 roundings of it."""
+    gen, t = _gen(rows), torch.bfloat16
+    x, w = _rand(gen, rows, 72, dtype=t), _rand(gen, 40, 72, scale=0.2, dtype=t)
+    dy, z = _rand(gen, rows, 40, dtype=t), _rand(gen, rows, 40, dtype=t)
+    dx, dw, db = gs.gs_linear_bwd(x, w, dy, z, _act_id(gs, act))
+    ws = torch.empty(gs.gs_linear_workspace_size(rows, 72, 40, 0, gs.GS_TYPE_BF16, _act_id(gs, act)),
+                     dtype=torch.uint8, device="cuda")
+    s = torch.cuda.current_stream().cuda_stream
+
+    def call(dx=None, dw=None, db=None, x=x, w=w):
+        st = gs.lib().gs_linear_bwd(None if x is None else x.data_ptr(), 72, None if w is None else w.data_ptr(), 72,
+                                    z.data_ptr(), 40, dy.data_ptr(), 40, rows, 72, 40, 0, _act_id(gs, act),
+                                    None if dx is None else dx.data_ptr(), 72, None if dw is None else dw.data_ptr(),
+                                    0, None if db is None else db.data_ptr(), ws.data_ptr(), ws.numel(), s)
+        assert st == gs.GS_OK, gs.gs_last_error()
+    a, b, c = torch.zeros_like(dx), torch.zeros_like(dw), torch.zeros_like(db)
+    call(dx=a, x=None)
+    call(dw=b, w=None)
+    call(db=c, x=None, w=None)
+    call()
+    assert torch.equal(a, dx) and torch.equal(b, dw)
+    g = dy.double() * _slope(z.double(), act)
+    _close(c, g.sum(0), 2 ** -18 * dy.double().abs().sum(0) + (rows + 4) * EPS32 * g.abs().sum(0), "db")
+    # the norm's parts
+    y, mean, rstd = gs.gs_layer_norm_fwd(x)
+    ex, eg, eb = gs.gs_layer_norm_bwd(x, y, None, mean, rstd)
+    ws = torch.empty(gs.gs_workspace_size(gs.GS_OP_LAYER_NORM_BWD, rows, 72), dtype=torch.uint8, device="cuda")
+    for parts in ((True, False, False), (False, True, False), (False, False, True), (False, False, False)):
+        out = [torch.zeros_like(v) if p else None for v, p in zip((ex, eg, eb), parts)]
+        px, pg, pb = (None if v is None else v.data_ptr() for v in out)
+        assert gs.lib().gs_layer_norm_bwd(x.data_ptr(), 72, y.data_ptr(), 72, None, mean.data_ptr(), rstd.data_ptr(),
+                                          None, 0, rows, 72, 0, px, 72, pg, pb, ws.data_ptr(), ws.numel(),
+                                          s) == gs.GS_OK
+        for v, want in zip(out, (ex, eg, eb)):
+            assert v is None or torch.equal(v, want)
