@@ -145,20 +145,41 @@ __device__ __forceinline__ typename Frag<T>::V read_frag(const char* tile, int d
   }
 }
 
-// Global -> registers -> LDS for one operand, at any alignment.  `row` and
-// `col` extents are what is left of the operand from the tile's corner: rows
-// and columns past them read as 0.
+// Global -> registers -> LDS for one operand, at any alignment.  `rows` and
+// `cols`: what is left of the operand from the tile's corner; values past
+// them are 0 along k, and anything across it (in columns whose results are
+// never stored).  Whole k steps load 16 bytes everywhere, unconditionally:
+// rows past the end repeat the last one, and a chunk over a row's end reads on
+// into the row that follows.  Only the last step has to look where the
+// operand's memory ends (`mem` rows from the corner on).  `narrow`: rows of
+// under 8 values, which no chunk fits.
 template <typename T, int D, bool ACROSS, int THREADS>
 struct Stage {
   static constexpr int kPer = D * 8 / THREADS;
   static constexpr int kAcross = ACROSS ? D / kChunk<T> : 8;   // chunks of a tile row
   Chunk<T> c[kPer];
-  __device__ __forceinline__ void load(const T* __restrict__ p, int64_t ld, int rows, int cols, int tid) {
+  __device__ __forceinline__ void load(const T* __restrict__ p, int64_t ld, int rows, int cols, int mem, bool narrow,
+                                       int tid) {
+    if (!narrow && (ACROSS ? rows > kStep<T> : cols >= kStep<T>)) {
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int id = j * THREADS + tid, r = id / kAcross, at = (id % kAcross) * kChunk<T>;
-      const int n = r < rows ? cols - at : 0;
-      c[j] = load_chunk_n(p + r * ld + at, n < 0 ? 0 : n);
+      for (int j = 0; j < kPer; ++j) {
+        const int id = j * THREADS + tid, r = id / kAcross, at = (id % kAcross) * kChunk<T>;
+        if constexpr (ACROSS)
+          c[j] = load_chunk(p + int64_t(r) * ld + (at < cols ? at : 0));
+        else
+          c[j] = load_chunk(p + int64_t(r < rows ? r : rows - 1) * ld + at);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int id = j * THREADS + tid, r = id / kAcross, at = (id % kAcross) * kChunk<T>;
+        const int left = r < rows ? cols - at : 0, n = left < 0 ? 0 : left;
+        const bool safe = n >= kChunk<T> || (n > 0 && !narrow && r + 1 < mem);
+        if (safe) c[j] = load_chunk(p + int64_t(r) * ld + at);
+#pragma unroll
+        for (int i = 0; i < kChunk<T>; ++i) c[j].v[i] = i < n ? c[j].v[i] : T(0.0f);
+        if (!safe && n > 0) c[j] = load_chunk_n(p + int64_t(r) * ld + at, n);
+      }
     }
   }
   __device__ __forceinline__ void store(char* tile, int tid) const {
@@ -296,15 +317,21 @@ __device__ __forceinline__ void multiply_step(const char* ta, const char* tb, in
 // neighbours along n; each wave then turns 16 rows at a time through LDS
 // into whole chunks of output rows.  DIRECT: both operands in whole aligned
 // chunks, loaded straight into one of two LDS stages while the other is
-// multiplied; else through registers, at any alignment.
-template <typename T, Mode MODE, int BM, int BN, int WM, int WN, bool DIRECT>
+// multiplied; else through registers, at any alignment.  KW > 1: so many sets
+// of WM x WN waves take the k steps in turn, for products of few tiles and a
+// long k, whose time is the steps that wait on each other; the first set adds
+// the others' results.
+template <typename T, Mode MODE, int BM, int BN, int WM, int WN, bool DIRECT, int KW>
 __device__ __forceinline__ void product_tile(const ProductArgs& p, int tile, char* lds) {
   constexpr int THREADS = 64 * WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
   constexpr bool A_ACROSS = MODE == kDw, B_ACROSS = MODE != kFwd;
   constexpr int kPatch = TN + 4;   // floats of a patch row: 4 more keep its 16-byte writes off each other's banks
   constexpr int kTiles = (BM + BN) * 128;
-  const int tid = threadIdx.x, lane = tid & 63;
+  const int set = KW > 1 ? __builtin_amdgcn_readfirstlane(int(threadIdx.x) / THREADS) : 0;
+  const int tid = KW > 1 ? int(threadIdx.x) % THREADS : int(threadIdx.x), lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
+  char* const base = lds;
+  if (KW > 1) lds += set * kTiles * (DIRECT ? 2 : 1);
 
   // Which tile.  kFwd, kDx: the height index picks group and rows; kDw: the
   // stretch does (without planes to join, every group is one stretch, and
@@ -335,6 +362,10 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, int tile, cha
   for (f32x4& v : sum) v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   const bool sums = MODE == kDw && p.db != nullptr && n0 == 0 && wn == 0;
 
+  // the sets' first steps lie side by side
+  const int first = k_all - set * kStep<T>;
+  a += set * step_a;
+  b += set * step_b;
   if (MODE == kDw && k_all == 0) {
     // an empty group's zeros
   } else if constexpr (DIRECT) {
@@ -342,52 +373,99 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, int tile, cha
     Direct<T, BN, B_ACROSS, THREADS> db;
     da.init(p.lda, tid);
     db.init(p.ldb, tid);
-    da.load(a, p.lda, A_ACROSS ? k_all : m_left, A_ACROSS ? m_left : k_all, lds, wave);
-    db.load(b, p.ldb, B_ACROSS ? k_all : n_left, B_ACROSS ? n_left : k_all, lds + BM * 128, wave);
+    if (KW == 1 || first > 0) {
+      da.load(a, p.lda, A_ACROSS ? first : m_left, A_ACROSS ? m_left : first, lds, wave);
+      db.load(b, p.ldb, B_ACROSS ? first : n_left, B_ACROSS ? n_left : first, lds + BM * 128, wave);
+    }
     int stage = 0;
-    for (int left = k_all; left > 0; left -= kStep<T>) {
+    for (int all = k_all, left = first; all > 0; all -= KW * kStep<T>, left -= KW * kStep<T>) {
       tile_barrier();
-      const int next = left - kStep<T>;
+      const int next = left - KW * kStep<T>;
       if (next > 0) {
-        a += step_a;
-        b += step_b;
+        a += KW * step_a;
+        b += KW * step_b;
         char* t = lds + (stage ^ 1) * kTiles;
         da.load(a, p.lda, A_ACROSS ? next : m_left, A_ACROSS ? m_left : next, t, wave);
         db.load(b, p.ldb, B_ACROSS ? next : n_left, B_ACROSS ? n_left : next, t + BM * 128, wave);
       }
       const char* t = lds + stage * kTiles;
-      multiply_step<T, BM, BN, A_ACROSS, B_ACROSS, FM, FN>(t, t + BM * 128, wm * TM, wn * TN, lane, acc, sum, sums);
+      if (KW == 1 || left > 0)
+        multiply_step<T, BM, BN, A_ACROSS, B_ACROSS, FM, FN>(t, t + BM * 128, wm * TM, wn * TN, lane, acc, sum, sums);
       stage ^= 1;
     }
     tile_barrier();
   } else {
     char* const ta = lds;
     char* const tb = lds + BM * 128;
+    // rows of memory from the corners on: the weights' groups follow each other
+    const int a_mem = p.rows - s.row0 - (A_ACROSS ? set * kStep<T> : 0);
+    const int64_t w_rows = int64_t(std::max(1, p.groups) - s.e) * (MODE == kFwd ? p.n : p.k);
+    const int64_t b_rows = MODE == kDw ? a_mem : w_rows - (MODE == kFwd ? n0 : set * kStep<T>);
+    const int b_mem = b_rows < (1 << 30) ? int(b_rows) : 1 << 30;
+    const bool a_narrow = (A_ACROSS ? p.m : p.k) < 8, b_narrow = (B_ACROSS ? p.n : p.k) < 8;
     Stage<T, BM, A_ACROSS, THREADS> sa;
     Stage<T, BN, B_ACROSS, THREADS> sb;
-    sa.load(a, p.lda, A_ACROSS ? k_all : m_left, A_ACROSS ? m_left : k_all, tid);
-    sb.load(b, p.ldb, B_ACROSS ? k_all : n_left, B_ACROSS ? n_left : k_all, tid);
-    for (int k0 = 0; k0 < k_all; k0 += kStep<T>) {
-      sa.store(ta, tid);
-      sb.store(tb, tid);
-      __syncthreads();
-      const int left = k_all - k0 - kStep<T>;
-      if (left > 0) {   // the next step's loads fly while this one is multiplied
-        a += step_a;
-        b += step_b;
-        sa.load(a, p.lda, A_ACROSS ? left : m_left, A_ACROSS ? m_left : left, tid);
-        sb.load(b, p.ldb, B_ACROSS ? left : n_left, B_ACROSS ? n_left : left, tid);
+    if (KW == 1 || first > 0) {
+      sa.load(a, p.lda, A_ACROSS ? first : m_left, A_ACROSS ? m_left : first, a_mem, a_narrow, tid);
+      sb.load(b, p.ldb, B_ACROSS ? first : n_left, B_ACROSS ? n_left : first, b_mem, b_narrow, tid);
+    }
+    for (int all = k_all, left = first, done = 0; all > 0; all -= KW * kStep<T>, left -= KW * kStep<T>) {
+      if (KW == 1 || left > 0) {
+        sa.store(ta, tid);
+        sb.store(tb, tid);
       }
-      multiply_step<T, BM, BN, A_ACROSS, B_ACROSS, FM, FN>(ta, tb, wm * TM, wn * TN, lane, acc, sum, sums);
+      __syncthreads();
+      const int next = left - KW * kStep<T>;
+      if (next > 0) {   // the next step's loads fly while this one is multiplied
+        a += KW * step_a;
+        b += KW * step_b;
+        done += KW * kStep<T>;
+        sa.load(a, p.lda, A_ACROSS ? next : m_left, A_ACROSS ? m_left : next, A_ACROSS ? a_mem - done : a_mem, a_narrow,
+                tid);
+        sb.load(b, p.ldb, B_ACROSS ? next : n_left, B_ACROSS ? n_left : next, B_ACROSS ? b_mem - done : b_mem, b_narrow,
+                tid);
+      }
+      if (KW == 1 || left > 0)
+        multiply_step<T, BM, BN, A_ACROSS, B_ACROSS, FM, FN>(ta, tb, wm * TM, wn * TN, lane, acc, sum, sums);
       __syncthreads();
     }
+  }
+
+  if constexpr (KW > 1) {
+    // sets 1 .. KW - 1 leave their results in LDS, register by register
+    constexpr int kRegs = FM * FN + (MODE == kDw ? FM : 0);
+    f32x4* box = reinterpret_cast<f32x4*>(base);
+    if (set > 0) {
+      f32x4* mine = box + (set - 1) * kRegs * THREADS + tid;
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) mine[(i * FN + j) * THREADS] = acc[i][j];
+      if constexpr (MODE == kDw)
+#pragma unroll
+        for (int i = 0; i < FM; ++i) mine[(FM * FN + i) * THREADS] = sum[i];
+    }
+    __syncthreads();
+    if (set > 0) return;
+#pragma unroll
+    for (int q = 0; q < KW - 1; ++q) {
+      const f32x4* theirs = box + q * kRegs * THREADS + tid;
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] += theirs[(i * FN + j) * THREADS];
+      if constexpr (MODE == kDw)
+#pragma unroll
+        for (int i = 0; i < FM; ++i) sum[i] += theirs[(FM * FN + i) * THREADS];
+    }
+    lds = base + (KW - 1) * kRegs * THREADS * 16;   // the patches lie past the boxes, which others may still read
   }
 
   // Epilogue: 16 rows at a time through the wave's patch.  A lane has the
   // same eight columns in every pass, so their bias stays in registers; the
   // residual's chunks are all asked for before the first is needed.
   constexpr int kAcross = TN / 8, kRows = 64 / kAcross, kPasses = 16 / kRows;   // lanes of a row, rows a pass
-  constexpr int kBatch = std::min(FM, 16 / (kPasses * Eight<T>::kParts));       // fragments whose residual is in flight
+  constexpr int kBatch = std::min(FM, (FM > 4 ? 8 : 16) / (kPasses * Eight<T>::kParts));   // their residual in flight
   const int col = wn * TN + (lane % kAcross) * 8, n = std::min(8, n_left - col);
   const int64_t row0 = MODE == kDw ? m0 : s.row0;
   float* plane = nullptr;
@@ -475,10 +553,20 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, int tile, cha
   }
 }
 
-template <typename T, Mode MODE, int BM, int BN, int WM, int WN, bool DIRECT>
-__global__ __launch_bounds__(64 * WM * WN) void k_product(ProductArgs p) {
+// LDS of a workgroup: two stages of tiles a set (one where they come through
+// registers, or where `steps` is 1), later the boxes of the sets' results and
+// the patches.
+constexpr int product_lds(int bm, int bn, int wm, int wn, int kw, bool direct, int steps) {
+  const int tiles = (bm + bn) * 128 * (direct && steps > 1 ? 2 : 1) * kw;
+  const int regs = (bm / wm / 16) * (bn / wn / 16 + 1);   // kDw's, the largest
+  const int after = (kw - 1) * regs * 64 * wm * wn * 16 + wm * wn * 16 * (bn / wn + 4) * 4;
+  return tiles > after ? tiles : after;
+}
+
+template <typename T, Mode MODE, int BM, int BN, int WM, int WN, bool DIRECT, int KW>
+__global__ __launch_bounds__(64 * WM * WN * KW, KW > 1 ? 4 : 2) void k_product(ProductArgs p) {
   extern __shared__ __align__(16) char lds[];
-  product_tile<T, MODE, BM, BN, WM, WN, DIRECT>(p, xcd_tile(blockIdx.x, gridDim.x), lds);
+  product_tile<T, MODE, BM, BN, WM, WN, DIRECT, KW>(p, xcd_tile(blockIdx.x, gridDim.x), lds);
 }
 
 // --- the product over many rows of a short k ---------------------------------------
@@ -799,23 +887,23 @@ struct DbJoin {
 __device__ __forceinline__ void join_db(const DbJoin& j, const ProductArgs& p, int block) {
   const Span s = group_span(p.offsets, p.groups, p.rows, j.unit, block / j.blocks);
   const int col = block % j.blocks * 256 + threadIdx.x;
-  if (col < j.out) j.db[int64_t(s.e) * j.out + col] = plane_sum(j.part, j.out, s, col);
+  if (threadIdx.x < 256 && col < j.out) j.db[int64_t(s.e) * j.out + col] = plane_sum(j.part, j.out, s, col);
 }
 __global__ __launch_bounds__(256) void k_join_db(DbJoin j, ProductArgs p) { join_db(j, p, blockIdx.x); }
 
 // Small problems, whose cost is their launches: dx, dw and what is left of
 // db in one, the workgroups shared out among the three.
-template <typename T, bool DIRECT>
-__global__ __launch_bounds__(256) void k_bwd(ProductArgs x, int x_tiles, ProductArgs w, int w_tiles, DbJoin j) {
+template <typename T, bool DIRECT, int KW>
+__global__ __launch_bounds__(256 * KW) void k_bwd(ProductArgs x, int x_tiles, ProductArgs w, int w_tiles, DbJoin j) {
   extern __shared__ __align__(16) char lds[];
   int b = blockIdx.x;
   if (b < x_tiles) {
-    product_tile<T, kDx, 64, 64, 2, 2, DIRECT>(x, b, lds);
+    product_tile<T, kDx, 64, 64, 2, 2, DIRECT, KW>(x, b, lds);
     return;
   }
   b -= x_tiles;
   if (b < w_tiles)
-    product_tile<T, kDw, 64, 64, 2, 2, DIRECT>(w, b, lds);
+    product_tile<T, kDw, 64, 64, 2, 2, DIRECT, KW>(w, b, lds);
   else
     join_db(j, w, b - w_tiles);
 }
@@ -838,26 +926,29 @@ bool direct_ok(const ProductArgs& p, Mode mode) {
   return whole(p.a, p.lda) && whole(p.b, p.ldb) && (mode == kDw || p.k % kChunk<T> == 0);
 }
 
-template <typename T, Mode MODE, int BM, int BN, int WM, int WN, bool DIRECT>
+// Kernels of more than 64 KB of LDS have to ask for it, once per device.
+template <class K>
+void ask_lds(K kernel, int bytes, std::atomic<uint64_t>& asked) {
+  int dev = 0;
+  (void)hipGetDevice(&dev);
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if ((asked.load(std::memory_order_relaxed) & bit) == 0) {
+    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    asked.fetch_or(bit, std::memory_order_relaxed);
+  }
+}
+
+template <typename T, Mode MODE, int BM, int BN, int WM, int WN, bool DIRECT, int KW>
 void go_tile(const ProductArgs& p, int64_t grid, hipStream_t st) {
-  constexpr int tiles = (BM + BN) * 128, patches = WM * WN * 16 * (BN / WN + 4) * 4;
-  constexpr int most = std::max(2 * tiles, patches);
+  constexpr int most = product_lds(BM, BN, WM, WN, KW, DIRECT, 2);
   if constexpr (most > 65536) {
-    // more LDS than a launch gets unasked; once per device
     static std::atomic<uint64_t> asked{0};
-    int dev = 0;
-    (void)hipGetDevice(&dev);
-    const uint64_t bit = uint64_t(1) << (dev & 63);
-    if ((asked.load(std::memory_order_relaxed) & bit) == 0) {
-      (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&k_product<T, MODE, BM, BN, WM, WN, DIRECT>),
-                                hipFuncAttributeMaxDynamicSharedMemorySize, most);
-      asked.fetch_or(bit, std::memory_order_relaxed);
-    }
+    ask_lds(&k_product<T, MODE, BM, BN, WM, WN, DIRECT, KW>, most, asked);
   }
   // one k step needs one stage, and leaves LDS for more workgroups
-  const int steps = MODE == kDw ? 2 : (p.k > kStep<T> ? 2 : 1);
-  const int lds = std::max(patches, tiles * (DIRECT ? steps : 1));
-  k_product<T, MODE, BM, BN, WM, WN, DIRECT><<<int(grid), 64 * WM * WN, lds, st>>>(p);
+  const int steps = MODE == kDw || KW > 1 || p.k > kStep<T> ? 2 : 1;
+  k_product<T, MODE, BM, BN, WM, WN, DIRECT, KW>
+      <<<int(grid), 64 * WM * WN * KW, product_lds(BM, BN, WM, WN, KW, DIRECT, steps), st>>>(p);
 }
 
 // Tiles of the product and the shape of its grid.
@@ -873,13 +964,20 @@ int64_t lay_out(ProductArgs& p, int bm, int bn) {
   return max_slots(p.rows, p.groups, bm) * p.tiles_n;
 }
 
-template <typename T, Mode MODE, int BM, int BN, int WM, int WN>
+template <typename T, Mode MODE, int BM, int BN, int WM, int WN, int KW = 1>
 void go_product(ProductArgs p, hipStream_t st) {
   const int64_t grid = lay_out<MODE>(p, BM, BN);
   if (direct_ok<T>(p, MODE))
-    go_tile<T, MODE, BM, BN, WM, WN, true>(p, grid, st);
+    go_tile<T, MODE, BM, BN, WM, WN, true, KW>(p, grid, st);
   else if constexpr (BM <= 128 && BN <= 128)
-    go_tile<T, MODE, BM, BN, WM, WN, false>(p, grid, st);
+    go_tile<T, MODE, BM, BN, WM, WN, false, KW>(p, grid, st);
+}
+
+// Four wave sets a tile: few tiles (two workgroups of four sets do not share a
+// CU) and a k of eight steps at least.
+template <typename T>
+bool split_k(int64_t tiles, int64_t k) {
+  return tiles <= 512 && k >= 8 * kStep<T>;
 }
 
 // k_rows: a short k, whole chunks everywhere, and rows enough that every
@@ -926,6 +1024,8 @@ void run_rows(const ProductArgs& p, hipStream_t st) {
     go_product<T, MODE, 256, 256, 2, 4>(p, st);
   else if (big >= 256)
     go_product<T, MODE, 128, 128, 2, 2>(p, st);
+  else if (split_k<T>(max_slots(p.rows, p.groups, 64) * ceil_div(p.n, 64), p.k))
+    go_product<T, MODE, 64, 64, 2, 2, 4>(p, st);
   else
     go_product<T, MODE, 64, 64, 2, 2>(p, st);
 }
@@ -934,6 +1034,7 @@ void run_rows(const ProductArgs& p, hipStream_t st) {
 // can be sized for it.
 struct BwdPlan {
   bool small;              // dx and dw in one launch of 64 x 64 tiles
+  bool sets;               // and that of four wave sets a tile
   int32_t unit_b, unit_w;  // rows of a stretch of db (with an activation) and of dw
   bool part_b, part_w;     // more than one stretch a group: partial sums to join
   int64_t plane;           // values of a plane of dw
@@ -948,8 +1049,12 @@ BwdPlan bwd_plan(int64_t rows, int32_t in, int32_t out, int32_t groups, int act)
   s.small = slots * ceil_div(in, 128) < 256 && slots * ceil_div(out, 128) < 256;
   const int64_t side = s.small ? 64 : 128;
   const int64_t tiles = ceil_div(out, side) * ceil_div(in, side);
-  // stretches so that about 768 workgroups share the rows, 256 rows at least
-  s.unit_w = int32_t(std::max<int64_t>(256, ceil_div(ceil_div(rows * tiles, 768), 64) * 64));
+  const int64_t x_tiles = max_slots(rows, groups, 64) * ceil_div(in, 64);
+  s.sets = s.small && (split_k<T>(x_tiles, out) ||
+                       (rows >= 8 * kStep<T> * std::max(1, groups) && tiles * std::max(1, groups) <= 512));
+  // stretches so that about 768 workgroups (of four sets: 256) share the rows, of 4 k steps a set at least
+  const int64_t cut = ceil_div(rows * tiles, s.sets ? 256 : 768);
+  s.unit_w = int32_t(std::max<int64_t>((s.sets ? 16 : 4) * kStep<T>, ceil_div(cut, 64) * 64));
   s.part_w = rows > s.unit_w;
   s.plane = ceil_div(int64_t(out) * in + out, 64) * 64;
   // about 2048 workgroups of the slope's kernel, 64 rows at least
@@ -1046,12 +1151,23 @@ hipError_t linear_bwd(const LinearArgs& a, char* ws, hipStream_t st) {
   if (plan.small) {
     const int64_t x_tiles = want_dx ? lay_out<kDx>(x, 64, 64) : 0, w_tiles = want_dw ? lay_out<kDw>(w, 64, 64) : 0;
     const int64_t grid = x_tiles + w_tiles + int64_t(j.blocks) * groups;
-    constexpr int tiles = 128 * 128, patches = 4 * 16 * 36 * 4;
     if (grid > 0) {
-      if ((!want_dx || direct_ok<T>(x, kDx)) && (!want_dw || direct_ok<T>(w, kDw)))
-        k_bwd<T, true><<<int(grid), 256, std::max(2 * tiles, patches), st>>>(x, int(x_tiles), w, int(w_tiles), j);
+      const bool direct = (!want_dx || direct_ok<T>(x, kDx)) && (!want_dw || direct_ok<T>(w, kDw));
+      const auto go = [&](auto d, auto kw) {
+        constexpr bool D = decltype(d)::value;
+        constexpr int KW = decltype(kw)::value, lds = product_lds(64, 64, 2, 2, KW, D, 2);
+        if constexpr (lds > 65536) {
+          static std::atomic<uint64_t> asked{0};
+          ask_lds(&k_bwd<T, D, KW>, lds, asked);
+        }
+        k_bwd<T, D, KW><<<int(grid), 256 * KW, lds, st>>>(x, int(x_tiles), w, int(w_tiles), j);
+      };
+      using One = std::integral_constant<int, 1>;
+      using Four = std::integral_constant<int, 4>;
+      if (direct)
+        plan.sets ? go(std::true_type{}, Four{}) : go(std::true_type{}, One{});
       else
-        k_bwd<T, false><<<int(grid), 256, std::max(tiles, patches), st>>>(x, int(x_tiles), w, int(w_tiles), j);
+        plan.sets ? go(std::false_type{}, Four{}) : go(std::false_type{}, One{});
     }
   } else {
     if (j.blocks > 0) k_join_db<<<j.blocks * groups, 256, 0, st>>>(j, p);
