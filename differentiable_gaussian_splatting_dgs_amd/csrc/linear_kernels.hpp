@@ -145,6 +145,25 @@ __device__ __forceinline__ typename Frag<T>::V read_frag(const char* tile, int d
   }
 }
 
+// The fragment of columns d0 .. d0 + 15 over rows 32 kk .. of a tile that lies
+// along k, [step][ROWS][128 bytes] (16-bit types).
+template <typename T, int ROWS>
+__device__ __forceinline__ typename Frag<T>::V read_across(const char* tile, int d0, int kk, int lane) {
+  const int i = lane & 15, g = lane >> 4, c = (d0 >> 3) + ((i & 3) >> 1);
+  s16x8 v;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = 32 * kk + 8 * g + 4 * h + (i >> 2);
+    const char* p = tile + (c >> 3) * ROWS * 128 + tile_at<T, ROWS, false>(r, c & 7) + (i & 1) * 8;
+    const s16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p));
+    v[4 * h] = u[0];
+    v[4 * h + 1] = u[1];
+    v[4 * h + 2] = u[2];
+    v[4 * h + 3] = u[3];
+  }
+  return __builtin_bit_cast(typename Frag<T>::V, v);
+}
+
 // Global -> registers -> LDS for one operand, at any alignment.  `rows` and
 // `cols`: what is left of the operand from the tile's corner; values past
 // them are 0 along k, and anything across it (in columns whose results are
@@ -233,9 +252,20 @@ struct Direct {
 };
 
 // Every wave's loads into LDS have landed and its reads of LDS are done,
-// then the workgroup meets.
+// then the workgroup meets (a set of one wave has nobody to meet).
+template <int WAVES>
 __device__ __forceinline__ void tile_barrier() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  if constexpr (WAVES > 1)
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  else
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+}
+template <int WAVES>
+__device__ __forceinline__ void stage_barrier() {
+  if constexpr (WAVES > 1)
+    __syncthreads();
+  else
+    wave_sync();
 }
 
 // --- epilogue -----------------------------------------------------------------------------
@@ -272,6 +302,20 @@ __device__ __forceinline__ void act_eight(float (&v)[8], int act) {   // act is 
   } else if (act == kActGelu) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = act_apply<T>(v[i], kActGelu);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void slope_eight(float (&v)[8], int act) {
+  if (act == kActRelu) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = act_slope<T>(v[i], kActRelu);
+  } else if (act == kActSilu) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = act_slope<T>(v[i], kActSilu);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = act_slope<T>(v[i], kActGelu);
   }
 }
 
@@ -379,7 +423,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, int tile, cha
     }
     int stage = 0;
     for (int all = k_all, left = first; all > 0; all -= KW * kStep<T>, left -= KW * kStep<T>) {
-      tile_barrier();
+      tile_barrier<WM * WN>();
       const int next = left - KW * kStep<T>;
       if (next > 0) {
         a += KW * step_a;
@@ -393,7 +437,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, int tile, cha
         multiply_step<T, BM, BN, A_ACROSS, B_ACROSS, FM, FN>(t, t + BM * 128, wm * TM, wn * TN, lane, acc, sum, sums);
       stage ^= 1;
     }
-    tile_barrier();
+    tile_barrier<WM * WN * KW>();
   } else {
     char* const ta = lds;
     char* const tb = lds + BM * 128;
@@ -414,7 +458,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, int tile, cha
         sa.store(ta, tid);
         sb.store(tb, tid);
       }
-      __syncthreads();
+      stage_barrier<WM * WN>();
       const int next = left - KW * kStep<T>;
       if (next > 0) {   // the next step's loads fly while this one is multiplied
         a += KW * step_a;
@@ -427,8 +471,9 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, int tile, cha
       }
       if (KW == 1 || left > 0)
         multiply_step<T, BM, BN, A_ACROSS, B_ACROSS, FM, FN>(ta, tb, wm * TM, wn * TN, lane, acc, sum, sums);
-      __syncthreads();
+      stage_barrier<WM * WN>();
     }
+    if (WM * WN == 1) __syncthreads();
   }
 
   if constexpr (KW > 1) {
@@ -564,7 +609,7 @@ constexpr int product_lds(int bm, int bn, int wm, int wn, int kw, bool direct, i
 }
 
 template <typename T, Mode MODE, int BM, int BN, int WM, int WN, bool DIRECT, int KW>
-__global__ __launch_bounds__(64 * WM * WN * KW, KW > 1 ? 4 : 2) void k_product(ProductArgs p) {
+__global__ __launch_bounds__(64 * WM * WN * KW, KW == 4 ? 4 : 2) void k_product(ProductArgs p) {
   extern __shared__ __align__(16) char lds[];
   product_tile<T, MODE, BM, BN, WM, WN, DIRECT, KW>(p, xcd_tile(blockIdx.x, gridDim.x), lds);
 }
@@ -878,34 +923,323 @@ __global__ __launch_bounds__(256) void k_join(const float* __restrict__ part, in
   }
 }
 
-// db from the partial rows of k_act_grad.
+// db from the partial rows of k_act_grad: 16 columns a workgroup, 16 shares
+// of a group's rows, joined in a fixed order.
 struct DbJoin {
   const float* part;
   float* db;
-  int32_t out, unit, blocks;   // blocks: workgroups of 256 columns a group
+  int32_t out, unit, blocks;   // blocks: workgroups of a group
 };
-__device__ __forceinline__ void join_db(const DbJoin& j, const ProductArgs& p, int block) {
+__device__ __forceinline__ void join_db(const DbJoin& j, const ProductArgs& p, int block, float* box) {
   const Span s = group_span(p.offsets, p.groups, p.rows, j.unit, block / j.blocks);
-  const int col = block % j.blocks * 256 + threadIdx.x;
-  if (threadIdx.x < 256 && col < j.out) j.db[int64_t(s.e) * j.out + col] = plane_sum(j.part, j.out, s, col);
+  const int tid = threadIdx.x, col = block % j.blocks * 16 + (tid & 15);
+  if (tid < 256) {
+    float v = 0.0f;
+    if (col < j.out)
+#pragma unroll 4
+      for (int t = tid >> 4; t < s.slots; t += 16) v += j.part[(int64_t(s.slot0) + t) * j.out + col];
+    box[tid] = v;
+  }
+  __syncthreads();
+  if (tid >= 16 || col >= j.out) return;
+  float v = 0.0f;
+#pragma unroll
+  for (int t = 0; t < 16; ++t) v += box[16 * t + tid];
+  j.db[int64_t(s.e) * j.out + col] = v;
 }
-__global__ __launch_bounds__(256) void k_join_db(DbJoin j, ProductArgs p) { join_db(j, p, blockIdx.x); }
+__global__ __launch_bounds__(256) void k_join_db(DbJoin j, ProductArgs p) {
+  __shared__ float box[256];
+  join_db(j, p, blockIdx.x, box);
+}
 
 // Small problems, whose cost is their launches: dx, dw and what is left of
-// db in one, the workgroups shared out among the three.
-template <typename T, bool DIRECT, int KW>
-__global__ __launch_bounds__(256 * KW) void k_bwd(ProductArgs x, int x_tiles, ProductArgs w, int w_tiles, DbJoin j) {
+// db in one, the workgroups shared out among the three.  Tiles of 64 x 64, or
+// of 32 x 32 with eight wave sets where the k of one of them is long.
+template <typename T, int TILE, int W, bool DIRECT, int KW>
+__global__ __launch_bounds__(64 * W * W * KW) void k_bwd(ProductArgs x, int x_tiles, ProductArgs w, int w_tiles, DbJoin j) {
   extern __shared__ __align__(16) char lds[];
   int b = blockIdx.x;
   if (b < x_tiles) {
-    product_tile<T, kDx, 64, 64, 2, 2, DIRECT, KW>(x, b, lds);
+    product_tile<T, kDx, TILE, TILE, W, W, DIRECT, KW>(x, b, lds);
     return;
   }
   b -= x_tiles;
   if (b < w_tiles)
-    product_tile<T, kDw, 64, 64, 2, 2, DIRECT, KW>(w, b, lds);
+    product_tile<T, kDw, TILE, TILE, W, W, DIRECT, KW>(w, b, lds);
   else
-    join_db(j, w, b - w_tiles);
+    join_db(j, w, b - w_tiles, reinterpret_cast<float*>(lds));
+}
+
+// --- the whole backward pass over many rows of a narrow layer --------------------------
+
+struct FusedArgs {
+  const void* dy;
+  const void* z;       // NULL: no activation
+  const void* x;
+  const void* w;
+  void* dx;            // or NULL, and w with it
+  float* part;         // planes of [m = out][n = in], then [m] of db
+  const int64_t* offsets;
+  int64_t lddy, ldz, ldx, ldw, lddx, w_group, plane;
+  int32_t rows, groups, in, out, act, shares;
+};
+
+// Which share of the tiles tile t is in: share s holds total s / shares ..
+// total (s + 1) / shares - 1.
+__host__ __device__ inline int32_t share_of(int64_t t, int64_t total, int32_t shares) {
+  int64_t s = t * shares / total;
+  while (total * (s + 1) / shares <= t) ++s;
+  return int32_t(s);
+}
+
+// Layers of up to 64 KS columns on both sides: one pass reads dy, z and x and
+// writes dx, and dw never leaves the registers until the rows run out.  Each
+// of 8 waves holds the weights' fragments of 32 columns of dx (16 KS
+// registers) and 16 KS x 32 KS of dw's sums; the workgroup walks its share of
+// the row tiles (128 / KS rows; dy, z, x 16 KB each, two LDS stages):
+//   dz = dy act'(z) in place, rounded for the matrix instructions, db summed
+//   unrounded; dx = dz w; dw += dz^T x, its operands read transposed.
+// A share that ends inside a group, or a group inside a share, leaves one
+// plane of partial sums, number share + group.  Bound by HBM: 3 or 4 planes of
+// the rows, each once.
+template <typename T, int KS>
+__global__ __launch_bounds__(512, 2) void k_bwd_rows(FusedArgs p) {
+#ifdef __HIP_DEVICE_COMPILE__
+  static_assert(sizeof(T) == 2, "transposed LDS reads are 16 bit");
+  constexpr int BM = 128 / KS, WN = 2 * KS, WM = 8 / WN, TM = BM / WM, FM = TM / 16, FN = 2;
+  constexpr int DM = KS, DN = 2 * KS;                  // dw fragments of a wave; the waves lie 4 x 2
+  constexpr int kStage = 49152, kPatch = 36, kTile = 16384, K = 8;
+  constexpr int kStores = FM * Eight<T>::kParts;
+  __shared__ __align__(16) char lds[2 * kStage + 8 * 16 * kPatch * 4];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
+  float* patch = reinterpret_cast<float*>(lds + 2 * kStage) + wave * 16 * kPatch;
+
+  const int share = xcd_tile(blockIdx.x, gridDim.x);
+  const int64_t total = total_slots(p.offsets, p.groups, p.rows, BM);
+  const int t0 = int(total * share / p.shares), t1 = int(total * (share + 1) / p.shares);
+  if (t0 >= t1) return;
+
+  // a thread's chunks of a tile: 8 of a row and step, row by row, step by step
+  const auto fetch_one = [&](const void* q, int64_t ld, int cols, const Span& s, int th, char* to) {
+    const __amdgpu_buffer_rsrc_t rsrc =
+        buffer_of(static_cast<const T*>(q) + int64_t(s.row0) * ld, ld, s.e < 0 ? 0 : s.row1 - s.row0, cols);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int at = j * 512 + th, step = at / (BM * 8), r = at / 8 % BM, col = (step * 8 + ((at & 7) ^ (r & 7))) * K;
+      const uint32_t off = col < cols ? uint32_t(r) * uint32_t(ld * 2) + uint32_t(col * 2) : 0xfffffff0u;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rsrc, (__attribute__((address_space(3))) void*)(to + j * 8192 + wave * 1024), 16, off, 0, 0, 0);
+    }
+  };
+  const auto fetch = [&](const Span& s, int stage) {
+    char* to = lds + stage * kStage;
+    int th = tid;
+    asm volatile("" : "+v"(th));   // addresses kept through the loop would spill
+    fetch_one(p.dy, p.lddy, p.out, s, th, to);
+    if (p.z != nullptr) fetch_one(p.z, p.ldz, p.out, s, th, to + kTile);
+    fetch_one(p.x, p.ldx, p.in, s, th, to + 2 * kTile);
+  };
+  const auto after = [&](const Span& s, int t) {
+    if (t >= t1) return Span{-1, 0, 0, 0, 0, 0};
+    if (p.groups > 0 && t >= s.slot0 + s.slots) return find_span(p.offsets, p.groups, p.rows, BM, t);
+    Span q = s;
+    q.row0 = s.row0 + BM;
+    q.row1 = std::min(s.end, q.row0 + BM);
+    return q;
+  };
+  Span now = find_span(p.offsets, p.groups, p.rows, BM, t0);
+  fetch(now, 0);
+
+  typename Frag<T>::V fw[KS * 2][FN];
+  f32x4 dw[DM][DN];
+  float db[K];
+#pragma unroll
+  for (int i = 0; i < DM; ++i)
+#pragma unroll
+    for (int j = 0; j < DN; ++j) dw[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < K; ++i) db[i] = 0.0f;
+  // dz: this thread's chunk column and first row
+  constexpr int kCols = KS * 8, kApart = 512 / kCols;    // chunk columns, rows between a thread's rows
+  const int zc = tid % kCols, zr = tid / kCols;
+  const int am = (wave >> 1) * 16 * DM, bn = (wave & 1) * 16 * DN;   // this wave's corner of dw
+  const int col = wn * 32 + (lane & 3) * 8;
+  const bool live = col < p.in;
+  int group = -1, stage = 0;
+
+  for (int t = t0; t < t1; ++t) {
+    if (t == t0 || p.dx == nullptr)
+      rows_barrier<0>();
+    else
+      rows_barrier<kStores>();   // behind this stage's loads lie the last tile's stores
+    const Span next = after(now, t + 1);
+    fetch(next, stage ^ 1);
+    asm volatile("" ::: "memory");
+
+    if (now.e != group) {
+      group = now.e;
+      if (p.dx != nullptr) {
+        const T* w = static_cast<const T*>(p.w) + int64_t(group) * p.w_group;
+        int ln = lane;
+        asm volatile("" : "+v"(ln));
+#pragma unroll
+        for (int kk = 0; kk < KS * 2; ++kk)
+#pragma unroll
+          for (int j = 0; j < FN; ++j) {
+            const int n = wn * 32 + 16 * j + (ln & 15), k = (4 * kk + (ln >> 4)) * K;
+            const T* q = w + std::min(n, p.in - 1) + int64_t(k < p.out ? k : 0) * p.ldw;
+            Chunk<T> c;
+#pragma unroll
+            for (int i = 0; i < K; ++i) c.v[i] = q[i * p.ldw];
+#pragma unroll
+            for (int i = 0; i < K; ++i) c.v[i] = n < p.in && k < p.out ? c.v[i] : T(0.0f);
+            fw[kk][j] = __builtin_bit_cast(typename Frag<T>::V, c);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+      }
+    }
+
+    char* const ty = lds + stage * kStage;
+    const char* const tz = ty + kTile;
+    const char* const tx = ty + 2 * kTile;
+#pragma unroll
+    for (int r = zr; r < BM; r += kApart) {
+      const int at = (zc >> 3) * BM * 128 + tile_at<T, BM, false>(r, zc & 7);
+      Chunk<T> c = *reinterpret_cast<const Chunk<T>*>(ty + at);
+      if (p.z != nullptr) {
+        const Chunk<T> q = *reinterpret_cast<const Chunk<T>*>(tz + at);
+        float v[8], s[8];
+#pragma unroll
+        for (int i = 0; i < K; ++i) s[i] = float(q.v[i]);
+        slope_eight<T>(s, p.act);
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+          v[i] = float(c.v[i]) * s[i];
+          db[i] += v[i];
+          c.v[i] = T(v[i]);
+        }
+        *reinterpret_cast<Chunk<T>*>(ty + at) = c;
+      } else {
+#pragma unroll
+        for (int i = 0; i < K; ++i) db[i] += float(c.v[i]);
+      }
+    }
+    if (p.z != nullptr) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
+    if (p.dx != nullptr) {
+      const auto ro = buffer_of(static_cast<T*>(p.dx) + int64_t(now.row0) * p.lddx, p.lddx, now.row1 - now.row0, p.in);
+      f32x4 acc[FM][FN];
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int kk = 0; kk < KS * 2; ++kk) {
+        typename Frag<T>::V fa[FM];
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+          fa[i] = read_frag<T, BM, false>(ty + (kk >> 1) * BM * 128, wm * TM + 16 * i, kk & 1, lane);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j) acc[i][j] = Frag<T>::mma(fw[kk][j], fa[i], acc[i][j]);
+      }
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          *reinterpret_cast<f32x4*>(patch + (lane & 15) * kPatch + 16 * j + 4 * (lane >> 4)) = acc[i][j];
+        wave_sync();
+        const f32x4 lo = *reinterpret_cast<const f32x4*>(patch + (lane >> 2) * kPatch + (lane & 3) * 8);
+        const f32x4 hi = *reinterpret_cast<const f32x4*>(patch + (lane >> 2) * kPatch + (lane & 3) * 8 + 4);
+        Eight<T> o;
+        float v[8];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          v[c] = lo[c];
+          v[4 + c] = hi[c];
+        }
+        o.set(v);
+        const int r = wm * TM + 16 * i + (lane >> 2);
+        buffer_store_eight(ro, o, live ? uint32_t(r) * uint32_t(p.lddx * 2) + uint32_t(col * 2) : 0xffffff00u);
+        wave_sync();
+      }
+    }
+
+    // dw: rows past the group's end are 0 in both operands
+    int ln = lane;
+    asm volatile("" : "+v"(ln));   // its LDS addresses are made here: kept through the loop they would spill
+#pragma unroll
+    for (int kk = 0; kk < BM / 32; ++kk) {
+      typename Frag<T>::V fa[DM];
+#pragma unroll
+      for (int i = 0; i < DM; ++i) fa[i] = read_across<T, BM>(ty, am + 16 * i, kk, ln);
+#pragma unroll
+      for (int j = 0; j < DN; ++j) {
+        const auto fb = read_across<T, BM>(tx, bn + 16 * j, kk, ln);
+#pragma unroll
+        for (int i = 0; i < DM; ++i) dw[i][j] = Frag<T>::mma(fb, fa[i], dw[i][j]);
+      }
+    }
+
+    if (next.e != group) {   // the group or the share ends: its plane
+      float* plane = p.part + int64_t(share + group) * p.plane;
+#pragma unroll
+      for (int i = 0; i < DM; ++i)
+#pragma unroll
+        for (int j = 0; j < DN; ++j) {
+          const int m = am + 16 * i + (ln & 15), n = bn + 16 * j + 4 * (ln >> 4);
+          if (m < p.out && n < p.in) *reinterpret_cast<f32x4*>(plane + int64_t(m) * p.in + n) = dw[i][j];
+          dw[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+      // db: a column's sums lie kCols threads apart; the z tile is free
+      float* box = reinterpret_cast<float*>(ty + kTile);
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        box[i * 512 + tid] = db[i];
+        db[i] = 0.0f;
+      }
+      __syncthreads();
+      if (tid < kCols * K) {
+        const float* b = box + tid / kCols * 512 + tid % kCols;
+        float v = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kApart; ++q) v += b[q * kCols];
+        const int m = (tid % kCols) * K + tid / kCols;
+        if (m < p.out) plane[int64_t(p.out) * p.in + m] = v;
+      }
+    }
+    now = next;
+    stage ^= 1;
+  }
+  rows_barrier<0>();
+#endif
+}
+
+// Joins k_bwd_rows' planes: group e's are those of the shares its tiles are
+// in, numbers share + e.
+template <typename O>
+__global__ __launch_bounds__(256) void k_join_rows(FusedArgs p, int bm, O* __restrict__ out, float* __restrict__ db) {
+  const Span s = group_span(p.offsets, p.groups, p.rows, bm, blockIdx.y);
+  const int64_t total = total_slots(p.offsets, p.groups, p.rows, bm);
+  const int64_t size = int64_t(p.in) * p.out, all = size + p.out;
+  int lo = 0, n = 0;
+  if (s.slots > 0) {
+    lo = share_of(s.slot0, total, p.shares);
+    n = share_of(s.slot0 + s.slots - 1, total, p.shares) - lo + 1;
+  }
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += int64_t(gridDim.x) * 256) {
+    const float* q = p.part + int64_t(lo + int(blockIdx.y)) * p.plane + i;
+    float v = 0.0f;
+#pragma unroll 8
+    for (int t = 0; t < n; ++t) v += q[t * p.plane];
+    if (i < size)
+      out[int64_t(blockIdx.y) * size + i] = O(v);
+    else if (db != nullptr)
+      db[int64_t(blockIdx.y) * p.out + (i - size)] = v;
+  }
 }
 
 // --- launch ----------------------------------------------------------------------------------------
@@ -973,11 +1307,12 @@ void go_product(ProductArgs p, hipStream_t st) {
     go_tile<T, MODE, BM, BN, WM, WN, false, KW>(p, grid, st);
 }
 
-// Four wave sets a tile: few tiles (two workgroups of four sets do not share a
-// CU) and a k of eight steps at least.
+// Wave sets that share the k steps of a tile: for few tiles and a k of
+// eight steps at least.
 template <typename T>
-bool split_k(int64_t tiles, int64_t k) {
-  return tiles <= 512 && k >= 8 * kStep<T>;
+int wave_sets(int64_t tiles64, int64_t k) {
+  if (k < 8 * kStep<T> || tiles64 > 512) return 1;
+  return tiles64 <= 64 ? 8 : 4;
 }
 
 // k_rows: a short k, whole chunks everywhere, and rows enough that every
@@ -1024,17 +1359,24 @@ void run_rows(const ProductArgs& p, hipStream_t st) {
     go_product<T, MODE, 256, 256, 2, 4>(p, st);
   else if (big >= 256)
     go_product<T, MODE, 128, 128, 2, 2>(p, st);
-  else if (split_k<T>(max_slots(p.rows, p.groups, 64) * ceil_div(p.n, 64), p.k))
-    go_product<T, MODE, 64, 64, 2, 2, 4>(p, st);
-  else
-    go_product<T, MODE, 64, 64, 2, 2>(p, st);
+  else {
+    const int sets = wave_sets<T>(max_slots(p.rows, p.groups, 64) * ceil_div(p.n, 64), p.k);
+    if (sets == 8)
+      go_product<T, MODE, 32, 32, 1, 1, 8>(p, st);
+    else if (sets == 4)
+      go_product<T, MODE, 64, 64, 2, 2, 4>(p, st);
+    else
+      go_product<T, MODE, 64, 64, 2, 2>(p, st);
+  }
 }
 
 // How the backward pass is cut: from the sizes alone, so that the workspace
 // can be sized for it.
 struct BwdPlan {
+  bool fused;              // k_bwd_rows may run (the alignment decides), of so many steps and shares
+  int32_t steps, shares;
   bool small;              // dx and dw in one launch of 64 x 64 tiles
-  bool sets;               // and that of four wave sets a tile
+  bool sets;               // and that of 32 x 32 tiles of eight wave sets
   int32_t unit_b, unit_w;  // rows of a stretch of db (with an activation) and of dw
   bool part_b, part_w;     // more than one stretch a group: partial sums to join
   int64_t plane;           // values of a plane of dw
@@ -1044,17 +1386,22 @@ inline int64_t dz_ld(int32_t out, int chunk) { return ceil_div(out, chunk) * chu
 
 template <typename T>
 BwdPlan bwd_plan(int64_t rows, int32_t in, int32_t out, int32_t groups, int act) {
-  BwdPlan s;
+  BwdPlan s{};
   const int64_t slots = max_slots(rows, groups, 128);
+  s.steps = int32_t(ceil_div(std::max(in, out), 64));
+  s.steps = s.steps == 3 ? 4 : s.steps;
+  s.fused = sizeof(T) == 2 && s.steps <= 4 && in % 8 == 0 && out % 8 == 0 && rows >= 32768;
+  s.shares = 256;   // a workgroup a CU
   s.small = slots * ceil_div(in, 128) < 256 && slots * ceil_div(out, 128) < 256;
-  const int64_t side = s.small ? 64 : 128;
-  const int64_t tiles = ceil_div(out, side) * ceil_div(in, side);
   const int64_t x_tiles = max_slots(rows, groups, 64) * ceil_div(in, 64);
-  s.sets = s.small && (split_k<T>(x_tiles, out) ||
-                       (rows >= 8 * kStep<T> * std::max(1, groups) && tiles * std::max(1, groups) <= 512));
-  // stretches so that about 768 workgroups (of four sets: 256) share the rows, of 4 k steps a set at least
-  const int64_t cut = ceil_div(rows * tiles, s.sets ? 256 : 768);
-  s.unit_w = int32_t(std::max<int64_t>((s.sets ? 16 : 4) * kStep<T>, ceil_div(cut, 64) * 64));
+  const int64_t w_tiles = ceil_div(out, 64) * ceil_div(in, 64) * std::max(1, groups);
+  s.sets = s.small && x_tiles + w_tiles <= 512 &&
+           (out >= 8 * kStep<T> || rows >= 8 * kStep<T> * std::max(1, groups));
+  const int64_t side = s.sets ? 32 : s.small ? 64 : 128;
+  const int64_t tiles = ceil_div(out, side) * ceil_div(in, side);
+  // stretches so that about 768 workgroups share the rows, of 4 k steps a set at least
+  const int64_t cut = ceil_div(rows * tiles, 768);
+  s.unit_w = int32_t(std::max<int64_t>((s.sets ? 32 : 4) * kStep<T>, ceil_div(cut, 64) * 64));
   s.part_w = rows > s.unit_w;
   s.plane = ceil_div(int64_t(out) * in + out, 64) * 64;
   // about 2048 workgroups of the slope's kernel, 64 rows at least
@@ -1064,6 +1411,7 @@ BwdPlan bwd_plan(int64_t rows, int32_t in, int32_t out, int32_t groups, int act)
   s.dz = act == kActNone ? 0 : align_up(size_t(rows) * dz_ld(out, kChunk<T>) * sizeof(T), 256);
   s.db = !s.part_b ? 0 : align_up(size_t(max_slots(rows, groups, s.unit_b)) * out * 4, 256);
   s.dw = !s.part_w ? 0 : align_up(size_t(max_slots(rows, groups, s.unit_w)) * s.plane * 4, 256);
+  if (s.fused) s.dw = std::max(s.dw, size_t(s.shares + std::max(1, groups)) * s.plane * 4);
   s.total = s.dz + s.db + s.dw;
   return s;
 }
@@ -1096,6 +1444,47 @@ hipError_t linear_fwd(const LinearArgs& a, hipStream_t st) {
 template <typename T>
 hipError_t linear_bwd(const LinearArgs& a, char* ws, hipStream_t st) {
   const BwdPlan plan = bwd_plan<T>(a.rows, a.in, a.out, a.groups, a.act);
+  if constexpr (sizeof(T) == 2) {
+    const auto whole = [](const void* q, int64_t ld) {
+      return q != nullptr && (reinterpret_cast<uintptr_t>(q) & 15u) == 0 && ld % 8 == 0 && ld <= (1 << 20);
+    };
+    if (plan.fused && a.dw != nullptr && (a.dx == nullptr || whole(a.dx, a.lddx)) && whole(a.dy, a.lddy) &&
+        whole(a.x, a.ldx) && (a.act == kActNone || whole(a.z, a.ldz))) {
+      FusedArgs f{};
+      f.dy = a.dy;
+      f.z = a.act == kActNone ? nullptr : a.z;
+      f.x = a.x;
+      f.w = a.w;
+      f.dx = a.dx;
+      f.part = reinterpret_cast<float*>(ws + plan.dz + plan.db);
+      f.offsets = a.offsets;
+      f.lddy = a.lddy;
+      f.ldz = a.ldz;
+      f.ldx = a.ldx;
+      f.ldw = a.ldw;
+      f.lddx = a.lddx;
+      f.w_group = int64_t(a.out) * a.ldw;
+      f.plane = plan.plane;
+      f.rows = a.rows;
+      f.groups = a.groups;
+      f.in = a.in;
+      f.out = a.out;
+      f.act = a.act;
+      f.shares = plan.shares;
+      if (plan.steps == 4)
+        k_bwd_rows<T, 4><<<plan.shares, 512, 0, st>>>(f);
+      else if (plan.steps == 2)
+        k_bwd_rows<T, 2><<<plan.shares, 512, 0, st>>>(f);
+      else
+        k_bwd_rows<T, 1><<<plan.shares, 512, 0, st>>>(f);
+      const dim3 grid(int(ceil_div(int64_t(a.out) * a.in + a.out, 256)), std::max(1, a.groups));
+      if (a.dw_f32)
+        k_join_rows<float><<<grid, 256, 0, st>>>(f, 128 / plan.steps, static_cast<float*>(a.dw), a.db);
+      else
+        k_join_rows<T><<<grid, 256, 0, st>>>(f, 128 / plan.steps, static_cast<T*>(a.dw), a.db);
+      return hipGetLastError();
+    }
+  }
   T* dz = reinterpret_cast<T*>(ws);
   const bool slope = a.act != kActNone;
   const int groups = std::max(1, a.groups);
@@ -1119,7 +1508,7 @@ hipError_t linear_bwd(const LinearArgs& a, char* ws, hipStream_t st) {
                     256, 0, st>>>(static_cast<const T*>(a.dy), a.lddy, static_cast<const T*>(a.z), a.ldz,
                                   slope ? dz : nullptr, dz_ld(a.out, kChunk<T>), a.offsets, a.groups, a.rows,
                                   plan.unit_b, a.out, a.act, lanes, cut ? part : nullptr, a.db);
-    if (parts) j = DbJoin{part, a.db, a.out, plan.unit_b, int32_t(ceil_div(a.out, 256))};
+    if (parts) j = DbJoin{part, a.db, a.out, plan.unit_b, int32_t(ceil_div(a.out, 16))};
   }
 
   ProductArgs p{};
@@ -1149,25 +1538,25 @@ hipError_t linear_bwd(const LinearArgs& a, char* ws, hipStream_t st) {
   w.db = own_db && any ? nullptr : a.db;
   const bool want_dx = a.dx != nullptr && any, want_dw = a.dw != nullptr || (w.db != nullptr && !any);
   if (plan.small) {
-    const int64_t x_tiles = want_dx ? lay_out<kDx>(x, 64, 64) : 0, w_tiles = want_dw ? lay_out<kDw>(w, 64, 64) : 0;
+    const int side = plan.sets ? 32 : 64;
+    const int64_t x_tiles = want_dx ? lay_out<kDx>(x, side, side) : 0;
+    const int64_t w_tiles = want_dw ? lay_out<kDw>(w, side, side) : 0;
     const int64_t grid = x_tiles + w_tiles + int64_t(j.blocks) * groups;
     if (grid > 0) {
       const bool direct = (!want_dx || direct_ok<T>(x, kDx)) && (!want_dw || direct_ok<T>(w, kDw));
-      const auto go = [&](auto d, auto kw) {
-        constexpr bool D = decltype(d)::value;
-        constexpr int KW = decltype(kw)::value, lds = product_lds(64, 64, 2, 2, KW, D, 2);
+      const auto go = [&](auto d, auto sets) {
+        constexpr bool D = decltype(d)::value, S = decltype(sets)::value;
+        constexpr int TILE = S ? 32 : 64, W = S ? 1 : 2, KW = S ? 8 : 1, lds = product_lds(TILE, TILE, W, W, KW, D, 2);
         if constexpr (lds > 65536) {
           static std::atomic<uint64_t> asked{0};
-          ask_lds(&k_bwd<T, D, KW>, lds, asked);
+          ask_lds(&k_bwd<T, TILE, W, D, KW>, lds, asked);
         }
-        k_bwd<T, D, KW><<<int(grid), 256 * KW, lds, st>>>(x, int(x_tiles), w, int(w_tiles), j);
+        k_bwd<T, TILE, W, D, KW><<<int(grid), 64 * W * W * KW, lds, st>>>(x, int(x_tiles), w, int(w_tiles), j);
       };
-      using One = std::integral_constant<int, 1>;
-      using Four = std::integral_constant<int, 4>;
       if (direct)
-        plan.sets ? go(std::true_type{}, Four{}) : go(std::true_type{}, One{});
+        plan.sets ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
       else
-        plan.sets ? go(std::false_type{}, Four{}) : go(std::false_type{}, One{});
+        plan.sets ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{});
     }
   } else {
     if (j.blocks > 0) k_join_db<<<j.blocks * groups, 256, 0, st>>>(j, p);
