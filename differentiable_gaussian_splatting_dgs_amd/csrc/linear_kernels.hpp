@@ -145,24 +145,38 @@ __device__ __forceinline__ typename Frag<T>::V read_frag(const char* tile, int d
   }
 }
 
-// The fragment of columns d0 .. d0 + 15 over rows 32 kk .. of a tile that lies
-// along k, [step][ROWS][128 bytes] (16-bit types).
-template <typename T, int ROWS>
-__device__ __forceinline__ typename Frag<T>::V read_across(const char* tile, int d0, int kk, int lane) {
-  const int i = lane & 15, g = lane >> 4, c = (d0 >> 3) + ((i & 3) >> 1);
-  s16x8 v;
+// Transposed fragments of a tile that lies along k, [step][ROWS][128 bytes]
+// (16-bit types): columns d0 .. d0 + 15 over rows 32 kk ...  Of the chunk
+// address c ^ (r % 8) a lane's own bits are few: with c = 2 jj + b (jj the 16
+// columns within the step) and r % 8 = 4 h + q it is (b ^ (q & 1)) + 2 (jj ^ 2 h
+// ^ (q >> 1)), so four lane addresses, one for each jj ^ 2 h, serve every
+// fragment; the rest are constants of the instruction.
+struct Across {
+  uint32_t at[4];   // byte offsets from the tile
+  // first: the 16 columns of the step that block 0 is (blocks j go on from
+  // there by ^, which is + where a wave has first + j <= 3 blocks a step)
+  __device__ __forceinline__ void init(int lane, int first) {
+    const int i = lane & 15, g = lane >> 4, q = i >> 2;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r = 32 * kk + 8 * g + 4 * h + (i >> 2);
-    const char* p = tile + (c >> 3) * ROWS * 128 + tile_at<T, ROWS, false>(r, c & 7) + (i & 1) * 8;
-    const s16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p));
-    v[4 * h] = u[0];
-    v[4 * h + 1] = u[1];
-    v[4 * h + 2] = u[2];
-    v[4 * h + 3] = u[3];
+    for (int m = 0; m < 4; ++m)
+      at[m] = uint32_t((8 * g + q) * 128 + ((((i & 3) >> 1) ^ (q & 1)) + 2 * (m ^ first ^ (q >> 1))) * 16 + (i & 1) * 8);
   }
-  return __builtin_bit_cast(typename Frag<T>::V, v);
-}
+  // j: block from the step that `tile` points at
+  template <typename T, int ROWS>
+  __device__ __forceinline__ typename Frag<T>::V read(const char* tile, int j, int kk) const {
+    s16x8 v;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const s16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_s16x4*)(tile + at[(j & 3) ^ (2 * h)] + ((j >> 2) * ROWS * 128 + kk * 4096 + h * 512)));
+      v[4 * h] = u[0];
+      v[4 * h + 1] = u[1];
+      v[4 * h + 2] = u[2];
+      v[4 * h + 3] = u[3];
+    }
+    return __builtin_bit_cast(typename Frag<T>::V, v);
+  }
+};
 
 // Global -> registers -> LDS for one operand, at any alignment.  `rows` and
 // `cols`: what is left of the operand from the tile's corner; values past
@@ -996,9 +1010,14 @@ __host__ __device__ inline int32_t share_of(int64_t t, int64_t total, int32_t sh
 // writes dx, and dw never leaves the registers until the rows run out.  Each
 // of 8 waves holds the weights' fragments of 32 columns of dx (16 KS
 // registers) and 16 KS x 32 KS of dw's sums; the workgroup walks its share of
-// the row tiles (128 / KS rows; dy, z, x 16 KB each, two LDS stages):
-//   dz = dy act'(z) in place, rounded for the matrix instructions, db summed
-//   unrounded; dx = dz w; dw += dz^T x, its operands read transposed.
+// the row tiles (128 / KS rows; dy, z, x 16 KB each):
+//   slope   dz = dy act'(z) in place, rounded for the matrix instructions, db
+//           summed unrounded
+//   product dx = dz w; dw += dz^T x, its operands read transposed
+// While tile t is multiplied, tile t + 1 gets its slope and tile t + 2 is
+// fetched; of the two waves that share a SIMD one multiplies first and the
+// other computes slopes first, so that the matrix and the vector unit work
+// side by side, with one barrier a tile.
 // A share that ends inside a group, or a group inside a share, leaves one
 // plane of partial sums, number share + group.  Bound by HBM: 3 or 4 planes of
 // the rows, each once.
@@ -1008,12 +1027,16 @@ __global__ __launch_bounds__(512, 2) void k_bwd_rows(FusedArgs p) {
   static_assert(sizeof(T) == 2, "transposed LDS reads are 16 bit");
   constexpr int BM = 128 / KS, WN = 2 * KS, WM = 8 / WN, TM = BM / WM, FM = TM / 16, FN = 2;
   constexpr int DM = KS, DN = 2 * KS;                  // dw fragments of a wave; the waves lie 4 x 2
-  constexpr int kStage = 49152, kPatch = 36, kTile = 16384, K = 8;
+  constexpr int kPatch = 40, kTile = 16384, K = 8;
   constexpr int kStores = FM * Eight<T>::kParts;
-  __shared__ __align__(16) char lds[2 * kStage + 8 * 16 * kPatch * 4];
+  // three tiles of dy (then dz), x and z, and the patches (in the storage
+  // type: nothing is added to dx)
+  __shared__ __align__(16) char lds[9 * kTile + 8 * 16 * kPatch * 2];
+  char* const lds_x = lds + 3 * kTile;
+  char* const lds_z = lds + 6 * kTile;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
-  float* patch = reinterpret_cast<float*>(lds + 2 * kStage) + wave * 16 * kPatch;
+  T* patch = reinterpret_cast<T*>(lds + 9 * kTile) + wave * 16 * kPatch;
 
   const int share = xcd_tile(blockIdx.x, gridDim.x);
   const int64_t total = total_slots(p.offsets, p.groups, p.rows, BM);
@@ -1027,18 +1050,17 @@ __global__ __launch_bounds__(512, 2) void k_bwd_rows(FusedArgs p) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int at = j * 512 + th, step = at / (BM * 8), r = at / 8 % BM, col = (step * 8 + ((at & 7) ^ (r & 7))) * K;
-      const uint32_t off = col < cols ? uint32_t(r) * uint32_t(ld * 2) + uint32_t(col * 2) : 0xfffffff0u;
+      const uint32_t off = col < cols ? __umul24(r, uint32_t(ld * 2)) + uint32_t(col * 2) : 0xfffffff0u;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           rsrc, (__attribute__((address_space(3))) void*)(to + j * 8192 + wave * 1024), 16, off, 0, 0, 0);
     }
   };
-  const auto fetch = [&](const Span& s, int stage) {
-    char* to = lds + stage * kStage;
+  const auto fetch = [&](const Span& s, int ring) {
     int th = tid;
     asm volatile("" : "+v"(th));   // addresses kept through the loop would spill
-    fetch_one(p.dy, p.lddy, p.out, s, th, to);
-    if (p.z != nullptr) fetch_one(p.z, p.ldz, p.out, s, th, to + kTile);
-    fetch_one(p.x, p.ldx, p.in, s, th, to + 2 * kTile);
+    fetch_one(p.dy, p.lddy, p.out, s, th, lds + ring * kTile);
+    if (p.z != nullptr) fetch_one(p.z, p.ldz, p.out, s, th, lds_z + ring * kTile);
+    fetch_one(p.x, p.ldx, p.in, s, th, lds_x + ring * kTile);
   };
   const auto after = [&](const Span& s, int t) {
     if (t >= t1) return Span{-1, 0, 0, 0, 0, 0};
@@ -1048,8 +1070,9 @@ __global__ __launch_bounds__(512, 2) void k_bwd_rows(FusedArgs p) {
     q.row1 = std::min(s.end, q.row0 + BM);
     return q;
   };
-  Span now = find_span(p.offsets, p.groups, p.rows, BM, t0);
+  Span now = find_span(p.offsets, p.groups, p.rows, BM, t0), next = after(now, t0 + 1);
   fetch(now, 0);
+  fetch(next, 1);
 
   typename Frag<T>::V fw[KS * 2][FN];
   f32x4 dw[DM][DN];
@@ -1060,22 +1083,86 @@ __global__ __launch_bounds__(512, 2) void k_bwd_rows(FusedArgs p) {
     for (int j = 0; j < DN; ++j) dw[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < K; ++i) db[i] = 0.0f;
-  // dz: this thread's chunk column and first row
+  // dz: a thread's chunk column is the same in all its rows
   constexpr int kCols = KS * 8, kApart = 512 / kCols;    // chunk columns, rows between a thread's rows
-  const int zc = tid % kCols, zr = tid / kCols;
   const int am = (wave >> 1) * 16 * DM, bn = (wave & 1) * 16 * DN;   // this wave's corner of dw
-  const int col = wn * 32 + (lane & 3) * 8;
-  const bool live = col < p.in;
-  int group = -1, stage = 0;
+  Across across_y, across_x;   // of its blocks, which may begin inside a step
+  across_y.init(lane, (am >> 4) & 3);
+  across_x.init(lane, (bn >> 4) & 3);
+  const auto slope = [&](int ring) {
+    char* const ty = lds + ring * kTile;
+    const char* const tz = lds_z + ring * kTile;
+    int th = tid;
+    asm volatile("" : "+v"(th));
+    const int zc = th % kCols, zr = th / kCols;
+#pragma unroll
+    for (int j = 0; j < BM / kApart; ++j) {
+      const int r = zr + j * kApart;
+      const int at = (zc >> 3) * BM * 128 + tile_at<T, BM, false>(r, zc & 7);
+      Chunk<T> c = *reinterpret_cast<const Chunk<T>*>(ty + at);
+      if (p.z != nullptr) {
+        const Chunk<T> q = *reinterpret_cast<const Chunk<T>*>(tz + at);
+        float s[8];
+#pragma unroll
+        for (int i = 0; i < K; ++i) s[i] = float(q.v[i]);
+        slope_eight<T>(s, p.act);
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+          const float v = float(c.v[i]) * s[i];
+          db[i] += v;
+          c.v[i] = T(v);
+        }
+        *reinterpret_cast<Chunk<T>*>(ty + at) = c;
+      } else {
+#pragma unroll
+        for (int i = 0; i < K; ++i) db[i] += float(c.v[i]);
+      }
+    }
+  };
 
+  int group = -1, ring = 0;
   for (int t = t0; t < t1; ++t) {
-    if (t == t0 || p.dx == nullptr)
-      rows_barrier<0>();
-    else
-      rows_barrier<kStores>();   // behind this stage's loads lie the last tile's stores
-    const Span next = after(now, t + 1);
-    fetch(next, stage ^ 1);
+    // behind this tile's loads lie the next one's and two tiles' stores (less
+    // of them at the start)
+    constexpr int kFetch = 6;
+    if (p.z == nullptr) {
+      if (t - t0 < 2 || p.dx == nullptr)
+        rows_barrier<4>();
+      else
+        rows_barrier<4 + 2 * kStores>();
+    } else {
+      if (t - t0 < 2 || p.dx == nullptr)
+        rows_barrier<kFetch>();
+      else
+        rows_barrier<kFetch + 2 * kStores>();
+    }
+    const Span later = after(next, t + 2);
+    const int ring1 = ring == 2 ? 0 : ring + 1, ring2 = ring1 == 2 ? 0 : ring1 + 1;
+    fetch(later, ring2);
     asm volatile("" ::: "memory");
+    slope(ring);
+
+    if (next.e != now.e) {
+      // the group or the share ends with tile t: a column's sums of db lie
+      // kCols threads apart, joined where this tile's z was
+      float* plane = p.part + int64_t(share + now.e) * p.plane;
+      float* box = reinterpret_cast<float*>(lds_z + ring * kTile);
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        box[i * 512 + tid] = db[i];
+        db[i] = 0.0f;
+      }
+      __syncthreads();
+      if (tid < kCols * K) {
+        const float* b = box + tid / kCols * 512 + tid % kCols;
+        float v = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kApart; ++q) v += b[q * kCols];
+        const int m = (tid % kCols) * K + tid / kCols;
+        if (m < p.out) plane[int64_t(p.out) * p.in + m] = v;
+      }
+    }
 
     if (now.e != group) {
       group = now.e;
@@ -1100,33 +1187,12 @@ __global__ __launch_bounds__(512, 2) void k_bwd_rows(FusedArgs p) {
       }
     }
 
-    char* const ty = lds + stage * kStage;
-    const char* const tz = ty + kTile;
-    const char* const tx = ty + 2 * kTile;
-#pragma unroll
-    for (int r = zr; r < BM; r += kApart) {
-      const int at = (zc >> 3) * BM * 128 + tile_at<T, BM, false>(r, zc & 7);
-      Chunk<T> c = *reinterpret_cast<const Chunk<T>*>(ty + at);
-      if (p.z != nullptr) {
-        const Chunk<T> q = *reinterpret_cast<const Chunk<T>*>(tz + at);
-        float v[8], s[8];
-#pragma unroll
-        for (int i = 0; i < K; ++i) s[i] = float(q.v[i]);
-        slope_eight<T>(s, p.act);
-#pragma unroll
-        for (int i = 0; i < K; ++i) {
-          v[i] = float(c.v[i]) * s[i];
-          db[i] += v[i];
-          c.v[i] = T(v[i]);
-        }
-        *reinterpret_cast<Chunk<T>*>(ty + at) = c;
-      } else {
-#pragma unroll
-        for (int i = 0; i < K; ++i) db[i] += float(c.v[i]);
-      }
-    }
     if (p.z != nullptr) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-
+    {
+      const char* const ty = lds + ring * kTile;
+      const char* const tx = lds_x + ring * kTile;
+    int ln = lane;
+    asm volatile("" : "+v"(ln));   // as in fetch
     if (p.dx != nullptr) {
       const auto ro = buffer_of(static_cast<T*>(p.dx) + int64_t(now.row0) * p.lddx, p.lddx, now.row1 - now.row0, p.in);
       f32x4 acc[FM][FN];
@@ -1139,7 +1205,7 @@ __global__ __launch_bounds__(512, 2) void k_bwd_rows(FusedArgs p) {
         typename Frag<T>::V fa[FM];
 #pragma unroll
         for (int i = 0; i < FM; ++i)
-          fa[i] = read_frag<T, BM, false>(ty + (kk >> 1) * BM * 128, wm * TM + 16 * i, kk & 1, lane);
+          fa[i] = read_frag<T, BM, false>(ty + (kk >> 1) * BM * 128, wm * TM + 16 * i, kk & 1, ln);
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -1148,71 +1214,55 @@ __global__ __launch_bounds__(512, 2) void k_bwd_rows(FusedArgs p) {
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
-          *reinterpret_cast<f32x4*>(patch + (lane & 15) * kPatch + 16 * j + 4 * (lane >> 4)) = acc[i][j];
-        wave_sync();
-        const f32x4 lo = *reinterpret_cast<const f32x4*>(patch + (lane >> 2) * kPatch + (lane & 3) * 8);
-        const f32x4 hi = *reinterpret_cast<const f32x4*>(patch + (lane >> 2) * kPatch + (lane & 3) * 8 + 4);
-        Eight<T> o;
-        float v[8];
+        for (int j = 0; j < FN; ++j) {
+          struct alignas(8) Four {
+            T v[4];
+          } q;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          v[c] = lo[c];
-          v[4 + c] = hi[c];
+          for (int c = 0; c < 4; ++c) q.v[c] = T(acc[i][j][c]);
+          *reinterpret_cast<Four*>(patch + (ln & 15) * kPatch + 16 * j + 4 * (ln >> 4)) = q;
         }
-        o.set(v);
-        const int r = wm * TM + 16 * i + (lane >> 2);
-        buffer_store_eight(ro, o, live ? uint32_t(r) * uint32_t(p.lddx * 2) + uint32_t(col * 2) : 0xffffff00u);
+        wave_sync();
+        Eight<T> o;
+        o.c[0] = *reinterpret_cast<const Chunk<T>*>(patch + (ln >> 2) * kPatch + (ln & 3) * 8);
+        const int r = wm * TM + 16 * i + (ln >> 2), col = wn * 32 + (ln & 3) * 8;
+        buffer_store_eight(ro, o, col < p.in ? __umul24(r, uint32_t(p.lddx * 2)) + uint32_t(col * 2) : 0xffffff00u);
         wave_sync();
       }
     }
 
-    // dw: rows past the group's end are 0 in both operands
-    int ln = lane;
-    asm volatile("" : "+v"(ln));   // its LDS addresses are made here: kept through the loop they would spill
+    // dw: rows past the group's end are 0 in both operands.  The corners of
+    // a wave's block: whole steps, but for DM = 1, 2 the columns inside one.
+    const char* const wy = ty + (am >> 6) * BM * 128;
+    const char* const wx = tx + (bn >> 6) * BM * 128;
 #pragma unroll
     for (int kk = 0; kk < BM / 32; ++kk) {
-      typename Frag<T>::V fa[DM];
+      typename Frag<T>::V fa[DM], fb[2];
+      fb[0] = across_x.template read<T, BM>(wx, 0, kk);
 #pragma unroll
-      for (int i = 0; i < DM; ++i) fa[i] = read_across<T, BM>(ty, am + 16 * i, kk, ln);
+      for (int i = 0; i < DM; ++i) fa[i] = across_y.template read<T, BM>(wy, i, kk);
 #pragma unroll
-      for (int j = 0; j < DN; ++j) {
-        const auto fb = read_across<T, BM>(tx, bn + 16 * j, kk, ln);
+      for (int j = 0; j < DN; ++j) {   // the next fragment is read while this one is multiplied
+        if (j + 1 < DN) fb[(j + 1) & 1] = across_x.template read<T, BM>(wx, j + 1, kk);
 #pragma unroll
-        for (int i = 0; i < DM; ++i) dw[i][j] = Frag<T>::mma(fb, fa[i], dw[i][j]);
+        for (int i = 0; i < DM; ++i) dw[i][j] = Frag<T>::mma(fb[j & 1], fa[i], dw[i][j]);
       }
     }
-
-    if (next.e != group) {   // the group or the share ends: its plane
-      float* plane = p.part + int64_t(share + group) * p.plane;
+    if (next.e != now.e) {
+      float* plane = p.part + int64_t(share + now.e) * p.plane;
 #pragma unroll
       for (int i = 0; i < DM; ++i)
 #pragma unroll
         for (int j = 0; j < DN; ++j) {
-          const int m = am + 16 * i + (ln & 15), n = bn + 16 * j + 4 * (ln >> 4);
+          const int m = am + 16 * i + (lane & 15), n = bn + 16 * j + 4 * (lane >> 4);
           if (m < p.out && n < p.in) *reinterpret_cast<f32x4*>(plane + int64_t(m) * p.in + n) = dw[i][j];
           dw[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-      // db: a column's sums lie kCols threads apart; the z tile is free
-      float* box = reinterpret_cast<float*>(ty + kTile);
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < K; ++i) {
-        box[i * 512 + tid] = db[i];
-        db[i] = 0.0f;
-      }
-      __syncthreads();
-      if (tid < kCols * K) {
-        const float* b = box + tid / kCols * 512 + tid % kCols;
-        float v = 0.0f;
-#pragma unroll
-        for (int q = 0; q < kApart; ++q) v += b[q * kCols];
-        const int m = (tid % kCols) * K + tid / kCols;
-        if (m < p.out) plane[int64_t(p.out) * p.in + m] = v;
-      }
+    }
     }
     now = next;
-    stage ^= 1;
+    next = later;
+    ring = ring1;
   }
   rows_barrier<0>();
 #endif

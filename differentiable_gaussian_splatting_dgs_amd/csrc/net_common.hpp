@@ -113,6 +113,34 @@ __device__ __forceinline__ float act_apply(float v, int act) {
   if (act == kActGelu) return v * normal_cdf<T>(v);
   return v;
 }
+// gelu'(v) = Phi(v) + v phi(v).  16-bit storage: with x = |v|, gelu'(-x) =
+// e^(-x^2 / 2) P(x) and gelu'(x) = 1 - gelu'(-x), P of degree 10 the minimax
+// fit on [0, 6] with the error weighted by the exponential (5e-7 off at most):
+// 20 instruction slots a value where Phi and phi take 23, in a pass that the
+// slope of a 256-wide layer bounds.
+template <typename T>
+__device__ __forceinline__ float gelu_slope(float v) {
+  if constexpr (sizeof(T) == 4) {
+    const float density = 0.39894228040143267794f * expf(-0.5f * v * v);
+    return fmaf(fminf(fmaxf(v, -64.0f), 64.0f), density, normal_cdf<T>(v));   // no infinity times 0
+  } else {
+    const float x = fminf(fabsf(v), 7.0f);
+    const float e = __builtin_amdgcn_exp2f(v * v * -0.72134752044448170368f);
+    float p = fmaf(5.42516376e-07f, x, -1.54095325e-05f);
+    p = fmaf(p, x, 1.90652152e-04f);
+    p = fmaf(p, x, -1.37058932e-03f);
+    p = fmaf(p, x, 6.5064465e-03f);
+    p = fmaf(p, x, -2.22826763e-02f);
+    p = fmaf(p, x, 5.94712761e-02f);
+    p = fmaf(p, x, -1.31751587e-01f);
+    p = fmaf(p, x, 2.49754565e-01f);
+    p = fmaf(p, x, -7.97867768e-01f);
+    p = fmaf(p, x, 0.5f);
+    const float h = e * p;
+    return v < 0.0f ? h : 1.0f - h;
+  }
+}
+
 // act'(v); relu's is 0 at 0 and at NaN.
 template <typename T>
 __device__ __forceinline__ float act_slope(float v, int act) {
@@ -121,10 +149,7 @@ __device__ __forceinline__ float act_slope(float v, int act) {
     const float p = rcp_t<T>(1.0f + exp_t<T>(-v));
     return p * fmaf(v, 1.0f - p, 1.0f);
   }
-  if (act == kActGelu) {
-    const float density = 0.39894228040143267794f * exp_t<T>(-0.5f * v * v);
-    return fmaf(v, density, normal_cdf<T>(v));
-  }
+  if (act == kActGelu) return gelu_slope<T>(v);
   return 1.0f;
 }
 
