@@ -78,10 +78,11 @@ struct Frag<float> {
 
 // --- tiles in LDS ---------------------------------------------------------------------
 
-// A k step is 128 bytes of k: 64 16-bit or 32 fp32 values.  Two layouts of a
-// D-row operand, both of D * 128 bytes:
-//   along k    [D][128 bytes]: 8 chunks a row, chunk c of row r at c ^ (r % 8),
-//              so that the 16 rows a fragment reads spread over all banks
+// A k step is KB = 128 bytes of k (64 16-bit or 32 fp32 values), or 64 where
+// the tiles come straight from memory.  Two layouts of a D-row operand, both
+// of D * KB bytes:
+//   along k    [D][KB bytes]: the chunks of row r permuted by r so that the 8
+//              rows of a 128-byte LDS access lie on different banks
 //   across k   [k][D]: read back transposed, 16-bit types with the LDS
 //              transpose read (4 x 16 blocks), fp32 value by value; the
 //              chunks of row k are permuted in pairs (16-bit) or fours
@@ -98,13 +99,18 @@ __device__ __forceinline__ int across_swizzle(int k) {
     return (((k >> 2) & 3) << 2) & (chunks - 1);
 }
 
+template <int KB>
+__device__ __forceinline__ int along_swizzle(int r) {
+  return KB == 128 ? r & 7 : (r >> 1) & 3;
+}
+
 // Byte offset of chunk c of row r.
-template <typename T, int D, bool ACROSS>
+template <typename T, int D, bool ACROSS, int KB = 128>
 __device__ __forceinline__ int tile_at(int r, int c) {
   if constexpr (ACROSS)
     return (r * (D / kChunk<T>) + (c ^ across_swizzle<T, D>(r))) * 16;
   else
-    return (r * 8 + (c ^ (r & 7))) * 16;
+    return (r * (KB / 16) + (c ^ along_swizzle<KB>(r))) * 16;
 }
 
 typedef __attribute__((address_space(3))) char lds_char;
@@ -113,12 +119,12 @@ typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 // The fragment of rows d0 .. d0 + 15, k chunk group kk (64 bytes of k).
-template <typename T, int D, bool ACROSS>
+template <typename T, int D, bool ACROSS, int KB = 128>
 __device__ __forceinline__ typename Frag<T>::V read_frag(const char* tile, int d0, int kk, int lane) {
   using V = typename Frag<T>::V;
   const int i = lane & 15, g = lane >> 4;
   if constexpr (!ACROSS) {
-    return *reinterpret_cast<const V*>(tile + tile_at<T, D, false>(d0 + i, 4 * kk + g));
+    return *reinterpret_cast<const V*>(tile + tile_at<T, D, false, KB>(d0 + i, 4 * kk + g));
   } else if constexpr (sizeof(T) == 2) {
     // lane i of a quarter wave reads 4 values of row k + i / 4 at column
     // 4 (i % 4); the read hands it column i of the four rows
@@ -229,31 +235,31 @@ struct Stage {
 // permutation of the chunks is done on the addresses.  Rows past the end
 // lie past the buffer's size and read as 0; across k, columns past the end
 // hold whatever follows in the row (their results are never stored).
-template <typename T, int D, bool ACROSS, int THREADS>
+template <typename T, int D, bool ACROSS, int THREADS, int KB>
 struct Direct {
-  static constexpr int kPer = D * 8 / THREADS;
-  static constexpr int kAcross = ACROSS ? D / kChunk<T> : 8;
-  static_assert(ACROSS || (THREADS / 8) % 8 == 0, "one chunk for all of a thread's rows");
+  static constexpr int kPer = D * KB / 16 / THREADS;
+  static constexpr int kAcross = ACROSS ? D / kChunk<T> : KB / 16;
+  static_assert(ACROSS || (THREADS / kAcross) % 8 == 0, "one chunk for all of a thread's rows");
   uint32_t off[kPer];
   int chunk;   // along k: the chunk of the row this thread fetches
   __device__ __forceinline__ void init(int64_t ld, int tid) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int id = j * THREADS + tid, r = id / kAcross;
-      const int c = (id % kAcross) ^ (ACROSS ? across_swizzle<T, D>(r) : (r & 7));
+      const int c = (id % kAcross) ^ (ACROSS ? across_swizzle<T, D>(r) : along_swizzle<KB>(r));
       off[j] = uint32_t(r) * uint32_t(ld * sizeof(T)) + uint32_t(c) * 16u;
       if (j == 0) chunk = c;
     }
   }
-  // `rows`, `cols`: the operand's extent from p on (both > 0), cols in whole
-  // chunks along k.
+  // `rows`, `cols`: the operand's extent from p on, cols in whole chunks along
+  // k; none of either: zeros.
   __device__ __forceinline__ void load(const T* p, int64_t ld, int rows, int cols, char* tile, int wave) const {
 #ifdef __HIP_DEVICE_COMPILE__   // the host pass does not know the buffer builtins
-    constexpr int most_rows = ACROSS ? kStep<T> : D, most_cols = ACROSS ? D : kStep<T>;
+    constexpr int step = KB / int(sizeof(T)), most_rows = ACROSS ? step : D, most_cols = ACROSS ? D : step;
     const int r = rows < most_rows ? rows : most_rows, c = cols < most_cols ? cols : most_cols;
     // whole chunks: an aligned chunk that holds a value of the row lies inside its padding
     const int whole = (c + kChunk<T> - 1) / kChunk<T> * kChunk<T>;
-    const uint32_t bytes = uint32_t(((r - 1) * ld + whole) * int64_t(sizeof(T)));
+    const uint32_t bytes = r > 0 && c > 0 ? uint32_t(((r - 1) * ld + whole) * int64_t(sizeof(T))) : 0u;
     const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(p), 0, bytes, 0x00020000);
     const bool past = !ACROSS && chunk * kChunk<T> >= cols;
 #pragma unroll
@@ -265,14 +271,15 @@ struct Direct {
   }
 };
 
-// Every wave's loads into LDS have landed and its reads of LDS are done,
-// then the workgroup meets (a set of one wave has nobody to meet).
-template <int WAVES>
+// All but the last LOADS of every wave's loads into LDS have landed and its
+// reads of LDS are done, then the workgroup meets (a set of one wave has
+// nobody to meet).
+template <int WAVES, int LOADS = 0>
 __device__ __forceinline__ void tile_barrier() {
   if constexpr (WAVES > 1)
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LOADS) : "memory");
   else
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LOADS) : "memory");
 }
 template <int WAVES>
 __device__ __forceinline__ void stage_barrier() {
@@ -344,16 +351,16 @@ __device__ __forceinline__ int xcd_tile(int id, int n) {
 
 // What one wave does with a k step in LDS.  `sums`: also adds the columns
 // of a (a product with a row of ones: exact, in fp32).
-template <typename T, int BM, int BN, bool A_ACROSS, bool B_ACROSS, int FM, int FN, int FS>
+template <typename T, int BM, int BN, bool A_ACROSS, bool B_ACROSS, int KB, int FM, int FN, int FS>
 __device__ __forceinline__ void multiply_step(const char* ta, const char* tb, int am, int bn, int lane,
                                               f32x4 (&acc)[FM][FN], f32x4 (&sum)[FS], bool sums) {
 #pragma unroll
-  for (int kk = 0; kk < 2; ++kk) {
+  for (int kk = 0; kk < KB / 64; ++kk) {
     typename Frag<T>::V fa[FM], fb[FN];
 #pragma unroll
-    for (int i = 0; i < FM; ++i) fa[i] = read_frag<T, BM, A_ACROSS>(ta, am + 16 * i, kk, lane);
+    for (int i = 0; i < FM; ++i) fa[i] = read_frag<T, BM, A_ACROSS, KB>(ta, am + 16 * i, kk, lane);
 #pragma unroll
-    for (int j = 0; j < FN; ++j) fb[j] = read_frag<T, BN, B_ACROSS>(tb, bn + 16 * j, kk, lane);
+    for (int j = 0; j < FN; ++j) fb[j] = read_frag<T, BN, B_ACROSS, KB>(tb, bn + 16 * j, kk, lane);
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -370,11 +377,19 @@ __device__ __forceinline__ void multiply_step(const char* ta, const char* tb, in
   }
 }
 
+// How the tiles that come straight from memory are staged: dw, whose
+// transposed reads leave the loads less time, in four half steps of 64 bytes of
+// k (64 heads of 512 x 512 over 131,072 rows: 137 us against 147), the others in
+// two whole steps, with half the barriers (16384 x 4096 x 4096 fp16: 497 us
+// against 510).
+constexpr int direct_bytes(bool across_both) { return across_both ? 64 : 128; }
+constexpr int direct_stages(bool across_both) { return across_both ? 4 : 2; }
+
 // BM x BN outputs a workgroup, WM x WN waves.  The n side is the first
 // operand of the matrix instruction, so that a lane's four results are
 // neighbours along n; each wave then turns 16 rows at a time through LDS
 // into whole chunks of output rows.  DIRECT: both operands in whole aligned
-// chunks, loaded straight into one of two LDS stages while the other is
+// chunks, loaded straight into the LDS stages ahead of the one that is
 // multiplied; else through registers, at any alignment.  KW > 1: so many sets
 // of WM x WN waves take the k steps in turn, for products of few tiles and a
 // long k, whose time is the steps that wait on each other; the first set adds
@@ -384,12 +399,12 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, int tile, cha
   constexpr int THREADS = 64 * WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
   constexpr bool A_ACROSS = MODE == kDw, B_ACROSS = MODE != kFwd;
   constexpr int kPatch = TN + 4;   // floats of a patch row: 4 more keep its 16-byte writes off each other's banks
-  constexpr int kTiles = (BM + BN) * 128;
   const int set = KW > 1 ? __builtin_amdgcn_readfirstlane(int(threadIdx.x) / THREADS) : 0;
   const int tid = KW > 1 ? int(threadIdx.x) % THREADS : int(threadIdx.x), lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
   char* const base = lds;
-  if (KW > 1) lds += set * kTiles * (DIRECT ? 2 : 1);
+  constexpr int kStages = direct_stages(MODE == kDw), kB = DIRECT ? direct_bytes(MODE == kDw) : 128;
+  if (KW > 1) lds += set * (BM + BN) * kB * (DIRECT ? kStages : 1);
 
   // Which tile.  kFwd, kDx: the height index picks group and rows; kDw: the
   // stretch does (without planes to join, every group is one stretch, and
@@ -408,7 +423,8 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, int tile, cha
   if constexpr (MODE == kFwd) b += int64_t(s.e) * p.b_group + int64_t(n0) * p.ldb;
   if constexpr (MODE == kDx) b += int64_t(s.e) * p.b_group + n0;
   if constexpr (MODE == kDw) b += int64_t(s.row0) * p.ldb + n0;
-  const int64_t step_a = A_ACROSS ? kStep<T> * p.lda : kStep<T>, step_b = B_ACROSS ? kStep<T> * p.ldb : kStep<T>;
+  constexpr int kK = kB / int(sizeof(T));   // k of a step
+  const int64_t step_a = A_ACROSS ? kK * p.lda : kK, step_b = B_ACROSS ? kK * p.ldb : kK;
 
   f32x4 acc[FM][FN];
 #pragma unroll
@@ -421,35 +437,37 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, int tile, cha
   const bool sums = MODE == kDw && p.db != nullptr && n0 == 0 && wn == 0;
 
   // the sets' first steps lie side by side
-  const int first = k_all - set * kStep<T>;
+  const int first = k_all - set * kK;
   a += set * step_a;
   b += set * step_b;
   if (MODE == kDw && k_all == 0) {
     // an empty group's zeros
   } else if constexpr (DIRECT) {
-    Direct<T, BM, A_ACROSS, THREADS> da;
-    Direct<T, BN, B_ACROSS, THREADS> db;
+    constexpr int kBytes = (BM + BN) * kB, kLoads = kBytes / 16 / THREADS;
+    Direct<T, BM, A_ACROSS, THREADS, kB> da;
+    Direct<T, BN, B_ACROSS, THREADS, kB> db;
     da.init(p.lda, tid);
     db.init(p.ldb, tid);
-    if (KW == 1 || first > 0) {
-      da.load(a, p.lda, A_ACROSS ? first : m_left, A_ACROSS ? m_left : first, lds, wave);
-      db.load(b, p.ldb, B_ACROSS ? first : n_left, B_ACROSS ? n_left : first, lds + BM * 128, wave);
-    }
+    // every step loads the same number of times, past the end nothing but zeros
+    int ahead = first;
+    const auto load = [&](int stage) {
+      char* t = lds + stage * kBytes;
+      da.load(a, p.lda, A_ACROSS ? ahead : m_left, A_ACROSS ? m_left : ahead, t, wave);
+      db.load(b, p.ldb, B_ACROSS ? ahead : n_left, B_ACROSS ? n_left : ahead, t + BM * kB, wave);
+      ahead -= KW * kK;
+      a += KW * step_a;
+      b += KW * step_b;
+    };
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) load(s);
     int stage = 0;
-    for (int all = k_all, left = first; all > 0; all -= KW * kStep<T>, left -= KW * kStep<T>) {
-      tile_barrier<WM * WN>();
-      const int next = left - KW * kStep<T>;
-      if (next > 0) {
-        a += KW * step_a;
-        b += KW * step_b;
-        char* t = lds + (stage ^ 1) * kTiles;
-        da.load(a, p.lda, A_ACROSS ? next : m_left, A_ACROSS ? m_left : next, t, wave);
-        db.load(b, p.ldb, B_ACROSS ? next : n_left, B_ACROSS ? n_left : next, t + BM * 128, wave);
-      }
-      const char* t = lds + stage * kTiles;
+    for (int all = k_all, left = first; all > 0; all -= KW * kK, left -= KW * kK) {
+      tile_barrier<WM * WN, (kStages - 2) * kLoads>();
+      load(stage == 0 ? kStages - 1 : stage - 1);
+      const char* t = lds + stage * kBytes;
       if (KW == 1 || left > 0)
-        multiply_step<T, BM, BN, A_ACROSS, B_ACROSS, FM, FN>(t, t + BM * 128, wm * TM, wn * TN, lane, acc, sum, sums);
-      stage ^= 1;
+        multiply_step<T, BM, BN, A_ACROSS, B_ACROSS, kB>(t, t + BM * kB, wm * TM, wn * TN, lane, acc, sum, sums);
+      stage = stage == kStages - 1 ? 0 : stage + 1;
     }
     tile_barrier<WM * WN * KW>();
   } else {
@@ -484,7 +502,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, int tile, cha
                 tid);
       }
       if (KW == 1 || left > 0)
-        multiply_step<T, BM, BN, A_ACROSS, B_ACROSS, FM, FN>(ta, tb, wm * TM, wn * TN, lane, acc, sum, sums);
+        multiply_step<T, BM, BN, A_ACROSS, B_ACROSS, 128>(ta, tb, wm * TM, wn * TN, lane, acc, sum, sums);
       stage_barrier<WM * WN>();
     }
     if (WM * WN == 1) __syncthreads();
@@ -612,20 +630,27 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, int tile, cha
   }
 }
 
-// LDS of a workgroup: two stages of tiles a set (one where they come through
-// registers, or where `steps` is 1), later the boxes of the sets' results and
-// the patches.
-constexpr int product_lds(int bm, int bn, int wm, int wn, int kw, bool direct, int steps) {
-  const int tiles = (bm + bn) * 128 * (direct && steps > 1 ? 2 : 1) * kw;
+// LDS of a workgroup: the stages of its sets (one whole step where the tiles
+// come through registers), later the boxes of the sets' results and the
+// patches.
+constexpr int product_lds(int bm, int bn, int wm, int wn, int kw, bool direct) {
+  const int tiles = (bm + bn) * (direct ? 256 : 128) * kw;   // either staging
   const int regs = (bm / wm / 16) * (bn / wn / 16 + 1);   // kDw's, the largest
   const int after = (kw - 1) * regs * 64 * wm * wn * 16 + wm * wn * 16 * (bn / wn + 4) * 4;
   return tiles > after ? tiles : after;
 }
 
 template <typename T, Mode MODE, int BM, int BN, int WM, int WN, bool DIRECT, int KW>
-__global__ __launch_bounds__(64 * WM * WN * KW, KW == 4 ? 4 : 2) void k_product(ProductArgs p) {
+__global__ __launch_bounds__(64 * WM * WN * KW, KW == 4 ? 4 : BM == 256 && WM * WN == 4 ? 1 : 2) void k_product(ProductArgs p) {
   extern __shared__ __align__(16) char lds[];
-  product_tile<T, MODE, BM, BN, WM, WN, DIRECT, KW>(p, xcd_tile(blockIdx.x, gridDim.x), lds);
+  // the grid is sized for the most slots the groups can make; the tiles that
+  // there are go evenly to the XCDs
+  int tiles = gridDim.x;
+  if (p.groups > 0 && (MODE != kDw || p.part != nullptr)) {
+    tiles = total_slots(p.offsets, p.groups, p.rows, p.unit) * (MODE == kDw ? p.tiles : p.tiles_n);
+    if (int(blockIdx.x) >= tiles) return;
+  }
+  product_tile<T, MODE, BM, BN, WM, WN, DIRECT, KW>(p, xcd_tile(blockIdx.x, tiles), lds);
 }
 
 // --- the product over many rows of a short k ---------------------------------------
@@ -1324,15 +1349,12 @@ void ask_lds(K kernel, int bytes, std::atomic<uint64_t>& asked) {
 
 template <typename T, Mode MODE, int BM, int BN, int WM, int WN, bool DIRECT, int KW>
 void go_tile(const ProductArgs& p, int64_t grid, hipStream_t st) {
-  constexpr int most = product_lds(BM, BN, WM, WN, KW, DIRECT, 2);
+  constexpr int most = product_lds(BM, BN, WM, WN, KW, DIRECT);
   if constexpr (most > 65536) {
     static std::atomic<uint64_t> asked{0};
     ask_lds(&k_product<T, MODE, BM, BN, WM, WN, DIRECT, KW>, most, asked);
   }
-  // one k step needs one stage, and leaves LDS for more workgroups
-  const int steps = MODE == kDw || KW > 1 || p.k > kStep<T> ? 2 : 1;
-  k_product<T, MODE, BM, BN, WM, WN, DIRECT, KW>
-      <<<int(grid), 64 * WM * WN * KW, product_lds(BM, BN, WM, WN, KW, DIRECT, steps), st>>>(p);
+  k_product<T, MODE, BM, BN, WM, WN, DIRECT, KW><<<int(grid), 64 * WM * WN * KW, most, st>>>(p);
 }
 
 // Tiles of the product and the shape of its grid.
@@ -1427,6 +1449,7 @@ struct BwdPlan {
   int32_t steps, shares;
   bool small;              // dx and dw in one launch of 64 x 64 tiles
   bool sets;               // and that of 32 x 32 tiles of eight wave sets
+  int32_t side_w;          // tile of dw
   int32_t unit_b, unit_w;  // rows of a stretch of db (with an activation) and of dw
   bool part_b, part_w;     // more than one stretch a group: partial sums to join
   int64_t plane;           // values of a plane of dw
@@ -1447,11 +1470,15 @@ BwdPlan bwd_plan(int64_t rows, int32_t in, int32_t out, int32_t groups, int act)
   const int64_t w_tiles = ceil_div(out, 64) * ceil_div(in, 64) * std::max(1, groups);
   s.sets = s.small && x_tiles + w_tiles <= 512 &&
            (out >= 8 * kStep<T> || rows >= 8 * kStep<T> * std::max(1, groups));
-  const int64_t side = s.sets ? 32 : s.small ? 64 : 128;
-  const int64_t tiles = ceil_div(out, side) * ceil_div(in, side);
+  // a side of at most 64 would leave half of a 128 tile empty (50,001 rows, 251 ->
+  // 59 fp32: dw 61 us of 128 x 128, 40 us of 64 x 64)
+  s.side_w = s.sets ? 32 : s.small || std::min(in, out) <= 64 ? 64 : 128;
+  const int64_t tiles = ceil_div(out, s.side_w) * ceil_div(in, s.side_w);
   // stretches so that about 768 workgroups share the rows, of 4 k steps a set at least
   const int64_t cut = ceil_div(rows * tiles, 768);
   s.unit_w = int32_t(std::max<int64_t>((s.sets ? 32 : 4) * kStep<T>, ceil_div(cut, 64) * 64));
+  // groups enough by themselves: only those of over twice the mean are cut
+  if (groups * tiles >= 512) s.unit_w = int32_t(std::max<int64_t>(s.unit_w, ceil_div(2 * rows, int64_t(groups) * 64) * 64));
   s.part_w = rows > s.unit_w;
   s.plane = ceil_div(int64_t(out) * in + out, 64) * 64;
   // about 2048 workgroups of the slope's kernel, 64 rows at least
@@ -1527,7 +1554,8 @@ hipError_t linear_bwd(const LinearArgs& a, char* ws, hipStream_t st) {
         k_bwd_rows<T, 2><<<plan.shares, 512, 0, st>>>(f);
       else
         k_bwd_rows<T, 1><<<plan.shares, 512, 0, st>>>(f);
-      const dim3 grid(int(ceil_div(int64_t(a.out) * a.in + a.out, 256)), std::max(1, a.groups));
+      const dim3 grid(int(std::min<int64_t>(ceil_div(int64_t(a.out) * a.in + a.out, 256), std::max(16, 4096 / std::max(1, a.groups)))),
+                      std::max(1, a.groups));
       if (a.dw_f32)
         k_join_rows<float><<<grid, 256, 0, st>>>(f, 128 / plan.steps, static_cast<float*>(a.dw), a.db);
       else
@@ -1588,7 +1616,7 @@ hipError_t linear_bwd(const LinearArgs& a, char* ws, hipStream_t st) {
   w.db = own_db && any ? nullptr : a.db;
   const bool want_dx = a.dx != nullptr && any, want_dw = a.dw != nullptr || (w.db != nullptr && !any);
   if (plan.small) {
-    const int side = plan.sets ? 32 : 64;
+    const int side = plan.side_w;
     const int64_t x_tiles = want_dx ? lay_out<kDx>(x, side, side) : 0;
     const int64_t w_tiles = want_dw ? lay_out<kDw>(w, side, side) : 0;
     const int64_t grid = x_tiles + w_tiles + int64_t(j.blocks) * groups;
@@ -1596,7 +1624,7 @@ hipError_t linear_bwd(const LinearArgs& a, char* ws, hipStream_t st) {
       const bool direct = (!want_dx || direct_ok<T>(x, kDx)) && (!want_dw || direct_ok<T>(w, kDw));
       const auto go = [&](auto d, auto sets) {
         constexpr bool D = decltype(d)::value, S = decltype(sets)::value;
-        constexpr int TILE = S ? 32 : 64, W = S ? 1 : 2, KW = S ? 8 : 1, lds = product_lds(TILE, TILE, W, W, KW, D, 2);
+        constexpr int TILE = S ? 32 : 64, W = S ? 1 : 2, KW = S ? 8 : 1, lds = product_lds(TILE, TILE, W, W, KW, D);
         if constexpr (lds > 65536) {
           static std::atomic<uint64_t> asked{0};
           ask_lds(&k_bwd<T, TILE, W, D, KW>, lds, asked);
@@ -1611,11 +1639,14 @@ hipError_t linear_bwd(const LinearArgs& a, char* ws, hipStream_t st) {
   } else {
     if (j.blocks > 0) k_join_db<<<j.blocks * groups, 256, 0, st>>>(j, p);
     if (want_dx) run_rows<T, kDx>(x, st);
-    if (want_dw) go_product<T, kDw, 128, 128, 2, 2>(w, st);
+    if (want_dw && plan.side_w == 64)
+      go_product<T, kDw, 64, 64, 2, 2>(w, st);
+    else if (want_dw)
+      go_product<T, kDw, 128, 128, 2, 2>(w, st);
   }
   if (want_dw && w.part != nullptr) {
     const int64_t size = int64_t(a.out) * a.in;
-    const dim3 grid(int(std::min<int64_t>(ceil_div(size + a.out, 256), 4096)), groups);
+    const dim3 grid(int(std::min<int64_t>(ceil_div(size + a.out, 256), std::max(16, 4096 / groups))), groups);
     if (a.dw_f32)
       k_join<float><<<grid, 256, 0, st>>>(w.part, w.plane, a.offsets, a.groups, a.rows, plan.unit_w, size,
                                           static_cast<float*>(a.dw), a.out, w.db);
