@@ -20,7 +20,11 @@ import torch
 from . import GS_ACT_NONE, GS_OP_LAYER_NORM_BWD, _check, gs_workspace_size, lib
 
 _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_F32, _I64, _U8 = torch.float32, torch.int64, torch.uint8
+_empty = torch.empty
 _byref, _size_t = C.byref, C.c_size_t
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch.cuda.current_device
 
 
 def _type(x, name="x"):
@@ -32,29 +36,22 @@ def _type(x, name="x"):
     return t
 
 
-def _ld(t, rows, width):
-    """The leading dimension (a tensor of one row may hold any stride)."""
-    return t.stride(0) if rows > 1 else max(t.stride(0), width)
-
-
 def _matrix(t, rows, width, like, name):
+    """The leading dimension of t [rows][width] (one row may hold any stride)."""
     if t.dtype != like.dtype or t.shape != (rows, width):
         raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}: {like.dtype} ({rows}, {width}) expected")
-    _placed(t, like, name)
-    return _ld(t, rows, width)
-
-
-def _placed(t, like, name):
     if t.device != like.device:
         raise ValueError(f"{name} is on {t.device}, x on {like.device}")
-    if t.stride(-1) != 1 and t.shape[-1] != 1:
-        raise ValueError(f"{name}: last stride {t.stride(-1)}, 1 expected")
+    ld, last = t.stride()
+    if last != 1 and width != 1:
+        raise ValueError(f"{name}: last stride {last}, 1 expected")
+    return ld if rows > 1 or ld >= width else width
 
 
 def _vector(t, shape, like, name):
     if t is None:
         return None
-    if t.dtype != torch.float32 or t.shape != shape:
+    if t.dtype != _F32 or t.shape != shape:
         raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}: torch.float32 {tuple(shape)} expected")
     if t.device != like.device or not t.is_contiguous():
         raise ValueError(f"{name} has to be contiguous and on {like.device}")
@@ -62,25 +59,30 @@ def _vector(t, shape, like, name):
 
 
 def _weights(w, groups, like, inner):
-    """(leading dimension, out) of w [out][in] or [groups][out][in]."""
+    """(leading dimension, out) of w [out][inner], or of [groups][out][inner]
+    whose groups follow each other without a gap."""
     if w.dtype != like.dtype or w.dim() != (3 if groups else 2) or w.shape[-1] != inner:
         want = "(groups, out, in)" if groups else "(out, in)"
         raise ValueError(f"w is {w.dtype} {tuple(w.shape)}: {like.dtype} {want} with in = {inner} expected")
-    _placed(w, like, "w")
     out = w.shape[-2]
-    ld = _ld(w, out if not groups else out * groups, inner) if not groups else max(w.stride(1), inner)
-    if groups:
-        if w.shape[0] != groups:
-            raise ValueError(f"w holds {w.shape[0]} groups, offsets {groups}")
-        if out == 1:
-            ld = max(w.stride(0), inner) if groups > 1 else inner
-        elif groups > 1 and w.stride(0) != out * ld:
-            raise ValueError("w: the groups have to follow each other without a gap")
-    return ld, out
+    if not groups:
+        return _matrix(w, out, inner, like, "w"), out
+    if w.device != like.device:
+        raise ValueError(f"w is on {w.device}, x on {like.device}")
+    if w.shape[0] != groups:
+        raise ValueError(f"w holds {w.shape[0]} groups, offsets {groups}")
+    apart, ld, last = w.stride()
+    if last != 1 and inner != 1:
+        raise ValueError(f"w: last stride {last}, 1 expected")
+    if out == 1:
+        ld = apart      # a group's one row may hold any stride
+    if groups > 1 and apart != out * ld:
+        raise ValueError("w: the groups have to follow each other without a gap")
+    return (ld if groups > 1 or out > 1 else max(ld, inner)), out
 
 
 def _groups(offsets, like):
-    if offsets.dtype != torch.int64 or offsets.dim() != 1 or offsets.shape[0] < 2:
+    if offsets.dtype != _I64 or offsets.dim() != 1 or offsets.shape[0] < 2:
         raise ValueError(f"offsets is {offsets.dtype} {tuple(offsets.shape)}: torch.int64 (groups + 1,) expected")
     if offsets.device != like.device or not offsets.is_contiguous():
         raise ValueError(f"offsets has to be contiguous and on {like.device}")
@@ -91,114 +93,130 @@ def _optional(t):
     return None if t is None else t.data_ptr()
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
-def _launch(x, stream, call):
-    """call(stream handle) with the tensors it makes, workspaces among them,
-    belonging to the stream and the device of x."""
+def _on_gpu(x):
     if not x.is_cuda:
         raise ValueError(f"x is on {x.device}: the kernels need a GPU tensor")
-    device = x.device.index
+
+
+def _launch(call, x, stream, *args):
+    """call(stream handle, x, *args) with the tensors it makes, workspaces
+    among them, belonging to the stream and the device of x."""
+    device = x.get_device()
+    if device < 0:
+        return call(0, x, *args)      # the checks of the other arguments, then _on_gpu's refusal
     if stream is not None:
         with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
-    if device != torch.cuda.current_device():
+            return call(stream.cuda_stream, x, *args)
+    if device != _current_device():
         with torch.cuda.device(device):
-            return call(_raw_stream(device))
-    return call(_raw_stream(device))
+            return call(_raw_stream(device), x, *args)
+    return call(_raw_stream(device), x, *args)
 
 
-def _workspace(ws, need, like):
+def _workspace(ws, need, device):
     if ws is None:
-        return torch.empty(need, dtype=torch.uint8, device=like.device), need
+        return _empty(need, dtype=_U8, device=device), need
     return ws, ws.numel() * ws.element_size()
+
+
+def _norm_fwd(s, x, gamma, beta, eps, y, mean, rstd):
+    t = _type(x)
+    rows, width = x.shape
+    ldx, device = _matrix(x, rows, width, x, "x"), x.device
+    g = _vector(gamma, (width,), x, "gamma")
+    b = _vector(beta, (width,), x, "beta")
+    _on_gpu(x)
+    if y is None:
+        y, ldy = _empty(rows, width, dtype=x.dtype, device=device), width
+    else:
+        ldy = _matrix(y, rows, width, x, "y")
+    if mean is None:
+        mean = _empty(rows, dtype=_F32, device=device)
+    if rstd is None:
+        rstd = _empty(rows, dtype=_F32, device=device)
+    st = lib().gs_layer_norm_fwd(x.data_ptr(), ldx, g, b, rows, width, eps, t, y.data_ptr(), ldy,
+                                 _vector(mean, (rows,), x, "mean"), _vector(rstd, (rows,), x, "rstd"), s)
+    if st:
+        _check(st, "gs_layer_norm_fwd")
+    return y, mean, rstd
 
 
 def gs_layer_norm_fwd(x, gamma=None, beta=None, eps=1e-5, y=None, mean=None, rstd=None, stream=None):
     """y, mean and rstd of the rows of ``x`` (``mean``, ``rstd``: [rows]
     float32, what the backward pass reads)."""
+    return _launch(_norm_fwd, x, stream, gamma, beta, eps, y, mean, rstd)
+
+
+def _norm_bwd(s, x, dy, gamma, mean, rstd, dres, dx, dgamma, dbeta, workspace):
     t = _type(x)
     rows, width = x.shape
-    _placed(x, x, "x")
-    g, b = _vector(gamma, (width,), x, "gamma"), _vector(beta, (width,), x, "beta")
-
-    def call(s):
-        nonlocal y, mean, rstd
-        if y is None:
-            y = torch.empty(rows, width, dtype=x.dtype, device=x.device)
-        if mean is None:
-            mean = torch.empty(rows, dtype=torch.float32, device=x.device)
-        if rstd is None:
-            rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
-        _check(lib().gs_layer_norm_fwd(x.data_ptr(), _ld(x, rows, width), g, b, rows, width, eps, t, y.data_ptr(),
-                                       _matrix(y, rows, width, x, "y"), _vector(mean, (rows,), x, "mean"),
-                                       _vector(rstd, (rows,), x, "rstd"), s), "gs_layer_norm_fwd")
-    _launch(x, stream, call)
-    return y, mean, rstd
+    ldx, device = _matrix(x, rows, width, x, "x"), x.device
+    lddy = _matrix(dy, rows, width, x, "dy")
+    ldr = 0 if dres is None else _matrix(dres, rows, width, x, "dres")
+    if mean is None or rstd is None:
+        raise ValueError("the backward pass reads the forward's mean and rstd")
+    _on_gpu(x)
+    if dx is None:
+        dx, lddx = _empty(rows, width, dtype=x.dtype, device=device), width
+    else:
+        lddx = _matrix(dx, rows, width, x, "dx")
+    if dgamma is None:
+        dgamma = _empty(width, dtype=_F32, device=device)
+    if dbeta is None:
+        dbeta = _empty(width, dtype=_F32, device=device)
+    ws, nbytes = _workspace(workspace, gs_workspace_size(GS_OP_LAYER_NORM_BWD, rows, width), device)
+    st = lib().gs_layer_norm_bwd(x.data_ptr(), ldx, dy.data_ptr(), lddy, _vector(gamma, (width,), x, "gamma"),
+                                 _vector(mean, (rows,), x, "mean"), _vector(rstd, (rows,), x, "rstd"),
+                                 _optional(dres), ldr, rows, width, t, dx.data_ptr(), lddx,
+                                 _vector(dgamma, (width,), x, "dgamma"), _vector(dbeta, (width,), x, "dbeta"),
+                                 ws.data_ptr(), nbytes, s)
+    if st:
+        _check(st, "gs_layer_norm_bwd")
+    return dx, dgamma, dbeta
 
 
 def gs_layer_norm_bwd(x, dy, gamma, mean, rstd, dres=None, dx=None, dgamma=None, dbeta=None, workspace=None,
                       stream=None):
     """(dx, dgamma, dbeta); ``dres`` is added into dx (the gradient that
     reaches x past the norm)."""
-    t = _type(x)
-    rows, width = x.shape
-    _placed(x, x, "x")
-    lddy = _matrix(dy, rows, width, x, "dy")
-    ldr = 0 if dres is None else _matrix(dres, rows, width, x, "dres")
-    g = _vector(gamma, (width,), x, "gamma")
-    m, r = _vector(mean, (rows,), x, "mean"), _vector(rstd, (rows,), x, "rstd")
-
-    def call(s):
-        nonlocal dx, dgamma, dbeta
-        if dx is None:
-            dx = torch.empty(rows, width, dtype=x.dtype, device=x.device)
-        if dgamma is None:
-            dgamma = torch.empty(width, dtype=torch.float32, device=x.device)
-        if dbeta is None:
-            dbeta = torch.empty(width, dtype=torch.float32, device=x.device)
-        ws, nbytes = _workspace(workspace, gs_workspace_size(GS_OP_LAYER_NORM_BWD, rows, width), x)
-        _check(lib().gs_layer_norm_bwd(x.data_ptr(), _ld(x, rows, width), dy.data_ptr(), lddy, g, m, r,
-                                       _optional(dres), ldr, rows, width, t, dx.data_ptr(),
-                                       _matrix(dx, rows, width, x, "dx"), _vector(dgamma, (width,), x, "dgamma"),
-                                       _vector(dbeta, (width,), x, "dbeta"), ws.data_ptr(), nbytes, s),
-               "gs_layer_norm_bwd")
-    _launch(x, stream, call)
-    return dx, dgamma, dbeta
+    return _launch(_norm_bwd, x, stream, dy, gamma, mean, rstd, dres, dx, dgamma, dbeta, workspace)
 
 
-def _fwd(x, w, offsets, bias, act, residual, y, z, save_z, stream, where):
+def _fwd(s, x, w, offsets, bias, act, residual, y, z, save_z):
     t = _type(x)
     rows, inner = x.shape
-    _placed(x, x, "x")
+    ldx, device = _matrix(x, rows, inner, x, "x"), x.device
     groups = 0 if offsets is None else _groups(offsets, x)
     ldw, out = _weights(w, groups, x, inner)
     b = _vector(bias, (groups, out) if groups else (out,), x, "bias")
     ldr = 0 if residual is None else _matrix(residual, rows, out, x, "residual")
-
-    def call(s):
-        nonlocal y, z
-        if y is None:
-            y = torch.empty(rows, out, dtype=x.dtype, device=x.device)
-        if z is None and save_z:
-            z = torch.empty(rows, out, dtype=x.dtype, device=x.device)
-        ldz = 0 if z is None else _matrix(z, rows, out, x, "z")
-        head = (x.data_ptr(), _ld(x, rows, inner), w.data_ptr(), ldw, b)
-        tail = (_optional(residual), ldr, rows, inner, out, t, act, y.data_ptr(), _matrix(y, rows, out, x, "y"),
-                _optional(z), ldz, s)
-        if groups:
-            _check(lib().gs_grouped_linear_fwd(*head, offsets.data_ptr(), groups, *tail), where)
-        else:
-            _check(lib().gs_linear_fwd(*head, *tail), where)
-    _launch(x, stream, call)
+    _on_gpu(x)
+    if y is None:
+        y, ldy = _empty(rows, out, dtype=x.dtype, device=device), out
+    else:
+        ldy = _matrix(y, rows, out, x, "y")
+    if z is not None:
+        ldz = _matrix(z, rows, out, x, "z")
+    elif save_z:
+        z, ldz = _empty(rows, out, dtype=x.dtype, device=device), out
+    else:
+        ldz = 0
+    if groups:
+        st = lib().gs_grouped_linear_fwd(x.data_ptr(), ldx, w.data_ptr(), ldw, b, offsets.data_ptr(), groups,
+                                         _optional(residual), ldr, rows, inner, out, t, act, y.data_ptr(), ldy,
+                                         _optional(z), ldz, s)
+    else:
+        st = lib().gs_linear_fwd(x.data_ptr(), ldx, w.data_ptr(), ldw, b, _optional(residual), ldr, rows, inner, out,
+                                 t, act, y.data_ptr(), ldy, _optional(z), ldz, s)
+    if st:
+        _check(st, "gs_grouped_linear_fwd" if groups else "gs_linear_fwd")
     return y if z is None else (y, z)
 
 
 def gs_linear_fwd(x, w, bias=None, act=GS_ACT_NONE, residual=None, y=None, z=None, save_z=False, stream=None):
     """y = act(x w^T + bias) + residual; with ``save_z`` (or a ``z`` to
     write) also the value before the activation: (y, z)."""
-    return _fwd(x, w, None, bias, act, residual, y, z, save_z, stream, "gs_linear_fwd")
+    return _launch(_fwd, x, stream, w, None, bias, act, residual, y, z, save_z)
 
 
 def gs_grouped_linear_fwd(x, w, offsets, bias=None, act=GS_ACT_NONE, residual=None, y=None, z=None, save_z=False,
@@ -206,7 +224,7 @@ def gs_grouped_linear_fwd(x, w, offsets, bias=None, act=GS_ACT_NONE, residual=No
     """gs_linear_fwd with w[e], bias[e] for the rows offsets[e] ..
     offsets[e + 1] - 1 (``offsets``: int64 on the device, read there).
     Rows in no group are not written."""
-    return _fwd(x, w, offsets, bias, act, residual, y, z, save_z, stream, "gs_grouped_linear_fwd")
+    return _launch(_fwd, x, stream, w, offsets, bias, act, residual, y, z, save_z)
 
 
 def gs_linear_workspace_size(rows, inner, out, num_groups, type, act) -> int:
@@ -216,40 +234,44 @@ def gs_linear_workspace_size(rows, inner, out, num_groups, type, act) -> int:
     return b.value
 
 
-def _bwd(x, w, offsets, dy, z, act, dx, dw, db, want_dx, workspace, stream, where):
+def _bwd(s, x, w, offsets, dy, z, act, dx, dw, db, want_dx, workspace):
     t = _type(x)
     rows, inner = x.shape
-    _placed(x, x, "x")
+    ldx, device = _matrix(x, rows, inner, x, "x"), x.device
     groups = 0 if offsets is None else _groups(offsets, x)
     ldw, out = _weights(w, groups, x, inner)
     lddy = _matrix(dy, rows, out, x, "dy")
     if z is None and act != GS_ACT_NONE:
         raise ValueError("the activation's slope needs z, the value before it")
     ldz = 0 if z is None else _matrix(z, rows, out, x, "z")
-    bshape = (groups, out) if groups else (out,)
-
-    def call(s):
-        nonlocal dx, dw, db
-        if dx is None and want_dx:
-            dx = torch.empty(rows, inner, dtype=x.dtype, device=x.device)
-        if dw is None:
-            dw = torch.empty(w.shape, dtype=w.dtype, device=x.device)
-        elif dw.shape != w.shape or dw.dtype not in (w.dtype, torch.float32) or not dw.is_contiguous():
+    _on_gpu(x)
+    if dx is not None:
+        lddx = _matrix(dx, rows, inner, x, "dx")
+    elif want_dx:
+        dx, lddx = _empty(rows, inner, dtype=x.dtype, device=device), inner
+    else:
+        lddx = 0
+    if dw is None:
+        dw, dw_type = _empty(w.shape, dtype=w.dtype, device=device), t
+    else:
+        dw_type = 2 if dw.dtype == _F32 else t
+        if (dw.shape != w.shape or dw.dtype not in (w.dtype, _F32) or not dw.is_contiguous()
+                or dw.device != device):
             raise ValueError(f"dw is {dw.dtype} {tuple(dw.shape)}: contiguous {w.dtype} or torch.float32 "
-                             f"{tuple(w.shape)} expected")
-        _placed(dw, x, "dw")
-        if db is None:
-            db = torch.empty(bshape, dtype=torch.float32, device=x.device)
-        ws, nbytes = _workspace(workspace, gs_linear_workspace_size(rows, inner, out, groups, t, act), x)
-        head = (x.data_ptr(), _ld(x, rows, inner), w.data_ptr(), ldw)
-        tail = (_optional(z), ldz, dy.data_ptr(), lddy, rows, inner, out, t, act, _optional(dx),
-                0 if dx is None else _matrix(dx, rows, inner, x, "dx"), dw.data_ptr(), _TYPES[dw.dtype],
-                _vector(db, bshape, x, "db"), ws.data_ptr(), nbytes, s)
-        if groups:
-            _check(lib().gs_grouped_linear_bwd(*head, offsets.data_ptr(), groups, *tail), where)
-        else:
-            _check(lib().gs_linear_bwd(*head, *tail), where)
-    _launch(x, stream, call)
+                             f"{tuple(w.shape)} on {device} expected")
+    bshape = (groups, out) if groups else (out,)
+    if db is None:
+        db = _empty(bshape, dtype=_F32, device=device)
+    ws, nbytes = _workspace(workspace, gs_linear_workspace_size(rows, inner, out, groups, t, act), device)
+    head = (x.data_ptr(), ldx, w.data_ptr(), ldw)
+    tail = (_optional(z), ldz, dy.data_ptr(), lddy, rows, inner, out, t, act, _optional(dx), lddx, dw.data_ptr(),
+            dw_type, _vector(db, bshape, x, "db"), ws.data_ptr(), nbytes, s)
+    if groups:
+        st = lib().gs_grouped_linear_bwd(*head, offsets.data_ptr(), groups, *tail)
+    else:
+        st = lib().gs_linear_bwd(*head, *tail)
+    if st:
+        _check(st, "gs_grouped_linear_bwd" if groups else "gs_linear_bwd")
     return dx, dw, db
 
 
@@ -258,11 +280,11 @@ def gs_linear_bwd(x, w, dy, z=None, act=GS_ACT_NONE, dx=None, dw=None, db=None, 
     """(dx, dw, db) of gs_linear_fwd for the gradient ``dy`` of y (the
     residual's gradient is dy itself).  ``dw`` is of w's type, or float32
     where such a tensor is passed in; ``want_dx`` false leaves dx out."""
-    return _bwd(x, w, None, dy, z, act, dx, dw, db, want_dx, workspace, stream, "gs_linear_bwd")
+    return _launch(_bwd, x, stream, w, None, dy, z, act, dx, dw, db, want_dx, workspace)
 
 
 def gs_grouped_linear_bwd(x, w, offsets, dy, z=None, act=GS_ACT_NONE, dx=None, dw=None, db=None, want_dx=True,
                           workspace=None, stream=None):
     """(dx, dw, db) of gs_grouped_linear_fwd; dw[e] and db[e] are 0 for an
     empty group, rows in no group have no dx."""
-    return _bwd(x, w, offsets, dy, z, act, dx, dw, db, want_dx, workspace, stream, "gs_grouped_linear_bwd")
+    return _launch(_bwd, x, stream, w, offsets, dy, z, act, dx, dw, db, want_dx, workspace)
