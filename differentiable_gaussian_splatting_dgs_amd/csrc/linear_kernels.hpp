@@ -908,7 +908,7 @@ __global__ __launch_bounds__(256) void k_act_grad(const T* __restrict__ dy, int6
 #pragma unroll
   for (int i = 0; i < K; ++i) sum[i] = 0.0f;
   if (n > 0)
-#pragma unroll 2
+#pragma unroll 4
     for (int r = sp.row0 + rl; r < sp.row1; r += 256 / lanes) {
       const Chunk<T> c = load_chunk_n(dy + int64_t(r) * lddy + col, n);
       float v[K];
@@ -1459,6 +1459,7 @@ struct BwdPlan {
   int32_t steps, shares;
   bool small;              // dx and dw in one launch of 64 x 64 tiles
   bool sets;               // and that of 32 x 32 tiles of eight wave sets
+  bool apart;              // dx by itself, in such tiles
   int32_t side_w;          // tile of dw
   int32_t unit_b, unit_w;  // rows of a stretch of db (with an activation) and of dw
   bool part_b, part_w;     // more than one stretch a group: partial sums to join
@@ -1478,8 +1479,20 @@ BwdPlan bwd_plan(int64_t rows, int32_t in, int32_t out, int32_t groups, int act)
   s.small = slots * ceil_div(in, 128) < 256 && slots * ceil_div(out, 128) < 256;
   const int64_t x_tiles = max_slots(rows, groups, 64) * ceil_div(in, 64);
   const int64_t w_tiles = ceil_div(out, 64) * ceil_div(in, 64) * std::max(1, groups);
-  s.sets = s.small && x_tiles + w_tiles <= 512 &&
-           (out >= 8 * kStep<T> || rows >= 8 * kStep<T> * std::max(1, groups));
+  // Small problems: steps one after the other at about 1 us each, in 64 x 64
+  // tiles, three workgroups a CU (dw cut to 4 steps and joined by another
+  // launch), or in 32 x 32 tiles of eight sets, one workgroup a CU; both
+  // products alike in one launch, or dx in small tiles by itself (1 x 4096 ->
+  // 4096: 48 us in one launch, 34 us in two)
+  const int64_t heads = std::max(1, groups), x_steps = ceil_div(out, kStep<T>);
+  const int64_t w_steps = ceil_div(ceil_div(rows, std::min<int64_t>(heads, std::max<int64_t>(1, rows))), kStep<T>);
+  const int64_t launch = 6, join = w_steps > 4 ? launch : 0, w_cut = std::min<int64_t>(w_steps, 4);
+  const int64_t x32 = (2 + ceil_div(x_steps, 8)) * ceil_div(4 * x_tiles, 256);
+  const int64_t both64 = join + std::max(x_steps, w_cut) * ceil_div(x_tiles + w_tiles, 768);
+  const int64_t both32 = (2 + ceil_div(std::max(x_steps, w_steps), 8)) * ceil_div(4 * (x_tiles + w_tiles), 256);
+  const int64_t apart = launch + join + x32 + w_cut * ceil_div(w_tiles, 768);
+  s.sets = s.small && both32 <= std::min(both64, apart);
+  s.apart = s.small && !s.sets && apart < both64;
   // a side of at most 64 would leave half of a 128 tile empty (50,001 rows, 251 ->
   // 59 fp32: dw 61 us of 128 x 128, 40 us of 64 x 64)
   s.side_w = s.sets ? 32 : s.small || std::min(in, out) <= 64 ? 64 : 128;
@@ -1491,9 +1504,11 @@ BwdPlan bwd_plan(int64_t rows, int32_t in, int32_t out, int32_t groups, int act)
   if (groups * tiles >= 512) s.unit_w = int32_t(std::max<int64_t>(s.unit_w, ceil_div(2 * rows, int64_t(groups) * 64) * 64));
   s.part_w = rows > s.unit_w;
   s.plane = ceil_div(int64_t(out) * in + out, 64) * 64;
-  // about 2048 workgroups of the slope's kernel, 64 rows at least
+  // about 2048 workgroups of the slope's kernel, 16 rows at least (4096 rows 256 ->
+  // 256 bf16 with gelu, the whole backward: 38 us with 64, whose rows wait on each
+  // other, 22 us with 16)
   const int64_t across = ceil_div(out, 64 * kChunk<T>);
-  s.unit_b = int32_t(std::max<int64_t>(64, ceil_div(ceil_div(rows * across, 2048), 64) * 64));
+  s.unit_b = int32_t(std::max<int64_t>(16, ceil_div(ceil_div(rows * across, 2048), 16) * 16));
   s.part_b = rows > s.unit_b;
   s.dz = act == kActNone ? 0 : align_up(size_t(rows) * dz_ld(out, kChunk<T>) * sizeof(T), 256);
   s.db = !s.part_b ? 0 : align_up(size_t(max_slots(rows, groups, s.unit_b)) * out * 4, 256);
@@ -1627,11 +1642,13 @@ hipError_t linear_bwd(const LinearArgs& a, char* ws, hipStream_t st) {
   const bool want_dx = a.dx != nullptr && any, want_dw = a.dw != nullptr || (w.db != nullptr && !any);
   if (plan.small) {
     const int side = plan.side_w;
-    const int64_t x_tiles = want_dx ? lay_out<kDx>(x, side, side) : 0;
+    if (plan.apart && want_dx) go_product<T, kDx, 32, 32, 1, 1, 8>(x, st);
+    const bool here = want_dx && !plan.apart;
+    const int64_t x_tiles = here ? lay_out<kDx>(x, side, side) : 0;
     const int64_t w_tiles = want_dw ? lay_out<kDw>(w, side, side) : 0;
     const int64_t grid = x_tiles + w_tiles + int64_t(j.blocks) * groups;
     if (grid > 0) {
-      const bool direct = (!want_dx || direct_ok<T>(x, kDx)) && (!want_dw || direct_ok<T>(w, kDw));
+      const bool direct = (!here || direct_ok<T>(x, kDx)) && (!want_dw || direct_ok<T>(w, kDw));
       const auto go = [&](auto d, auto sets) {
         constexpr bool D = decltype(d)::value, S = decltype(sets)::value;
         constexpr int TILE = S ? 32 : 64, W = S ? 1 : 2, KW = S ? 8 : 1, lds = product_lds(TILE, TILE, W, W, KW, D);
