@@ -1468,6 +1468,15 @@ struct BwdPlan {
 };
 inline int64_t dz_ld(int32_t out, int chunk) { return ceil_div(out, chunk) * chunk; }
 
+// dw in 256 x 256 tiles: 16-bit types, little of the edge tiles empty, and
+// rows enough for a workgroup a CU.
+template <typename T>
+bool wide_dw(int64_t rows, int32_t in, int32_t out, int32_t groups) {
+  const int64_t tiles = ceil_div(out, 256) * ceil_div(in, 256);
+  return sizeof(T) == 2 && out % 8 == 0 && in % 8 == 0 && 4 * int64_t(out) * in >= 3 * tiles * 65536 &&
+         rows * tiles >= 256 * 512;
+}
+
 template <typename T>
 BwdPlan bwd_plan(int64_t rows, int32_t in, int32_t out, int32_t groups, int act) {
   BwdPlan s{};
@@ -1496,12 +1505,13 @@ BwdPlan bwd_plan(int64_t rows, int32_t in, int32_t out, int32_t groups, int act)
   // a side of at most 64 would leave half of a 128 tile empty (50,001 rows, 251 ->
   // 59 fp32: dw 61 us of 128 x 128, 40 us of 64 x 64)
   s.side_w = s.sets ? 32 : s.small || std::min(in, out) <= 64 ? 64 : 128;
+  if (s.side_w == 128 && wide_dw<T>(rows, in, out, groups)) s.side_w = 256;
   const int64_t tiles = ceil_div(out, s.side_w) * ceil_div(in, s.side_w);
-  // stretches so that about 768 workgroups share the rows, of 4 k steps a set at least
-  const int64_t cut = ceil_div(rows * tiles, 768);
+  // stretches so that about 768 workgroups (of 256 x 256: 256, one a CU) share the rows, of 4 k steps a set at least
+  const int64_t cut = ceil_div(rows * tiles, s.side_w == 256 ? 256 : 768);
   s.unit_w = int32_t(std::max<int64_t>((s.sets ? 32 : 4) * kStep<T>, ceil_div(cut, 64) * 64));
   // groups enough by themselves: only those of over twice the mean are cut
-  if (groups * tiles >= 512) s.unit_w = int32_t(std::max<int64_t>(s.unit_w, ceil_div(2 * rows, int64_t(groups) * 64) * 64));
+  if (groups * tiles >= (s.side_w == 256 ? 192 : 512)) s.unit_w = int32_t(std::max<int64_t>(s.unit_w, ceil_div(2 * rows, int64_t(groups) * 64) * 64));
   s.part_w = rows > s.unit_w;
   s.plane = ceil_div(int64_t(out) * in + out, 64) * 64;
   // about 2048 workgroups of the slope's kernel, 16 rows at least (4096 rows 256 ->
@@ -1668,6 +1678,8 @@ hipError_t linear_bwd(const LinearArgs& a, char* ws, hipStream_t st) {
     if (want_dx) run_rows<T, kDx>(x, st);
     if (want_dw && plan.side_w == 64)
       go_product<T, kDw, 64, 64, 2, 2>(w, st);
+    else if (want_dw && plan.side_w == 256 && direct_ok<T>(w, kDw))
+      go_product<T, kDw, 256, 256, 2, 4>(w, st);
     else if (want_dw)
       go_product<T, kDw, 128, 128, 2, 2>(w, st);
   }

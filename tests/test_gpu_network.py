@@ -346,7 +346,7 @@ def test_linear_activations(gs, name, act):
 
 
 @pytest.mark.parametrize("name", TYPES)
-@pytest.mark.parametrize("rows,inner,out", LINEAR_SHAPES + MANY_ROWS + [(5000, 256, 250)])
+@pytest.mark.parametrize("rows,inner,out", LINEAR_SHAPES + MANY_ROWS + [(5000, 256, 250), (33001, 512, 512), (70001, 504, 256)])
 def test_linear_backward(gs, name, rows, inner, out):
     gen, t = _gen(rows + 17 * inner + 13 * out), _dtype(name)
     x, w = _rand(gen, rows, inner, dtype=t), _rand(gen, out, inner, scale=2 * inner ** -0.5, dtype=t)
@@ -499,7 +499,7 @@ def test_grouped_linear_many_groups(gs, name):
 
 
 @pytest.mark.parametrize("name", TYPES)
-@pytest.mark.parametrize("inner,out", [(64, 256), (256, 64), (120, 136)])
+@pytest.mark.parametrize("inner,out", [(64, 256), (256, 64), (120, 136), (512, 248)])
 def test_grouped_linear_many_rows(gs, name, inner, out):
     gen, t = _gen(79), _dtype(name)
     offsets = [3, 50000, 50000, 50001, 90000, 90040, 90040, 132000]
