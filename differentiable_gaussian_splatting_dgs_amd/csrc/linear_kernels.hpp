@@ -377,13 +377,12 @@ __device__ __forceinline__ void multiply_step(const char* ta, const char* tb, in
   }
 }
 
-// How the tiles that come straight from memory are staged: dw, whose
-// transposed reads leave the loads less time, in four half steps of 64 bytes of
-// k (64 heads of 512 x 512 over 131,072 rows: 137 us against 147), the others in
-// two whole steps, with half the barriers (16384 x 4096 x 4096 fp16: 497 us
-// against 510).
-constexpr int direct_bytes(bool across_both) { return across_both ? 64 : 128; }
-constexpr int direct_stages(bool across_both) { return across_both ? 4 : 2; }
+// How the tiles that come straight from memory are staged: dw's smaller tiles,
+// whose transposed reads leave the loads less time, in four half steps of 64
+// bytes of k (64 heads of 512 x 512 over 131,072 rows in 128 x 128: 137 us against
+// 147), the others in two whole steps, with half the barriers (16384 x 4096 x
+// 4096 fp16, 256 x 256: forward 497 us against 510, dw 569 against 643).
+constexpr bool half_steps(Mode mode, int bm) { return mode == kDw && bm < 256; }
 
 // BM x BN outputs a workgroup, WM x WN waves.  The n side is the first
 // operand of the matrix instruction, so that a lane's four results are
@@ -403,7 +402,8 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, int tile, cha
   const int tid = KW > 1 ? int(threadIdx.x) % THREADS : int(threadIdx.x), lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
   char* const base = lds;
-  constexpr int kStages = direct_stages(MODE == kDw), kB = DIRECT ? direct_bytes(MODE == kDw) : 128;
+  constexpr bool kHalf = DIRECT && half_steps(MODE, BM);
+  constexpr int kStages = kHalf ? 4 : 2, kB = kHalf ? 64 : 128;
   if (KW > 1) lds += set * (BM + BN) * kB * (DIRECT ? kStages : 1);
 
   // Which tile.  kFwd, kDx: the height index picks group and rows; kDw: the
@@ -653,8 +653,8 @@ __global__ __launch_bounds__(64 * WM * WN * KW, KW == 4 ? 4 : BM == 256 && WM * 
   int tile = xcd_tile(blockIdx.x, tiles);
   if (MODE != kDw && p.tiles_n >= 8) {
     // kRun heights at a time, all their tiles across: what runs together on an
-    // XCD shares rows and weights about evenly (16384 x 4096 x 4096 fp16: 490 -> 470 us;
-    // below 8 tiles across the heights are as near anyway)
+    // XCD shares rows and weights about evenly (16384 x 4096 x 4096 fp16: 490 ->
+    // 470 us; below 8 tiles across the heights are as near anyway)
     constexpr int kRun = 4;
     const int run = tile / (kRun * p.tiles_n), in = tile - run * kRun * p.tiles_n;
     const int high = std::min(kRun, tiles / p.tiles_n - run * kRun);
