@@ -945,11 +945,22 @@ __global__ __launch_bounds__(256) void k_act_grad(const T* __restrict__ dy, int6
       if (i < n) to[col + i] = s[threadIdx.x][i];
 }
 
-// Sum over a group's stretches, in order: value i of planes `plane` apart.
-__device__ __forceinline__ float plane_sum(const float* __restrict__ part, int64_t plane, const Span& s, int64_t i) {
+// Joins planes that lie `plane` apart, n of them from q on: values are shared
+// out 64 a workgroup, their planes among its four waves, whose sums are added
+// in order.
+__device__ __forceinline__ float join_planes(const float* __restrict__ q, int64_t plane, int n, bool live,
+                                             float (&box)[256]) {
+  const int w = threadIdx.x >> 6;
   float v = 0.0f;
+  if (live)
 #pragma unroll 8
-  for (int t = 0; t < s.slots; ++t) v += part[(int64_t(s.slot0) + t) * plane + i];
+    for (int t = w; t < n; t += 4) v += q[t * plane];
+  if (n > 1) {
+    __syncthreads();   // the box's last readers
+    box[threadIdx.x] = v;
+    __syncthreads();
+    if (w == 0) v = (box[threadIdx.x] + box[threadIdx.x + 64]) + (box[threadIdx.x + 128] + box[threadIdx.x + 192]);
+  }
   return v;
 }
 
@@ -960,11 +971,14 @@ __global__ __launch_bounds__(256) void k_join(const float* __restrict__ part, in
                                               const int64_t* __restrict__ offsets, int32_t groups, int32_t rows,
                                               int32_t unit, int64_t size, O* __restrict__ out, int32_t m,
                                               float* __restrict__ db) {
+  __shared__ float box[256];
   const Span s = group_span(offsets, groups, rows, unit, blockIdx.y);
   if (s.slots == 1) return;
   const int64_t all = size + (db != nullptr ? m : 0);
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += int64_t(gridDim.x) * 256) {
-    const float v = plane_sum(part, plane, s, i);
+  for (int64_t i0 = int64_t(blockIdx.x) * 64; i0 < all; i0 += int64_t(gridDim.x) * 64) {
+    const int64_t i = i0 + (threadIdx.x & 63);
+    const float v = join_planes(part + int64_t(s.slot0) * plane + i, plane, s.slots, i < all, box);
+    if (threadIdx.x >= 64 || i >= all) continue;
     if (i < size)
       out[int64_t(blockIdx.y) * size + i] = O(v);
     else
@@ -1041,37 +1055,49 @@ __host__ __device__ inline int32_t share_of(int64_t t, int64_t total, int32_t sh
   return int32_t(s);
 }
 
-// Layers of up to 64 KS columns on both sides: one pass reads dy, z and x and
-// writes dx, and dw never leaves the registers until the rows run out.  Each
-// of 8 waves holds the weights' fragments of 32 columns of dx (16 KS
-// registers) and 16 KS x 32 KS of dw's sums; the workgroup walks its share of
-// the row tiles (128 / KS rows; dy, z, x 16 KB each):
+// Layers of up to 64 KO columns out and 64 KI in (KO, KI = 1, 2, 4): one pass
+// reads dy, z and x and writes dx, and dw never leaves the registers until the
+// rows run out.  Each of 8 waves holds the weights' fragments of 32 columns of
+// dx (16 KO registers) and an eighth of dw's sums (up to 128); the workgroup
+// walks its share of the row tiles (128 / max(KO, KI) rows; dy, z, x up to 16 KB
+// each, two tiles in flight with counted waits):
 //   slope   dz = dy act'(z) in place, rounded for the matrix instructions, db
 //           summed unrounded
 //   product dx = dz w; dw += dz^T x, its operands read transposed
-// While tile t is multiplied, tile t + 1 gets its slope and tile t + 2 is
-// fetched; of the two waves that share a SIMD one multiplies first and the
-// other computes slopes first, so that the matrix and the vector unit work
-// side by side, with one barrier a tile.
 // A share that ends inside a group, or a group inside a share, leaves one
-// plane of partial sums, number share + group.  Bound by HBM: 3 or 4 planes of
-// the rows, each once.
-template <typename T, int KS>
+// plane of partial sums, number share + group.  What it has to move is 3 or 4
+// planes of the rows, each once; what bounds it at 256 x 256 is the issue of
+// one tile's phases one after the other on 2 waves a SIMD (the vector unit is
+// busy half of the time, the matrix unit a fifth): 1,000,000 rows with gelu 583
+// us, 3.5 TB/s, where a pass for dz and two products took 972 us.  Measured
+// and not taken: slopes a tile ahead in turn with the products of the other
+// wave of a SIMD (645 us), x fetched a tile further ahead (no change).
+template <typename T, int KO, int KI>
 __global__ __launch_bounds__(512, 2) void k_bwd_rows(FusedArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__
   static_assert(sizeof(T) == 2, "transposed LDS reads are 16 bit");
-  constexpr int BM = 128 / KS, WN = 2 * KS, WM = 8 / WN, TM = BM / WM, FM = TM / 16, FN = 2;
-  constexpr int DM = KS, DN = 2 * KS;                  // dw fragments of a wave; the waves lie 4 x 2
-  constexpr int kPatch = 40, kTile = 16384, K = 8;
-  constexpr int kStores = FM * Eight<T>::kParts;
-  // three tiles of dy (then dz), x and z, and the patches (in the storage
-  // type: nothing is added to dx)
-  __shared__ __align__(16) char lds[9 * kTile + 8 * 16 * kPatch * 2];
-  char* const lds_x = lds + 3 * kTile;
-  char* const lds_z = lds + 6 * kTile;
+  constexpr int BM = 128 / std::max(KO, KI), K = 8, FN = 2;
+  // dx: WM x WN waves of TM x 32 outputs (of the narrowest, some have none)
+  constexpr int WN = 2 * KI, WM = std::min(8 / WN, BM / 16), TM = BM / WM, FM = TM / 16;
+  // dw: WO x WI waves
+  constexpr int WO = KO == KI ? 4 : KO == 4 * KI ? 8 : KO > KI ? 4 : KI == 4 * KO ? 1 : 2, WI = 8 / WO;
+  constexpr int DM = KO * 4 / WO, DN = KI * 4 / WI;
+  constexpr int kPatch = 40, kStores = FM * Eight<T>::kParts;
+  // tiles in LDS: of whole kilobytes for every wave, so that each has as many loads
+  constexpr int kLoadsY = (BM * KO * 128 + 8191) / 8192, kLoadsX = (BM * KI * 128 + 8191) / 8192;
+  constexpr int kTileY = kLoadsY * 8192, kTileX = kLoadsX * 8192;
+  // three tiles each of dy (then dz), x and z, the patches (in the storage
+  // type: nothing is added to dx), and 16 KB for db's sums, which lie in a z
+  // tile where that is large enough
+  constexpr int kPatches = 8 * 16 * kPatch * 2;
+  constexpr bool kBoxInZ = kTileY >= 16384;
+  __shared__ __align__(16) char lds[6 * kTileY + 3 * kTileX + kPatches + (kBoxInZ ? 0 : 16384)];
+  char* const lds_z = lds + 3 * kTileY;
+  char* const lds_x = lds + 6 * kTileY;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
-  T* patch = reinterpret_cast<T*>(lds + 9 * kTile) + wave * 16 * kPatch;
+  const bool has_dx = p.dx != nullptr && wm < WM;
+  T* patch = reinterpret_cast<T*>(lds_x + 3 * kTileX) + wave * 16 * kPatch;
 
   const int share = xcd_tile(blockIdx.x, gridDim.x);
   const int64_t total = total_slots(p.offsets, p.groups, p.rows, BM);
@@ -1079,13 +1105,14 @@ __global__ __launch_bounds__(512, 2) void k_bwd_rows(FusedArgs p) {
   if (t0 >= t1) return;
 
   // a thread's chunks of a tile: 8 of a row and step, row by row, step by step
-  const auto fetch_one = [&](const void* q, int64_t ld, int cols, const Span& s, int th, char* to) {
+  const auto fetch_one = [&](auto loads, auto steps, const void* q, int64_t ld, int cols, const Span& s, int th,
+                             char* to) {
     const __amdgpu_buffer_rsrc_t rsrc =
         buffer_of(static_cast<const T*>(q) + int64_t(s.row0) * ld, ld, s.e < 0 ? 0 : s.row1 - s.row0, cols);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < decltype(loads)::value; ++j) {
       const int at = j * 512 + th, step = at / (BM * 8), r = at / 8 % BM, col = (step * 8 + ((at & 7) ^ (r & 7))) * K;
-      const uint32_t off = col < cols ? __umul24(r, uint32_t(ld * 2)) + uint32_t(col * 2) : 0xfffffff0u;
+      const uint32_t off = col < cols && step < decltype(steps)::value ? __umul24(r, uint32_t(ld * 2)) + uint32_t(col * 2) : 0xfffffff0u;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           rsrc, (__attribute__((address_space(3))) void*)(to + j * 8192 + wave * 1024), 16, off, 0, 0, 0);
     }
@@ -1093,9 +1120,14 @@ __global__ __launch_bounds__(512, 2) void k_bwd_rows(FusedArgs p) {
   const auto fetch = [&](const Span& s, int ring) {
     int th = tid;
     asm volatile("" : "+v"(th));   // addresses kept through the loop would spill
-    fetch_one(p.dy, p.lddy, p.out, s, th, lds + ring * kTile);
-    if (p.z != nullptr) fetch_one(p.z, p.ldz, p.out, s, th, lds_z + ring * kTile);
-    fetch_one(p.x, p.ldx, p.in, s, th, lds_x + ring * kTile);
+    using std::integral_constant;
+    const integral_constant<int, kLoadsY> ly{};
+    const integral_constant<int, kLoadsX> lx{};
+    const integral_constant<int, KO> ko{};
+    const integral_constant<int, KI> ki{};
+    fetch_one(ly, ko, p.dy, p.lddy, p.out, s, th, lds + ring * kTileY);
+    if (p.z != nullptr) fetch_one(ly, ko, p.z, p.ldz, p.out, s, th, lds_z + ring * kTileY);
+    fetch_one(lx, ki, p.x, p.ldx, p.in, s, th, lds_x + ring * kTileX);
   };
   const auto after = [&](const Span& s, int t) {
     if (t >= t1) return Span{-1, 0, 0, 0, 0, 0};
@@ -1109,7 +1141,7 @@ __global__ __launch_bounds__(512, 2) void k_bwd_rows(FusedArgs p) {
   fetch(now, 0);
   fetch(next, 1);
 
-  typename Frag<T>::V fw[KS * 2][FN];
+  typename Frag<T>::V fw[KO * 2][FN];
   f32x4 dw[DM][DN];
   float db[K];
 #pragma unroll
@@ -1119,20 +1151,21 @@ __global__ __launch_bounds__(512, 2) void k_bwd_rows(FusedArgs p) {
 #pragma unroll
   for (int i = 0; i < K; ++i) db[i] = 0.0f;
   // dz: a thread's chunk column is the same in all its rows
-  constexpr int kCols = KS * 8, kApart = 512 / kCols;    // chunk columns, rows between a thread's rows
-  const int am = (wave >> 1) * 16 * DM, bn = (wave & 1) * 16 * DN;   // this wave's corner of dw
+  constexpr int kCols = KO * 8, kApart = 512 / kCols;    // chunk columns, rows between a thread's rows
+  const int am = wave / WI * 16 * DM, bn = wave % WI * 16 * DN;   // this wave's corner of dw
   Across across_y, across_x;   // of its blocks, which may begin inside a step
   across_y.init(lane, (am >> 4) & 3);
   across_x.init(lane, (bn >> 4) & 3);
   const auto slope = [&](int ring) {
-    char* const ty = lds + ring * kTile;
-    const char* const tz = lds_z + ring * kTile;
+    char* const ty = lds + ring * kTileY;
+    const char* const tz = lds_z + ring * kTileY;
     int th = tid;
     asm volatile("" : "+v"(th));
     const int zc = th % kCols, zr = th / kCols;
 #pragma unroll
-    for (int j = 0; j < BM / kApart; ++j) {
+    for (int j = 0; j < (BM + kApart - 1) / kApart; ++j) {
       const int r = zr + j * kApart;
+      if (BM < kApart && r >= BM) break;
       const int at = (zc >> 3) * BM * 128 + tile_at<T, BM, false>(r, zc & 7);
       Chunk<T> c = *reinterpret_cast<const Chunk<T>*>(ty + at);
       if (p.z != nullptr) {
@@ -1159,17 +1192,17 @@ __global__ __launch_bounds__(512, 2) void k_bwd_rows(FusedArgs p) {
   for (int t = t0; t < t1; ++t) {
     // behind this tile's loads lie the next one's and two tiles' stores (less
     // of them at the start)
-    constexpr int kFetch = 6;
+    constexpr int kFetch = kLoadsY + kLoadsX;
     if (p.z == nullptr) {
-      if (t - t0 < 2 || p.dx == nullptr)
-        rows_barrier<4>();
-      else
-        rows_barrier<4 + 2 * kStores>();
-    } else {
-      if (t - t0 < 2 || p.dx == nullptr)
+      if (t - t0 < 2 || !has_dx)
         rows_barrier<kFetch>();
       else
         rows_barrier<kFetch + 2 * kStores>();
+    } else {
+      if (t - t0 < 2 || !has_dx)
+        rows_barrier<kFetch + kLoadsY>();
+      else
+        rows_barrier<kFetch + kLoadsY + 2 * kStores>();
     }
     const Span later = after(next, t + 2);
     const int ring1 = ring == 2 ? 0 : ring + 1, ring2 = ring1 == 2 ? 0 : ring1 + 1;
@@ -1181,7 +1214,7 @@ __global__ __launch_bounds__(512, 2) void k_bwd_rows(FusedArgs p) {
       // the group or the share ends with tile t: a column's sums of db lie
       // kCols threads apart, joined where this tile's z was
       float* plane = p.part + int64_t(share + now.e) * p.plane;
-      float* box = reinterpret_cast<float*>(lds_z + ring * kTile);
+      float* box = reinterpret_cast<float*>(kBoxInZ ? lds_z + ring * kTileY : lds_x + 3 * kTileX + kPatches);
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < K; ++i) {
@@ -1201,12 +1234,12 @@ __global__ __launch_bounds__(512, 2) void k_bwd_rows(FusedArgs p) {
 
     if (now.e != group) {
       group = now.e;
-      if (p.dx != nullptr) {
+      if (has_dx) {
         const T* w = static_cast<const T*>(p.w) + int64_t(group) * p.w_group;
         int ln = lane;
         asm volatile("" : "+v"(ln));
 #pragma unroll
-        for (int kk = 0; kk < KS * 2; ++kk)
+        for (int kk = 0; kk < KO * 2; ++kk)
 #pragma unroll
           for (int j = 0; j < FN; ++j) {
             const int n = wn * 32 + 16 * j + (ln & 15), k = (4 * kk + (ln >> 4)) * K;
@@ -1223,12 +1256,11 @@ __global__ __launch_bounds__(512, 2) void k_bwd_rows(FusedArgs p) {
     }
 
     if (p.z != nullptr) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    {
-      const char* const ty = lds + ring * kTile;
-      const char* const tx = lds_x + ring * kTile;
+    const char* const ty = lds + ring * kTileY;
+    const char* const tx = lds_x + ring * kTileX;
     int ln = lane;
     asm volatile("" : "+v"(ln));   // as in fetch
-    if (p.dx != nullptr) {
+    if (has_dx) {
       const auto ro = buffer_of(static_cast<T*>(p.dx) + int64_t(now.row0) * p.lddx, p.lddx, now.row1 - now.row0, p.in);
       f32x4 acc[FM][FN];
 #pragma unroll
@@ -1236,7 +1268,7 @@ __global__ __launch_bounds__(512, 2) void k_bwd_rows(FusedArgs p) {
 #pragma unroll
         for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int kk = 0; kk < KS * 2; ++kk) {
+      for (int kk = 0; kk < KO * 2; ++kk) {
         typename Frag<T>::V fa[FM];
 #pragma unroll
         for (int i = 0; i < FM; ++i)
@@ -1294,7 +1326,6 @@ __global__ __launch_bounds__(512, 2) void k_bwd_rows(FusedArgs p) {
           dw[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
     }
-    }
     now = next;
     next = later;
     ring = ring1;
@@ -1315,11 +1346,11 @@ __global__ __launch_bounds__(256) void k_join_rows(FusedArgs p, int bm, O* __res
     lo = share_of(s.slot0, total, p.shares);
     n = share_of(s.slot0 + s.slots - 1, total, p.shares) - lo + 1;
   }
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += int64_t(gridDim.x) * 256) {
-    const float* q = p.part + int64_t(lo + int(blockIdx.y)) * p.plane + i;
-    float v = 0.0f;
-#pragma unroll 8
-    for (int t = 0; t < n; ++t) v += q[t * p.plane];
+  __shared__ float box[256];
+  for (int64_t i0 = int64_t(blockIdx.x) * 64; i0 < all; i0 += int64_t(gridDim.x) * 64) {
+    const int64_t i = i0 + (threadIdx.x & 63);
+    const float v = join_planes(p.part + int64_t(lo + int(blockIdx.y)) * p.plane + i, p.plane, n, i < all, box);
+    if (threadIdx.x >= 64 || i >= all) continue;
     if (i < size)
       out[int64_t(blockIdx.y) * size + i] = O(v);
     else if (db != nullptr)
@@ -1456,7 +1487,7 @@ void run_rows(const ProductArgs& p, hipStream_t st) {
 // can be sized for it.
 struct BwdPlan {
   bool fused;              // k_bwd_rows may run (the alignment decides), of so many steps and shares
-  int32_t steps, shares;
+  int32_t ko, ki, shares;
   bool small;              // dx and dw in one launch of 64 x 64 tiles
   bool sets;               // and that of 32 x 32 tiles of eight wave sets
   bool apart;              // dx by itself, in such tiles
@@ -1481,11 +1512,15 @@ template <typename T>
 BwdPlan bwd_plan(int64_t rows, int32_t in, int32_t out, int32_t groups, int act) {
   BwdPlan s{};
   const int64_t slots = max_slots(rows, groups, 128);
-  s.steps = int32_t(ceil_div(std::max(in, out), 64));
-  s.steps = s.steps == 3 ? 4 : s.steps;
-  s.fused = sizeof(T) == 2 && s.steps <= 4 && in % 8 == 0 && out % 8 == 0 && rows >= 32768;
+  const auto steps = [](int32_t n) { return n <= 64 ? 1 : n <= 128 ? 2 : n <= 256 ? 4 : 8; };
+  s.ko = steps(out);
+  s.ki = steps(in);
+  s.fused = sizeof(T) == 2 && s.ko <= 4 && s.ki <= 4 && in % 8 == 0 && out % 8 == 0 && rows >= 32768;
   s.shares = 256;   // a workgroup a CU
-  s.small = slots * ceil_div(in, 128) < 256 && slots * ceil_div(out, 128) < 256;
+  // (to 1024 tiles of 128 x 128 where both sides are narrow: 16384 rows 256 -> 256 bf16
+  // with gelu 44 -> 37 us; 20,000 rows 777 -> 777 would take 254 us instead of 209)
+  const int64_t few = std::max(in, out) <= 256 ? 1024 : 256;
+  s.small = slots * ceil_div(in, 128) < few && slots * ceil_div(out, 128) < few;
   const int64_t x_tiles = max_slots(rows, groups, 64) * ceil_div(in, 64);
   const int64_t w_tiles = ceil_div(out, 64) * ceil_div(in, 64) * std::max(1, groups);
   // Small problems: steps one after the other at about 1 us each, in 64 x 64
@@ -1583,18 +1618,31 @@ hipError_t linear_bwd(const LinearArgs& a, char* ws, hipStream_t st) {
       f.out = a.out;
       f.act = a.act;
       f.shares = plan.shares;
-      if (plan.steps == 4)
-        k_bwd_rows<T, 4><<<plan.shares, 512, 0, st>>>(f);
-      else if (plan.steps == 2)
-        k_bwd_rows<T, 2><<<plan.shares, 512, 0, st>>>(f);
+      const auto go = [&](auto ko, auto ki) {
+        k_bwd_rows<T, decltype(ko)::value, decltype(ki)::value><<<plan.shares, 512, 0, st>>>(f);
+      };
+      const auto go_in = [&](auto ko) {
+        using std::integral_constant;
+        if (plan.ki == 4)
+          go(ko, integral_constant<int, 4>{});
+        else if (plan.ki == 2)
+          go(ko, integral_constant<int, 2>{});
+        else
+          go(ko, integral_constant<int, 1>{});
+      };
+      if (plan.ko == 4)
+        go_in(std::integral_constant<int, 4>{});
+      else if (plan.ko == 2)
+        go_in(std::integral_constant<int, 2>{});
       else
-        k_bwd_rows<T, 1><<<plan.shares, 512, 0, st>>>(f);
-      const dim3 grid(int(std::min<int64_t>(ceil_div(int64_t(a.out) * a.in + a.out, 256), std::max(16, 4096 / std::max(1, a.groups)))),
+        go_in(std::integral_constant<int, 1>{});
+      const int bm = 128 / std::max(plan.ko, plan.ki);
+      const dim3 grid(int(std::min<int64_t>(ceil_div(int64_t(a.out) * a.in + a.out, 64), std::max(16, 4096 / std::max(1, a.groups)))),
                       std::max(1, a.groups));
       if (a.dw_f32)
-        k_join_rows<float><<<grid, 256, 0, st>>>(f, 128 / plan.steps, static_cast<float*>(a.dw), a.db);
+        k_join_rows<float><<<grid, 256, 0, st>>>(f, bm, static_cast<float*>(a.dw), a.db);
       else
-        k_join_rows<T><<<grid, 256, 0, st>>>(f, 128 / plan.steps, static_cast<T*>(a.dw), a.db);
+        k_join_rows<T><<<grid, 256, 0, st>>>(f, bm, static_cast<T*>(a.dw), a.db);
       return hipGetLastError();
     }
   }
@@ -1685,7 +1733,7 @@ hipError_t linear_bwd(const LinearArgs& a, char* ws, hipStream_t st) {
   }
   if (want_dw && w.part != nullptr) {
     const int64_t size = int64_t(a.out) * a.in;
-    const dim3 grid(int(std::min<int64_t>(ceil_div(size + a.out, 256), std::max(16, 4096 / groups))), groups);
+    const dim3 grid(int(std::min<int64_t>(ceil_div(size + a.out, 64), std::max(16, 4096 / groups))), groups);
     if (a.dw_f32)
       k_join<float><<<grid, 256, 0, st>>>(w.part, w.plane, a.offsets, a.groups, a.rows, plan.unit_w, size,
                                           static_cast<float*>(a.dw), a.out, w.db);

@@ -314,7 +314,8 @@ LINEAR_SHAPES = [(1, 1, 1), (2, 3, 5), (7, 64, 64), (1, 256, 130), (19, 59, 48),
 
 # rows enough for the kernels that keep their weights, at every width of theirs
 MANY_ROWS = [(20000, 40, 136), (9000, 264, 520), (33001, 64, 64), (66001, 128, 128), (132001, 256, 256),
-             (33000, 24, 256), (66000, 96, 120), (100003, 184, 512), (132001, 192, 48), (33000, 56, 104), (66000, 72, 264)]
+             (33000, 24, 256), (66000, 96, 120), (100003, 184, 512), (132001, 192, 48), (33000, 56, 104), (66000, 72, 264), (40001, 104, 56),
+             (40000, 104, 200), (40003, 200, 104)]
 
 
 @pytest.mark.parametrize("name", TYPES)
