@@ -48,33 +48,47 @@ struct ProductArgs {
 // A fragment is 16 bytes of one row along k: lane l holds row l % 16 and
 // k-chunk l / 16 of a 16 x (64 bytes) block.  16-bit types: one 16x16x32
 // instruction; fp32: four 16x16x4, component c of every lane's chunk in the
-// c-th (the same order of k on both sides, so the sum is the same).
+// c-th (`part`; the same order of k on both sides, so the sum is the same).
 // D: lane l holds rows 4 (l / 16) .. + 3 of column l % 16.
 template <typename T>
 struct Frag;
 template <>
 struct Frag<bf16> {
   typedef __bf16 V __attribute__((ext_vector_type(8)));
-  static __device__ __forceinline__ f32x4 mma(V a, V b, f32x4 c) {
+  static constexpr int kParts = 1;
+  static __device__ __forceinline__ f32x4 mma(V a, V b, f32x4 c, int) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
 };
 template <>
 struct Frag<f16> {
   typedef _Float16 V __attribute__((ext_vector_type(8)));
-  static __device__ __forceinline__ f32x4 mma(V a, V b, f32x4 c) {
+  static constexpr int kParts = 1;
+  static __device__ __forceinline__ f32x4 mma(V a, V b, f32x4 c, int) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
   }
 };
 template <>
 struct Frag<float> {
   typedef float V __attribute__((ext_vector_type(4)));
-  static __device__ __forceinline__ f32x4 mma(V a, V b, f32x4 c) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
-    return c;
+  static constexpr int kParts = 4;
+  static __device__ __forceinline__ f32x4 mma(V a, V b, f32x4 c, int part) {
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a[part], b[part], c, 0, 0, 0);
   }
 };
+
+// All pairs of a step's fragments; the parts of one pair, which wait for each
+// other, lie as far apart as they can.
+template <typename T, int FM, int FN>
+__device__ __forceinline__ void mma_all(const typename Frag<T>::V (&fb)[FN], const typename Frag<T>::V (&fa)[FM],
+                                        f32x4 (&acc)[FM][FN]) {
+#pragma unroll
+  for (int c = 0; c < Frag<T>::kParts; ++c)
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] = Frag<T>::mma(fb[j], fa[i], acc[i][j], c);
+}
 
 // --- tiles in LDS ---------------------------------------------------------------------
 
@@ -361,17 +375,16 @@ __device__ __forceinline__ void multiply_step(const char* ta, const char* tb, in
     for (int i = 0; i < FM; ++i) fa[i] = read_frag<T, BM, A_ACROSS, KB>(ta, am + 16 * i, kk, lane);
 #pragma unroll
     for (int j = 0; j < FN; ++j) fb[j] = read_frag<T, BN, B_ACROSS, KB>(tb, bn + 16 * j, kk, lane);
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int j = 0; j < FN; ++j) acc[i][j] = Frag<T>::mma(fb[j], fa[i], acc[i][j]);
+    mma_all<T, FM, FN>(fb, fa, acc);
     if constexpr (FS == FM) {
       if (sums) {
         typename Frag<T>::V one;
 #pragma unroll
         for (int c = 0; c < kChunk<T>; ++c) one[c] = T(1.0f);
 #pragma unroll
-        for (int i = 0; i < FM; ++i) sum[i] = Frag<T>::mma(one, fa[i], sum[i]);
+        for (int c = 0; c < Frag<T>::kParts; ++c)
+#pragma unroll
+          for (int i = 0; i < FM; ++i) sum[i] = Frag<T>::mma(one, fa[i], sum[i], c);
       }
     }
   }
@@ -836,10 +849,7 @@ __global__ __launch_bounds__(512, 4) void k_rows(ProductArgs p, int shares) {
 #pragma unroll
         for (int i = 0; i < FB; ++i)
           fa[i] = read_frag<T, BM, false>(tile + (kk >> 1) * BM * 128, wm * TM + 16 * (i0 + i), kk & 1, lane);
-#pragma unroll
-        for (int i = 0; i < FB; ++i)
-#pragma unroll
-          for (int j = 0; j < FN; ++j) acc[i][j] = Frag<T>::mma(fw[kk][j], fa[i], acc[i][j]);
+        mma_all<T, FB, FN>(fw[kk], fa, acc);
       }
 #pragma unroll
       for (int i = 0; i < FB; ++i) {
@@ -1273,10 +1283,7 @@ __global__ __launch_bounds__(512, 2) void k_bwd_rows(FusedArgs p) {
 #pragma unroll
         for (int i = 0; i < FM; ++i)
           fa[i] = read_frag<T, BM, false>(ty + (kk >> 1) * BM * 128, wm * TM + 16 * i, kk & 1, ln);
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-          for (int j = 0; j < FN; ++j) acc[i][j] = Frag<T>::mma(fw[kk][j], fa[i], acc[i][j]);
+        mma_all<T, FM, FN>(fw[kk], fa, acc);
       }
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
@@ -1312,7 +1319,7 @@ __global__ __launch_bounds__(512, 2) void k_bwd_rows(FusedArgs p) {
       for (int j = 0; j < DN; ++j) {   // the next fragment is read while this one is multiplied
         if (j + 1 < DN) fb[(j + 1) & 1] = across_x.template read<T, BM>(wx, j + 1, kk);
 #pragma unroll
-        for (int i = 0; i < DM; ++i) dw[i][j] = Frag<T>::mma(fb[j & 1], fa[i], dw[i][j]);
+        for (int i = 0; i < DM; ++i) dw[i][j] = Frag<T>::mma(fb[j & 1], fa[i], dw[i][j], 0);
       }
     }
     if (next.e != now.e) {
@@ -1466,11 +1473,16 @@ void run_rows(const ProductArgs& p, hipStream_t st) {
            : p.n <= 128 ? go_rows<T, MODE, 1, 2, 4>(p, st)
                         : go_rows<T, MODE, 1, 1, 8>(p, st);
   }
-  const int64_t large = max_slots(p.rows, p.groups, 256) * ceil_div(p.n, 256);
+  // 256 x 256, a workgroup a CU: where the last round of them is mostly full
+  // (20,000 rows 1024 -> 1024 fp32, 316 tiles: 508 us, 128 x 128 tiles 331 us) and
+  // little of a tile lies past the columns (100,000 rows 1024 -> 48 fp32 498 us, 64 x 64
+  // tiles 130 us)
+  const int64_t across = ceil_div(p.n, 256), large = max_slots(p.rows, p.groups, 256) * across;
+  const bool full = 4 * large >= 3 * ceil_div(large, 256) * 256 && 4 * p.n >= 3 * across * 256;
   const int64_t big = max_slots(p.rows, p.groups, 128) * ceil_div(p.n, 128);
-  if (large >= 256 && p.k >= 512 && direct_ok<T>(p, MODE))
+  if (large >= 200 && full && p.k >= 512 && direct_ok<T>(p, MODE))
     go_product<T, MODE, 256, 256, 2, 4>(p, st);
-  else if (big >= 256)
+  else if (big >= 256 && p.n > 64)
     go_product<T, MODE, 128, 128, 2, 2>(p, st);
   else {
     const int sets = wave_sets<T>(max_slots(p.rows, p.groups, 64) * ceil_div(p.n, 64), p.k);

@@ -319,7 +319,7 @@ MANY_ROWS = [(20000, 40, 136), (9000, 264, 520), (33001, 64, 64), (66001, 128, 1
 
 
 @pytest.mark.parametrize("name", TYPES)
-@pytest.mark.parametrize("rows,inner,out", LINEAR_SHAPES + MANY_ROWS)
+@pytest.mark.parametrize("rows,inner,out", LINEAR_SHAPES + MANY_ROWS + [(52000, 520, 256), (9000, 512, 1800)])
 def test_linear_forward(gs, name, rows, inner, out):
     gen, t = _gen(rows + 7 * inner + 13 * out), _dtype(name)
     x, w = _rand(gen, rows, inner, dtype=t), _rand(gen, out, inner, scale=2 * inner ** -0.5, dtype=t)
@@ -347,7 +347,7 @@ def test_linear_activations(gs, name, act):
 
 
 @pytest.mark.parametrize("name", TYPES)
-@pytest.mark.parametrize("rows,inner,out", LINEAR_SHAPES + MANY_ROWS + [(5000, 256, 250), (33001, 512, 512), (70001, 504, 256)])
+@pytest.mark.parametrize("rows,inner,out", LINEAR_SHAPES + MANY_ROWS + [(5000, 256, 250), (52000, 512, 256), (33001, 512, 512), (70001, 504, 256)])
 def test_linear_backward(gs, name, rows, inner, out):
     gen, t = _gen(rows + 17 * inner + 13 * out), _dtype(name)
     x, w = _rand(gen, rows, inner, dtype=t), _rand(gen, out, inner, scale=2 * inner ** -0.5, dtype=t)
