@@ -461,7 +461,8 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, int tile, cha
     Direct<T, BN, B_ACROSS, THREADS, kB> db;
     da.init(p.lda, tid);
     db.init(p.ldb, tid);
-    // every step loads the same number of times, past the end nothing but zeros
+    // with more than two stages every step loads the same number of times, past
+    // the end nothing but zeros
     int ahead = first;
     const auto load = [&](int stage) {
       char* t = lds + stage * kBytes;
@@ -476,7 +477,8 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, int tile, cha
     int stage = 0;
     for (int all = k_all, left = first; all > 0; all -= KW * kK, left -= KW * kK) {
       tile_barrier<WM * WN, (kStages - 2) * kLoads>();
-      load(stage == 0 ? kStages - 1 : stage - 1);
+      // two stages wait for everything anyway, and a single step has but one
+      if (kStages > 2 || all > KW * kK) load(stage == 0 ? kStages - 1 : stage - 1);
       const char* t = lds + stage * kBytes;
       if (KW == 1 || left > 0)
         multiply_step<T, BM, BN, A_ACROSS, B_ACROSS, kB>(t, t + BM * kB, wm * TM, wn * TN, lane, acc, sum, sums);
@@ -643,11 +645,11 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, int tile, cha
   }
 }
 
-// LDS of a workgroup: the stages of its sets (one whole step where the tiles
-// come through registers), later the boxes of the sets' results and the
-// patches.
-constexpr int product_lds(int bm, int bn, int wm, int wn, int kw, bool direct) {
-  const int tiles = (bm + bn) * (direct ? 256 : 128) * kw;   // either staging
+// LDS of a workgroup: the stages of its sets (256 bytes of k in all of them
+// together; one step of 128 where the tiles come through registers or there
+// is but one), later the boxes of the sets' results and the patches.
+constexpr int product_lds(int bm, int bn, int wm, int wn, int kw, bool staged) {
+  const int tiles = (bm + bn) * (staged ? 256 : 128) * kw;
   const int regs = (bm / wm / 16) * (bn / wn / 16 + 1);   // kDw's, the largest
   const int after = (kw - 1) * regs * 64 * wm * wn * 16 + wm * wn * 16 * (bn / wn + 4) * 4;
   return tiles > after ? tiles : after;
@@ -1402,7 +1404,11 @@ void go_tile(const ProductArgs& p, int64_t grid, hipStream_t st) {
     static std::atomic<uint64_t> asked{0};
     ask_lds(&k_product<T, MODE, BM, BN, WM, WN, DIRECT, KW>, most, asked);
   }
-  k_product<T, MODE, BM, BN, WM, WN, DIRECT, KW><<<int(grid), 64 * WM * WN * KW, most, st>>>(p);
+  // a single step needs one stage, and leaves LDS for more workgroups (21,856 rows
+  // 48 -> 768 fp16 with everything in the epilogue 35 -> 25 us)
+  const bool staged = DIRECT && (MODE == kDw || KW > 1 || p.k > kStep<T>);
+  k_product<T, MODE, BM, BN, WM, WN, DIRECT, KW>
+      <<<int(grid), 64 * WM * WN * KW, product_lds(BM, BN, WM, WN, KW, staged), st>>>(p);
 }
 
 // Tiles of the product and the shape of its grid.
@@ -1473,26 +1479,30 @@ void run_rows(const ProductArgs& p, hipStream_t st) {
            : p.n <= 128 ? go_rows<T, MODE, 1, 2, 4>(p, st)
                         : go_rows<T, MODE, 1, 1, 8>(p, st);
   }
-  // 256 x 256, a workgroup a CU: where the last round of them is mostly full
-  // (20,000 rows 1024 -> 1024 fp32, 316 tiles: 508 us, 128 x 128 tiles 331 us) and
-  // little of a tile lies past the columns (100,000 rows 1024 -> 48 fp32 498 us, 64 x 64
-  // tiles 130 us)
-  const int64_t across = ceil_div(p.n, 256), large = max_slots(p.rows, p.groups, 256) * across;
-  const bool full = 4 * large >= 3 * ceil_div(large, 256) * 256 && 4 * p.n >= 3 * across * 256;
-  const int64_t big = max_slots(p.rows, p.groups, 128) * ceil_div(p.n, 128);
-  if (large >= 200 && full && p.k >= 512 && direct_ok<T>(p, MODE))
-    go_product<T, MODE, 256, 256, 2, 4>(p, st);
-  else if (big >= 256 && p.n > 64)
-    go_product<T, MODE, 128, 128, 2, 2>(p, st);
-  else {
-    const int sets = wave_sets<T>(max_slots(p.rows, p.groups, 64) * ceil_div(p.n, 64), p.k);
-    if (sets == 8)
-      go_product<T, MODE, 32, 32, 1, 1, 8>(p, st);
-    else if (sets == 4)
-      go_product<T, MODE, 64, 64, 2, 2, 4>(p, st);
-    else
-      go_product<T, MODE, 64, 64, 2, 2>(p, st);
+  if constexpr (sizeof(T) == 2) {
+    // 256 x 256, a workgroup a CU: where the last round of them is mostly full and
+    // little of a tile lies past the columns (300,000 rows 512 -> 64 bf16: 107 us,
+    // 64 x 64 tiles 77 us).  fp32 has its matrix rate, a sixteenth, as the
+    // bound at any tile, and 64 x 64 leave the least of it to empty columns
+    // (20,000 rows 1024 -> 1024, 316 tiles of 256 x 256: 508 us, 337 us of 64 x 64).
+    const int64_t across = ceil_div(p.n, 256), large = max_slots(p.rows, p.groups, 256) * across;
+    const bool full = 4 * large >= 3 * ceil_div(large, 256) * 256 && 4 * p.n >= 3 * across * 256;
+    if (large >= 200 && full && p.k >= 512 && direct_ok<T>(p, MODE)) {
+      go_product<T, MODE, 256, 256, 2, 4>(p, st);
+      return;
+    }
+    if (max_slots(p.rows, p.groups, 128) * ceil_div(p.n, 128) >= 256 && p.n > 64) {
+      go_product<T, MODE, 128, 128, 2, 2>(p, st);
+      return;
+    }
   }
+  const int sets = wave_sets<T>(max_slots(p.rows, p.groups, 64) * ceil_div(p.n, 64), p.k);
+  if (sets == 8)
+    go_product<T, MODE, 32, 32, 1, 1, 8>(p, st);
+  else if (sets == 4)
+    go_product<T, MODE, 64, 64, 2, 2, 4>(p, st);
+  else
+    go_product<T, MODE, 64, 64, 2, 2>(p, st);
 }
 
 // How the backward pass is cut: from the sizes alone, so that the workspace
@@ -1551,7 +1561,7 @@ BwdPlan bwd_plan(int64_t rows, int32_t in, int32_t out, int32_t groups, int act)
   s.apart = s.small && !s.sets && apart < both64;
   // a side of at most 64 would leave half of a 128 tile empty (50,001 rows, 251 ->
   // 59 fp32: dw 61 us of 128 x 128, 40 us of 64 x 64)
-  s.side_w = s.sets ? 32 : s.small || std::min(in, out) <= 64 ? 64 : 128;
+  s.side_w = s.sets ? 32 : s.small || sizeof(T) == 4 || std::min(in, out) <= 64 ? 64 : 128;
   if (s.side_w == 128 && wide_dw<T>(rows, in, out, groups)) s.side_w = 256;
   const int64_t tiles = ceil_div(out, s.side_w) * ceil_div(in, s.side_w);
   // stretches so that about 768 workgroups (of 256 x 256: 256, one a CU) share the rows, of 4 k steps a set at least
@@ -1738,10 +1748,12 @@ hipError_t linear_bwd(const LinearArgs& a, char* ws, hipStream_t st) {
     if (want_dx) run_rows<T, kDx>(x, st);
     if (want_dw && plan.side_w == 64)
       go_product<T, kDw, 64, 64, 2, 2>(w, st);
-    else if (want_dw && plan.side_w == 256 && direct_ok<T>(w, kDw))
-      go_product<T, kDw, 256, 256, 2, 4>(w, st);
-    else if (want_dw)
-      go_product<T, kDw, 128, 128, 2, 2>(w, st);
+    if constexpr (sizeof(T) == 2) {
+      if (want_dw && plan.side_w == 256 && direct_ok<T>(w, kDw))
+        go_product<T, kDw, 256, 256, 2, 4>(w, st);
+      else if (want_dw && plan.side_w != 64)
+        go_product<T, kDw, 128, 128, 2, 2>(w, st);
+    }
   }
   if (want_dw && w.part != nullptr) {
     const int64_t size = int64_t(a.out) * a.in;
