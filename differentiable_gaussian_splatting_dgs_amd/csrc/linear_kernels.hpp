@@ -1485,13 +1485,15 @@ void run_rows(const ProductArgs& p, hipStream_t st) {
     // 64 x 64 tiles 77 us).  fp32 has its matrix rate, a sixteenth, as the
     // bound at any tile, and 64 x 64 leave the least of it to empty columns
     // (20,000 rows 1024 -> 1024, 316 tiles of 256 x 256: 508 us, 337 us of 64 x 64).
+    // A tile's rows are of one group, so groups have to fill it on average.
     const int64_t across = ceil_div(p.n, 256), large = max_slots(p.rows, p.groups, 256) * across;
     const bool full = 4 * large >= 3 * ceil_div(large, 256) * 256 && 4 * p.n >= 3 * across * 256;
-    if (large >= 200 && full && p.k >= 512 && direct_ok<T>(p, MODE)) {
+    const int64_t rows = p.rows / std::max(1, p.groups);
+    if (large >= 200 && full && rows >= 256 && p.k >= 512 && direct_ok<T>(p, MODE)) {
       go_product<T, MODE, 256, 256, 2, 4>(p, st);
       return;
     }
-    if (max_slots(p.rows, p.groups, 128) * ceil_div(p.n, 128) >= 256 && p.n > 64) {
+    if (max_slots(p.rows, p.groups, 128) * ceil_div(p.n, 128) >= 256 && p.n > 64 && rows >= 96) {
       go_product<T, MODE, 128, 128, 2, 2>(p, st);
       return;
     }
