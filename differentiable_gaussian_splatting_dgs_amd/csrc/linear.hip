@@ -16,9 +16,9 @@ size_t linear_bwd_ws_f16(int64_t rows, int32_t in, int32_t out, int32_t groups, 
 size_t linear_bwd_ws_f32(int64_t rows, int32_t in, int32_t out, int32_t groups, int act);
 
 bool linear_fits(int64_t rows, int32_t in, int32_t out, int32_t groups) {
-  // 256 threads a workgroup and a launch below 2^32 threads; the smallest
-  // tile is 64 x 64
-  const int64_t most = int64_t(1) << 24, side = std::max(in, out);
+  // 256 threads a workgroup and a launch below 2^32 threads, which dx's and
+  // dw's tiles may share; the smallest tile is 64 x 64
+  const int64_t most = int64_t(1) << 23, side = std::max(in, out);
   const int64_t high = rows / 64 + std::max(groups, 1), wide = (side + 63) / 64;
   const int64_t planes = ((int64_t(in) + 63) / 64) * ((int64_t(out) + 63) / 64);
   return high * wide < most && (planes + 768) * (std::max(groups, 1) + 1) < most;

@@ -768,7 +768,7 @@ __global__ __launch_bounds__(512, 4) void k_rows(ProductArgs p, int shares) {
     if (p.groups > 0 && t >= s.slot0 + s.slots) return find_span(p.offsets, p.groups, p.rows, BM, t);
     Span q = s;
     q.row0 = s.row0 + BM;
-    q.row1 = std::min(s.end, q.row0 + BM);
+    q.row1 = s.end - q.row0 < BM ? s.end : q.row0 + BM;
     return q;
   };
   Span now = find_span(p.offsets, p.groups, p.rows, BM, t0), next = after(now, t0 + 1);
@@ -921,20 +921,20 @@ __global__ __launch_bounds__(256) void k_act_grad(const T* __restrict__ dy, int6
   for (int i = 0; i < K; ++i) sum[i] = 0.0f;
   if (n > 0)
 #pragma unroll 4
-    for (int r = sp.row0 + rl; r < sp.row1; r += 256 / lanes) {
-      const Chunk<T> c = load_chunk_n(dy + int64_t(r) * lddy + col, n);
+    for (int64_t r = sp.row0 + rl; r < sp.row1; r += 256 / lanes) {
+      const Chunk<T> c = load_chunk_n(dy + r * lddy + col, n);
       float v[K];
 #pragma unroll
       for (int i = 0; i < K; ++i) v[i] = float(c.v[i]);
       if (dz != nullptr) {
-        const Chunk<T> zc = load_chunk_n(z + int64_t(r) * ldz + col, n);
+        const Chunk<T> zc = load_chunk_n(z + r * ldz + col, n);
         Chunk<T> o;
 #pragma unroll
         for (int i = 0; i < K; ++i) {
           v[i] *= act_slope<T>(float(zc.v[i]), act);
           o.v[i] = T(v[i]);
         }
-        store_chunk(dz + int64_t(r) * lddz + col, o);   // lddz is whole chunks: the padding is written too
+        store_chunk(dz + r * lddz + col, o);   // lddz is whole chunks: the padding is written too
       }
 #pragma unroll
       for (int i = 0; i < K; ++i) sum[i] += v[i];
@@ -1146,7 +1146,7 @@ __global__ __launch_bounds__(512, 2) void k_bwd_rows(FusedArgs p) {
     if (p.groups > 0 && t >= s.slot0 + s.slots) return find_span(p.offsets, p.groups, p.rows, BM, t);
     Span q = s;
     q.row0 = s.row0 + BM;
-    q.row1 = std::min(s.end, q.row0 + BM);
+    q.row1 = s.end - q.row0 < BM ? s.end : q.row0 + BM;
     return q;
   };
   Span now = find_span(p.offsets, p.groups, p.rows, BM, t0), next = after(now, t0 + 1);
@@ -1568,9 +1568,11 @@ BwdPlan bwd_plan(int64_t rows, int32_t in, int32_t out, int32_t groups, int act)
   const int64_t tiles = ceil_div(out, s.side_w) * ceil_div(in, s.side_w);
   // stretches so that about 768 workgroups (of 256 x 256: 256, one a CU) share the rows, of 4 k steps a set at least
   const int64_t cut = ceil_div(rows * tiles, s.side_w == 256 ? 256 : 768);
-  s.unit_w = int32_t(std::max<int64_t>((s.sets ? 32 : 4) * kStep<T>, ceil_div(cut, 64) * 64));
+  int64_t unit = std::max<int64_t>((s.sets ? 32 : 4) * kStep<T>, ceil_div(cut, 64) * 64);
   // groups enough by themselves: only those of over twice the mean are cut
-  if (groups * tiles >= (s.side_w == 256 ? 192 : 512)) s.unit_w = int32_t(std::max<int64_t>(s.unit_w, ceil_div(2 * rows, int64_t(groups) * 64) * 64));
+  if (groups * tiles >= (s.side_w == 256 ? 192 : 512))
+    unit = std::max<int64_t>(unit, ceil_div(2 * rows, int64_t(groups) * 64) * 64);
+  s.unit_w = int32_t(std::min<int64_t>(unit, 1 << 30));
   s.part_w = rows > s.unit_w;
   s.plane = ceil_div(int64_t(out) * in + out, 64) * 64;
   // about 2048 workgroups of the slope's kernel, 16 rows at least (4096 rows 256 ->

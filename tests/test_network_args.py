@@ -93,6 +93,10 @@ def test_workspace_sizes():
     assert size(1 << 20, 64, 64, 0, gs.GS_TYPE_BF16, gs.GS_ACT_NONE) < (1 << 20) * 64 * 2
     assert size(0, 64, 64, 0, gs.GS_TYPE_F32, gs.GS_ACT_NONE) >= 256
     assert size(0, 64, 64, 9, gs.GS_TYPE_F32, gs.GS_ACT_GELU) >= 256
+    # many rows: partial sums do not grow with them
+    big = size(1 << 28, 64, 64, 0, gs.GS_TYPE_BF16, gs.GS_ACT_NONE)
+    assert 0 < big < 1 << 28
+    assert size(1 << 28, 64, 64, 1000, gs.GS_TYPE_F32, gs.GS_ACT_NONE) < 1 << 30
     for bad in (dict(rows=-1), dict(inner=0), dict(num_groups=-1), dict(num_groups=5000), dict(type=4), dict(act=9)):
         args = dict(rows=10, inner=8, out=8, num_groups=0, type=0, act=0) | bad
         with pytest.raises(gs.GSError):
