@@ -998,28 +998,28 @@ __global__ __launch_bounds__(256) void k_join(const float* __restrict__ part, in
   }
 }
 
-// db from the partial rows of k_act_grad: 16 columns a workgroup, 16 shares
-// of a group's rows, joined in a fixed order.
+// db from the partial rows of k_act_grad: `cols` columns a workgroup, 256 /
+// cols shares of a group's rows, joined in a fixed order.
 struct DbJoin {
   const float* part;
   float* db;
-  int32_t out, unit, blocks;   // blocks: workgroups of a group
+  int32_t out, unit, cols, blocks;   // blocks: workgroups of a group
 };
 __device__ __forceinline__ void join_db(const DbJoin& j, const ProductArgs& p, int block, float* box) {
   const Span s = group_span(p.offsets, p.groups, p.rows, j.unit, block / j.blocks);
-  const int tid = threadIdx.x, col = block % j.blocks * 16 + (tid & 15);
+  const int tid = threadIdx.x, c = tid % j.cols, share = tid / j.cols, shares = 256 / j.cols;
+  const int col = block % j.blocks * j.cols + c;
   if (tid < 256) {
     float v = 0.0f;
     if (col < j.out)
 #pragma unroll 4
-      for (int t = tid >> 4; t < s.slots; t += 16) v += j.part[(int64_t(s.slot0) + t) * j.out + col];
+      for (int t = share; t < s.slots; t += shares) v += j.part[(int64_t(s.slot0) + t) * j.out + col];
     box[tid] = v;
   }
   __syncthreads();
-  if (tid >= 16 || col >= j.out) return;
+  if (tid >= j.cols || col >= j.out) return;
   float v = 0.0f;
-#pragma unroll
-  for (int t = 0; t < 16; ++t) v += box[16 * t + tid];
+  for (int t = 0; t < shares; ++t) v += box[j.cols * t + tid];
   j.db[int64_t(s.e) * j.out + col] = v;
 }
 __global__ __launch_bounds__(256) void k_join_db(DbJoin j, ProductArgs p) {
@@ -1033,16 +1033,18 @@ __global__ __launch_bounds__(256) void k_join_db(DbJoin j, ProductArgs p) {
 template <typename T, int TILE, int W, bool DIRECT, int KW>
 __global__ __launch_bounds__(64 * W * W * KW) void k_bwd(ProductArgs x, int x_tiles, ProductArgs w, int w_tiles, DbJoin j) {
   extern __shared__ __align__(16) char lds[];
+  // dw's workgroups, the longest, first (50,001 rows 251 -> 59 fp32, the whole
+  // backward: 69 us, 86 us with them last)
   int b = blockIdx.x;
-  if (b < x_tiles) {
-    product_tile<T, kDx, TILE, TILE, W, W, DIRECT, KW>(x, b, lds);
+  if (b < w_tiles) {
+    product_tile<T, kDw, TILE, TILE, W, W, DIRECT, KW>(w, b, lds);
     return;
   }
-  b -= x_tiles;
-  if (b < w_tiles)
-    product_tile<T, kDw, TILE, TILE, W, W, DIRECT, KW>(w, b, lds);
+  b -= w_tiles;
+  if (b < x_tiles)
+    product_tile<T, kDx, TILE, TILE, W, W, DIRECT, KW>(x, b, lds);
   else
-    join_db(j, w, b - w_tiles, reinterpret_cast<float*>(lds));
+    join_db(j, w, b - x_tiles, reinterpret_cast<float*>(lds));
 }
 
 // --- the whole backward pass over many rows of a narrow layer --------------------------
@@ -1695,7 +1697,11 @@ hipError_t linear_bwd(const LinearArgs& a, char* ws, hipStream_t st) {
                     256, 0, st>>>(static_cast<const T*>(a.dy), a.lddy, static_cast<const T*>(a.z), a.ldz,
                                   slope ? dz : nullptr, dz_ld(a.out, kChunk<T>), a.offsets, a.groups, a.rows,
                                   plan.unit_b, a.out, a.act, lanes, cut ? part : nullptr, a.db);
-    if (parts) j = DbJoin{part, a.db, a.out, plan.unit_b, int32_t(ceil_div(a.out, 16))};
+    if (parts) {
+      // one group has many partial rows, each of many groups few
+      const int32_t cols = groups >= 16 ? 64 : 16;
+      j = DbJoin{part, a.db, a.out, plan.unit_b, cols, int32_t(ceil_div(a.out, cols))};
+    }
   }
 
   ProductArgs p{};
