@@ -655,17 +655,17 @@ constexpr int product_lds(int bm, int bn, int wm, int wn, int kw, bool staged) {
   return tiles > after ? tiles : after;
 }
 
+// Workgroup `id` of `grid` of a product.
 template <typename T, Mode MODE, int BM, int BN, int WM, int WN, bool DIRECT, int KW>
-__global__ __launch_bounds__(64 * WM * WN * KW, KW == 4 ? 4 : BM == 256 && WM * WN == 4 ? 1 : 2) void k_product(ProductArgs p) {
-  extern __shared__ __align__(16) char lds[];
+__device__ __forceinline__ void product_block(const ProductArgs& p, int id, int grid, char* lds) {
   // the grid is sized for the most slots the groups can make; the tiles that
   // there are go evenly to the XCDs
-  int tiles = gridDim.x;
+  int tiles = grid;
   if (p.groups > 0 && (MODE != kDw || p.part != nullptr)) {
     tiles = total_slots(p.offsets, p.groups, p.rows, p.unit) * (MODE == kDw ? p.tiles : p.tiles_n);
-    if (int(blockIdx.x) >= tiles) return;
+    if (id >= tiles) return;
   }
-  int tile = xcd_tile(blockIdx.x, tiles);
+  int tile = xcd_tile(id, tiles);
   if (MODE != kDw && p.tiles_n >= 8) {
     // kRun heights at a time, all their tiles across: what runs together on an
     // XCD shares rows and weights about evenly (16384 x 4096 x 4096 fp16: 490 ->
@@ -676,6 +676,28 @@ __global__ __launch_bounds__(64 * WM * WN * KW, KW == 4 ? 4 : BM == 256 && WM * 
     tile = (run * kRun + in % high) * p.tiles_n + in / high;
   }
   product_tile<T, MODE, BM, BN, WM, WN, DIRECT, KW>(p, tile, lds);
+}
+
+template <typename T, Mode MODE, int BM, int BN, int WM, int WN, bool DIRECT, int KW>
+__global__ __launch_bounds__(64 * WM * WN * KW, KW == 4 ? 4 : BM == 256 && WM * WN == 4 ? 1 : 2) void k_product(ProductArgs p) {
+  extern __shared__ __align__(16) char lds[];
+  product_block<T, MODE, BM, BN, WM, WN, DIRECT, KW>(p, blockIdx.x, gridDim.x, lds);
+}
+
+// dw and dx of ragged groups, both in 256 x 256 tiles, a workgroup a CU: dw's
+// workgroups last as long as their groups, so dx's, short and alike, fill the
+// CUs that the smaller groups leave.  The whole backward in bf16 with silu against
+// two launches: 131,072 rows on 64 ragged heads 512 -> 512 328 us, 368; 262,144 on
+// 16 649 us, 766; 100,000 on 32 768 -> 512 327 us, 414.  (Without groups the two
+// are within 4 % of each other, either way.)
+template <typename T>
+__global__ __launch_bounds__(512, 2) void k_bwd_groups(ProductArgs x, ProductArgs w, int w_grid) {
+  extern __shared__ __align__(16) char lds[];
+  const int b = blockIdx.x;
+  if (b < w_grid)
+    product_block<T, kDw, 256, 256, 2, 4, true, 1>(w, b, w_grid, lds);
+  else
+    product_block<T, kDx, 256, 256, 2, 4, true, 1>(x, b - w_grid, int(gridDim.x) - w_grid, lds);
 }
 
 // --- the product over many rows of a short k ---------------------------------------
@@ -1468,6 +1490,22 @@ void go_rows(ProductArgs p, hipStream_t st) {
   k_rows<T, MODE, KS, WM, WN><<<shares * p.tiles_n, 512, 0, st>>>(p, shares);
 }
 
+// 256 x 256, a workgroup a CU: where the last round of them is mostly full and
+// little of a tile lies past the columns (300,000 rows 512 -> 64 bf16: 107 us,
+// 64 x 64 tiles 77 us).  fp32 has its matrix rate, a sixteenth, as the
+// bound at any tile, and 64 x 64 leave the least of it to empty columns
+// (20,000 rows 1024 -> 1024, 316 tiles of 256 x 256: 508 us, 337 us of 64 x 64).
+// A tile's rows are of one group, so groups have to fill it on average.
+// `filled`: other work fills the last round, which may be as empty as it likes
+// (k_bwd_groups: 32,768 rows on 8 heads 512 -> 512 bf16, 272 tiles: the whole
+// backward 158 us -> 136).
+template <typename T, Mode MODE>
+bool wide_rows(const ProductArgs& p, bool filled) {
+  const int64_t across = ceil_div(p.n, 256), large = max_slots(p.rows, p.groups, 256) * across;
+  const bool full = (filled || 4 * large >= 3 * ceil_div(large, 256) * 256) && 4 * p.n >= 3 * across * 256;
+  return large >= 200 && full && p.rows / std::max(1, p.groups) >= 256 && p.k >= 512 && direct_ok<T>(p, MODE);
+}
+
 template <typename T, Mode MODE>
 void run_rows(const ProductArgs& p, hipStream_t st) {
   if (rows_ok<T, MODE>(p)) {
@@ -1482,20 +1520,11 @@ void run_rows(const ProductArgs& p, hipStream_t st) {
                         : go_rows<T, MODE, 1, 1, 8>(p, st);
   }
   if constexpr (sizeof(T) == 2) {
-    // 256 x 256, a workgroup a CU: where the last round of them is mostly full and
-    // little of a tile lies past the columns (300,000 rows 512 -> 64 bf16: 107 us,
-    // 64 x 64 tiles 77 us).  fp32 has its matrix rate, a sixteenth, as the
-    // bound at any tile, and 64 x 64 leave the least of it to empty columns
-    // (20,000 rows 1024 -> 1024, 316 tiles of 256 x 256: 508 us, 337 us of 64 x 64).
-    // A tile's rows are of one group, so groups have to fill it on average.
-    const int64_t across = ceil_div(p.n, 256), large = max_slots(p.rows, p.groups, 256) * across;
-    const bool full = 4 * large >= 3 * ceil_div(large, 256) * 256 && 4 * p.n >= 3 * across * 256;
-    const int64_t rows = p.rows / std::max(1, p.groups);
-    if (large >= 200 && full && rows >= 256 && p.k >= 512 && direct_ok<T>(p, MODE)) {
+    if (wide_rows<T, MODE>(p, false)) {
       go_product<T, MODE, 256, 256, 2, 4>(p, st);
       return;
     }
-    if (max_slots(p.rows, p.groups, 128) * ceil_div(p.n, 128) >= 256 && p.n > 64 && rows >= 96) {
+    if (max_slots(p.rows, p.groups, 128) * ceil_div(p.n, 128) >= 256 && p.n > 64 && p.rows / std::max(1, p.groups) >= 96) {
       go_product<T, MODE, 128, 128, 2, 2>(p, st);
       return;
     }
@@ -1729,7 +1758,8 @@ hipError_t linear_bwd(const LinearArgs& a, char* ws, hipStream_t st) {
   w.part = plan.part_w ? reinterpret_cast<float*>(ws + plan.dz + plan.db) : nullptr;
   w.plane = plan.plane;
   w.db = own_db && any ? nullptr : a.db;
-  const bool want_dx = a.dx != nullptr && any, want_dw = a.dw != nullptr || (w.db != nullptr && !any);
+  bool want_dx = a.dx != nullptr && any;
+  const bool want_dw = a.dw != nullptr || (w.db != nullptr && !any);
   if (plan.small) {
     const int side = plan.side_w;
     if (plan.apart && want_dx) go_product<T, kDx, 32, 32, 1, 1, 8>(x, st);
@@ -1755,13 +1785,24 @@ hipError_t linear_bwd(const LinearArgs& a, char* ws, hipStream_t st) {
     }
   } else {
     if (j.blocks > 0) k_join_db<<<j.blocks * groups, 256, 0, st>>>(j, p);
+    bool want_w = want_dw;
+    if constexpr (sizeof(T) == 2) {
+      if (want_dx && want_dw && a.groups > 0 && plan.side_w == 256 && wide_rows<T, kDx>(x, true) && direct_ok<T>(w, kDw)) {
+        const int64_t w_grid = lay_out<kDw>(w, 256, 256), x_grid = lay_out<kDx>(x, 256, 256);
+        constexpr int lds = product_lds(256, 256, 2, 4, 1, true);
+        static std::atomic<uint64_t> asked{0};
+        ask_lds(&k_bwd_groups<T>, lds, asked);
+        k_bwd_groups<T><<<int(w_grid + x_grid), 512, lds, st>>>(x, w, int(w_grid));
+        want_dx = want_w = false;
+      }
+    }
     if (want_dx) run_rows<T, kDx>(x, st);
-    if (want_dw && plan.side_w == 64)
+    if (want_w && plan.side_w == 64)
       go_product<T, kDw, 64, 64, 2, 2>(w, st);
     if constexpr (sizeof(T) == 2) {
-      if (want_dw && plan.side_w == 256 && direct_ok<T>(w, kDw))
+      if (want_w && plan.side_w == 256 && direct_ok<T>(w, kDw))
         go_product<T, kDw, 256, 256, 2, 4>(w, st);
-      else if (want_dw && plan.side_w != 64)
+      else if (want_w && plan.side_w != 64)
         go_product<T, kDw, 128, 128, 2, 2>(w, st);
     }
   }

@@ -512,6 +512,28 @@ def test_grouped_linear_many_rows(gs, name, inner, out):
     _linear_bwd_check(gs, x, w, dy, z, "silu", offsets)
 
 
+@pytest.mark.parametrize("name", ["bf16", "fp16"])
+@pytest.mark.parametrize("groups,inner,out", [(7, 600, 512), (64, 512, 512), (1, 1000, 760)])
+def test_grouped_linear_backward_in_one_launch(gs, name, groups, inner, out):
+    """Rows and columns enough for dx and dw in the largest tiles together:
+    groups that are cut and joined, empty ones, rows of nobody."""
+    gen, t = _gen(80 + groups), _dtype(name)
+    sizes = np.random.default_rng(groups).integers(0, 2 * 40000 // groups, groups)
+    sizes[groups // 2] = 0 if groups > 1 else 40000
+    offsets = [2] + (2 + np.cumsum(sizes)).tolist()
+    rows = max(offsets[-1] + 3, 39000)
+    x, w = _rand(gen, rows, inner, dtype=t), _rand(gen, groups, out, inner, scale=0.1, dtype=t)
+    dy, z = _rand(gen, rows, out, dtype=t), _rand(gen, rows, out, dtype=t)
+    _linear_bwd_check(gs, x, w, dy, z, "silu", offsets)
+    _linear_bwd_check(gs, x, w, dy, None, "none", offsets)
+    # dw alone, in a launch of its own, has the same bits
+    off = torch.tensor(offsets, dtype=torch.int64, device="cuda")
+    _, dw, _ = gs.gs_grouped_linear_bwd(x, w, off, dy, z, gs.GS_ACT_SILU)
+    only = torch.empty_like(dw)
+    gs.gs_grouped_linear_bwd(x, w, off, dy, z, gs.GS_ACT_SILU, dw=only, want_dx=False)
+    assert torch.equal(only, dw)
+
+
 def test_grouped_linear_any_offsets_are_safe(gs):
     """Bounds below 0, past the rows and falling: clamped, and a bound below
     an earlier one counts as that one."""
