@@ -1080,8 +1080,16 @@ struct FusedArgs {
   float* part;         // planes of [m = out][n = in], then [m] of db
   const int64_t* offsets;
   int64_t lddy, ldz, ldx, ldw, lddx, w_group, plane;
-  int32_t rows, groups, in, out, act, shares;
+  int32_t rows, groups, in, out, act;
+  int32_t shares;      // at most
 };
+
+// The tiles lie in the rows that groups cover, which may be few of them: no
+// more shares than tiles, so that every share has a tile and writes its planes
+// (k_join_rows adds all planes between a group's first share and its last).
+__device__ __forceinline__ int32_t shares_in_use(int64_t total, int32_t shares) {
+  return total < shares ? int32_t(total) : shares;
+}
 
 // Which share of the tiles tile t is in: share s holds total s / shares ..
 // total (s + 1) / shares - 1.
@@ -1135,10 +1143,11 @@ __global__ __launch_bounds__(512, 2) void k_bwd_rows(FusedArgs p) {
   const bool has_dx = p.dx != nullptr && wm < WM;
   T* patch = reinterpret_cast<T*>(lds_x + 3 * kTileX) + wave * 16 * kPatch;
 
-  const int share = xcd_tile(blockIdx.x, gridDim.x);
   const int64_t total = total_slots(p.offsets, p.groups, p.rows, BM);
-  const int t0 = int(total * share / p.shares), t1 = int(total * (share + 1) / p.shares);
-  if (t0 >= t1) return;
+  const int shares = shares_in_use(total, p.shares);
+  if (int(blockIdx.x) >= shares) return;
+  const int share = xcd_tile(blockIdx.x, shares);
+  const int t0 = int(total * share / shares), t1 = int(total * (share + 1) / shares);
 
   // a thread's chunks of a tile: 8 of a row and step, row by row, step by step
   const auto fetch_one = [&](auto loads, auto steps, const void* q, int64_t ld, int cols, const Span& s, int th,
@@ -1374,10 +1383,11 @@ __global__ __launch_bounds__(256) void k_join_rows(FusedArgs p, int bm, O* __res
   const Span s = group_span(p.offsets, p.groups, p.rows, bm, blockIdx.y);
   const int64_t total = total_slots(p.offsets, p.groups, p.rows, bm);
   const int64_t size = int64_t(p.in) * p.out, all = size + p.out;
+  const int shares = shares_in_use(total, p.shares);
   int lo = 0, n = 0;
   if (s.slots > 0) {
-    lo = share_of(s.slot0, total, p.shares);
-    n = share_of(s.slot0 + s.slots - 1, total, p.shares) - lo + 1;
+    lo = share_of(s.slot0, total, shares);
+    n = share_of(s.slot0 + s.slots - 1, total, shares) - lo + 1;
   }
   __shared__ float box[256];
   for (int64_t i0 = int64_t(blockIdx.x) * 64; i0 < all; i0 += int64_t(gridDim.x) * 64) {

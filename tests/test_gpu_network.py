@@ -648,3 +648,73 @@ def test_linear_backward_in_parts(gs, rows, act):
                                           s) == gs.GS_OK
         for v, want in zip(out, (ex, eg, eb)):
             assert v is None or torch.equal(v, want)
+
+
+# --- workspaces that hold anything ------------------------------------------------------
+
+def _filled_workspace(gs, rows, inner, out, groups, t, act, byte):
+    """A workspace whose every byte is `byte` (255: NaN wherever it is read
+    as a number)."""
+    kind = {torch.bfloat16: gs.GS_TYPE_BF16, torch.float16: gs.GS_TYPE_F16, torch.float32: gs.GS_TYPE_F32}[t]
+    size = gs.gs_linear_workspace_size(rows, inner, out, groups, kind, _act_id(gs, act))
+    return torch.full((size,), byte, dtype=torch.uint8, device="cuda")
+
+
+@pytest.mark.parametrize("name", ["bf16", "fp16"])
+@pytest.mark.parametrize("inner,out", [(64, 64), (128, 72), (56, 256), (256, 256)])
+@pytest.mark.parametrize("offsets", [[9, 9, 9], [35000, 35001], [7, 1007], [0, 6000], [20000, 23000, 23000, 25000],
+                                     [1] + [39000 + 20 * e for e in range(40)]],
+                         ids=["no rows", "one row", "a thousand", "six thousand", "three groups", "forty groups"])
+def test_grouped_backward_of_few_rows_among_many(gs, name, inner, out, offsets):
+    """Groups that cover a small part of the rows, in a workspace of NaN: dw
+    and db hold the covered rows alone, whatever the workspace held."""
+    t, rows, groups = _dtype(name), 40000, len(offsets) - 1
+    gen = _gen(inner + out + groups)
+    x, w = _rand(gen, rows, inner, dtype=t), _rand(gen, groups, out, inner, scale=0.2, dtype=t)
+    dy, z = _rand(gen, rows, out, dtype=t), _rand(gen, rows, out, dtype=t)
+    for act in ("none", "silu"):
+        ws = _filled_workspace(gs, rows, inner, out, groups, t, act, 255)
+        _linear_bwd_check(gs, x, w, dy, z if act != "none" else None, act, offsets, workspace=ws)
+
+
+@pytest.mark.parametrize("name", TYPES)
+@pytest.mark.parametrize("groups", [0, 5])
+@pytest.mark.parametrize("rows,inner,out", [(1, 4096, 4096), (60, 72, 59), (3000, 520, 40), (9000, 264, 520),
+                                            (20000, 1024, 512), (40000, 512, 512), (70000, 64, 256), (70000, 256, 56),
+                                            (33000, 251, 59)])
+def test_linear_backward_reads_what_it_wrote(gs, name, groups, rows, inner, out):
+    """The same bits from a workspace of zeros and from one of NaN, for every
+    way the backward pass is cut."""
+    t, act = _dtype(name), "gelu"
+    gen = _gen(rows + inner + out + groups)
+    lead = (groups,) if groups else ()
+    x, w = _rand(gen, rows, inner, dtype=t), _rand(gen, *lead, out, inner, scale=0.2, dtype=t)
+    dy, z = _rand(gen, rows, out, dtype=t), _rand(gen, rows, out, dtype=t)
+    # one group long enough to be cut, one empty, a few rows of nobody
+    cuts = [0, rows // 8, rows // 8, rows * 7 // 8, rows * 7 // 8 + 1, rows - rows // 100]
+    off = torch.tensor([min(c, rows) for c in cuts], dtype=torch.int64, device="cuda")
+    for a in (act, "none"):
+        results = []
+        for byte in (0, 255):
+            ws = _filled_workspace(gs, rows, inner, out, groups, t, a, byte)
+            zz = z if a != "none" else None
+            dx = torch.zeros_like(x)
+            results.append(gs.gs_grouped_linear_bwd(x, w, off, dy, zz, _act_id(gs, a), dx=dx, workspace=ws) if groups
+                           else gs.gs_linear_bwd(x, w, dy, zz, _act_id(gs, a), dx=dx, workspace=ws))
+        for zeros, nans in zip(*results):
+            assert nans.isfinite().all() and torch.equal(zeros, nans)
+
+
+@pytest.mark.parametrize("name", TYPES)
+@pytest.mark.parametrize("rows,width", [(1, 7), (300, 515), (5000, 64), (40, 9001)])
+def test_layer_norm_backward_reads_what_it_wrote(gs, name, rows, width):
+    t, gen = _dtype(name), _gen(rows + width)
+    x, dy = _rand(gen, rows, width, dtype=t), _rand(gen, rows, width, dtype=t)
+    _, mean, rstd = gs.gs_layer_norm_fwd(x)
+    results = []
+    for byte in (0, 255):
+        ws = torch.full((gs.gs_workspace_size(gs.GS_OP_LAYER_NORM_BWD, rows, width),), byte, dtype=torch.uint8,
+                        device="cuda")
+        results.append(gs.gs_layer_norm_bwd(x, dy, None, mean, rstd, workspace=ws))
+    for zeros, nans in zip(*results):
+        assert nans.isfinite().all() and torch.equal(zeros, nans)
