@@ -1008,6 +1008,12 @@ class TrainStep:
         self.grads.zero_()
         for g2 in self.g2d:
             g2.zero_()
+        self.drop_next_view()
+
+    def drop_next_view(self):
+        """Forget what the last Adam pass left for the next step's first view
+        (records, visibility bytes, union flags): after a change of the
+        parameters that view has to be projected afresh."""
         self.touched.zero_()
         self.union_flags.zero_()
         self.next_flags.zero_()

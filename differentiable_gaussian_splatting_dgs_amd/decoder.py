@@ -94,6 +94,7 @@ class AttributeDecoder:
         the views, and leave the gradients in the masters.  Returns the
         views' losses (device tensor)."""
         attr = self.forward()
+        step.drop_next_view()       # its parameters change here
         step.params.copy_(base)
         step.params[:, :attr.shape[0]] += attr[:, :PLANES].t()
         losses = []

@@ -61,3 +61,88 @@ def test_block_offsets():
     pos = torch.tensor([[0.0, 3.9, 1.0, 4.0, 0.5, 2.1], [0.0] * 6, [0.0] * 6])
     order, off = block_offsets(pos, 4)
     assert off.tolist() == [0, 2, 3, 4, 6] and order.tolist() == [0, 4, 2, 5, 1, 3]
+
+
+def _scene():
+    """The small reference scene in four blocks: (fresh TrainStep, offsets)."""
+    import synth
+    from differentiable_gaussian_splatting_dgs_amd import TrainStep
+    from differentiable_gaussian_splatting_dgs_amd.decoder import block_offsets
+    work = synth.cut_down(synth.workload(2), 320, 180, n=20000)
+    order, offsets = block_offsets(work.params[:3], 4)
+    base = torch.as_tensor(work.params)[:, order].contiguous()
+    return lambda: TrainStep(base, work.cameras, work.targets, work.w_l1, work.w_ssim, work.lr, work.beta1,
+                             work.beta2, work.eps), offsets
+
+
+def _moving_decoder(offsets, **kw):
+    """A decoder whose attributes move and recolour every Gaussian."""
+    from differentiable_gaussian_splatting_dgs_amd.decoder import AttributeDecoder
+    dec = AttributeDecoder(offsets, width=32, hidden=64, seed=5, **kw)
+    dec.masters["hb"][:, :3] += 0.05
+    dec.masters["hb"][:, 11:14] += 0.3
+    return dec
+
+
+def test_views_after_steps_of_the_base_are_of_the_decoded_parameters():
+    """Steps of the TrainStep leave records for its next step's first view;
+    a decoder's pass takes none of them, nor leaves them for the step after
+    it."""
+    fresh, offsets = _scene()
+    used = fresh()
+    for _ in range(2):
+        used.step()
+    state, base = used.state(), used.params.clone()
+    new = fresh()
+    mine, other = _moving_decoder(offsets), _moving_decoder(offsets)
+    losses, want = mine.train_views(used, base), other.train_views(new, base)
+    assert torch.equal(losses, want), (losses.tolist(), want.tolist())
+    # the sums over pairs are atomic, in another order: a value on its way may
+    # then round the other way, a whole step off, at most 8 times (above)
+    for k, v in mine.masters.items():
+        ref = other.masters[k].grad
+        assert float((v.grad - ref).norm()) <= 8 * torch.finfo(mine.dtype).eps * float(ref.norm()), k
+    # a pass without the first view, then a step of the base again
+    used.load_state(state)
+    used.step()
+    after = used.state()
+    mine.train_views(used, after["params"], views=range(1, len(used.views)))
+    used.params.copy_(after["params"])
+    new.load_state(after)
+    used.step()
+    new.step()
+    assert torch.equal(used.views[0].image, new.views[0].image)
+    assert torch.equal(used.union_count, new.union_count)
+    n = int(new.union_count.item())
+    assert torch.equal(used.union_idx[:n], new.union_idx[:n])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_gradients_through_the_rasteriser(dtype):
+    """train_views' gradients are those of the network in 64 bits for the sum
+    of the views' parameter gradients, as a TrainStep with the decoded
+    parameters computes them.  Tolerance as in test_decoder_gradients, with
+    two roundings more (the attributes, the sum's storage); the atomic sums
+    over pairs add fp32 roundings, under 2^-12 in a 2-norm."""
+    fresh, offsets = _scene()
+    step, check = fresh(), fresh()
+    base = step.params.clone()
+    dec = _moving_decoder(offsets, dtype=dtype)
+    dec.sync()
+    losses = dec.train_views(step, base)
+    assert losses.shape == (len(step.views),) and not step.grads.any()
+    assert torch.equal(step.params, base + dec.forward()[:, :59].t())
+    check.params.copy_(step.params)
+    for k in range(len(check.views)):
+        check.forward_view(k)
+        check.backward_view(k)
+        assert torch.equal(check.views[k].loss.reshape(()), losses[k])
+    leaves = {k: dec.stored.get(k, v).double().requires_grad_() for k, v in dec.masters.items()}
+    d = torch.nn.functional.pad(check.grads.t().double(), (0, 64 - 59))
+    _plain(dec, leaves).backward(d)
+    tol = 10 * torch.finfo(dtype).eps / 2 + 2.0 ** -12
+    for k, v in dec.masters.items():
+        ref = leaves[k].grad
+        assert float(ref.norm()) > 0
+        err = float((v.grad.double() - ref).norm() / ref.norm())
+        assert err <= tol, (k, err, tol)
