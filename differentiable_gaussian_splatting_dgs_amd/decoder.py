@@ -31,9 +31,9 @@ class AttributeDecoder:
     """Features of n Gaussians, the network, and its gradients.
 
     ``masters``: name -> float32 tensor (features, norm, layers, heads), with
-    ``.grad`` filled by ``backward``: hand ``parameters()`` to any
-    torch.optim optimiser, then call ``sync()`` so that the storage copies
-    the kernels read follow."""
+    ``.grad`` filled (not added to) by ``backward``: hand ``parameters()`` to
+    any torch.optim optimiser, then call ``sync()`` so that the storage
+    copies the kernels read follow."""
 
     def __init__(self, offsets, width=64, hidden=256, dtype=torch.bfloat16, device="cuda", seed=0):
         self.device, self.dtype = torch.device(device), dtype
@@ -79,6 +79,9 @@ class AttributeDecoder:
         """Gradients of every master from those of forward()'s attributes
         ([n][HEAD], of the storage type; unused columns 0)."""
         m, s = self.masters, self.stored
+        for v in m.values():
+            if v.grad is None:      # as an optimiser's zero_grad() leaves it
+                v.grad = torch.empty_like(v)
         g = {k: v.grad for k, v in m.items()}
         dh, _, _ = gs_grouped_linear_bwd(self._h, s["heads"], self.offsets, dattr, dw=g["heads"], db=g["hb"])
         da, _, _ = gs_linear_bwd(self._a, s["w2"], dh, dw=g["w2"], db=g["b2"])

@@ -117,6 +117,23 @@ def test_views_after_steps_of_the_base_are_of_the_decoded_parameters():
     assert torch.equal(used.union_idx[:n], new.union_idx[:n])
 
 
+def test_gradients_cleared_by_the_optimiser():
+    """zero_grad() takes the gradients away (its default): backward makes
+    them again."""
+    from differentiable_gaussian_splatting_dgs_amd.decoder import AttributeDecoder
+    dec = AttributeDecoder([0, 300, 501], width=48, hidden=64, seed=3)
+    opt = torch.optim.Adam(dec.parameters(), lr=1e-3)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(1)
+    d = torch.randn(dec.forward().shape, generator=gen, device="cuda").to(dec.dtype)
+    dec.backward(d)
+    want = {k: v.grad.clone() for k, v in dec.masters.items()}
+    opt.zero_grad()
+    dec.backward(d)
+    for k, v in dec.masters.items():
+        assert v.grad is not None and v.grad.dtype == torch.float32 and torch.equal(v.grad, want[k]), k
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_gradients_through_the_rasteriser(dtype):
     """train_views' gradients are those of the network in 64 bits for the sum
