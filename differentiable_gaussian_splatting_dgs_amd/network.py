@@ -113,6 +113,12 @@ def _launch(call, x, stream, *args):
     return call(_raw_stream(device), x, *args)
 
 
+def _scratch(ws, like):
+    """Checks a caller's workspace: the library sees its address and size alone."""
+    if ws is not None and (ws.device != like.device or not ws.is_contiguous()):
+        raise ValueError(f"workspace has to be contiguous and on {like.device}")
+
+
 def _workspace(ws, need, device):
     if ws is None:
         return _empty(need, dtype=_U8, device=device), need
@@ -155,6 +161,7 @@ def _norm_bwd(s, x, dy, gamma, mean, rstd, dres, dx, dgamma, dbeta, workspace):
     ldr = 0 if dres is None else _matrix(dres, rows, width, x, "dres")
     if mean is None or rstd is None:
         raise ValueError("the backward pass reads the forward's mean and rstd")
+    _scratch(workspace, x)
     _on_gpu(x)
     if dx is None:
         dx, lddx = _empty(rows, width, dtype=x.dtype, device=device), width
@@ -244,6 +251,7 @@ def _bwd(s, x, w, offsets, dy, z, act, dx, dw, db, want_dx, workspace):
     if z is None and act != GS_ACT_NONE:
         raise ValueError("the activation's slope needs z, the value before it")
     ldz = 0 if z is None else _matrix(z, rows, out, x, "z")
+    _scratch(workspace, x)
     _on_gpu(x)
     if dx is not None:
         lddx = _matrix(dx, rows, inner, x, "dx")

@@ -133,3 +133,18 @@ def test_the_binding_checks_what_only_tensors_show():
         gs.gs_linear_bwd(x, torch.zeros(3, 8), torch.zeros(4, 3), None, gs.GS_ACT_RELU)
     with pytest.raises(ValueError, match="dy"):
         gs.gs_linear_bwd(x, torch.zeros(3, 8), torch.zeros(4, 5))
+
+
+@pytest.mark.parametrize("workspace", [torch.empty(1 << 16, dtype=torch.uint8, device="meta"),
+                                       torch.zeros(1 << 16, 2, dtype=torch.uint8)[:, 0],
+                                       torch.zeros(64, 64).t()], ids=["device", "strided", "transposed"])
+def test_the_binding_checks_workspaces(workspace):
+    """On another device than x, or with gaps: refused before anything else
+    sees its address."""
+    x, dy, w, v = torch.zeros(4, 8), torch.zeros(4, 3), torch.zeros(3, 8), torch.ones(4)
+    offsets = torch.zeros(3, dtype=torch.int64)
+    for call in (lambda: gs.gs_layer_norm_bwd(x, x, None, v, v, workspace=workspace),
+                 lambda: gs.gs_linear_bwd(x, w, dy, workspace=workspace),
+                 lambda: gs.gs_grouped_linear_bwd(x, torch.zeros(2, 3, 8), offsets, dy, workspace=workspace)):
+        with pytest.raises(ValueError, match="workspace"):
+            call()
