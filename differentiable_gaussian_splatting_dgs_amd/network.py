@@ -105,6 +105,8 @@ def _launch(call, x, stream, *args):
     if device < 0:
         return call(0, x, *args)      # the checks of the other arguments, then _on_gpu's refusal
     if stream is not None:
+        if stream.device != x.device:
+            raise ValueError(f"stream is on {stream.device}, x on {x.device}")
         with torch.cuda.stream(stream):
             return call(stream.cuda_stream, x, *args)
     if device != _current_device():

@@ -148,3 +148,16 @@ def test_the_binding_checks_workspaces(workspace):
                  lambda: gs.gs_grouped_linear_bwd(x, torch.zeros(2, 3, 8), offsets, dy, workspace=workspace)):
         with pytest.raises(ValueError, match="workspace"):
             call()
+
+
+def test_the_binding_checks_streams():
+    """A stream of another device than x: refused, nothing is called."""
+    from types import SimpleNamespace
+
+    from differentiable_gaussian_splatting_dgs_amd import network
+    x = SimpleNamespace(device=torch.device("cuda", 0), get_device=lambda: 0)
+    stream = SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0)
+    called = []
+    with pytest.raises(ValueError, match="stream"):
+        network._launch(lambda *a: called.append(a), x, stream)
+    assert not called
