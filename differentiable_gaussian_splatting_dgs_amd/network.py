@@ -23,7 +23,9 @@ _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _F32, _I64, _U8 = torch.float32, torch.int64, torch.uint8
 _empty = torch.empty
 _byref, _size_t = C.byref, C.c_size_t
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# the stream's handle without a Stream object, where this torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda device: torch.cuda.current_stream(device).cuda_stream)
 _current_device = torch.cuda.current_device
 
 

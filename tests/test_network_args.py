@@ -161,3 +161,17 @@ def test_the_binding_checks_streams():
     with pytest.raises(ValueError, match="stream"):
         network._launch(lambda *a: called.append(a), x, stream)
     assert not called
+
+
+def test_the_package_imports_without_torch_internals():
+    """A torch without CUDA's internal functions (a build for the CPU) imports
+    the package."""
+    import subprocess
+    import sys
+    code = ("import torch\n"
+            "del torch._C._cuda_getCurrentRawStream\n"
+            "import differentiable_gaussian_splatting_dgs_amd as gs\n"
+            "assert callable(gs.gs_linear_fwd)\n")
+    root = __file__.rsplit("/", 2)[0]
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
