@@ -37,8 +37,11 @@ class AttributeDecoder:
 
     def __init__(self, offsets, width=64, hidden=256, dtype=torch.bfloat16, device="cuda", seed=0):
         self.device, self.dtype = torch.device(device), dtype
-        self.offsets = torch.as_tensor(offsets, dtype=torch.int64).to(self.device).contiguous()
-        blocks, n = self.offsets.numel() - 1, int(self.offsets[-1].item())
+        bounds = torch.as_tensor(offsets, dtype=torch.int64).cpu()
+        if bounds.dim() != 1 or bounds.numel() < 2 or bounds[0] != 0 or (bounds[1:] < bounds[:-1]).any():
+            raise ValueError(f"offsets {bounds.tolist()}: (blocks + 1,) bounds from 0 on, ascending, expected")
+        self.offsets = bounds.to(self.device).contiguous()
+        blocks, n = bounds.numel() - 1, int(bounds[-1])
         gen = torch.Generator(device="cpu")
         gen.manual_seed(seed)
 
