@@ -96,9 +96,11 @@ class AttributeDecoder:
 
     def train_views(self, step, base, views=None):
         """One training pass through the rasteriser of a ``TrainStep``: decode
-        its parameters (base [59][n] + attributes), render and back-propagate
-        the views, and leave the gradients in the masters.  Returns the
-        views' losses (device tensor)."""
+        its parameters (``base`` [59][n], not the step's own, + attributes),
+        render and back-propagate the views, and leave the gradients in the
+        masters.  Returns the views' losses (device tensor)."""
+        if base.untyped_storage().data_ptr() == step.params.untyped_storage().data_ptr():
+            raise ValueError("base is the step's own parameters, which this pass overwrites: pass a copy")
         attr = self.forward()
         step.drop_next_view()       # its parameters change here
         step.params.copy_(base)

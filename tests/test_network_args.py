@@ -190,3 +190,16 @@ def test_the_decoder_takes_blocks_that_cover_the_rows():
     from differentiable_gaussian_splatting_dgs_amd.decoder import AttributeDecoder
     dec = AttributeDecoder(torch.tensor([0, 3, 3, 9]), width=8, hidden=8, device="cpu")
     assert dec.masters["features"].shape == (9, 8) and dec.offsets.dtype == torch.int64
+
+
+def test_the_decoder_refuses_the_steps_parameters_as_base():
+    """train_views writes base + attributes into the step's parameters: with
+    those as the base, every pass would add to the last."""
+    from types import SimpleNamespace
+
+    from differentiable_gaussian_splatting_dgs_amd.decoder import AttributeDecoder
+    dec = AttributeDecoder([0, 4], width=8, hidden=8, device="cpu")
+    step = SimpleNamespace(params=torch.zeros(59, 4))
+    for base in (step.params, step.params[:, :]):
+        with pytest.raises(ValueError, match="base"):
+            dec.train_views(step, base)
