@@ -245,7 +245,7 @@ def gs_linear_workspace_size(rows, inner, out, num_groups, type, act) -> int:
     return b.value
 
 
-def _bwd(s, x, w, offsets, dy, z, act, dx, dw, db, want_dx, workspace):
+def _bwd(s, x, w, offsets, dy, z, act, dx, dw, db, want_dx, workspace, want_dw):
     t = _type(x)
     rows, inner = x.shape
     ldx, device = _matrix(x, rows, inner, x, "x"), x.device
@@ -263,8 +263,10 @@ def _bwd(s, x, w, offsets, dy, z, act, dx, dw, db, want_dx, workspace):
         dx, lddx = _empty(rows, inner, dtype=x.dtype, device=device), inner
     else:
         lddx = 0
+    dw_type = t
     if dw is None:
-        dw, dw_type = _empty(w.shape, dtype=w.dtype, device=device), t
+        if want_dw:
+            dw = _empty(w.shape, dtype=w.dtype, device=device)
     else:
         dw_type = 2 if dw.dtype == _F32 else t
         if (dw.shape != w.shape or dw.dtype not in (w.dtype, _F32) or not dw.is_contiguous()
@@ -272,11 +274,11 @@ def _bwd(s, x, w, offsets, dy, z, act, dx, dw, db, want_dx, workspace):
             raise ValueError(f"dw is {dw.dtype} {tuple(dw.shape)}: contiguous {w.dtype} or torch.float32 "
                              f"{tuple(w.shape)} on {device} expected")
     bshape = (groups, out) if groups else (out,)
-    if db is None:
+    if db is None and want_dw:
         db = _empty(bshape, dtype=_F32, device=device)
     ws, nbytes = _workspace(workspace, gs_linear_workspace_size(rows, inner, out, groups, t, act), device)
     head = (x.data_ptr(), ldx, w.data_ptr(), ldw)
-    tail = (_optional(z), ldz, dy.data_ptr(), lddy, rows, inner, out, t, act, _optional(dx), lddx, dw.data_ptr(),
+    tail = (_optional(z), ldz, dy.data_ptr(), lddy, rows, inner, out, t, act, _optional(dx), lddx, _optional(dw),
             dw_type, _vector(db, bshape, x, "db"), ws.data_ptr(), nbytes, s)
     if groups:
         st = lib().gs_grouped_linear_bwd(*head, offsets.data_ptr(), groups, *tail)
@@ -288,15 +290,16 @@ def _bwd(s, x, w, offsets, dy, z, act, dx, dw, db, want_dx, workspace):
 
 
 def gs_linear_bwd(x, w, dy, z=None, act=GS_ACT_NONE, dx=None, dw=None, db=None, want_dx=True, workspace=None,
-                  stream=None):
+                  stream=None, want_dw=True):
     """(dx, dw, db) of gs_linear_fwd for the gradient ``dy`` of y (the
     residual's gradient is dy itself).  ``dw`` is of w's type, or float32
-    where such a tensor is passed in; ``want_dx`` false leaves dx out."""
-    return _launch(_bwd, x, stream, w, None, dy, z, act, dx, dw, db, want_dx, workspace)
+    where such a tensor is passed in; ``want_dx`` false leaves dx out,
+    ``want_dw`` false (frozen weights) dw and db, unless they are passed in."""
+    return _launch(_bwd, x, stream, w, None, dy, z, act, dx, dw, db, want_dx, workspace, want_dw)
 
 
 def gs_grouped_linear_bwd(x, w, offsets, dy, z=None, act=GS_ACT_NONE, dx=None, dw=None, db=None, want_dx=True,
-                          workspace=None, stream=None):
+                          workspace=None, stream=None, want_dw=True):
     """(dx, dw, db) of gs_grouped_linear_fwd; dw[e] and db[e] are 0 for an
     empty group, rows in no group have no dx."""
-    return _launch(_bwd, x, stream, w, offsets, dy, z, act, dx, dw, db, want_dx, workspace)
+    return _launch(_bwd, x, stream, w, offsets, dy, z, act, dx, dw, db, want_dx, workspace, want_dw)

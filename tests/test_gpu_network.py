@@ -718,3 +718,23 @@ def test_layer_norm_backward_reads_what_it_wrote(gs, name, rows, width):
         results.append(gs.gs_layer_norm_bwd(x, dy, None, mean, rstd, workspace=ws))
     for zeros, nans in zip(*results):
         assert nans.isfinite().all() and torch.equal(zeros, nans)
+
+
+@pytest.mark.parametrize("rows", [37, 3000, 40000])
+@pytest.mark.parametrize("act", ["none", "gelu"])
+def test_linear_backward_of_frozen_weights(gs, rows, act):
+    """want_dw false: dx alone, with the bits it has beside dw and db; what is
+    passed in is written all the same."""
+    gen, t = _gen(rows), torch.bfloat16
+    x, w = _rand(gen, rows, 72, dtype=t), _rand(gen, 40, 72, scale=0.2, dtype=t)
+    dy, z = _rand(gen, rows, 40, dtype=t), _rand(gen, rows, 40, dtype=t)
+    off = torch.tensor([0, rows // 3, rows], dtype=torch.int64, device="cuda")
+    w2 = torch.stack([w, -w])
+    dx, dw, db = gs.gs_linear_bwd(x, w, dy, z, _act_id(gs, act))
+    only = gs.gs_linear_bwd(x, w, dy, z, _act_id(gs, act), want_dw=False)
+    assert only[1] is None and only[2] is None and torch.equal(only[0], dx)
+    mine = gs.gs_linear_bwd(x, w, dy, z, _act_id(gs, act), dw=torch.empty_like(dw), want_dw=False)
+    assert mine[2] is None and torch.equal(mine[1], dw)
+    gx, gw, gb = gs.gs_grouped_linear_bwd(x, w2, off, dy, z, _act_id(gs, act))
+    only = gs.gs_grouped_linear_bwd(x, w2, off, dy, z, _act_id(gs, act), want_dw=False)
+    assert only[1] is None and only[2] is None and torch.equal(only[0], gx)
