@@ -1145,8 +1145,8 @@ __global__ __launch_bounds__(512, 2) void k_bwd_rows(FusedArgs p) {
 
   const int64_t total = total_slots(p.offsets, p.groups, p.rows, BM);
   const int shares = shares_in_use(total, p.shares);
-  if (int(blockIdx.x) >= shares) return;
-  const int share = xcd_tile(blockIdx.x, shares);
+  const int share = xcd_tile(blockIdx.x, gridDim.x);
+  if (share >= shares) return;
   const int t0 = int(total * share / shares), t1 = int(total * (share + 1) / shares);
 
   // a thread's chunks of a tile: 8 of a row and step, row by row, step by step
