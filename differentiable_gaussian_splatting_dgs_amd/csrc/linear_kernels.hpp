@@ -679,7 +679,7 @@ __device__ __forceinline__ void product_block(const ProductArgs& p, int id, int 
 }
 
 template <typename T, Mode MODE, int BM, int BN, int WM, int WN, bool DIRECT, int KW>
-__global__ __launch_bounds__(64 * WM * WN * KW, KW == 4 ? 4 : BM == 256 && WM * WN == 4 ? 1 : 2) void k_product(ProductArgs p) {
+__global__ __launch_bounds__(64 * WM * WN * KW, KW == 4 ? 4 : 2) void k_product(ProductArgs p) {
   extern __shared__ __align__(16) char lds[];
   product_block<T, MODE, BM, BN, WM, WN, DIRECT, KW>(p, blockIdx.x, gridDim.x, lds);
 }
@@ -921,10 +921,14 @@ __global__ __launch_bounds__(512, 4) void k_rows(ProductArgs p, int shares) {
 
 // --- dz and db ----------------------------------------------------------------------------------
 
-// dz = dy act'(z) rounded into the storage type (what the matrix
-// instructions take; db is summed from the unrounded values, in fp32; no dz:
-// the sums of dy alone), and one partial row of db per stretch of rows, part[slot][out], or without
-// `part` db itself, one stretch a group.
+// dz = dy act'(z) rounded into the storage type, and one partial row of db per
+// stretch of rows, part[slot][out], or without `part` db itself, one stretch a
+// group.  The rounding is a choice: one matrix instruction takes 16-bit values,
+// and a dz of a high and a low part would double both products' instructions
+// and LDS reads and the bytes of dz; dx and dw then have 1.4 times the error of a 32-bit
+// dz (1,000,000 x 256 -> 256 bf16: 0.0024 of their norm against 0.0017), as a
+// program of 16-bit tensors has.  db is summed from the unrounded values, in
+// fp32.  No dz: the sums of dy alone.
 template <typename T>
 __global__ __launch_bounds__(256) void k_act_grad(const T* __restrict__ dy, int64_t lddy, const T* __restrict__ z,
                                                   int64_t ldz, T* __restrict__ dz, int64_t lddz,
@@ -1105,8 +1109,8 @@ __host__ __device__ inline int32_t share_of(int64_t t, int64_t total, int32_t sh
 // dx (16 KO registers) and an eighth of dw's sums (up to 128); the workgroup
 // walks its share of the row tiles (128 / max(KO, KI) rows; dy, z, x up to 16 KB
 // each, two tiles in flight with counted waits):
-//   slope   dz = dy act'(z) in place, rounded for the matrix instructions, db
-//           summed unrounded
+//   slope   dz = dy act'(z) in place, rounded into the storage type (as in
+//           k_act_grad), db summed unrounded
 //   product dx = dz w; dw += dz^T x, its operands read transposed
 // A share that ends inside a group, or a group inside a share, leaves one
 // plane of partial sums, number share + group.  What it has to move is 3 or 4
@@ -1476,11 +1480,19 @@ int wave_sets(int64_t tiles64, int64_t k) {
 }
 
 // k_rows: a short k, whole chunks everywhere, and rows enough that every
-// workgroup walks several tiles for each time it fetches its weights: by
-// measurement (bf16, gelu, this kernel against 128 x 128 tiles) 64 -> 256
-// at 65,536 rows 17 us against 19, 128 -> 128 at 65,536 rows 15 against 12 and
-// at 262,144 rows 32 against 39, 256 -> 256 at 65,536 rows 26 against 25 and at
-// 262,144 rows 71 against 86.
+// workgroup walks several tiles for each time it fetches its weights.  Forward,
+// bf16, gelu, this kernel against tiles, us:
+//   rows      64 -> 64     64 -> 256    128 -> 128   256 -> 256
+//   32,768    9.0   9.0    11.8  11.6   10.5  10.0   17.7  16.1
+//   65,536    9.3   8.7    16.2  18.0   14.2  12.5   26.9  28.4
+//   131,072   12.3  10.6   26.4  29.0   21.9  22.9   41.7  49.3
+//   262,144   19.8  17.7   42.8  51.1   32.2  39.4   74.9  94.2
+// and the same on 64 ragged groups:
+//   65,536    14.1  9.5    26.7  22.4   18.6  20.4   37.4  37.3
+//   262,144   22.9  22.1   48.8  59.8   37.7  49.5   83.3  117.6
+// So the bound by the k steps is near the crossing from 256 columns on; the
+// tiles keep up to 2 us at 128 -> 128 and at 64 -> 64, and up to 5 us with many
+// groups near the bound.
 template <typename T, Mode MODE>
 bool rows_ok(const ProductArgs& p) {
   const auto whole = [](const void* q, int64_t ld) {
@@ -1580,6 +1592,18 @@ BwdPlan bwd_plan(int64_t rows, int32_t in, int32_t out, int32_t groups, int act)
   const auto steps = [](int32_t n) { return n <= 64 ? 1 : n <= 128 ? 2 : n <= 256 ? 4 : 8; };
   s.ko = steps(out);
   s.ki = steps(in);
+  // One pass against slope, dx, dw and joins apart, bf16, gelu, us (without
+  // groups; on 64; on 256):
+  //   rows      64 -> 64     128 -> 128   256 -> 256
+  //   16,384    18.5  21.1   24.6  25.6   41.3  38.6
+  //   32,768    17.8  32.1   26.2  42.0   50.0  63.1
+  //             31.1  29.6   45.0  41.1   90.7  58.8   on 64
+  //             47.0  35.2   73.3  48.3   161   90     on 256
+  //   131,072   29.5  59.0   46.7  88.9   112   159
+  //             44.0  56.0   67.5  99.4   155   212    on 64
+  //             62.2  73.5   98.4  125    253   179    on 256
+  // Every group adds a plane of sums, written and read again, which the bound
+  // does not count: with many groups for the rows the parts would be faster.
   s.fused = sizeof(T) == 2 && s.ko <= 4 && s.ki <= 4 && in % 8 == 0 && out % 8 == 0 && rows >= 32768;
   s.shares = 256;   // a workgroup a CU
   // (to 1024 tiles of 128 x 128 where both sides are narrow: 16384 rows 256 -> 256 bf16
@@ -1622,6 +1646,8 @@ BwdPlan bwd_plan(int64_t rows, int32_t in, int32_t out, int32_t groups, int act)
   const int64_t across = ceil_div(out, 64 * kChunk<T>);
   s.unit_b = int32_t(std::max<int64_t>(16, ceil_div(ceil_div(rows * across, 2048), 16) * 16));
   s.part_b = rows > s.unit_b;
+  // (a fused pass writes no dz, but whether it runs is up to the alignment of
+  // the call's operands)
   s.dz = act == kActNone ? 0 : align_up(size_t(rows) * dz_ld(out, kChunk<T>) * sizeof(T), 256);
   s.db = !s.part_b ? 0 : align_up(size_t(max_slots(rows, groups, s.unit_b)) * out * 4, 256);
   s.dw = !s.part_w ? 0 : align_up(size_t(max_slots(rows, groups, s.unit_w)) * s.plane * 4, 256);

@@ -58,9 +58,11 @@ __device__ __forceinline__ void store_chunk_n(T* __restrict__ p, const Chunk<T>&
 
 // --- activations ----------------------------------------------------------------
 
-// e^x and 1/x for 16-bit storage: the native exp2 and reciprocal (relative
-// error below 2^-20, under the storage's half step); fp32 storage takes the
-// library function and the IEEE division.
+// e^x and 1/x for 16-bit storage: the native exp2 and reciprocal.  The
+// rounded argument of exp2 makes e^x off by about |x| 2^-23 of itself, beside
+// the instruction's own 2^-22 (below 2^-16 up to |x| = 88, where fp32 ends;
+// the half step is 2^-8 of bf16, 2^-11 of fp16); 1/x by 2^-22.  fp32 storage
+// takes the library function and the IEEE division.
 template <typename T>
 __device__ __forceinline__ float exp_t(float x) {
   if constexpr (sizeof(T) == 4)

@@ -98,7 +98,8 @@ class AttributeDecoder:
         """One training pass through the rasteriser of a ``TrainStep``: decode
         its parameters (``base`` [59][n], not the step's own, + attributes),
         render and back-propagate the views, and leave the gradients in the
-        masters.  Returns the views' losses (device tensor)."""
+        masters.  Returns the views' losses (device tensor).  In float16 a
+        gradient under 6e-8 is 0: raise the step's loss weights for it."""
         if base.untyped_storage().data_ptr() == step.params.untyped_storage().data_ptr():
             raise ValueError("base is the step's own parameters, which this pass overwrites: pass a copy")
         attr = self.forward()

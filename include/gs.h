@@ -116,7 +116,11 @@ typedef enum gs_op {
 } gs_op;
 
 /* Storage types of the network operators (gs_layer_norm_*, gs_linear_*,
- * gs_grouped_linear_*); every sum, statistic and epilogue is fp32. */
+ * gs_grouped_linear_*); every sum, statistic and epilogue is fp32.  The one
+ * value between them that is rounded to the type is dz, the gradient behind an
+ * activation: once, before the products that make dx and dw of it (db is summed
+ * from the unrounded values).  Before their rounding the activations of 16-bit
+ * types are off by at most 2^-19 of the argument, their slopes by 2^-18. */
 typedef enum gs_type {
   GS_TYPE_BF16 = 0,
   GS_TYPE_F16 = 1,
