@@ -5,7 +5,7 @@
 // square root, no contraction: the library is built with
 // -ffp-contract=off), so every discrete decision -- culling, radius, tile
 // rectangle, alpha skip, transmittance stop, colour clamp -- is taken on
-// exactly the same fp32 values as the checker's.
+// exactly the same fp32 values as the oracle's.
 #pragma once
 
 #include <hip/hip_runtime.h>

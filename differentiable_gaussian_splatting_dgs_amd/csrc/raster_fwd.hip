@@ -6,7 +6,7 @@
 // Waves own 8x8 quarters of a tile (see raster_common.hpp).  Per pixel the
 // canonical fp32 rule decides skip / composite / stop, evaluated without
 // branches (selects), so the image and every decision are bit-identical to
-// the checker's.  A wave ends at the first chunk boundary after all 64 of
+// the oracle's.  A wave ends at the first chunk boundary after all 64 of
 // its pixels have stopped.
 #include <algorithm>
 
