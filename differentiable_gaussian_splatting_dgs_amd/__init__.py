@@ -30,6 +30,7 @@ GS_TYPE_BF16, GS_TYPE_F16, GS_TYPE_F32 = 0, 1, 2
 GS_ACT_NONE, GS_ACT_RELU, GS_ACT_SILU, GS_ACT_GELU = 0, 1, 2, 3
 GS_MAX_NET_DIM = 65536
 GS_MAX_NET_GROUPS = 1024
+GS_MAX_SORT_GROUPS = 1 << 30
 GS_PROJ_WORDS = 16
 GS_GRAD2D_WORDS = 12
 GS_MAX_FUSED_VIEWS = 16
@@ -48,7 +49,9 @@ EXPORTS = ["gs_status_string", "gs_last_error", "gs_version", "gs_workspace_size
            "gs_sparse_adam", "gs_project_bwd_adam", "gs_visible_list", "gs_view_overlap", "gs_view_priority",
            "gs_tile_partition", "gs_pack_records", "gs_unpack_grads", "gs_densify_stats", "gs_densify",
            "gs_sparse_adam_noalloc", "gs_preprocess_views", "gs_layer_norm_fwd", "gs_layer_norm_bwd", "gs_linear_fwd",
-           "gs_linear_workspace_size", "gs_linear_bwd", "gs_grouped_linear_fwd", "gs_grouped_linear_bwd"]
+           "gs_linear_workspace_size", "gs_linear_bwd", "gs_grouped_linear_fwd", "gs_grouped_linear_bwd",
+           "gs_group_sort", "gs_group_sort_workspace_size", "gs_embedding_fwd", "gs_embedding_bwd",
+           "gs_embedding_workspace_size"]
 GS_NOALLOC_SCRATCH_BYTES = 256 * 1024
 GS_NOALLOC_MAX_N = (GS_NOALLOC_SCRATCH_BYTES // 4 - 1) * 4096
 
@@ -124,6 +127,12 @@ def lib():
                                         _i64, _P, _i64, _P]
     L.gs_grouped_linear_bwd.argtypes = [_P, _i64, _P, _i64, _P, _i32, _P, _i64, _P, _i64, _i64, _i32, _i32, _i32,
                                         _i32, _P, _i64, _P, _i32, _P, _P, _sz, _P]
+    L.gs_group_sort.argtypes = [_P, _i32, _i64, _i64, _P, _P, _P, _P, _sz, _P]
+    L.gs_group_sort_workspace_size.argtypes = [_i64, _i64, C.POINTER(_sz)]
+    L.gs_embedding_fwd.argtypes = [_P, _i64, _i64, _P, _i32, _i64, _i32, _f32, _i32, _P, _i64, _P]
+    L.gs_embedding_bwd.argtypes = [_P, _i64, _P, _i32, _P, _P, _i64, _i64, _i32, _f32, _i32, _P, _i64, _i32, _P, _sz,
+                                   _P]
+    L.gs_embedding_workspace_size.argtypes = [_i64, _i64, _i32, _i32, C.POINTER(_sz)]
     for name in EXPORTS[3:]:
         getattr(L, name).restype = C.c_int
     _handle = L
@@ -1026,5 +1035,6 @@ def from_workload(work, device="cuda", **kw) -> TrainStep:
                      work.beta2, work.eps, device=device, **kw)
 
 
-from .network import (gs_grouped_linear_bwd, gs_grouped_linear_fwd, gs_layer_norm_bwd, gs_layer_norm_fwd,  # noqa: E402
-                      gs_linear_bwd, gs_linear_fwd, gs_linear_workspace_size)
+from .network import (gs_embedding_bwd, gs_embedding_fwd, gs_embedding_workspace_size,  # noqa: E402
+                      gs_group_sort, gs_group_sort_workspace_size, gs_grouped_linear_bwd, gs_grouped_linear_fwd,
+                      gs_layer_norm_bwd, gs_layer_norm_fwd, gs_linear_bwd, gs_linear_fwd, gs_linear_workspace_size)

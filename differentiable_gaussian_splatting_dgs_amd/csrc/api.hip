@@ -24,6 +24,7 @@ static_assert(GS_ACT_NONE == gs::kActNone && GS_ACT_RELU == gs::kActRelu && GS_A
                   GS_ACT_GELU == gs::kActGelu,
               "activations");
 static_assert(GS_MAX_NET_DIM == gs::kMaxNetDim && GS_MAX_NET_GROUPS == gs::kMaxNetGroups, "network limits");
+static_assert(GS_MAX_SORT_GROUPS == gs::kMaxSortGroups, "sort limit");
 
 namespace {
 
@@ -228,6 +229,26 @@ gs_status scratch_address(void** out) {
     g_scratch_ptr[dev] = p;
   }
   *out = g_scratch_ptr[dev];
+  return GS_OK;
+}
+
+gs_status check_ids(const void* ids, int32_t id_bytes, int64_t n) {
+  REQUIRE(id_bytes == 4 || id_bytes == 8, "id_bytes = %d: 4 or 8 expected", int(id_bytes));
+  REQUIRE(n == 0 || (ids != nullptr && aligned(ids, size_t(id_bytes))), "ids NULL or not aligned to its elements");
+  return GS_OK;
+}
+
+gs_status check_sort_sizes(int64_t n, int64_t num_groups) {
+  REQUIRE(n >= 0 && n < (int64_t(1) << 31), "n = %lld out of range", (long long)n);
+  REQUIRE(num_groups >= 1 && num_groups <= GS_MAX_SORT_GROUPS, "num_groups = %lld out of range",
+          (long long)num_groups);
+  return GS_OK;
+}
+
+gs_status check_embedding(int64_t rows, int64_t num_rows, int32_t width, int32_t type) {
+  CHECK(check_net_sizes(rows, type));
+  REQUIRE(num_rows >= 1 && num_rows <= GS_MAX_SORT_GROUPS, "num_rows = %lld out of range", (long long)num_rows);
+  REQUIRE(width >= 1 && width <= GS_MAX_NET_DIM, "width = %d out of range", int(width));
   return GS_OK;
 }
 
@@ -922,6 +943,96 @@ gs_status gs_grouped_linear_bwd(const void* x, int64_t ldx, const void* w, int64
   a.dw = dw;
   a.db = db;
   return linear_bwd(a, rows, type, dw_type, workspace, workspace_bytes, stream, "gs_grouped_linear_bwd");
+}
+
+gs_status gs_group_sort_workspace_size(int64_t n, int64_t num_groups, size_t* bytes) {
+  REQUIRE(bytes != nullptr, "bytes is NULL");
+  *bytes = 0;
+  CHECK(check_sort_sizes(n, num_groups));
+  *bytes = std::max<size_t>(256, gs::group_sort_ws_bytes(n, num_groups));
+  return ok();
+}
+
+gs_status gs_group_sort(const void* ids, int32_t id_bytes, int64_t n, int64_t num_groups, int64_t* offsets,
+                        int32_t* order, int32_t* place, void* workspace, size_t workspace_bytes, void* stream) {
+  CHECK(check_sort_sizes(n, num_groups));
+  CHECK(check_ids(ids, id_bytes, n));
+  REQUIRE(offsets != nullptr && aligned(offsets, 8), "offsets NULL or not 8-byte aligned");
+  CHECK(check_vector("order", order));
+  CHECK(check_vector("place", place));
+  REQUIRE(workspace != nullptr && aligned(workspace, 256), "workspace NULL or not 256-byte aligned");
+  const size_t need = gs::group_sort_ws_bytes(n, num_groups);
+  REQUIRE(workspace_bytes >= need, "workspace_bytes = %zu < %zu needed", workspace_bytes, need);
+  const gs::SortArgs a{ids, id_bytes, n, num_groups, offsets, order, place};
+  return hip_status(gs::launch_group_sort(a, workspace, static_cast<hipStream_t>(stream)), "gs_group_sort");
+}
+
+gs_status gs_embedding_fwd(const void* table, int64_t ldt, int64_t num_rows, const void* ids, int32_t id_bytes,
+                           int64_t rows, int32_t width, float scale, int32_t type, void* y, int64_t ldy,
+                           void* stream) {
+  CHECK(check_embedding(rows, num_rows, width, type));
+  REQUIRE(std::isfinite(scale), "scale not finite");
+  CHECK(check_ids(ids, id_bytes, rows));
+  if (rows == 0) return ok();
+  const size_t elem = gs::type_bytes(type);
+  CHECK(check_matrix("table", table, ldt, width, elem));
+  CHECK(check_matrix("y", y, ldy, width, elem));
+  gs::EmbedArgs a{};
+  a.table = table;
+  a.ldt = ldt;
+  a.num_rows = num_rows;
+  a.ids = ids;
+  a.id_bytes = id_bytes;
+  a.rows = rows;
+  a.width = width;
+  a.scale = scale;
+  a.y = y;
+  a.ldy = ldy;
+  return hip_status(gs::launch_embedding_fwd(type, a, static_cast<hipStream_t>(stream)), "gs_embedding_fwd");
+}
+
+gs_status gs_embedding_workspace_size(int64_t rows, int64_t num_rows, int32_t width, int32_t type, size_t* bytes) {
+  REQUIRE(bytes != nullptr, "bytes is NULL");
+  *bytes = 0;
+  CHECK(check_embedding(rows, num_rows, width, type));
+  *bytes = std::max<size_t>(256, gs::embedding_bwd_ws_bytes(type, rows, num_rows, width));
+  return ok();
+}
+
+gs_status gs_embedding_bwd(const void* dy, int64_t lddy, const void* ids, int32_t id_bytes, const int64_t* offsets,
+                           const int32_t* order, int64_t rows, int64_t num_rows, int32_t width, float scale,
+                           int32_t type, void* dtable, int64_t lddt, int32_t dtable_type, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  CHECK(check_embedding(rows, num_rows, width, type));
+  REQUIRE(std::isfinite(scale), "scale not finite");
+  CHECK(check_ids(ids, id_bytes, rows));
+  REQUIRE(offsets != nullptr && aligned(offsets, 8), "offsets NULL or not 8-byte aligned");
+  if (rows > 0) {
+    CHECK(check_matrix("dy", dy, lddy, width, gs::type_bytes(type)));
+    REQUIRE(order != nullptr && aligned(order, 4), "order NULL or not 4-byte aligned");
+  }
+  REQUIRE(dtable_type == type || dtable_type == GS_TYPE_F32, "dtable_type = %d is neither type nor GS_TYPE_F32",
+          int(dtable_type));
+  CHECK(check_matrix("dtable", dtable, lddt, width, gs::type_bytes(dtable_type)));
+  REQUIRE(workspace != nullptr && aligned(workspace, 256), "workspace NULL or not 256-byte aligned");
+  const size_t need = gs::embedding_bwd_ws_bytes(type, rows, num_rows, width);
+  REQUIRE(workspace_bytes >= need, "workspace_bytes = %zu < %zu needed", workspace_bytes, need);
+  gs::EmbedArgs a{};
+  a.dy = dy;
+  a.lddy = lddy;
+  a.ids = ids;
+  a.id_bytes = id_bytes;
+  a.offsets = offsets;
+  a.order = order;
+  a.rows = rows;
+  a.num_rows = num_rows;
+  a.width = width;
+  a.scale = scale;
+  a.dtable = dtable;
+  a.lddt = lddt;
+  a.dtable_f32 = dtable_type == GS_TYPE_F32;
+  return hip_status(gs::launch_embedding_bwd(type, a, workspace, static_cast<hipStream_t>(stream)),
+                    "gs_embedding_bwd");
 }
 
 }  // extern "C"

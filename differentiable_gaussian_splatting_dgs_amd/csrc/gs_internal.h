@@ -217,4 +217,34 @@ size_t linear_bwd_ws_bytes(int type, int64_t rows, int32_t in, int32_t out, int3
 hipError_t launch_linear_fwd(int type, const LinearArgs& a, hipStream_t st);
 hipError_t launch_linear_bwd(int type, const LinearArgs& a, void* ws, hipStream_t st);
 
+// --- shared features and routed rows (group_sort.hip, embedding.hip) -------------
+constexpr int64_t kMaxSortGroups = int64_t(1) << 30;
+struct SortArgs {
+  const void* ids;
+  int32_t id_bytes;
+  int64_t n, groups;
+  int64_t* offsets;
+  int32_t* order;      // or NULL
+  int32_t* place;      // or NULL
+};
+size_t group_sort_ws_bytes(int64_t n, int64_t groups);
+hipError_t launch_group_sort(const SortArgs& a, void* ws, hipStream_t st);
+
+struct EmbedArgs {
+  const void* table;   // forward
+  const void* dy;      // backward, as are offsets, order, dtable
+  const void* ids;
+  const int64_t* offsets;
+  const int32_t* order;
+  void* y;
+  void* dtable;
+  int64_t ldt, ldy, lddy, lddt, rows, num_rows;
+  int32_t width, id_bytes;
+  float scale;
+  int32_t dtable_f32;  // dtable is fp32 whatever the storage type
+};
+size_t embedding_bwd_ws_bytes(int type, int64_t rows, int64_t num_rows, int32_t width);
+hipError_t launch_embedding_fwd(int type, const EmbedArgs& a, hipStream_t st);
+hipError_t launch_embedding_bwd(int type, const EmbedArgs& a, void* ws, hipStream_t st);
+
 }  // namespace gs

@@ -1,6 +1,7 @@
 """The network operators of libgs: layer norm, the linear layer with bias,
-activation and residual in its epilogue, and the linear layer whose weights
-go by ragged group, each forward and backward.
+activation and residual in its epilogue, the linear layer whose weights
+go by ragged group, rows looked up in a shared table, each forward and
+backward, and the sort by group that ragged groups are made by.
 
 They carry the names of the C entry points (``include/gs.h``).  Matrices are
 torch tensors [rows][width] of bfloat16, float16 or float32 whose last
@@ -20,7 +21,8 @@ import torch
 from . import GS_ACT_NONE, GS_OP_LAYER_NORM_BWD, _check, gs_workspace_size, lib
 
 _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-_F32, _I64, _U8 = torch.float32, torch.int64, torch.uint8
+_F32, _I32, _I64, _U8 = torch.float32, torch.int32, torch.int64, torch.uint8
+_ID_BYTES = {_I32: 4, _I64: 8}
 _empty = torch.empty
 _byref, _size_t = C.byref, C.c_size_t
 # the stream's handle without a Stream object, where this torch has it
@@ -95,9 +97,9 @@ def _optional(t):
     return None if t is None else t.data_ptr()
 
 
-def _on_gpu(x):
+def _on_gpu(x, name="x"):
     if not x.is_cuda:
-        raise ValueError(f"x is on {x.device}: the kernels need a GPU tensor")
+        raise ValueError(f"{name} is on {x.device}: the kernels need a GPU tensor")
 
 
 def _launch(call, x, stream, *args):
@@ -303,3 +305,133 @@ def gs_grouped_linear_bwd(x, w, offsets, dy, z=None, act=GS_ACT_NONE, dx=None, d
     """(dx, dw, db) of gs_grouped_linear_fwd; dw[e] and db[e] are 0 for an
     empty group, rows in no group have no dx."""
     return _launch(_bwd, x, stream, w, offsets, dy, z, act, dx, dw, db, want_dx, workspace, want_dw)
+
+
+# --- shared features and routed rows ---------------------------------------------
+
+def _ids(ids, like_device, name="ids", dims=None):
+    """(address, bytes of an element) of a contiguous int32 or int64 tensor."""
+    if ids.dtype not in _ID_BYTES or (dims is not None and ids.dim() != dims):
+        raise ValueError(f"{name} is {ids.dtype} with {ids.dim()} dimensions: torch.int32 or torch.int64"
+                         f"{'' if dims is None else f' with {dims}'} expected")
+    if ids.device != like_device or not ids.is_contiguous():
+        raise ValueError(f"{name} has to be contiguous and on {like_device}")
+    return ids.data_ptr(), _ID_BYTES[ids.dtype]
+
+
+def _whole(t, dtype, shape, device, name):
+    """t, or a new tensor; [rows] and [rows][k] arrays of one element type."""
+    if t is None:
+        return _empty(shape, dtype=dtype, device=device)
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}: {dtype} {tuple(shape)} expected")
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} has to be contiguous and on {device}")
+    return t
+
+
+def gs_group_sort_workspace_size(n, num_groups) -> int:
+    b = _size_t(0)
+    _check(lib().gs_group_sort_workspace_size(n, num_groups, _byref(b)), "gs_group_sort_workspace_size")
+    return b.value
+
+
+def _group_sort(s, ids, num_groups, offsets, order, place, want_order, want_place, workspace):
+    device, n = ids.device, ids.numel()
+    at, id_bytes = _ids(ids, device)
+    _scratch(workspace, ids)
+    need = gs_group_sort_workspace_size(n, num_groups)
+    if not ids.is_cuda:
+        raise ValueError(f"ids is on {device}: the kernels need a GPU tensor")
+    offsets = _whole(offsets, _I64, (num_groups + 1,), device, "offsets")
+    if order is not None or want_order:
+        order = _whole(order, _I32, (n,), device, "order")
+    if place is not None or want_place:
+        place = _whole(place, _I32, ids.shape, device, "place")
+    ws, nbytes = _workspace(workspace, need, device)
+    st = lib().gs_group_sort(at, id_bytes, n, num_groups, offsets.data_ptr(), _optional(order), _optional(place),
+                             ws.data_ptr(), nbytes, s)
+    if st:
+        _check(st, "gs_group_sort")
+    return offsets, order, place
+
+
+def gs_group_sort(ids, num_groups, offsets=None, order=None, place=None, want_order=True, want_place=True,
+                  workspace=None, stream=None):
+    """(offsets, order, place) of a stable sort of ``ids`` (int32 or int64, any
+    shape) by group: ``offsets`` [num_groups + 1] int64 are the groups' bounds
+    (what ``gs_grouped_linear_fwd`` reads), ``order`` [n] int32 the entry at
+    each position, ``place`` (ids' shape, int32) each entry's position, -1 for
+    an id outside [0, num_groups).  None for what is not wanted."""
+    return _launch(_group_sort, ids, stream, num_groups, offsets, order, place, want_order, want_place, workspace)
+
+
+def _embed_fwd(s, table, ids, scale, y):
+    t = _type(table, "table")
+    num_rows, width = table.shape
+    ldt, device = _matrix(table, num_rows, width, table, "table"), table.device
+    at, id_bytes = _ids(ids, device)
+    rows = ids.numel()
+    _on_gpu(table, "table")
+    if y is None:
+        y, ldy = _empty(rows, width, dtype=table.dtype, device=device), width
+    else:
+        ldy = _matrix(y, rows, width, table, "y")
+    st = lib().gs_embedding_fwd(table.data_ptr(), ldt, num_rows, at, id_bytes, rows, width, scale, t, y.data_ptr(),
+                                ldy, s)
+    if st:
+        _check(st, "gs_embedding_fwd")
+    return y
+
+
+def gs_embedding_fwd(table, ids, scale=1.0, y=None, stream=None):
+    """y[i] = scale table[ids[i]] ([ids.numel()][width]; ``ids`` int32 or
+    int64); a row of zeros for an id outside the table."""
+    return _launch(_embed_fwd, table, stream, ids, scale, y)
+
+
+def gs_embedding_workspace_size(rows, num_rows, width, type) -> int:
+    b = _size_t(0)
+    _check(lib().gs_embedding_workspace_size(rows, num_rows, width, type, _byref(b)), "gs_embedding_workspace_size")
+    return b.value
+
+
+def _embed_bwd(s, dy, ids, offsets, order, scale, dtable, workspace):
+    t = _type(dy, "dy")
+    rows, width = dy.shape
+    lddy, device = _matrix(dy, rows, width, dy, "dy"), dy.device
+    at, id_bytes = _ids(ids, device)
+    if ids.numel() != rows:
+        raise ValueError(f"ids holds {ids.numel()} entries, dy {rows} rows")
+    num_rows = _groups(offsets, dy)
+    if order is None:
+        raise ValueError("the backward pass reads gs_group_sort's order")
+    _whole(order, _I32, (rows,), device, "order")
+    _scratch(workspace, dy)
+    need = gs_embedding_workspace_size(rows, num_rows, width, t)
+    _on_gpu(dy, "dy")
+    dt_type = t
+    if dtable is None:
+        dtable, lddt = _empty(num_rows, width, dtype=dy.dtype, device=device), width
+    else:
+        dt_type = 2 if dtable.dtype == _F32 else t
+        if dt_type == t:
+            lddt = _matrix(dtable, num_rows, width, dy, "dtable")
+        else:
+            if dtable.device != device:
+                raise ValueError(f"dtable is on {dtable.device}, dy on {device}")
+            lddt = _matrix(dtable, num_rows, width, dtable, "dtable")
+    ws, nbytes = _workspace(workspace, need, device)
+    st = lib().gs_embedding_bwd(dy.data_ptr(), lddy, at, id_bytes, offsets.data_ptr(), order.data_ptr(), rows,
+                                num_rows, width, scale, t, dtable.data_ptr(), lddt, dt_type, ws.data_ptr(), nbytes, s)
+    if st:
+        _check(st, "gs_embedding_bwd")
+    return dtable
+
+
+def gs_embedding_bwd(dy, ids, offsets, order, scale=1.0, dtable=None, workspace=None, stream=None):
+    """dtable of gs_embedding_fwd for the gradient ``dy`` of y; ``offsets`` and
+    ``order`` are those of ``gs_group_sort(ids, rows of the table)``.
+    ``dtable`` is of dy's type, or float32 where such a tensor is passed in;
+    every row is written."""
+    return _launch(_embed_bwd, dy, stream, ids, offsets, order, scale, dtable, workspace)

@@ -138,6 +138,8 @@ typedef enum gs_act {
 /* widest layer or norm, and most groups, of the network operators */
 #define GS_MAX_NET_DIM 65536
 #define GS_MAX_NET_GROUPS 1024
+/* most groups of gs_group_sort, and rows of a table */
+#define GS_MAX_SORT_GROUPS ((int64_t)1 << 30)
 
 /* Static description of a status code (never NULL). */
 const char* gs_status_string(int status);
@@ -774,6 +776,69 @@ gs_status gs_grouped_linear_bwd(const void* x, int64_t ldx, const void* w, int64
                                 int64_t rows, int32_t in, int32_t out, int32_t type, int32_t act, void* dx,
                                 int64_t lddx, void* dw, int32_t dw_type, float* db, void* workspace,
                                 size_t workspace_bytes, void* stream);
+
+/* ---- shared features and routed rows ------------------------------------------
+ * Several Gaussians may share a row of a feature table, and a Gaussian may
+ * take heads that do not go by where it is stored.  These operators feed the
+ * ones above: rows looked up in a table, rows sorted by group (whose bounds
+ * gs_grouped_linear_* reads) and brought back.  The notes on matrices,
+ * streams, workspaces and graphs of the network operators hold here too. */
+
+/* Stable sort of n group ids, as one stretch of positions for each group.
+ *   ids          device, [n] of id_bytes (4: int32, 8: int64).  An id outside
+ *                [0, num_groups) belongs to no group: its entries come after
+ *                the last group's.
+ *   offsets      device out, [num_groups + 1] int64: group e has the positions
+ *                offsets[e] .. offsets[e + 1] - 1; offsets[0] = 0
+ *   order        device out, [n] int32: the entry at each position, ascending
+ *                within a group (behind offsets[num_groups]: the entries of no
+ *                group, ascending); or NULL
+ *   place        device out, [n] int32: each entry's position, -1 for one of
+ *                no group; or NULL
+ *   workspace    device, >= gs_group_sort_workspace_size(...) bytes, 256-byte
+ *                aligned
+ * Errors: GS_ERR_INVALID_ARG for n outside [0, 2^31), num_groups outside
+ * [1, GS_MAX_SORT_GROUPS], id_bytes neither 4 nor 8, a NULL or misaligned
+ * array, a workspace that is too small. */
+gs_status gs_group_sort(const void* ids, int32_t id_bytes, int64_t n, int64_t num_groups, int64_t* offsets,
+                        int32_t* order, int32_t* place, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of gs_group_sort (host, no device work). */
+gs_status gs_group_sort_workspace_size(int64_t n, int64_t num_groups, size_t* bytes);
+
+/* Rows of a table: y[i] = scale table[ids[i]], rounded once; a row of zeros
+ * for an id outside [0, num_rows).
+ *   table        device, [num_rows][ldt]
+ *   ids          device, [rows] of id_bytes (4: int32, 8: int64)
+ *   y            device out, [rows][ldy]
+ * Errors: GS_ERR_INVALID_ARG for an unknown type, rows outside [0, 2^31),
+ * num_rows outside [1, GS_MAX_SORT_GROUPS], width outside [1,
+ * GS_MAX_NET_DIM], id_bytes neither 4 nor 8, a leading dimension below width,
+ * scale not finite, a NULL or misaligned array. */
+gs_status gs_embedding_fwd(const void* table, int64_t ldt, int64_t num_rows, const void* ids, int32_t id_bytes,
+                           int64_t rows, int32_t width, float scale, int32_t type, void* y, int64_t ldy,
+                           void* stream);
+
+/* Its backward pass: dtable[v] = scale times the sum of dy[i] over ids[i] = v,
+ * in fp32 and in an order that the sizes and ids fix; 0 for a row that no id names.
+ *   dy           device, [rows][lddy]
+ *   ids          device, as the forward pass read them
+ *   offsets, order   device, as gs_group_sort(ids, ..., num_groups = num_rows)
+ *                wrote them ([num_rows + 1], [rows]); other contents give
+ *                other sums but no access out of bounds
+ *   dtable       device out, [num_rows][lddt] of type dtable_type (`type` or
+ *                GS_TYPE_F32); every row is written
+ *   workspace    device, >= gs_embedding_workspace_size(...) bytes, 256-byte
+ *                aligned
+ * Errors: as the forward pass, a dtable_type that is neither, and a workspace
+ * that is too small. */
+gs_status gs_embedding_bwd(const void* dy, int64_t lddy, const void* ids, int32_t id_bytes, const int64_t* offsets,
+                           const int32_t* order, int64_t rows, int64_t num_rows, int32_t width, float scale,
+                           int32_t type, void* dtable, int64_t lddt, int32_t dtable_type, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of gs_embedding_bwd (host, no device work). */
+gs_status gs_embedding_workspace_size(int64_t rows, int64_t num_rows, int32_t width, int32_t type, size_t* bytes);
 
 #ifdef __cplusplus
 }

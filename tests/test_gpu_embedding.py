@@ -1,0 +1,269 @@
+"""gs_group_sort and gs_embedding_*: the order against numpy's stable sort,
+rows and gradients against their definitions in 64 bits.
+
+Tolerances: a looked-up value is one fp32 product (2^-24) and one rounding
+into storage (u); a gradient is an fp32 sum of c terms, in any order, off by
+at most (c + 4) 2^-24 of the sum of absolute values, times the scale, and one
+rounding."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+from net_helpers import EPS32, TYPES, close, gen, half_step, padding, rand, strided, tiny
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+@pytest.fixture(scope="module")
+def gs():
+    import differentiable_gaussian_splatting_dgs_amd as mod
+    return mod
+
+
+def _check_sort(gs, ids, groups, **kw):
+    offsets, order, place = gs.gs_group_sort(ids, groups, **kw)
+    flat = ids.cpu().numpy().reshape(-1).astype(np.int64)
+    key = np.where((flat < 0) | (flat >= groups), groups, flat)
+    want = np.argsort(key, kind="stable")
+    bounds = np.searchsorted(key[want], np.arange(groups + 1))
+    assert np.array_equal(offsets.cpu().numpy(), bounds)
+    if order is not None:
+        assert np.array_equal(order.cpu().numpy(), want)
+    if place is not None:
+        at = np.empty(flat.size, np.int64)
+        at[want] = np.arange(flat.size)
+        at[key == groups] = -1
+        assert place.shape == ids.shape
+        assert np.array_equal(place.cpu().numpy().reshape(-1), at)
+    return offsets, order, place
+
+
+def _ids(seed, n, groups, dtype=torch.int64, outside=0.05):
+    g = gen(seed)
+    ids = (torch.rand(n, generator=g, device="cuda").double() ** 2 * groups).long().clamp_(0, groups - 1)
+    bad = torch.rand(n, generator=g, device="cuda") < outside
+    far = torch.tensor([-1, groups, -2 ** 31, 2 ** 31 - 1], device="cuda")
+    if dtype == torch.int64:
+        far = torch.cat([far, torch.tensor([-2 ** 63, 2 ** 63 - 1, 2 ** 32, -2 ** 32 + 1], device="cuda")])
+    pick = torch.randint(far.numel(), (n,), generator=g, device="cuda")
+    return torch.where(bad, far[pick], ids).to(dtype)
+
+
+SORT_SIZES = [0, 1, 63, 64, 65, 1000, 2047, 2048, 2049, 8191, 8192, 8193, 20_000, 100_003, 300_000]
+
+
+@pytest.mark.parametrize("groups", [1, 2, 16, 255, 256, 511, 512, 1000, 1023, 1024, 5000, 50_021, 1_048_575,
+                                    1_048_576, 3_000_000])
+def test_group_sort(gs, groups):
+    for n in SORT_SIZES:
+        _check_sort(gs, _ids(n + groups, n, groups, torch.int32 if n % 2 else torch.int64), groups)
+
+
+def test_group_sort_of_millions(gs):
+    for n, groups in ((5_000_000, 700), (3_000_001, 200_000)):
+        _check_sort(gs, _ids(n, n, groups, torch.int32), groups)
+
+
+@pytest.mark.parametrize("n", [1, 5000, 9000, 200_000])
+def test_group_sort_extremes(gs, n):
+    """All of one group, none of any group, the most groups, and what is not wanted."""
+    for groups in (1, 300, 70_000):
+        one = torch.full((n,), groups - 1, dtype=torch.int64, device="cuda")
+        _check_sort(gs, one, groups)
+        _check_sort(gs, torch.full_like(one, -7), groups)
+        ids = _ids(n, n, groups)
+        offsets, order, place = _check_sort(gs, ids, groups, want_place=False)
+        assert place is None
+        offsets, order, place = _check_sort(gs, ids, groups, want_order=False)
+        assert order is None
+    _check_sort(gs, _ids(n, n, 40, torch.int32)[: n // 2 * 2].view(-1, 2) if n > 1 else _ids(n, n, 40), 40)
+
+
+def test_group_sort_workspace_of_anything(gs):
+    """What the workspace and the outputs held before does not matter."""
+    for n, groups in ((5000, 64), (30_000, 64), (5000, 9000), (30_000, 90_000)):
+        ids = _ids(3, n, groups, torch.int32)
+        ws = torch.full((gs.gs_group_sort_workspace_size(n, groups),), 255, dtype=torch.uint8, device="cuda")
+        offsets = torch.full((groups + 1,), -5, dtype=torch.int64, device="cuda")
+        order, place = (torch.full((n,), -9, dtype=torch.int32, device="cuda") for _ in range(2))
+        got = _check_sort(gs, ids, groups, offsets=offsets, order=order, place=place, workspace=ws)
+        assert got[0].data_ptr() == offsets.data_ptr() and got[1].data_ptr() == order.data_ptr()
+
+
+# --- the lookup -------------------------------------------------------------------
+
+WIDTHS = [1, 3, 7, 8, 9, 64, 100, 255, 515, 1024, 4100]
+
+
+def _lookup(table, ids, scale):
+    flat = ids.reshape(-1).long()
+    there = (flat >= 0) & (flat < table.shape[0])
+    return torch.where(there[:, None], table.double()[torch.where(there, flat, 0)] * scale, 0.0)
+
+
+@pytest.mark.parametrize("name", list(TYPES))
+@pytest.mark.parametrize("width", WIDTHS)
+def test_embedding_forward(gs, name, width):
+    t = TYPES[name]
+    for rows, table_rows in ((1, 1), (33, 5), (1001, 4096)):
+        g = gen(rows + width)
+        table = rand(g, table_rows, width, dtype=t)
+        table[0, 0] = float("inf")
+        ids = _ids(rows, rows, table_rows, torch.int32 if width % 2 else torch.int64)
+        for scale in (1.0, width ** 0.5):
+            s = float(torch.tensor(scale))      # what the call rounds it to
+            want = _lookup(table, ids, s)
+            tol = (half_step(t) + 2 * EPS32) * want.abs().nan_to_num(0, 0, 0) + tiny(t)
+            close(gs.gs_embedding_fwd(table, ids, scale), want, tol, "y")
+            y = strided(torch.full((rows, width), 5.0, dtype=t, device="cuda"), 3, 1, fill=7.0)
+            assert gs.gs_embedding_fwd(strided(table, 5, 1), ids, scale, y=y) is y
+            close(y, want, tol, "y, strided")
+            assert rows == 1 or bool((padding(y) == 7.0).all())
+
+
+def test_embedding_forward_no_rows(gs):
+    table = torch.ones(4, 8, device="cuda")
+    assert gs.gs_embedding_fwd(table, torch.empty(0, dtype=torch.int64, device="cuda")).shape == (0, 8)
+
+
+def test_embedding_past_32_bits(gs):
+    """A table of over 2^32 elements, and rows at its end."""
+    table = torch.empty(70_000, 65_536, dtype=torch.float16, device="cuda")
+    ids = torch.tensor([69_999, 32_768, 65_537, 0], device="cuda")
+    for r in ids.tolist():
+        table[r] = torch.arange(65_536, device="cuda") % 251 + r % 13
+    assert torch.equal(gs.gs_embedding_fwd(table, ids), table[ids])
+    del table
+    dy = torch.ones(3, 65_536, dtype=torch.float16, device="cuda")
+    ids = torch.tensor([69_999, 40_000, 69_999], device="cuda")
+    dtable = torch.full((70_000, 65_536), 3.0, dtype=torch.float16, device="cuda")
+    offsets, order, _ = gs.gs_group_sort(ids, 70_000, want_place=False)
+    gs.gs_embedding_bwd(dy, ids, offsets, order, dtable=dtable)
+    assert bool((dtable[69_999] == 2).all()) and bool((dtable[40_000] == 1).all())
+    for a in range(0, 70_000, 10_000):
+        part = dtable[a:a + 10_000]
+        assert int((part != 0).any(1).sum()) == (1 if a in (40_000, 60_000) else 0)
+
+
+# --- its gradient ---------------------------------------------------------------------
+
+def _check_bwd(gs, dy, ids, table_rows, scale=1.0, dtable=None, sort=None, **kw):
+    offsets, order, _ = sort or gs.gs_group_sort(ids, table_rows, want_place=False)
+    got = gs.gs_embedding_bwd(dy, ids, offsets, order, scale, dtable=dtable, **kw)
+    flat = ids.reshape(-1).long()
+    there = (flat >= 0) & (flat < table_rows)
+    at, d = flat[there], dy.double()[there]
+    want = torch.zeros(table_rows, dy.shape[1], dtype=torch.float64, device="cuda").index_add_(0, at, d)
+    size = torch.zeros_like(want).index_add_(0, at, d.abs())
+    terms = torch.bincount(at, minlength=table_rows).double()[:, None]
+    s = float(torch.tensor(scale))
+    t = got.dtype
+    close(got, want * s, (half_step(t) + EPS32) * (want * s).abs() + (terms + 4) * EPS32 * size * abs(s) + tiny(t),
+          "dtable")
+    return got
+
+
+@pytest.mark.parametrize("name", list(TYPES))
+@pytest.mark.parametrize("width", WIDTHS)
+def test_embedding_backward(gs, name, width):
+    t = TYPES[name]
+    for rows, table_rows in ((1, 1), (40, 7), (3001, 5), (2500, 3000)):
+        g = gen(rows + width)
+        dy = rand(g, rows, width, dtype=t)
+        ids = _ids(rows, rows, table_rows, torch.int64 if width % 2 else torch.int32)
+        _check_bwd(gs, dy, ids, table_rows, 1.5)
+        out = strided(torch.full((table_rows, width), 5.0, device="cuda"), 3, 1, fill=7.0)
+        _check_bwd(gs, strided(dy, 5, 1), ids, table_rows, width ** 0.5, dtable=out)
+        assert table_rows == 1 or bool((padding(out) == 7.0).all())
+
+
+@pytest.mark.parametrize("rows,width", [(200_000, 16), (60_000, 257), (9_000, 1500), (300_000, 64)])
+def test_embedding_backward_of_few_ids(gs, rows, width):
+    """Sums over a great many rows: all of one id, of two, and of a few of many;
+    and no row of any id."""
+    dy = rand(gen(1), rows, width, dtype=torch.bfloat16)
+    for table_rows, pick in ((1, [0]), (1000, [999]), (1000, [0, 998]), (70_000, [3, 4, 5, 69_999])):
+        at = torch.randint(len(pick), (rows,), generator=gen(2), device="cuda")
+        ids = torch.tensor(pick, device="cuda")[at]
+        _check_bwd(gs, dy, ids, table_rows)
+        _check_bwd(gs, dy, torch.full_like(ids, -1), table_rows)
+
+
+def test_embedding_backward_same_bits(gs):
+    dy = rand(gen(1), 50_000, 200, dtype=torch.float32)
+    ids = _ids(4, 50_000, 300)
+    first = _check_bwd(gs, dy, ids, 300)
+    for _ in range(3):
+        ws = torch.full((gs.gs_embedding_workspace_size(50_000, 300, 200, 2),), 255, dtype=torch.uint8, device="cuda")
+        assert torch.equal(_check_bwd(gs, dy, ids, 300, workspace=ws), first)
+
+
+def test_embedding_backward_special_values(gs):
+    """An infinity or NaN reaches its own row alone; rows of no id are not read."""
+    dy = torch.ones(6, 12, device="cuda")
+    dy[1, 3], dy[2, 4], dy[5] = float("inf"), float("nan"), float("nan")
+    ids = torch.tensor([0, 1, 2, 1, 0, -1], device="cuda")
+    got = _check_bwd(gs, dy, ids, 4)
+    assert bool(got[0].eq(2).all()) and bool(got[3].eq(0).all()) and bool(got[1, 3].isinf()) and bool(got[2, 4].isnan())
+
+
+def test_embedding_backward_is_the_transpose(gs):
+    """The lookup is linear in the table: <dy, lookup(d)> = <dtable, d> for any d,
+    which is what differences of the lookup say of its gradient.  Both sides are
+    sums of the same 400 x 96 products; each factor has roundings of 2^-24."""
+    g = gen(8)
+    d, dy = rand(g, 90, 96), rand(g, 400, 96)
+    ids = _ids(5, 400, 90)
+    offsets, order, _ = gs.gs_group_sort(ids, 90)
+    left = (dy.double() * gs.gs_embedding_fwd(d, ids, 3.0).double())
+    right = (gs.gs_embedding_bwd(dy, ids, offsets, order, 3.0).double() * d.double()).sum()
+    assert abs(left.sum() - right) <= 40 * EPS32 * left.abs().sum()
+
+
+def test_embedding_of_unfit_order(gs):
+    """Bounds and orders that no sort wrote: no access out of bounds, and a
+    call afterwards is right."""
+    rows, table_rows, width = 500, 40, 72
+    dy, ids = rand(gen(1), rows, width), _ids(6, rows, table_rows)
+    good = gs.gs_group_sort(ids, table_rows, want_place=False)
+    for offsets, order in ((good[0].flip(0), good[1]), (good[0] * 1000, good[1]), (good[0] - 300, good[1]),
+                           (good[0], good[1] - 250), (good[0], good[1] * 5_000_000)):
+        gs.gs_embedding_bwd(dy, ids, offsets.contiguous(), order.contiguous())
+    torch.cuda.synchronize()
+    _check_bwd(gs, dy, ids, table_rows)
+
+
+def test_sort_and_embedding_on_streams_and_in_graphs(gs):
+    rows, table_rows, width = 12_000, 3_000, 80
+    table = rand(gen(1), table_rows, width, dtype=torch.bfloat16)
+    dy = rand(gen(2), rows, width, dtype=torch.bfloat16)
+    ids = _ids(7, rows, table_rows)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    offsets, order, _ = gs.gs_group_sort(ids, table_rows, stream=side)
+    y = gs.gs_embedding_fwd(table, ids, 2.0, stream=side)
+    dt = gs.gs_embedding_bwd(dy, ids, offsets, order, 2.0, stream=side)
+    side.synchronize()
+    assert torch.equal(y, gs.gs_embedding_fwd(table, ids, 2.0))
+    assert torch.equal(dt, _check_bwd(gs, dy, ids, table_rows, 2.0))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        offsets, order, place = gs.gs_group_sort(ids, table_rows)
+        y = gs.gs_embedding_fwd(table, ids, 2.0)
+        dt = gs.gs_embedding_bwd(dy, ids, offsets, order, 2.0)
+    for k in range(4):
+        ids.copy_(_ids(20 + k, rows, table_rows))
+        dy.copy_(rand(gen(30 + k), rows, width))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = _check_sort(gs, ids, table_rows)
+        assert all(torch.equal(a, b) for a, b in zip((offsets, order, place), want))
+        assert torch.equal(y, gs.gs_embedding_fwd(table, ids, 2.0))
+        assert torch.equal(dt, _check_bwd(gs, dy, ids, table_rows, 2.0))
