@@ -31,6 +31,7 @@ GS_ACT_NONE, GS_ACT_RELU, GS_ACT_SILU, GS_ACT_GELU = 0, 1, 2, 3
 GS_MAX_NET_DIM = 65536
 GS_MAX_NET_GROUPS = 1024
 GS_MAX_SORT_GROUPS = 1 << 30
+GS_MAX_CHOICES = 16
 GS_PROJ_WORDS = 16
 GS_GRAD2D_WORDS = 12
 GS_MAX_FUSED_VIEWS = 16
@@ -51,7 +52,8 @@ EXPORTS = ["gs_status_string", "gs_last_error", "gs_version", "gs_workspace_size
            "gs_sparse_adam_noalloc", "gs_preprocess_views", "gs_layer_norm_fwd", "gs_layer_norm_bwd", "gs_linear_fwd",
            "gs_linear_workspace_size", "gs_linear_bwd", "gs_grouped_linear_fwd", "gs_grouped_linear_bwd",
            "gs_group_sort", "gs_group_sort_workspace_size", "gs_embedding_fwd", "gs_embedding_bwd",
-           "gs_embedding_workspace_size"]
+           "gs_embedding_workspace_size", "gs_gate_fwd", "gs_gate_bwd", "gs_dispatch_fwd", "gs_dispatch_bwd",
+           "gs_combine_fwd", "gs_combine_bwd"]
 GS_NOALLOC_SCRATCH_BYTES = 256 * 1024
 GS_NOALLOC_MAX_N = (GS_NOALLOC_SCRATCH_BYTES // 4 - 1) * 4096
 
@@ -133,6 +135,12 @@ def lib():
     L.gs_embedding_bwd.argtypes = [_P, _i64, _P, _i32, _P, _P, _i64, _i64, _i32, _f32, _i32, _P, _i64, _i32, _P, _sz,
                                    _P]
     L.gs_embedding_workspace_size.argtypes = [_i64, _i64, _i32, _i32, C.POINTER(_sz)]
+    L.gs_gate_fwd.argtypes = [_P, _i64, _i64, _i32, _i32, _i32, _i32, _P, _P, _P]
+    L.gs_gate_bwd.argtypes = [_P, _i64, _P, _P, _P, _i64, _i32, _i32, _i32, _i32, _P, _i64, _P]
+    L.gs_dispatch_fwd.argtypes = [_P, _i64, _P, _i64, _i32, _i32, _i32, _P, _i64, _P]
+    L.gs_dispatch_bwd.argtypes = [_P, _i64, _P, _i64, _i32, _i32, _i32, _P, _i64, _P, _i64, _P]
+    L.gs_combine_fwd.argtypes = [_P, _i64, _P, _P, _P, _i64, _i64, _i32, _i32, _i32, _P, _i64, _P]
+    L.gs_combine_bwd.argtypes = [_P, _i64, _P, _i64, _P, _P, _i64, _i32, _i32, _i32, _P, _i64, _P, _P]
     for name in EXPORTS[3:]:
         getattr(L, name).restype = C.c_int
     _handle = L
@@ -1035,6 +1043,7 @@ def from_workload(work, device="cuda", **kw) -> TrainStep:
                      work.beta2, work.eps, device=device, **kw)
 
 
-from .network import (gs_embedding_bwd, gs_embedding_fwd, gs_embedding_workspace_size,  # noqa: E402
+from .network import (gs_combine_bwd, gs_combine_fwd, gs_dispatch_bwd, gs_dispatch_fwd,  # noqa: E402
+                      gs_embedding_bwd, gs_embedding_fwd, gs_embedding_workspace_size, gs_gate_bwd, gs_gate_fwd,
                       gs_group_sort, gs_group_sort_workspace_size, gs_grouped_linear_bwd, gs_grouped_linear_fwd,
                       gs_layer_norm_bwd, gs_layer_norm_fwd, gs_linear_bwd, gs_linear_fwd, gs_linear_workspace_size)

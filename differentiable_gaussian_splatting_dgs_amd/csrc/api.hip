@@ -25,6 +25,7 @@ static_assert(GS_ACT_NONE == gs::kActNone && GS_ACT_RELU == gs::kActRelu && GS_A
               "activations");
 static_assert(GS_MAX_NET_DIM == gs::kMaxNetDim && GS_MAX_NET_GROUPS == gs::kMaxNetGroups, "network limits");
 static_assert(GS_MAX_SORT_GROUPS == gs::kMaxSortGroups, "sort limit");
+static_assert(GS_MAX_CHOICES == gs::kMaxChoices, "choices limit");
 
 namespace {
 
@@ -242,6 +243,29 @@ gs_status check_sort_sizes(int64_t n, int64_t num_groups) {
   REQUIRE(n >= 0 && n < (int64_t(1) << 31), "n = %lld out of range", (long long)n);
   REQUIRE(num_groups >= 1 && num_groups <= GS_MAX_SORT_GROUPS, "num_groups = %lld out of range",
           (long long)num_groups);
+  return GS_OK;
+}
+
+gs_status check_gate(const gs::GateArgs& a, int64_t rows, int32_t type) {
+  CHECK(check_net_sizes(rows, type));
+  REQUIRE(a.groups >= 1 && a.groups <= GS_MAX_NET_GROUPS, "groups = %d out of range", int(a.groups));
+  REQUIRE(a.k >= 1 && a.k <= std::min(a.groups, GS_MAX_CHOICES), "k = %d out of range", int(a.k));
+  if (rows == 0) return GS_OK;
+  REQUIRE(a.ids != nullptr && a.weights != nullptr, "ids / weights NULL");
+  CHECK(check_vector("ids", a.ids));
+  CHECK(check_vector("weights", a.weights));
+  return GS_OK;
+}
+
+gs_status check_route(const gs::RouteArgs& a, int64_t rows, int32_t type) {
+  CHECK(check_net_sizes(rows, type));
+  REQUIRE(a.k >= 1 && a.k <= GS_MAX_CHOICES, "k = %d out of range", int(a.k));
+  REQUIRE(rows * a.k < (int64_t(1) << 31), "rows = %lld with k = %d out of range", (long long)rows, int(a.k));
+  REQUIRE(a.width >= 1 && a.width <= GS_MAX_NET_DIM, "width = %d out of range", int(a.width));
+  if (rows == 0) return GS_OK;
+  REQUIRE(a.place != nullptr && aligned(a.place, 4), "place NULL or not 4-byte aligned");
+  CHECK(check_vector("weights", a.weights));
+  if (a.residual != nullptr) CHECK(check_matrix("residual", a.residual, a.ldr, a.width, gs::type_bytes(type)));
   return GS_OK;
 }
 
@@ -1033,6 +1057,137 @@ gs_status gs_embedding_bwd(const void* dy, int64_t lddy, const void* ids, int32_
   a.dtable_f32 = dtable_type == GS_TYPE_F32;
   return hip_status(gs::launch_embedding_bwd(type, a, workspace, static_cast<hipStream_t>(stream)),
                     "gs_embedding_bwd");
+}
+
+gs_status gs_gate_fwd(const void* logits, int64_t ld, int64_t rows, int32_t groups, int32_t k, int32_t renorm,
+                      int32_t type, int32_t* ids, float* weights, void* stream) {
+  gs::GateArgs a{};
+  a.logits = logits;
+  a.ld = ld;
+  a.rows = int32_t(rows);
+  a.groups = groups;
+  a.k = k;
+  a.renorm = renorm;
+  a.ids = ids;
+  a.weights = weights;
+  CHECK(check_gate(a, rows, type));
+  if (rows == 0) return ok();
+  CHECK(check_matrix("logits", logits, ld, groups, gs::type_bytes(type)));
+  return hip_status(gs::launch_gate_fwd(type, a, static_cast<hipStream_t>(stream)), "gs_gate_fwd");
+}
+
+gs_status gs_gate_bwd(const void* logits, int64_t ld, const int32_t* ids, const float* weights,
+                      const float* dweights, int64_t rows, int32_t groups, int32_t k, int32_t renorm, int32_t type,
+                      void* dlogits, int64_t lddl, void* stream) {
+  gs::GateArgs a{};
+  a.logits = logits;
+  a.ld = ld;
+  a.rows = int32_t(rows);
+  a.groups = groups;
+  a.k = k;
+  a.renorm = renorm;
+  a.ids = const_cast<int32_t*>(ids);
+  a.weights = const_cast<float*>(weights);
+  a.dweights = dweights;
+  a.dlogits = dlogits;
+  a.lddl = lddl;
+  CHECK(check_gate(a, rows, type));
+  if (rows == 0) return ok();
+  const size_t elem = gs::type_bytes(type);
+  CHECK(check_matrix("logits", logits, ld, groups, elem));
+  CHECK(check_matrix("dlogits", dlogits, lddl, groups, elem));
+  REQUIRE(dweights != nullptr && aligned(dweights, 4), "dweights NULL or not 4-byte aligned");
+  return hip_status(gs::launch_gate_bwd(type, a, static_cast<hipStream_t>(stream)), "gs_gate_bwd");
+}
+
+gs_status gs_dispatch_fwd(const void* x, int64_t ldx, const int32_t* place, int64_t rows, int32_t k, int32_t width,
+                          int32_t type, void* xs, int64_t ldxs, void* stream) {
+  gs::RouteArgs a{};
+  a.x = x;
+  a.ldx = ldx;
+  a.place = place;
+  a.rows = int32_t(rows);
+  a.k = k;
+  a.width = width;
+  a.y = xs;
+  a.ldy = ldxs;
+  CHECK(check_route(a, rows, type));
+  if (rows == 0) return ok();
+  const size_t elem = gs::type_bytes(type);
+  CHECK(check_matrix("x", x, ldx, width, elem));
+  CHECK(check_matrix("xs", xs, ldxs, width, elem));
+  return hip_status(gs::launch_dispatch(type, a, static_cast<hipStream_t>(stream)), "gs_dispatch_fwd");
+}
+
+gs_status gs_dispatch_bwd(const void* dxs, int64_t lddxs, const int32_t* place, int64_t rows, int32_t k,
+                          int32_t width, int32_t type, const void* dres, int64_t ldr, void* dx, int64_t lddx,
+                          void* stream) {
+  gs::RouteArgs a{};
+  a.x = dxs;
+  a.ldx = lddxs;
+  a.place = place;
+  a.rows = int32_t(rows);
+  a.k = k;
+  a.width = width;
+  a.residual = dres;
+  a.ldr = ldr;
+  a.y = dx;
+  a.ldy = lddx;
+  CHECK(check_route(a, rows, type));
+  if (rows == 0) return ok();
+  const size_t elem = gs::type_bytes(type);
+  CHECK(check_matrix("dxs", dxs, lddxs, width, elem));
+  CHECK(check_matrix("dx", dx, lddx, width, elem));
+  return hip_status(gs::launch_combine(type, a, static_cast<hipStream_t>(stream)), "gs_dispatch_bwd");
+}
+
+gs_status gs_combine_fwd(const void* ys, int64_t ldys, const int32_t* place, const float* weights,
+                         const void* residual, int64_t ldr, int64_t rows, int32_t k, int32_t width, int32_t type,
+                         void* y, int64_t ldy, void* stream) {
+  gs::RouteArgs a{};
+  a.x = ys;
+  a.ldx = ldys;
+  a.place = place;
+  a.weights = weights;
+  a.rows = int32_t(rows);
+  a.k = k;
+  a.width = width;
+  a.residual = residual;
+  a.ldr = ldr;
+  a.y = y;
+  a.ldy = ldy;
+  CHECK(check_route(a, rows, type));
+  if (rows == 0) return ok();
+  const size_t elem = gs::type_bytes(type);
+  CHECK(check_matrix("ys", ys, ldys, width, elem));
+  CHECK(check_matrix("y", y, ldy, width, elem));
+  return hip_status(gs::launch_combine(type, a, static_cast<hipStream_t>(stream)), "gs_combine_fwd");
+}
+
+gs_status gs_combine_bwd(const void* dy, int64_t lddy, const void* ys, int64_t ldys, const int32_t* place,
+                         const float* weights, int64_t rows, int32_t k, int32_t width, int32_t type, void* dys,
+                         int64_t lddys, float* dweights, void* stream) {
+  gs::RouteArgs a{};
+  a.x = ys;
+  a.ldx = ldys;
+  a.dy = dy;
+  a.lddy = lddy;
+  a.place = place;
+  a.weights = weights;
+  a.rows = int32_t(rows);
+  a.k = k;
+  a.width = width;
+  a.y = dys;
+  a.ldy = lddys;
+  a.dweights = dweights;
+  CHECK(check_route(a, rows, type));
+  if (rows == 0 || (dys == nullptr && dweights == nullptr)) return ok();
+  const size_t elem = gs::type_bytes(type);
+  CHECK(check_matrix("dy", dy, lddy, width, elem));
+  if (dweights != nullptr) CHECK(check_matrix("ys", ys, ldys, width, elem));
+  if (dys != nullptr) CHECK(check_matrix("dys", dys, lddys, width, elem));
+  CHECK(check_vector("dweights", dweights));
+  return hip_status(gs::launch_combine_bwd(type, a, static_cast<hipStream_t>(stream)), "gs_combine_bwd");
 }
 
 }  // extern "C"

@@ -247,4 +247,33 @@ size_t embedding_bwd_ws_bytes(int type, int64_t rows, int64_t num_rows, int32_t 
 hipError_t launch_embedding_fwd(int type, const EmbedArgs& a, hipStream_t st);
 hipError_t launch_embedding_bwd(int type, const EmbedArgs& a, void* ws, hipStream_t st);
 
+// --- the gate and routed rows (gate.hip, route.hip) -------------------------------
+constexpr int32_t kMaxChoices = 16;
+struct GateArgs {
+  const void* logits;
+  const float* dweights;   // backward only, as is dlogits
+  int32_t* ids;            // read by the backward pass, as are the weights
+  float* weights;
+  void* dlogits;
+  int64_t ld, lddl;
+  int32_t rows, groups, k, renorm;
+};
+hipError_t launch_gate_fwd(int type, const GateArgs& a, hipStream_t st);
+hipError_t launch_gate_bwd(int type, const GateArgs& a, hipStream_t st);
+
+struct RouteArgs {
+  const void* x;           // dispatch: x; combine and its backward: ys
+  const void* dy;          // combine's backward
+  const int32_t* place;
+  const float* weights;    // or NULL: 1
+  const void* residual;    // or NULL
+  void* y;                 // dispatch: xs; combine: y; its backward: dys or NULL
+  float* dweights;         // or NULL
+  int64_t ldx, lddy, ldr, ldy;
+  int32_t rows, k, width;
+};
+hipError_t launch_dispatch(int type, const RouteArgs& a, hipStream_t st);
+hipError_t launch_combine(int type, const RouteArgs& a, hipStream_t st);
+hipError_t launch_combine_bwd(int type, const RouteArgs& a, hipStream_t st);
+
 }  // namespace gs

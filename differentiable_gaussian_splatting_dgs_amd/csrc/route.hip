@@ -1,0 +1,199 @@
+// Rows to the places that the sort by group gave their choices, and back with
+// weights, each with its gradient.
+//
+//   dispatch       xs[place[i][j]] = x[i]
+//   combine        y[i] = sum_j w[i][j] ys[place[i][j]] + residual[i]
+//                  (w = 1: dispatch's gradient, residual the gradient past it)
+//   combine's gradient   dys[place[i][j]] = w[i][j] dy[i],
+//                  dw[i][j] = sum over the columns of dy[i] ys[place[i][j]]
+//
+// All go by the row i, not by the sorted position: x and dy are read once
+// for all k choices, the sums over j need no atomics and have a fixed order.
+// Bound by the bytes of the rows.  Sums are fp32; the rounding into storage is
+// the last step.
+#include <algorithm>
+
+#include "row_chunks.hpp"
+
+namespace gs {
+namespace net {
+namespace {
+
+constexpr int kThreads = 256;
+
+// The row's places, -1 for one outside its range.
+template <int KM>
+__device__ __forceinline__ void load_places(const RouteArgs& a, int64_t r, int32_t (&at)[KM]) {
+  const int32_t most = a.rows * a.k;
+#pragma unroll
+  for (int j = 0; j < KM; ++j) {
+    at[j] = j < a.k ? a.place[r * a.k + j] : -1;
+    if (uint32_t(at[j]) >= uint32_t(most)) at[j] = -1;
+  }
+}
+
+template <int KM>
+__device__ __forceinline__ void load_weights(const RouteArgs& a, int64_t r, float (&w)[KM]) {
+#pragma unroll
+  for (int j = 0; j < KM; ++j) w[j] = a.weights != nullptr && j < a.k ? a.weights[r * a.k + j] : 1.0f;
+}
+
+// L lanes a row, a chunk for each lane: `slices` of the row's chunks one
+// after the other.
+template <typename T, int L>
+__device__ __forceinline__ bool slice_of(const RouteArgs& a, const Row<T>& row, int slices, int64_t& r, int& c) {
+  const int64_t item = int64_t(blockIdx.x) * (kThreads / L) + threadIdx.x / L;
+  r = item / slices;
+  c = int(item - r * slices) * L + threadIdx.x % L;
+  return r < a.rows && c < row.chunks;
+}
+
+template <typename T, int L, int KM>
+__global__ __launch_bounds__(kThreads) void k_dispatch(RouteArgs a, int slices) {
+  const Row<T> row(a.width);
+  int64_t r;
+  int c;
+  if (!slice_of<T, L>(a, row, slices, r, c)) return;
+  const Chunk<T> x = row.load(static_cast<const T*>(a.x) + r * a.ldx, c);
+  int32_t at[KM];
+  load_places<KM>(a, r, at);
+  T* const xs = static_cast<T*>(a.y);
+#pragma unroll
+  for (int j = 0; j < KM; ++j)
+    if (at[j] >= 0) row.copy(xs + at[j] * a.ldy, c, x);
+}
+
+template <typename T, int L, int KM>
+__global__ __launch_bounds__(kThreads) void k_combine(RouteArgs a, int slices) {
+  constexpr int K = kChunk<T>;
+  const Row<T> row(a.width);
+  int64_t r;
+  int c;
+  if (!slice_of<T, L>(a, row, slices, r, c)) return;
+  int32_t at[KM];
+  float w[KM];
+  load_places<KM>(a, r, at);
+  load_weights<KM>(a, r, w);
+  const T* const ys = static_cast<const T*>(a.x);
+  // a place that was left out reads row 0, and drops it
+  Chunk<T> v[KM];
+#pragma unroll
+  for (int j = 0; j < KM; ++j) v[j] = row.load(ys + (at[j] < 0 ? 0 : at[j]) * a.ldx, c);
+  float sum[K] = {};
+#pragma unroll
+  for (int j = 0; j < KM; ++j)
+#pragma unroll
+    for (int i = 0; i < K; ++i) sum[i] = at[j] < 0 ? sum[i] : fmaf(w[j], float(v[j].v[i]), sum[i]);
+  T* const y = static_cast<T*>(a.y) + r * a.ldy;
+  if (a.residual != nullptr) {
+    const Chunk<T> res = row.load(static_cast<const T*>(a.residual) + r * a.ldr, c);
+#pragma unroll
+    for (int i = 0; i < K; ++i) sum[i] += float(res.v[i]);
+    if (a.residual == a.y) {
+      row.store_rest(y, c, sum);
+      return;
+    }
+  }
+  row.store(y, c, sum);
+}
+
+// L lanes a row, which they walk: the products' sums stay in registers.
+template <typename T, int L, int KM>
+__global__ __launch_bounds__(kThreads) void k_combine_bwd(RouteArgs a) {
+  constexpr int K = kChunk<T>;
+  const Row<T> row(a.width);
+  const int64_t r = int64_t(blockIdx.x) * (kThreads / L) + threadIdx.x / L;
+  const int l = threadIdx.x % L;
+  if (r >= a.rows) return;      // all lanes of a row together
+  int32_t at[KM];
+  float w[KM], dot[KM] = {};
+  load_places<KM>(a, r, at);
+  load_weights<KM>(a, r, w);
+  const T* const dy = static_cast<const T*>(a.dy) + r * a.lddy;
+  const T* const ys = static_cast<const T*>(a.x);
+  T* const dys = static_cast<T*>(a.y);
+  for (int c = l; c < row.chunks; c += L) {
+    const Chunk<T> g = row.load(dy, c);
+    if (a.dweights != nullptr) {
+      Chunk<T> v[KM];
+#pragma unroll
+      for (int j = 0; j < KM; ++j) v[j] = row.load(ys + (at[j] < 0 ? 0 : at[j]) * a.ldx, c);
+      const int again = row.again(c);
+#pragma unroll
+      for (int j = 0; j < KM; ++j)
+#pragma unroll
+        for (int i = 0; i < K; ++i) dot[j] = i < again ? dot[j] : fmaf(float(g.v[i]), float(v[j].v[i]), dot[j]);
+    }
+    if (dys != nullptr)
+#pragma unroll
+      for (int j = 0; j < KM; ++j)
+        if (at[j] >= 0) {
+          float o[K];
+#pragma unroll
+          for (int i = 0; i < K; ++i) o[i] = w[j] * float(g.v[i]);
+          row.store(dys + at[j] * a.ldy, c, o);
+        }
+  }
+  if (a.dweights == nullptr) return;
+#pragma unroll
+  for (int j = 0; j < KM; ++j) {
+#pragma unroll
+    for (int d = 1; d < L; d <<= 1) dot[j] += __shfl_xor(dot[j], d, 64);
+    if (j < a.k && l == 0) a.dweights[r * a.k + j] = at[j] < 0 ? 0.0f : dot[j];
+  }
+}
+
+enum Way { kDispatch, kCombine, kCombineBwd };
+
+template <typename T, int L, int KM>
+hipError_t go(Way way, const RouteArgs& a, hipStream_t st) {
+  const int64_t slices = way == kCombineBwd ? 1 : ((a.width + kChunk<T> - 1) / kChunk<T> + L - 1) / L;
+  const unsigned grid = unsigned((a.rows * slices + kThreads / L - 1) / (kThreads / L));
+  if (way == kDispatch)
+    k_dispatch<T, L, KM><<<grid, kThreads, 0, st>>>(a, int(slices));
+  else if (way == kCombine)
+    k_combine<T, L, KM><<<grid, kThreads, 0, st>>>(a, int(slices));
+  else
+    k_combine_bwd<T, L, KM><<<grid, kThreads, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+template <typename T, int L>
+hipError_t by_choices(Way way, const RouteArgs& a, hipStream_t st) {
+  if (a.k <= 1) return go<T, L, 1>(way, a, st);
+  if (a.k <= 2) return go<T, L, 2>(way, a, st);
+  if (a.k <= 4) return go<T, L, 4>(way, a, st);
+  if (a.k <= 8) return go<T, L, 8>(way, a, st);
+  return go<T, L, kMaxChoices>(way, a, st);
+}
+
+template <typename T>
+hipError_t by_width(Way way, const RouteArgs& a, hipStream_t st) {
+  switch (row_lanes((a.width + kChunk<T> - 1) / kChunk<T>)) {
+    case 8: return by_choices<T, 8>(way, a, st);
+    case 16: return by_choices<T, 16>(way, a, st);
+    case 32: return by_choices<T, 32>(way, a, st);
+    default: return by_choices<T, 64>(way, a, st);
+  }
+}
+
+hipError_t by_type(int type, Way way, const RouteArgs& a, hipStream_t st) {
+  if (type == kTypeBF16) return by_width<bf16>(way, a, st);
+  if (type == kTypeF16) return by_width<f16>(way, a, st);
+  return by_width<float>(way, a, st);
+}
+
+}  // namespace
+}  // namespace net
+
+hipError_t launch_dispatch(int type, const RouteArgs& a, hipStream_t st) {
+  return net::by_type(type, net::kDispatch, a, st);
+}
+hipError_t launch_combine(int type, const RouteArgs& a, hipStream_t st) {
+  return net::by_type(type, net::kCombine, a, st);
+}
+hipError_t launch_combine_bwd(int type, const RouteArgs& a, hipStream_t st) {
+  return net::by_type(type, net::kCombineBwd, a, st);
+}
+
+}  // namespace gs

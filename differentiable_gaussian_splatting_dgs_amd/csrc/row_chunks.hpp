@@ -51,6 +51,23 @@ struct Row {
       }
     }
   }
+  __device__ __forceinline__ void copy(T* __restrict__ row, int c, const Chunk<T>& v) const {
+    if (width >= K)
+      store_chunk(row + at(c), v);
+    else
+      store_chunk_n(row, v, width);
+  }
+  // Without the columns that the chunk before has too: what rows that are
+  // read and written in place need.
+  __device__ __forceinline__ void store_rest(T* __restrict__ row, int c, const float (&v)[K]) const {
+    if (width < K || again(c) == 0) {
+      store(row, c, v);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+      if (i >= again(c)) row[at(c) + i] = T(v[i]);
+  }
 };
 
 // Lanes that share a row: a power of two, 8 ... 64, that leaves few of them

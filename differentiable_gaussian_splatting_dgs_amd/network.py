@@ -1,6 +1,7 @@
 """The network operators of libgs: layer norm, the linear layer with bias,
 activation and residual in its epilogue, the linear layer whose weights
-go by ragged group, rows looked up in a shared table, each forward and
+go by ragged group, rows looked up in a shared table, the gate that picks
+groups for a row, rows brought to their groups and back, each forward and
 backward, and the sort by group that ragged groups are made by.
 
 They carry the names of the C entry points (``include/gs.h``).  Matrices are
@@ -435,3 +436,160 @@ def gs_embedding_bwd(dy, ids, offsets, order, scale=1.0, dtable=None, workspace=
     ``dtable`` is of dy's type, or float32 where such a tensor is passed in;
     every row is written."""
     return _launch(_embed_bwd, dy, stream, ids, offsets, order, scale, dtable, workspace)
+
+
+def _choices(t, dtype, rows, device, name, k=None):
+    """k of t, a contiguous [rows][k] tensor."""
+    if t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows or (k is not None and t.shape[1] != k):
+        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}: {dtype} ({rows}, {'k' if k is None else k}) expected")
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} has to be contiguous and on {device}")
+    return t.shape[1]
+
+
+def _gate_fwd(s, logits, k, renorm, ids, weights):
+    t = _type(logits, "logits")
+    rows, groups = logits.shape
+    ld, device = _matrix(logits, rows, groups, logits, "logits"), logits.device
+    _on_gpu(logits, "logits")
+    if not 1 <= k <= groups:
+        raise ValueError(f"k = {k} of {groups} groups")
+    ids = _whole(ids, _I32, (rows, k), device, "ids")
+    weights = _whole(weights, _F32, (rows, k), device, "weights")
+    st = lib().gs_gate_fwd(logits.data_ptr(), ld, rows, groups, k, 1 if renorm else 0, t, ids.data_ptr(),
+                           weights.data_ptr(), s)
+    if st:
+        _check(st, "gs_gate_fwd")
+    return ids, weights
+
+
+def gs_gate_fwd(logits, k, renorm=True, ids=None, weights=None, stream=None):
+    """(ids, weights), [rows][k] int32 and float32: each row's k largest logits
+    and their softmax over themselves (``renorm``) or over the whole row.  A
+    logit of minus infinity is never chosen; -1 and 0 where no other is left."""
+    return _launch(_gate_fwd, logits, stream, k, renorm, ids, weights)
+
+
+def _gate_bwd(s, logits, ids, weights, dweights, renorm, dlogits):
+    t = _type(logits, "logits")
+    rows, groups = logits.shape
+    ld, device = _matrix(logits, rows, groups, logits, "logits"), logits.device
+    k = _choices(ids, _I32, rows, device, "ids")
+    _choices(weights, _F32, rows, device, "weights", k)
+    _choices(dweights, _F32, rows, device, "dweights", k)
+    _on_gpu(logits, "logits")
+    if dlogits is None:
+        dlogits, lddl = _empty(rows, groups, dtype=logits.dtype, device=device), groups
+    else:
+        lddl = _matrix(dlogits, rows, groups, logits, "dlogits")
+    st = lib().gs_gate_bwd(logits.data_ptr(), ld, ids.data_ptr(), weights.data_ptr(), dweights.data_ptr(), rows,
+                           groups, k, 1 if renorm else 0, t, dlogits.data_ptr(), lddl, s)
+    if st:
+        _check(st, "gs_gate_bwd")
+    return dlogits
+
+
+def gs_gate_bwd(logits, ids, weights, dweights, renorm=True, dlogits=None, stream=None):
+    """dlogits of gs_gate_fwd, whose ``ids`` and ``weights`` it reads, for the
+    gradient ``dweights`` of the weights."""
+    return _launch(_gate_bwd, logits, stream, ids, weights, dweights, renorm, dlogits)
+
+
+def _dispatch_fwd(s, x, place, xs):
+    t = _type(x)
+    rows, width = x.shape
+    ldx, device = _matrix(x, rows, width, x, "x"), x.device
+    k = _choices(place, _I32, rows, device, "place")
+    _on_gpu(x)
+    if xs is None:
+        xs, ldxs = _empty(rows * k, width, dtype=x.dtype, device=device), width
+    else:
+        ldxs = _matrix(xs, rows * k, width, x, "xs")
+    st = lib().gs_dispatch_fwd(x.data_ptr(), ldx, place.data_ptr(), rows, k, width, t, xs.data_ptr(), ldxs, s)
+    if st:
+        _check(st, "gs_dispatch_fwd")
+    return xs
+
+
+def gs_dispatch_fwd(x, place, xs=None, stream=None):
+    """xs [rows k][width] with xs[place[i][j]] = x[i]; ``place`` is
+    gs_group_sort's of [rows][k] ids.  Rows behind the last group are not written."""
+    return _launch(_dispatch_fwd, x, stream, place, xs)
+
+
+def _back(s, x, place, weights, residual, y, weighted):
+    """gs_combine_fwd of x = ys, or gs_dispatch_bwd of x = dxs."""
+    name = "ys" if weighted else "dxs"
+    t = _type(x, name)
+    many, width = x.shape
+    ldx, device = _matrix(x, many, width, x, name), x.device
+    rows = place.shape[0] if place.dim() == 2 else -1
+    k = _choices(place, _I32, rows, device, "place")
+    if many != rows * k:
+        raise ValueError(f"{name} has {many} rows, place {rows} x {k}")
+    if weights is not None:
+        _choices(weights, _F32, rows, device, "weights", k)
+    ldr = 0 if residual is None else _matrix(residual, rows, width, x, "residual" if weighted else "dres")
+    _on_gpu(x, name)
+    if y is None:
+        y, ldy = _empty(rows, width, dtype=x.dtype, device=device), width
+    else:
+        ldy = _matrix(y, rows, width, x, "y" if weighted else "dx")
+    if weighted:
+        st = lib().gs_combine_fwd(x.data_ptr(), ldx, place.data_ptr(), _optional(weights), _optional(residual), ldr,
+                                  rows, k, width, t, y.data_ptr(), ldy, s)
+    else:
+        st = lib().gs_dispatch_bwd(x.data_ptr(), ldx, place.data_ptr(), rows, k, width, t, _optional(residual), ldr,
+                                   y.data_ptr(), ldy, s)
+    if st:
+        _check(st, "gs_combine_fwd" if weighted else "gs_dispatch_bwd")
+    return y
+
+
+def gs_dispatch_bwd(dxs, place, dres=None, dx=None, stream=None):
+    """dx[i] = sum_j dxs[place[i][j]] (+ dres[i], the gradient that reaches x
+    past the heads)."""
+    return _launch(_back, dxs, stream, place, None, dres, dx, False)
+
+
+def gs_combine_fwd(ys, place, weights=None, residual=None, y=None, stream=None):
+    """y[i] = sum_j weights[i][j] ys[place[i][j]] (+ residual[i]); places that
+    were left out (-1) add nothing."""
+    return _launch(_back, ys, stream, place, weights, residual, y, True)
+
+
+def _combine_bwd(s, dy, ys, place, weights, dys, dweights, want_dys, want_dw):
+    t = _type(dy, "dy")
+    rows, width = dy.shape
+    lddy, device = _matrix(dy, rows, width, dy, "dy"), dy.device
+    k = _choices(place, _I32, rows, device, "place")
+    if weights is not None:
+        _choices(weights, _F32, rows, device, "weights", k)
+    if dweights is not None:
+        _choices(dweights, _F32, rows, device, "dweights", k)
+    want_dw = want_dw or dweights is not None
+    if ys is None and want_dw:
+        raise ValueError("the weights' gradient reads ys")
+    ldys = 0 if ys is None else _matrix(ys, rows * k, width, dy, "ys")
+    _on_gpu(dy, "dy")
+    if dys is not None:
+        lddys = _matrix(dys, rows * k, width, dy, "dys")
+    elif want_dys:
+        dys, lddys = _empty(rows * k, width, dtype=dy.dtype, device=device), width
+    else:
+        lddys = 0
+    if dweights is None and want_dw:
+        dweights = _empty(rows, k, dtype=_F32, device=device)
+    st = lib().gs_combine_bwd(dy.data_ptr(), lddy, _optional(ys), ldys, place.data_ptr(), _optional(weights), rows, k,
+                              width, t, _optional(dys), lddys, _optional(dweights), s)
+    if st:
+        _check(st, "gs_combine_bwd")
+    return dys, dweights
+
+
+def gs_combine_bwd(dy, ys, place, weights=None, dys=None, dweights=None, want_dys=True, want_dw=True, stream=None):
+    """(dys, dweights) of gs_combine_fwd for the gradient ``dy`` of y (the
+    residual's gradient is dy itself); rows of dys behind the last group are
+    not written.  ``want_dw`` false leaves dweights out (``ys`` may be None
+    then), ``want_dys`` false dys, unless they are passed in."""
+    return _launch(_combine_bwd, dy, stream, ys, place, weights, dys, dweights, want_dys, want_dw)

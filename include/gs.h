@@ -140,6 +140,8 @@ typedef enum gs_act {
 #define GS_MAX_NET_GROUPS 1024
 /* most groups of gs_group_sort, and rows of a table */
 #define GS_MAX_SORT_GROUPS ((int64_t)1 << 30)
+/* most groups that the gate picks for a row, or that a row goes to */
+#define GS_MAX_CHOICES 16
 
 /* Static description of a status code (never NULL). */
 const char* gs_status_string(int status);
@@ -839,6 +841,84 @@ gs_status gs_embedding_bwd(const void* dy, int64_t lddy, const void* ids, int32_
 
 /* Workspace bytes of gs_embedding_bwd (host, no device work). */
 gs_status gs_embedding_workspace_size(int64_t rows, int64_t num_rows, int32_t width, int32_t type, size_t* bytes);
+
+/* The gate: the k largest logits of each row, in descending order (ties: the
+ * lower index first; NaN counts as the largest), and their weights
+ *   renorm != 0   e^l / sum of e^l over the row's chosen logits
+ *   renorm == 0   e^l / sum of e^l over all of the row's logits
+ * A logit of minus infinity is never chosen: where fewer than k others are
+ * there, ids is -1 and the weight 0 (an id of no group to gs_group_sort).
+ *   logits       device, [rows][ld]
+ *   ids          device out, [rows][k] int32
+ *   weights      device out, [rows][k] fp32
+ * Errors: GS_ERR_INVALID_ARG for an unknown type, rows outside [0, 2^31),
+ * groups outside [1, GS_MAX_NET_GROUPS], k outside [1, min(groups,
+ * GS_MAX_CHOICES)], a leading dimension below groups, a NULL or misaligned
+ * array. */
+gs_status gs_gate_fwd(const void* logits, int64_t ld, int64_t rows, int32_t groups, int32_t k, int32_t renorm,
+                      int32_t type, int32_t* ids, float* weights, void* stream);
+
+/* Its backward pass, with s = sum over the row's choices of weight dweight:
+ *   renorm != 0   dlogits = weight (dweight - s) where chosen, else 0
+ *   renorm == 0   dlogits = [chosen] weight dweight - p s, p = e^l / sum e^l,
+ *                 as weights[0] e^(l - logit of the first choice)
+ *   ids, weights   device, as the forward pass wrote them; an id outside
+ *                [0, groups) is no choice
+ *   dweights     device, [rows][k] fp32
+ *   dlogits      device out, [rows][lddl]
+ * Errors: as the forward pass. */
+gs_status gs_gate_bwd(const void* logits, int64_t ld, const int32_t* ids, const float* weights,
+                      const float* dweights, int64_t rows, int32_t groups, int32_t k, int32_t renorm, int32_t type,
+                      void* dlogits, int64_t lddl, void* stream);
+
+/* Rows to where gs_group_sort places their k choices: xs[place[i][j]] = x[i].
+ *   x            device, [rows][ldx]
+ *   place        device, [rows][k] int32, as gs_group_sort of [rows][k] ids
+ *                wrote it (distinct, in [0, rows k)); a place outside that
+ *                range is left out
+ *   xs           device out, [rows k][ldxs]; rows that no place names (those
+ *                behind the last group) are not written
+ * Errors: GS_ERR_INVALID_ARG for an unknown type, rows outside [0, 2^31) or
+ * rows k outside it, width outside [1, GS_MAX_NET_DIM], k outside [1,
+ * GS_MAX_CHOICES], a leading dimension below width, a NULL or misaligned
+ * array. */
+gs_status gs_dispatch_fwd(const void* x, int64_t ldx, const int32_t* place, int64_t rows, int32_t k, int32_t width,
+                          int32_t type, void* xs, int64_t ldxs, void* stream);
+
+/* Its backward pass: dx[i] = sum over j of dxs[place[i][j]] (+ dres[i]), in
+ * fp32, j ascending.  The sum has no term for a place that was left out.
+ *   dres         device, [rows][ldr] (the gradient that reaches x past the
+ *                heads), or NULL; dx may be dres itself
+ *   dx           device out, [rows][lddx]
+ * Errors: as the forward pass. */
+gs_status gs_dispatch_bwd(const void* dxs, int64_t lddxs, const int32_t* place, int64_t rows, int32_t k,
+                          int32_t width, int32_t type, const void* dres, int64_t ldr, void* dx, int64_t lddx,
+                          void* stream);
+
+/* Rows brought back: y[i] = sum over j of weights[i][j] ys[place[i][j]]
+ * (+ residual[i]), in fp32, j ascending.  Rows of ys that no place names do
+ * not matter; a place that was left out adds nothing, whatever its weight.
+ *   ys           device, [rows k][ldys]
+ *   weights      device, [rows][k] fp32, or NULL: 1
+ *   residual     device, [rows][ldr], or NULL; y may be residual itself
+ *   y            device out, [rows][ldy]
+ * Errors: as gs_dispatch_fwd. */
+gs_status gs_combine_fwd(const void* ys, int64_t ldys, const int32_t* place, const float* weights,
+                         const void* residual, int64_t ldr, int64_t rows, int32_t k, int32_t width, int32_t type,
+                         void* y, int64_t ldy, void* stream);
+
+/* Its backward pass: dys[place[i][j]] = weights[i][j] dy[i] and
+ * dweights[i][j] = sum over the columns of dy[i] ys[place[i][j]] in fp32 (0 for
+ * a place that was left out).  (The residual's gradient is dy itself.)
+ *   ys           device, as the forward pass read it; not read, and may be
+ *                NULL, without dweights
+ *   dys          device out, [rows k][lddys], or NULL; rows that no place
+ *                names are not written
+ *   dweights     device out, [rows][k] fp32, or NULL
+ * Errors: as gs_dispatch_fwd. */
+gs_status gs_combine_bwd(const void* dy, int64_t lddy, const void* ys, int64_t ldys, const int32_t* place,
+                         const float* weights, int64_t rows, int32_t k, int32_t width, int32_t type, void* dys,
+                         int64_t lddys, float* dweights, void* stream);
 
 #ifdef __cplusplus
 }

@@ -97,3 +97,95 @@ def _ids(*shape, dtype=torch.int64):
 def test_binding_refuses(call, match):
     with pytest.raises(ValueError, match=match):
         call()
+
+
+# --- the gate and routed rows ------------------------------------------------------
+
+def _gate(logits=P(16), ld=64, rows=4, groups=64, k=2, renorm=1, typ=0, ids=P(16), weights=P(16)):
+    return gs.lib().gs_gate_fwd(logits, ld, rows, groups, k, renorm, typ, ids, weights, None)
+
+
+def _gate_bwd(logits=P(16), ld=64, ids=P(16), weights=P(16), dweights=P(16), rows=4, groups=64, k=2, renorm=1, typ=0,
+              dlogits=P(16), lddl=64):
+    return gs.lib().gs_gate_bwd(logits, ld, ids, weights, dweights, rows, groups, k, renorm, typ, dlogits, lddl, None)
+
+
+def _dispatch(x=P(16), ldx=64, place=P(16), rows=4, k=2, width=64, typ=0, xs=P(16), ldxs=64):
+    return gs.lib().gs_dispatch_fwd(x, ldx, place, rows, k, width, typ, xs, ldxs, None)
+
+
+def _dispatch_bwd(dxs=P(16), ld=64, place=P(16), rows=4, k=2, width=64, typ=0, dres=None, ldr=0, dx=P(16), lddx=64):
+    return gs.lib().gs_dispatch_bwd(dxs, ld, place, rows, k, width, typ, dres, ldr, dx, lddx, None)
+
+
+def _combine(ys=P(16), ld=64, place=P(16), weights=P(16), res=None, ldr=0, rows=4, k=2, width=64, typ=0, y=P(16),
+             ldy=64):
+    return gs.lib().gs_combine_fwd(ys, ld, place, weights, res, ldr, rows, k, width, typ, y, ldy, None)
+
+
+def _combine_bwd(dy=P(16), lddy=64, ys=P(16), ldys=64, place=P(16), weights=P(16), rows=4, k=2, width=64, typ=0,
+                 dys=P(16), lddys=64, dw=P(16)):
+    return gs.lib().gs_combine_bwd(dy, lddy, ys, ldys, place, weights, rows, k, width, typ, dys, lddys, dw, None)
+
+
+@pytest.mark.parametrize("call,kw,word", [
+    (_gate, dict(typ=3), b"type"), (_gate, dict(rows=-1), b"rows"), (_gate, dict(groups=0), b"groups"),
+    (_gate, dict(groups=1025, ld=2000), b"groups"), (_gate, dict(k=0), b"k ="), (_gate, dict(k=17), b"k ="),
+    (_gate, dict(groups=4, k=5), b"k ="), (_gate, dict(ld=63), b"logits"), (_gate, dict(logits=None), b"logits"),
+    (_gate, dict(logits=P(17)), b"logits"), (_gate, dict(ids=None), b"ids"), (_gate, dict(ids=P(18)), b"ids"),
+    (_gate, dict(weights=None), b"weights"), (_gate, dict(weights=P(18)), b"weights"),
+    (_gate_bwd, dict(typ=-1), b"type"), (_gate_bwd, dict(k=0), b"k ="), (_gate_bwd, dict(dlogits=None), b"dlogits"),
+    (_gate_bwd, dict(lddl=9), b"dlogits"), (_gate_bwd, dict(ld=9), b"logits"), (_gate_bwd, dict(ids=None), b"ids"),
+    (_gate_bwd, dict(dweights=None), b"dweights"), (_gate_bwd, dict(dweights=P(18)), b"dweights"),
+    (_dispatch, dict(typ=7), b"type"), (_dispatch, dict(rows=1 << 31), b"rows"), (_dispatch, dict(k=0), b"k ="),
+    (_dispatch, dict(k=17), b"k ="), (_dispatch, dict(rows=1 << 30, k=2), b"rows"),
+    (_dispatch, dict(width=0), b"width"), (_dispatch, dict(width=65537), b"width"), (_dispatch, dict(ldx=63), b"x"),
+    (_dispatch, dict(ldxs=63), b"xs"), (_dispatch, dict(x=None), b"x"), (_dispatch, dict(xs=None), b"xs"),
+    (_dispatch, dict(place=None), b"place"), (_dispatch, dict(place=P(18)), b"place"),
+    (_dispatch_bwd, dict(dxs=None), b"dxs"), (_dispatch_bwd, dict(dx=None), b"dx"),
+    (_dispatch_bwd, dict(dres=P(16), ldr=1), b"residual"), (_dispatch_bwd, dict(lddx=2), b"dx"),
+    (_combine, dict(ys=None), b"ys"), (_combine, dict(y=None), b"y"), (_combine, dict(weights=P(18)), b"weights"),
+    (_combine, dict(res=P(17), ldr=64), b"residual"), (_combine, dict(ldy=63), b"y"),
+    (_combine_bwd, dict(dy=None), b"dy"), (_combine_bwd, dict(ys=None), b"ys"), (_combine_bwd, dict(lddys=1), b"dys"),
+    (_combine_bwd, dict(dw=P(18)), b"dweights"), (_combine_bwd, dict(place=None), b"place"),
+])
+def test_routing_refused(call, kw, word):
+    assert call(**kw) == gs.GS_ERR_INVALID_ARG
+    assert word in gs.lib().gs_last_error(), gs.lib().gs_last_error()
+
+
+def test_routing_nothing_to_do():
+    for call in (_gate, _gate_bwd, _dispatch, _dispatch_bwd, _combine, _combine_bwd):
+        assert call(rows=0) == gs.GS_OK
+    assert _combine_bwd(dys=None, dw=None) == gs.GS_OK
+
+
+I4 = torch.int32
+
+
+@pytest.mark.parametrize("call,match", [
+    (lambda: gs.gs_gate_fwd(_t(4), 2), "dimensions"), (lambda: gs.gs_gate_fwd(_t(8, 4).t(), 2), "stride"),
+    (lambda: gs.gs_gate_fwd(_t(4, 8), 2), "GPU tensor"),
+    (lambda: gs.gs_gate_bwd(_t(4, 8), _ids(4, 2), _t(4, 2), _t(4, 2)), "ids"),
+    (lambda: gs.gs_gate_bwd(_t(4, 8), _ids(4, 2, dtype=I4), _t(4, 3), _t(4, 2)), "weights"),
+    (lambda: gs.gs_gate_bwd(_t(4, 8), _ids(4, 2, dtype=I4), _t(4, 2), _t(3, 2)), "dweights"),
+    (lambda: gs.gs_gate_bwd(_t(4, 8), _ids(4, 2, dtype=I4), _t(4, 2), _t(4, 2)), "GPU tensor"),
+    (lambda: gs.gs_dispatch_fwd(_t(4, 8), _ids(4, 2)), "place"),
+    (lambda: gs.gs_dispatch_fwd(_t(4, 8), _ids(5, 2, dtype=I4)), "place"),
+    (lambda: gs.gs_dispatch_fwd(_t(4, 8), _ids(4, dtype=I4)), "place"),
+    (lambda: gs.gs_dispatch_fwd(_t(4, 8), _ids(4, 2, dtype=I4)), "GPU tensor"),
+    (lambda: gs.gs_dispatch_bwd(_t(7, 8), _ids(4, 2, dtype=I4)), "rows"),
+    (lambda: gs.gs_dispatch_bwd(_t(8, 8), _ids(4, 2, dtype=I4), dres=_t(4, 7)), "dres"),
+    (lambda: gs.gs_dispatch_bwd(_t(8, 8), _ids(8, dtype=I4)), "place"),
+    (lambda: gs.gs_dispatch_bwd(_t(8, 8), _ids(4, 2, dtype=I4)), "GPU tensor"),
+    (lambda: gs.gs_combine_fwd(_t(9, 8), _ids(4, 2, dtype=I4)), "rows"),
+    (lambda: gs.gs_combine_fwd(_t(8, 8), _ids(4, 2, dtype=I4), _t(4, 3)), "weights"),
+    (lambda: gs.gs_combine_fwd(_t(8, 8), _ids(4, 2, dtype=I4), _t(2, 4).t()), "contiguous"),
+    (lambda: gs.gs_combine_fwd(_t(8, 8), _ids(4, 2, dtype=I4)), "GPU tensor"),
+    (lambda: gs.gs_combine_bwd(_t(4, 8), None, _ids(4, 2, dtype=I4)), "reads ys"),
+    (lambda: gs.gs_combine_bwd(_t(4, 8), _t(7, 8), _ids(4, 2, dtype=I4)), "ys"),
+    (lambda: gs.gs_combine_bwd(_t(4, 8), _t(8, 8), _ids(4, 2, dtype=I4)), "GPU tensor"),
+])
+def test_routing_binding_refuses(call, match):
+    with pytest.raises(ValueError, match=match):
+        call()
