@@ -32,6 +32,8 @@ GS_MAX_NET_DIM = 65536
 GS_MAX_NET_GROUPS = 1024
 GS_MAX_SORT_GROUPS = 1 << 30
 GS_MAX_CHOICES = 16
+GS_ADAMW_BLOCK = 256
+GS_MAX_ADAMW_SIZE = 1 << 35
 GS_PROJ_WORDS = 16
 GS_GRAD2D_WORDS = 12
 GS_MAX_FUSED_VIEWS = 16
@@ -53,7 +55,7 @@ EXPORTS = ["gs_status_string", "gs_last_error", "gs_version", "gs_workspace_size
            "gs_linear_workspace_size", "gs_linear_bwd", "gs_grouped_linear_fwd", "gs_grouped_linear_bwd",
            "gs_group_sort", "gs_group_sort_workspace_size", "gs_embedding_fwd", "gs_embedding_bwd",
            "gs_embedding_workspace_size", "gs_gate_fwd", "gs_gate_bwd", "gs_dispatch_fwd", "gs_dispatch_bwd",
-           "gs_combine_fwd", "gs_combine_bwd"]
+           "gs_combine_fwd", "gs_combine_bwd", "gs_adamw", "gs_adamw_moment"]
 GS_NOALLOC_SCRATCH_BYTES = 256 * 1024
 GS_NOALLOC_MAX_N = (GS_NOALLOC_SCRATCH_BYTES // 4 - 1) * 4096
 
@@ -70,7 +72,13 @@ class gs_param_grads(C.Structure):
                 ("vis_idx", C.c_void_p), ("vis_count", C.c_void_p), ("grads", C.c_void_p)]
 
 
-_P, _i64, _i32, _f32, _sz = C.c_void_p, C.c_int64, C.c_int32, C.c_float, C.c_size_t
+class gs_adamw_tensor(C.Structure):
+    _fields_ = [("param", C.c_void_p), ("grad", C.c_void_p), ("m", C.c_void_p), ("v", C.c_void_p),
+                ("m_scale", C.c_void_p), ("v_scale", C.c_void_p), ("copy", C.c_void_p), ("n", C.c_int64),
+                ("grad_type", C.c_int32), ("copy_type", C.c_int32)]
+
+
+_P, _i64, _i32, _f32, _f64, _sz = C.c_void_p, C.c_int64, C.c_int32, C.c_float, C.c_double, C.c_size_t
 _handle = None
 
 
@@ -141,6 +149,8 @@ def lib():
     L.gs_dispatch_bwd.argtypes = [_P, _i64, _P, _i64, _i32, _i32, _i32, _P, _i64, _P, _i64, _P]
     L.gs_combine_fwd.argtypes = [_P, _i64, _P, _P, _P, _i64, _i64, _i32, _i32, _i32, _P, _i64, _P]
     L.gs_combine_bwd.argtypes = [_P, _i64, _P, _i64, _P, _P, _i64, _i32, _i32, _i32, _P, _i64, _P, _P]
+    L.gs_adamw.argtypes = [_P, _i32, _f64, _f64, _f64, _f64, _f64, _i64, _P, _P, C.c_uint64, _P]
+    L.gs_adamw_moment.argtypes = [_P, _P, _i64, _i32, _i32, _P, _P]
     for name in EXPORTS[3:]:
         getattr(L, name).restype = C.c_int
     _handle = L
@@ -1047,3 +1057,4 @@ from .network import (gs_combine_bwd, gs_combine_fwd, gs_dispatch_bwd, gs_dispat
                       gs_embedding_bwd, gs_embedding_fwd, gs_embedding_workspace_size, gs_gate_bwd, gs_gate_fwd,
                       gs_group_sort, gs_group_sort_workspace_size, gs_grouped_linear_bwd, gs_grouped_linear_fwd,
                       gs_layer_norm_bwd, gs_layer_norm_fwd, gs_linear_bwd, gs_linear_fwd, gs_linear_workspace_size)
+from .optim import AdamW, gs_adamw, gs_adamw_moment  # noqa: E402

@@ -26,7 +26,7 @@ ARCH = "gfx950"
 SOURCES = ["api.hip", "compact.hip", "preprocess.hip", "binsort.hip", "raster_fwd.hip", "raster_bwd.hip",
            "loss.hip", "adam.hip", "coupling.hip", "shard.hip", "densify.hip",
            "layer_norm.hip", "linear.hip", "linear_bf16.hip", "linear_f16.hip", "linear_f32.hip",
-           "group_sort.hip", "embedding.hip", "gate.hip", "route.hip"]
+           "group_sort.hip", "embedding.hip", "gate.hip", "route.hip", "adamw.hip"]
 
 FLAGS = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

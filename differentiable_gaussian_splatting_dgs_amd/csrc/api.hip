@@ -8,7 +8,10 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <memory>
 #include <mutex>
+#include <new>
+#include <utility>
 
 #include "../../include/gs.h"
 #include "gs_internal.h"
@@ -26,6 +29,7 @@ static_assert(GS_ACT_NONE == gs::kActNone && GS_ACT_RELU == gs::kActRelu && GS_A
 static_assert(GS_MAX_NET_DIM == gs::kMaxNetDim && GS_MAX_NET_GROUPS == gs::kMaxNetGroups, "network limits");
 static_assert(GS_MAX_SORT_GROUPS == gs::kMaxSortGroups, "sort limit");
 static_assert(GS_MAX_CHOICES == gs::kMaxChoices, "choices limit");
+static_assert(GS_ADAMW_BLOCK == gs::kAdamwBlock && GS_MAX_ADAMW_SIZE == gs::kMaxAdamwSize, "adamw limits");
 
 namespace {
 
@@ -1188,6 +1192,104 @@ gs_status gs_combine_bwd(const void* dy, int64_t lddy, const void* ys, int64_t l
   if (dys != nullptr) CHECK(check_matrix("dys", dys, lddys, width, elem));
   CHECK(check_vector("dweights", dweights));
   return hip_status(gs::launch_combine_bwd(type, a, static_cast<hipStream_t>(stream)), "gs_combine_bwd");
+}
+
+gs_status gs_adamw(const gs_adamw_tensor* tensors, int32_t count, double lr, double beta1, double beta2, double eps,
+                   double weight_decay, int64_t step, const int64_t* step_dev, const float* grad_scale,
+                   uint64_t seed, void* stream) {
+  REQUIRE(count >= 0 && (count == 0 || tensors != nullptr), "count = %d, or tensors NULL", int(count));
+  REQUIRE(std::isfinite(lr) && std::isfinite(weight_decay), "lr or weight_decay not finite");
+  REQUIRE(beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0, "a beta outside [0, 1)");
+  REQUIRE(std::isfinite(eps) && float(eps) > 0.0f && std::isfinite(float(eps)), "eps not above 0");
+  REQUIRE(step_dev != nullptr || step >= 1, "step = %lld: 1 or more expected", (long long)step);
+  REQUIRE(aligned(step_dev, 8) && aligned(grad_scale, 4), "step_dev or grad_scale misaligned");
+  // written ranges, as (first byte, one past the last), sorted to find overlaps
+  constexpr int kFew = 64 * 5;
+  std::pair<uintptr_t, uintptr_t> few[kFew];
+  std::unique_ptr<std::pair<uintptr_t, uintptr_t>[]> more;
+  std::pair<uintptr_t, uintptr_t>* ranges = few;
+  if (count > kFew / 5) {
+    more.reset(new (std::nothrow) std::pair<uintptr_t, uintptr_t>[size_t(count) * 6]);
+    if (more == nullptr) return fail(GS_ERR_INVALID_ARG, "no host memory for %d tensors", int(count));
+    ranges = more.get();
+  }
+  size_t written = 0;
+  auto writes = [&](const void* p, int64_t bytes) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    ranges[written++] = {at, at + uintptr_t(bytes)};
+  };
+  bool any[2] = {false, false};
+  for (int32_t i = 0; i < count; ++i) {
+    const gs_adamw_tensor& t = tensors[i];
+    REQUIRE(t.n >= 0 && t.n <= GS_MAX_ADAMW_SIZE, "tensor %d: n = %lld out of range", int(i), (long long)t.n);
+    if (t.n == 0) continue;
+    REQUIRE(t.grad_type >= GS_TYPE_BF16 && t.grad_type <= GS_TYPE_F32, "tensor %d: grad_type = %d unknown", int(i),
+            int(t.grad_type));
+    REQUIRE(t.param != nullptr && aligned(t.param, 4), "tensor %d: param NULL or misaligned", int(i));
+    REQUIRE(t.grad != nullptr && aligned(t.grad, gs::type_bytes(t.grad_type)), "tensor %d: grad NULL or misaligned",
+            int(i));
+    REQUIRE((t.m_scale == nullptr) == (t.v_scale == nullptr), "tensor %d: one scale of two", int(i));
+    const bool eight = t.m_scale != nullptr;
+    const size_t align = eight ? 1 : 4;
+    REQUIRE(t.m != nullptr && t.v != nullptr && aligned(t.m, align) && aligned(t.v, align),
+            "tensor %d: m or v NULL or misaligned", int(i));
+    REQUIRE(aligned(t.m_scale, 4) && aligned(t.v_scale, 4), "tensor %d: scale misaligned", int(i));
+    if (t.copy != nullptr) {
+      REQUIRE(t.copy_type >= GS_TYPE_BF16 && t.copy_type <= GS_TYPE_F32, "tensor %d: copy_type = %d unknown", int(i),
+              int(t.copy_type));
+      REQUIRE(aligned(t.copy, gs::type_bytes(t.copy_type)), "tensor %d: copy misaligned", int(i));
+      writes(t.copy, t.n * int64_t(gs::type_bytes(t.copy_type)));
+    }
+    writes(t.param, t.n * 4);
+    writes(t.m, t.n * (eight ? 1 : 4));
+    writes(t.v, t.n * (eight ? 1 : 4));
+    if (eight) {
+      const int64_t blocks = (t.n + GS_ADAMW_BLOCK - 1) / GS_ADAMW_BLOCK;
+      writes(t.m_scale, blocks * 4);
+      writes(t.v_scale, blocks * 4);
+    }
+    any[eight] = true;
+  }
+  std::sort(ranges, ranges + written);
+  for (size_t i = 1; i < written; ++i) REQUIRE(ranges[i].first >= ranges[i - 1].second, "written ranges overlap");
+  const gs::AdamwHyper h{lr, beta1, beta2, eps, weight_decay, step, step_dev, grad_scale};
+  for (int eight = 0; eight < 2; ++eight) {
+    if (!any[eight]) continue;
+    gs::AdamwTensor batch[gs::kAdamwTensors];
+    int held = 0;
+    uint32_t workgroups = 0;
+    for (int32_t i = 0; i <= count; ++i) {
+      const bool take = i < count && tensors[i].n > 0 && (tensors[i].m_scale != nullptr) == (eight != 0);
+      const uint32_t mine = take ? gs::adamw_workgroups(tensors[i].n) : 0;
+      // a launch ends with its room for tensors, or where its threads would pass 2^32 - 1
+      if (held > 0 && (i == count || (take && (held == gs::kAdamwTensors || workgroups + mine >= (1u << 24))))) {
+        const hipError_t e =
+            gs::launch_adamw(batch, held, eight != 0, workgroups, h, static_cast<hipStream_t>(stream));
+        if (e != hipSuccess) return hip_status(e, "gs_adamw");
+        held = 0;
+        workgroups = 0;
+      }
+      if (!take) continue;
+      const gs_adamw_tensor& t = tensors[i];
+      batch[held++] = {t.param, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.copy, t.n, workgroups,
+                       gs::adamw_key(seed, uint32_t(i)), int16_t(t.grad_type), int16_t(t.copy_type), 0};
+      workgroups += mine;
+    }
+  }
+  return ok();
+}
+
+gs_status gs_adamw_moment(const uint8_t* codes, const float* scales, int64_t n, int32_t moment, int32_t type,
+                          void* values, void* stream) {
+  REQUIRE(n >= 0 && n <= GS_MAX_ADAMW_SIZE, "n = %lld out of range", (long long)n);
+  REQUIRE(moment == 1 || moment == 2, "moment = %d: 1 or 2 expected", int(moment));
+  REQUIRE(type >= GS_TYPE_BF16 && type <= GS_TYPE_F32, "type = %d unknown", int(type));
+  if (n == 0) return ok();
+  REQUIRE(codes != nullptr, "codes is NULL");
+  REQUIRE(scales != nullptr && aligned(scales, 4), "scales NULL or misaligned");
+  REQUIRE(values != nullptr && aligned(values, gs::type_bytes(type)), "values NULL or misaligned");
+  return hip_status(gs::launch_adamw_moment(codes, scales, n, moment, type, values, static_cast<hipStream_t>(stream)),
+                    "gs_adamw_moment");
 }
 
 }  // extern "C"

@@ -24,20 +24,21 @@ template <typename T, int L>
 __global__ __launch_bounds__(kThreads) void k_lookup(EmbedArgs a) {
   constexpr int K = kChunk<T>;
   const Row<T> row(a.width);
-  const int64_t r = int64_t(blockIdx.x) * (kThreads / L) + threadIdx.x / L;
-  if (r >= a.rows) return;
-  const int64_t id = id_at(a.ids, a.id_bytes, r);
-  const bool there = id >= 0 && id < a.num_rows;
-  const T* __restrict__ src = static_cast<const T*>(a.table) + (there ? id : 0) * a.ldt;
-  T* __restrict__ dst = static_cast<T*>(a.y) + r * a.ldy;
-  for (int c = threadIdx.x % L; c < row.chunks; c += L) {
-    float v[K] = {};
-    if (there) {
-      const Chunk<T> x = row.load(src, c);
+  constexpr int kRows = kThreads / L;
+  for (int64_t r = int64_t(blockIdx.x) * kRows + threadIdx.x / L; r < a.rows; r += int64_t(gridDim.x) * kRows) {
+    const int64_t id = id_at(a.ids, a.id_bytes, r);
+    const bool there = id >= 0 && id < a.num_rows;
+    const T* __restrict__ src = static_cast<const T*>(a.table) + (there ? id : 0) * a.ldt;
+    T* __restrict__ dst = static_cast<T*>(a.y) + r * a.ldy;
+    for (int c = threadIdx.x % L; c < row.chunks; c += L) {
+      float v[K] = {};
+      if (there) {
+        const Chunk<T> x = row.load(src, c);
 #pragma unroll
-      for (int i = 0; i < K; ++i) v[i] = float(x.v[i]) * a.scale;
+        for (int i = 0; i < K; ++i) v[i] = float(x.v[i]) * a.scale;
+      }
+      row.store(dst, c, v);
     }
-    row.store(dst, c, v);
   }
 }
 
@@ -46,33 +47,34 @@ template <typename T, typename O, int L>
 __global__ __launch_bounds__(kThreads) void k_table_grad(EmbedArgs a) {
   constexpr int K = kChunk<T>;
   const Row<T> row(a.width);
-  const int64_t v = int64_t(blockIdx.x) * (kThreads / L) + threadIdx.x / L;
-  if (v >= a.num_rows) return;
-  const int64_t p0 = std::max<int64_t>(a.offsets[v], 0), p1 = std::min<int64_t>(a.offsets[v + 1], a.rows);
-  for (int c = threadIdx.x % L; c < row.chunks; c += L) {
-    float sum[K] = {};
-    for (int64_t p = p0; p < p1; ++p) {
-      const int64_t r = a.order[p];
-      if (r < 0 || r >= a.rows) continue;
-      const Chunk<T> x = row.load(static_cast<const T*>(a.dy) + r * a.lddy, c);
+  constexpr int kRows = kThreads / L;
+  for (int64_t v = int64_t(blockIdx.x) * kRows + threadIdx.x / L; v < a.num_rows; v += int64_t(gridDim.x) * kRows) {
+    const int64_t p0 = std::max<int64_t>(a.offsets[v], 0), p1 = std::min<int64_t>(a.offsets[v + 1], a.rows);
+    for (int c = threadIdx.x % L; c < row.chunks; c += L) {
+      float sum[K] = {};
+      for (int64_t p = p0; p < p1; ++p) {
+        const int64_t r = a.order[p];
+        if (r < 0 || r >= a.rows) continue;
+        const Chunk<T> x = row.load(static_cast<const T*>(a.dy) + r * a.lddy, c);
 #pragma unroll
-      for (int i = 0; i < K; ++i) sum[i] += float(x.v[i]);
+        for (int i = 0; i < K; ++i) sum[i] += float(x.v[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < K; ++i) sum[i] *= a.scale;
+      row.store(static_cast<O*>(a.dtable) + v * a.lddt, c, sum);
     }
-#pragma unroll
-    for (int i = 0; i < K; ++i) sum[i] *= a.scale;
-    row.store(static_cast<O*>(a.dtable) + v * a.lddt, c, sum);
   }
 }
 
 template <typename T, int L>
 hipError_t go_fwd(const EmbedArgs& a, hipStream_t st) {
-  k_lookup<T, L><<<unsigned((a.rows + kThreads / L - 1) / (kThreads / L)), kThreads, 0, st>>>(a);
+  k_lookup<T, L><<<grid_of((a.rows + kThreads / L - 1) / (kThreads / L)), kThreads, 0, st>>>(a);
   return hipGetLastError();
 }
 
 template <typename T, int L>
 hipError_t go_bwd(const EmbedArgs& a, hipStream_t st) {
-  const unsigned grid = unsigned((a.num_rows + kThreads / L - 1) / (kThreads / L));
+  const unsigned grid = grid_of((a.num_rows + kThreads / L - 1) / (kThreads / L));
   if (a.dtable_f32)
     k_table_grad<T, float, L><<<grid, kThreads, 0, st>>>(a);
   else

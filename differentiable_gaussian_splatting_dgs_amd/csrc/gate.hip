@@ -14,7 +14,7 @@
 // Bound by the bytes of the logits.
 #include <algorithm>
 
-#include "net_common.hpp"
+#include "row_chunks.hpp"
 
 namespace gs {
 namespace net {
@@ -88,13 +88,10 @@ __device__ __forceinline__ uint64_t row_max(uint64_t v) {
 
 // L lanes a row, C chunks a lane; KM: choices, rounded up.
 template <typename T, int L, int C, int KM>
-__global__ __launch_bounds__(kThreads) void k_gate(GateArgs a) {
+__device__ __forceinline__ void gate_row(const GateArgs& a, int64_t r, int l) {
   constexpr int K = kChunk<T>;
   using P = Pick<T>;
   using U = typename P::U;
-  const int64_t r = int64_t(blockIdx.x) * (kThreads / L) + threadIdx.x / L;
-  const int l = threadIdx.x % L;
-  if (r >= a.rows) return;      // all lanes of a row together
   const T* __restrict__ x = static_cast<const T*>(a.logits) + r * a.ld;
   U u[C][K];
 #pragma unroll
@@ -146,11 +143,8 @@ __global__ __launch_bounds__(kThreads) void k_gate(GateArgs a) {
 }
 
 template <typename T, int L, int C, int KM>
-__global__ __launch_bounds__(kThreads) void k_gate_bwd(GateArgs a) {
+__device__ __forceinline__ void gate_row_bwd(const GateArgs& a, int64_t r, int l) {
   constexpr int K = kChunk<T>;
-  const int64_t r = int64_t(blockIdx.x) * (kThreads / L) + threadIdx.x / L;
-  const int l = threadIdx.x % L;
-  if (r >= a.rows) return;
   const T* __restrict__ x = static_cast<const T*>(a.logits) + r * a.ld;
   T* __restrict__ dl = static_cast<T*>(a.dlogits) + r * a.lddl;
   int32_t id[KM];
@@ -191,13 +185,25 @@ __global__ __launch_bounds__(kThreads) void k_gate_bwd(GateArgs a) {
   }
 }
 
+template <typename T, int L, int C, int KM, bool kFwd>
+__global__ __launch_bounds__(kThreads) void k_gate(GateArgs a) {
+  constexpr int kRows = kThreads / L;
+  // all lanes of a row together
+  for (int64_t r = int64_t(blockIdx.x) * kRows + threadIdx.x / L; r < a.rows; r += int64_t(gridDim.x) * kRows) {
+    if constexpr (kFwd)
+      gate_row<T, L, C, KM>(a, r, threadIdx.x % L);
+    else
+      gate_row_bwd<T, L, C, KM>(a, r, threadIdx.x % L);
+  }
+}
+
 template <typename T, int L, int C, int KM>
 hipError_t go(bool fwd, const GateArgs& a, hipStream_t st) {
-  const unsigned grid = unsigned((int64_t(a.rows) + kThreads / L - 1) / (kThreads / L));
+  const unsigned grid = grid_of((int64_t(a.rows) + kThreads / L - 1) / (kThreads / L));
   if (fwd)
-    k_gate<T, L, C, KM><<<grid, kThreads, 0, st>>>(a);
+    k_gate<T, L, C, KM, true><<<grid, kThreads, 0, st>>>(a);
   else
-    k_gate_bwd<T, L, C, KM><<<grid, kThreads, 0, st>>>(a);
+    k_gate<T, L, C, KM, false><<<grid, kThreads, 0, st>>>(a);
   return hipGetLastError();
 }
 

@@ -38,63 +38,66 @@ __device__ __forceinline__ void load_weights(const RouteArgs& a, int64_t r, floa
   for (int j = 0; j < KM; ++j) w[j] = a.weights != nullptr && j < a.k ? a.weights[r * a.k + j] : 1.0f;
 }
 
-// L lanes a row, a chunk for each lane: `slices` of the row's chunks one
-// after the other.
-template <typename T, int L>
-__device__ __forceinline__ bool slice_of(const RouteArgs& a, const Row<T>& row, int slices, int64_t& r, int& c) {
-  const int64_t item = int64_t(blockIdx.x) * (kThreads / L) + threadIdx.x / L;
-  r = item / slices;
-  c = int(item - r * slices) * L + threadIdx.x % L;
-  return r < a.rows && c < row.chunks;
+// Items are slices of rows: L lanes, a chunk for each.
+template <int L>
+__device__ __forceinline__ int64_t first_item() {
+  return int64_t(blockIdx.x) * (kThreads / L) + threadIdx.x / L;
+}
+template <int L>
+__device__ __forceinline__ int64_t next_item() {
+  return int64_t(gridDim.x) * (kThreads / L);
 }
 
 template <typename T, int L, int KM>
 __global__ __launch_bounds__(kThreads) void k_dispatch(RouteArgs a, int slices) {
   const Row<T> row(a.width);
-  int64_t r;
-  int c;
-  if (!slice_of<T, L>(a, row, slices, r, c)) return;
-  const Chunk<T> x = row.load(static_cast<const T*>(a.x) + r * a.ldx, c);
-  int32_t at[KM];
-  load_places<KM>(a, r, at);
   T* const xs = static_cast<T*>(a.y);
+  for (int64_t item = first_item<L>(); item < int64_t(a.rows) * slices; item += next_item<L>()) {
+    const int64_t r = item / slices;
+    const int c = int(item - r * slices) * L + threadIdx.x % L;
+    if (c >= row.chunks) continue;
+    const Chunk<T> x = row.load(static_cast<const T*>(a.x) + r * a.ldx, c);
+    int32_t at[KM];
+    load_places<KM>(a, r, at);
 #pragma unroll
-  for (int j = 0; j < KM; ++j)
-    if (at[j] >= 0) row.copy(xs + at[j] * a.ldy, c, x);
+    for (int j = 0; j < KM; ++j)
+      if (at[j] >= 0) row.copy(xs + at[j] * a.ldy, c, x);
+  }
 }
 
 template <typename T, int L, int KM>
 __global__ __launch_bounds__(kThreads) void k_combine(RouteArgs a, int slices) {
   constexpr int K = kChunk<T>;
   const Row<T> row(a.width);
-  int64_t r;
-  int c;
-  if (!slice_of<T, L>(a, row, slices, r, c)) return;
-  int32_t at[KM];
-  float w[KM];
-  load_places<KM>(a, r, at);
-  load_weights<KM>(a, r, w);
   const T* const ys = static_cast<const T*>(a.x);
-  // a place that was left out reads row 0, and drops it
-  Chunk<T> v[KM];
+  for (int64_t item = first_item<L>(); item < int64_t(a.rows) * slices; item += next_item<L>()) {
+    const int64_t r = item / slices;
+    const int c = int(item - r * slices) * L + threadIdx.x % L;
+    if (c >= row.chunks) continue;
+    int32_t at[KM];
+    float w[KM];
+    load_places<KM>(a, r, at);
+    load_weights<KM>(a, r, w);
+    // a place that was left out reads row 0, and drops it
+    Chunk<T> v[KM];
 #pragma unroll
-  for (int j = 0; j < KM; ++j) v[j] = row.load(ys + (at[j] < 0 ? 0 : at[j]) * a.ldx, c);
-  float sum[K] = {};
+    for (int j = 0; j < KM; ++j) v[j] = row.load(ys + (at[j] < 0 ? 0 : at[j]) * a.ldx, c);
+    float sum[K] = {};
 #pragma unroll
-  for (int j = 0; j < KM; ++j)
+    for (int j = 0; j < KM; ++j)
 #pragma unroll
-    for (int i = 0; i < K; ++i) sum[i] = at[j] < 0 ? sum[i] : fmaf(w[j], float(v[j].v[i]), sum[i]);
-  T* const y = static_cast<T*>(a.y) + r * a.ldy;
-  if (a.residual != nullptr) {
-    const Chunk<T> res = row.load(static_cast<const T*>(a.residual) + r * a.ldr, c);
+      for (int i = 0; i < K; ++i) sum[i] = at[j] < 0 ? sum[i] : fmaf(w[j], float(v[j].v[i]), sum[i]);
+    T* const y = static_cast<T*>(a.y) + r * a.ldy;
+    if (a.residual != nullptr) {
+      const Chunk<T> res = row.load(static_cast<const T*>(a.residual) + r * a.ldr, c);
 #pragma unroll
-    for (int i = 0; i < K; ++i) sum[i] += float(res.v[i]);
-    if (a.residual == a.y) {
-      row.store_rest(y, c, sum);
-      return;
+      for (int i = 0; i < K; ++i) sum[i] += float(res.v[i]);
     }
+    if (a.residual == a.y)
+      row.store_rest(y, c, sum);
+    else
+      row.store(y, c, sum);
   }
-  row.store(y, c, sum);
 }
 
 // L lanes a row, which they walk: the products' sums stay in registers.
@@ -102,44 +105,45 @@ template <typename T, int L, int KM>
 __global__ __launch_bounds__(kThreads) void k_combine_bwd(RouteArgs a) {
   constexpr int K = kChunk<T>;
   const Row<T> row(a.width);
-  const int64_t r = int64_t(blockIdx.x) * (kThreads / L) + threadIdx.x / L;
   const int l = threadIdx.x % L;
-  if (r >= a.rows) return;      // all lanes of a row together
-  int32_t at[KM];
-  float w[KM], dot[KM] = {};
-  load_places<KM>(a, r, at);
-  load_weights<KM>(a, r, w);
-  const T* const dy = static_cast<const T*>(a.dy) + r * a.lddy;
-  const T* const ys = static_cast<const T*>(a.x);
-  T* const dys = static_cast<T*>(a.y);
-  for (int c = l; c < row.chunks; c += L) {
-    const Chunk<T> g = row.load(dy, c);
-    if (a.dweights != nullptr) {
-      Chunk<T> v[KM];
+  // all lanes of a row together
+  for (int64_t r = first_item<L>(); r < a.rows; r += next_item<L>()) {
+    int32_t at[KM];
+    float w[KM], dot[KM] = {};
+    load_places<KM>(a, r, at);
+    load_weights<KM>(a, r, w);
+    const T* const dy = static_cast<const T*>(a.dy) + r * a.lddy;
+    const T* const ys = static_cast<const T*>(a.x);
+    T* const dys = static_cast<T*>(a.y);
+    for (int c = l; c < row.chunks; c += L) {
+      const Chunk<T> g = row.load(dy, c);
+      if (a.dweights != nullptr) {
+        Chunk<T> v[KM];
 #pragma unroll
-      for (int j = 0; j < KM; ++j) v[j] = row.load(ys + (at[j] < 0 ? 0 : at[j]) * a.ldx, c);
-      const int again = row.again(c);
+        for (int j = 0; j < KM; ++j) v[j] = row.load(ys + (at[j] < 0 ? 0 : at[j]) * a.ldx, c);
+        const int again = row.again(c);
 #pragma unroll
-      for (int j = 0; j < KM; ++j)
+        for (int j = 0; j < KM; ++j)
 #pragma unroll
-        for (int i = 0; i < K; ++i) dot[j] = i < again ? dot[j] : fmaf(float(g.v[i]), float(v[j].v[i]), dot[j]);
+          for (int i = 0; i < K; ++i) dot[j] = i < again ? dot[j] : fmaf(float(g.v[i]), float(v[j].v[i]), dot[j]);
+      }
+      if (dys != nullptr)
+#pragma unroll
+        for (int j = 0; j < KM; ++j)
+          if (at[j] >= 0) {
+            float o[K];
+#pragma unroll
+            for (int i = 0; i < K; ++i) o[i] = w[j] * float(g.v[i]);
+            row.store(dys + at[j] * a.ldy, c, o);
+          }
     }
-    if (dys != nullptr)
+    if (a.dweights == nullptr) continue;
 #pragma unroll
-      for (int j = 0; j < KM; ++j)
-        if (at[j] >= 0) {
-          float o[K];
+    for (int j = 0; j < KM; ++j) {
 #pragma unroll
-          for (int i = 0; i < K; ++i) o[i] = w[j] * float(g.v[i]);
-          row.store(dys + at[j] * a.ldy, c, o);
-        }
-  }
-  if (a.dweights == nullptr) return;
-#pragma unroll
-  for (int j = 0; j < KM; ++j) {
-#pragma unroll
-    for (int d = 1; d < L; d <<= 1) dot[j] += __shfl_xor(dot[j], d, 64);
-    if (j < a.k && l == 0) a.dweights[r * a.k + j] = at[j] < 0 ? 0.0f : dot[j];
+      for (int d = 1; d < L; d <<= 1) dot[j] += __shfl_xor(dot[j], d, 64);
+      if (j < a.k && l == 0) a.dweights[r * a.k + j] = at[j] < 0 ? 0.0f : dot[j];
+    }
   }
 }
 
@@ -148,7 +152,7 @@ enum Way { kDispatch, kCombine, kCombineBwd };
 template <typename T, int L, int KM>
 hipError_t go(Way way, const RouteArgs& a, hipStream_t st) {
   const int64_t slices = way == kCombineBwd ? 1 : ((a.width + kChunk<T> - 1) / kChunk<T> + L - 1) / L;
-  const unsigned grid = unsigned((a.rows * slices + kThreads / L - 1) / (kThreads / L));
+  const unsigned grid = grid_of((a.rows * slices + kThreads / L - 1) / (kThreads / L));
   if (way == kDispatch)
     k_dispatch<T, L, KM><<<grid, kThreads, 0, st>>>(a, int(slices));
   else if (way == kCombine)

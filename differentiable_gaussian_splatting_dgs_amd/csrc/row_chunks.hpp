@@ -74,5 +74,12 @@ struct Row {
 // without a chunk.
 inline int row_lanes(int chunks) { return chunks <= 8 ? 8 : chunks <= 16 ? 16 : chunks <= 32 ? 32 : 64; }
 
+// A launch takes less than 2^32 threads: kernels whose items may be more walk
+// them with the grid's stride.
+inline unsigned grid_of(int64_t workgroups) {
+  constexpr int64_t kMost = int64_t(1) << 22;
+  return unsigned(workgroups < kMost ? workgroups : kMost);
+}
+
 }  // namespace net
 }  // namespace gs

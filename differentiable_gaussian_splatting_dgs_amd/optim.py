@@ -1,0 +1,210 @@
+"""AdamW over a network's tensors in one launch, moments in 32 or in 8 bits.
+
+``gs_adamw`` carries the C entry point's name (``include/gs.h``) and takes
+lists of tensors; ``AdamW`` keeps the moments and what a call has to know
+about them, as a training program does.  Parameters are contiguous float32
+tensors on one GPU; gradients bfloat16, float16 or float32; ``copies`` are the
+16-bit (or float32) tensors that kernels read in the parameters' place, written
+in the same pass.  Errors as in the network operators: ``ValueError`` or
+``GSError``, before any work is enqueued.
+"""
+from __future__ import annotations
+
+import ctypes as C
+
+import torch
+
+from . import GS_ADAMW_BLOCK, _check, gs_adamw_tensor, lib
+from .network import _F32, _I64, _TYPES, _U8, _launch, _on_gpu
+
+
+def _blocks(n):
+    return -(-n // GS_ADAMW_BLOCK)
+
+
+def _tensor(t, dtypes, n, device, name):
+    """The address of a contiguous tensor of n elements."""
+    if t.dtype not in dtypes or t.numel() != n:
+        raise ValueError(f"{name} is {t.dtype} of {t.numel()} elements: {' or '.join(map(str, dtypes))} of {n} expected")
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} has to be contiguous and on {device}")
+    return t.data_ptr()
+
+
+def _entry(e, device, i, param, m, v, m_scale, v_scale, copy):
+    n = param.numel()
+    e.param = _tensor(param, (_F32,), n, device, f"parameter {i}")
+    if (m_scale is None) != (v_scale is None):
+        raise ValueError(f"parameter {i}: one scale of two")
+    kinds = (_F32,) if m_scale is None else (_U8,)
+    e.m = _tensor(m, kinds, n, device, f"m of parameter {i}")
+    e.v = _tensor(v, kinds, n, device, f"v of parameter {i}")
+    e.m_scale = e.v_scale = e.copy = None
+    if m_scale is not None:
+        e.m_scale = _tensor(m_scale, (_F32,), _blocks(n), device, f"m's scales of parameter {i}")
+        e.v_scale = _tensor(v_scale, (_F32,), _blocks(n), device, f"v's scales of parameter {i}")
+    if copy is not None:
+        e.copy = _tensor(copy, tuple(_TYPES), n, device, f"copy of parameter {i}")
+        e.copy_type = _TYPES[copy.dtype]
+
+
+def _grad(e, device, i, param, grad):
+    """Fills in a gradient; None: nothing is done for this tensor."""
+    if grad is None:
+        e.n = 0
+        return
+    e.grad = _tensor(grad, tuple(_TYPES), param.numel(), device, f"gradient {i}")
+    e.grad_type = _TYPES[grad.dtype]
+    e.n = param.numel()
+
+
+def _scalar(t, dtype, device, name):
+    return None if t is None else _tensor(t, (dtype,), 1, device, name)
+
+
+def _call(s, first, table, count, numbers, step, grad_scale, seed):
+    device = first.device
+    step_at = _scalar(step, _I64, device, "step") if isinstance(step, torch.Tensor) else None
+    scale_at = _scalar(grad_scale, _F32, device, "grad_scale")
+    _on_gpu(first, "parameter 0")
+    st = lib().gs_adamw(table, count, *numbers, 0 if step_at is not None else step, step_at, scale_at, seed, s)
+    if st:
+        _check(st, "gs_adamw")
+
+
+def gs_adamw(params, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, m_scales=None,
+             v_scales=None, copies=None, grad_scale=None, seed=0, stream=None):
+    """One AdamW step, in place, over lists of tensors: ``params`` float32,
+    ``grads`` (an entry may be None: that tensor is left as it is), moments
+    ``m`` and ``v`` (float32, or uint8 codes where ``m_scales[i]`` and
+    ``v_scales[i]``, float32 of one for each 256 values, are given), ``copies``
+    (entries may be None).  ``step`` counts from 1 on: a number, or a device
+    int64 tensor read there (for a captured call).  ``grad_scale``: device
+    float32, times which the gradients are taken.  ``seed`` fixes the random
+    rounding of moments in 8 bits."""
+    count = len(params)
+    none = [None] * count
+    lists = (grads, m, v, m_scales or none, v_scales or none, copies or none)
+    if any(len(x) != count for x in lists):
+        raise ValueError(f"{count} parameters with lists of {[len(x) for x in lists]}")
+    if count == 0:
+        return
+    table = (gs_adamw_tensor * count)()
+    device = params[0].device
+    for i, (p, g, *rest) in enumerate(zip(params, *lists)):
+        _entry(table[i], device, i, p, *rest)
+        _grad(table[i], device, i, p, g)
+    _launch(_call, params[0], stream, table, count, (lr, beta1, beta2, eps, weight_decay), step, grad_scale, seed)
+
+
+def _moment(s, codes, scales, moment, dtype, values):
+    n, device = codes.numel(), codes.device
+    at = _tensor(codes, (_U8,), n, device, "codes")
+    scales_at = _tensor(scales, (_F32,), _blocks(n), device, "scales")
+    if dtype not in _TYPES:
+        raise ValueError(f"values of {dtype}: bfloat16, float16 or float32 expected")
+    _on_gpu(codes, "codes")
+    if values is None:
+        values = torch.empty(codes.shape, dtype=dtype, device=device)
+    else:
+        _tensor(values, (dtype,), n, device, "values")
+    st = lib().gs_adamw_moment(at, scales_at, n, moment, _TYPES[dtype], values.data_ptr(), s)
+    if st:
+        _check(st, "gs_adamw_moment")
+    return values
+
+
+def gs_adamw_moment(codes, scales, moment, dtype=torch.float32, values=None, stream=None):
+    """The values (of ``dtype``, in codes' shape) of a moment in 8 bits:
+    ``moment`` 1 for m, 2 for v."""
+    return _launch(_moment, codes, stream, scales, moment, dtype, values)
+
+
+class AdamW:
+    """The optimiser of a list of float32 parameters.
+
+    ``bits`` 8 holds the moments of tensors of at least ``min_8bit`` elements
+    in 8 bits (2 bytes a parameter instead of 8); ``copies[i]`` (or None) is
+    written with parameter i's new values.  ``capturable`` keeps the step's
+    number on the device, so that a captured ``step`` counts on with each
+    replay.  ``state``: (m, v, m_scale, v_scale) of each tensor to go on from,
+    taken as they are (scales None for moments in 32 bits), ``step`` the number
+    of steps done."""
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, bits=32, min_8bit=4096,
+                 copies=None, seed=0, capturable=False, state=None, step=0):
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("no parameters")
+        if bits not in (8, 32):
+            raise ValueError(f"bits = {bits}: 8 or 32 expected")
+        self.lr, self.betas, self.eps, self.weight_decay, self.seed = lr, betas, eps, weight_decay, seed
+        count, device = len(self.params), self.params[0].device
+        self.copies = list(copies) if copies is not None else [None] * count
+        if state is None:
+            state = []
+            for p in self.params:
+                n = p.numel()
+                if bits == 8 and n >= min_8bit:
+                    state.append(tuple(torch.zeros(n, dtype=_U8, device=device) for _ in range(2))
+                                 + tuple(torch.zeros(_blocks(n), device=device) for _ in range(2)))
+                else:
+                    state.append((torch.zeros(n, device=device), torch.zeros(n, device=device), None, None))
+        self.state = [tuple(s) for s in state]
+        if len(self.copies) != count or len(self.state) != count:
+            raise ValueError(f"{count} parameters, {len(self.copies)} copies, {len(self.state)} states")
+        self.steps = step
+        self.step_dev = torch.tensor([step], dtype=_I64, device=device) if capturable else None
+        self._table, self._held = None, None
+
+    def _tensors(self):
+        for p, c, s in zip(self.params, self.copies, self.state):
+            yield p
+            yield from (x for x in (c, *s) if x is not None)
+
+    def step(self, grads=None, grad_scale=None, stream=None):
+        """One step with ``grads`` (default: each parameter's .grad; None leaves
+        a tensor as it is), times the device float32 ``grad_scale``."""
+        grads = [p.grad for p in self.params] if grads is None else grads
+        count, device = len(self.params), self.params[0].device
+        if len(grads) != count:
+            raise ValueError(f"{len(grads)} gradients of {count} parameters")
+        # the addresses as they are now: a tensor's storage may have been replaced
+        held = [t.data_ptr() for t in self._tensors()]
+        if held != self._held:
+            table = (gs_adamw_tensor * count)()
+            for i, (p, c, (m, v, ms, vs)) in enumerate(zip(self.params, self.copies, self.state)):
+                _entry(table[i], device, i, p, m, v, ms, vs, c)
+            self._table, self._held = table, held
+        for i, g in enumerate(grads):
+            _grad(self._table[i], device, i, self.params[i], g)
+        numbers = (self.lr, *self.betas, self.eps, self.weight_decay)
+        _launch(self._enqueue, self.params[0], stream, numbers, grad_scale)
+        self.steps += 1
+
+    def _enqueue(self, s, first, numbers, grad_scale):
+        step = self.steps + 1
+        if self.step_dev is not None:
+            _on_gpu(first, "parameter 0")
+            step = self.step_dev.add_(1)
+        _call(s, first, self._table, len(self.params), numbers, step, grad_scale, self.seed)
+
+    def state_dict(self):
+        """The moments, as they are held, and the number of steps done."""
+        steps = self.steps if self.step_dev is None else int(self.step_dev)
+        return {"state": [tuple(None if x is None else x.clone() for x in s) for s in self.state], "steps": steps}
+
+    def load_state_dict(self, d):
+        if len(d["state"]) != len(self.state):
+            raise ValueError(f"state of {len(d['state'])} tensors for {len(self.state)}")
+        for mine, theirs in zip(self.state, d["state"]):
+            if any((a is None) != (b is None) or (a is not None and (a.dtype != b.dtype or a.shape != b.shape))
+                   for a, b in zip(mine, theirs)):
+                raise ValueError("state of other sizes or bits")
+        for mine, theirs in zip(self.state, d["state"]):
+            for a, b in zip(mine, theirs):
+                if a is not None:
+                    a.copy_(b)
+        self.steps = int(d["steps"])
+        if self.step_dev is not None:
+            self.step_dev.fill_(self.steps)

@@ -920,6 +920,65 @@ gs_status gs_combine_bwd(const void* dy, int64_t lddy, const void* ys, int64_t l
                          const float* weights, int64_t rows, int32_t k, int32_t width, int32_t type, void* dys,
                          int64_t lddys, float* dweights, void* stream);
 
+/* One tensor of gs_adamw.  All pointers are device memory, aligned to their
+ * elements; ranges that are written do not overlap any other of the call. */
+typedef struct gs_adamw_tensor {
+  float* param;        /* [n] in/out */
+  const void* grad;    /* [n] of grad_type */
+  void* m;             /* [n] in/out: fp32, or codes (uint8) with m_scale */
+  void* v;             /* the same, with v_scale */
+  float* m_scale;      /* NULL: moments in 32 bits; else [ceil(n / 256)] in/out */
+  float* v_scale;      /* NULL exactly where m_scale is */
+  void* copy;          /* [n] out: the new param rounded to copy_type; or NULL */
+  int64_t n;           /* 0: nothing is done for this tensor */
+  int32_t grad_type;   /* gs_type */
+  int32_t copy_type;   /* gs_type; read where copy is not NULL */
+} gs_adamw_tensor;
+
+/* values that share a scale, and most elements of a tensor */
+#define GS_ADAMW_BLOCK 256
+#define GS_MAX_ADAMW_SIZE ((int64_t)1 << 35)
+
+/* One AdamW step over many tensors, with t the step's number (from 1 on) and
+ * g = grad * *grad_scale:
+ *   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2;
+ *   param = param (1 - lr weight_decay)
+ *           - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ * param and 32-bit moments are fp32.  With scales, a moment is held in 8 bits,
+ * a power of two (the scale) for each 256 of its values:
+ *   m   sign, 4 bits e, 3 bits f;  |m| = scale 2^max(e - 1, 0) (f + (e > 0 ? 8 : 0))
+ *       (times 2^9, the scale's factor is the 8-bit float e4m3fn); 127, 255: NaN
+ *   v   5 bits e, 3 bits f, in the same way; 255: NaN
+ * All zeros are the moments before the first step.  The new moments are worked
+ * out in 64 bits, the update takes them unrounded (as fp32), and they are then
+ * rounded up or down at random, so that a moment that a step changes by less
+ * than half of an eighth still follows its mean.  The random numbers are a
+ * function of seed, t, the tensor's place in the list and the element's: the
+ * same call gives the same bits.  The scale is the smallest that holds the
+ * largest finite magnitude of the 256 and at least 2^-126; a v over 0 is never
+ * rounded to 0.  A moment that is infinite or NaN becomes NaN, that one alone.
+ *   tensors      host, [count]; read during the call.  Moments in 8 and in 32
+ *                bits may be mixed.
+ *   step         t, or ignored where
+ *   step_dev     is not NULL: device, t as read there (less than 1 counts as
+ *                1), for a captured call whose replays are further steps
+ *   grad_scale   device, fp32 scalar, or NULL: 1
+ * Errors: GS_ERR_INVALID_ARG for a negative count, n outside [0,
+ * GS_MAX_ADAMW_SIZE], step below 1, an unknown type, lr, eps or weight_decay
+ * not finite, a beta outside [0, 1), eps (as fp32) not above 0, scales that do
+ * not match, a NULL or misaligned array, or written ranges that overlap. */
+gs_status gs_adamw(const gs_adamw_tensor* tensors, int32_t count, double lr, double beta1, double beta2, double eps,
+                   double weight_decay, int64_t step, const int64_t* step_dev, const float* grad_scale,
+                   uint64_t seed, void* stream);
+
+/* The values of a moment in 8 bits: moment 1 is m, 2 is v.
+ *   codes, scales   device, [n] uint8 and [ceil(n / 256)] fp32
+ *   values       device out, [n] of `type` (bf16 and fp32 hold them exactly)
+ * Errors: GS_ERR_INVALID_ARG for an unknown type or moment, n outside [0,
+ * GS_MAX_ADAMW_SIZE], a NULL or misaligned array. */
+gs_status gs_adamw_moment(const uint8_t* codes, const float* scales, int64_t n, int32_t moment, int32_t type,
+                          void* values, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -189,3 +189,81 @@ I4 = torch.int32
 def test_routing_binding_refuses(call, match):
     with pytest.raises(ValueError, match=match):
         call()
+
+
+# --- AdamW -----------------------------------------------------------------------------
+
+def _adamw(count=1, lr=1e-3, b1=0.9, b2=0.999, eps=1e-8, wd=0.0, step=1, step_dev=None, scale=None, tensors=True, **kw):
+    t = gs.gs_adamw_tensor(param=1 << 20, grad=1 << 21, m=1 << 22, v=1 << 23, n=0, grad_type=2, copy_type=2)
+    for k, v in kw.items():
+        setattr(t, k, v)
+    return gs.lib().gs_adamw(C.byref(t) if tensors else None, count, lr, b1, b2, eps, wd, step, step_dev, scale, 0, None)
+
+
+NAN = float("nan")
+
+
+@pytest.mark.parametrize("kw,word", [
+    (dict(count=-1), b"count"), (dict(tensors=False), b"tensors"), (dict(lr=NAN), b"lr"),
+    (dict(wd=float("inf")), b"weight_decay"), (dict(b1=1.0), b"beta"), (dict(b1=-0.1), b"beta"), (dict(b2=NAN), b"beta"),
+    (dict(eps=0.0), b"eps"), (dict(eps=1e-60), b"eps"), (dict(eps=NAN), b"eps"), (dict(eps=1e60), b"eps"),
+    (dict(step=0), b"step"), (dict(step_dev=P(12)), b"step_dev"), (dict(scale=P(6)), b"grad_scale"),
+    (dict(n=-1), b"n ="), (dict(n=(1 << 35) + 1), b"n ="), (dict(n=4, grad_type=3), b"grad_type"),
+    (dict(n=4, param=None), b"param"), (dict(n=4, param=2), b"param"), (dict(n=4, grad=None), b"grad"),
+    (dict(n=4, grad=6), b"grad"), (dict(n=4, m=None), b"m or v"), (dict(n=4, v=10), b"m or v"),
+    (dict(n=4, m_scale=64), b"scale"), (dict(n=4, v_scale=64), b"scale"), (dict(n=4, m_scale=66, v_scale=128), b"scale"),
+    (dict(n=4, copy=1 << 24, copy_type=9), b"copy_type"), (dict(n=4, copy=2, copy_type=2), b"copy"),
+    (dict(n=4, m=1 << 20), b"overlap"), (dict(n=1 << 20, m=(1 << 20) + 64), b"overlap"),
+    (dict(n=4, copy=(1 << 23) + 14, copy_type=0), b"overlap"),
+    (dict(n=600, m_scale=1 << 24, v_scale=(1 << 24) + 8), b"overlap"),
+])
+def test_adamw_refused(kw, word):
+    assert _adamw(**kw) == gs.GS_ERR_INVALID_ARG
+    assert word in gs.lib().gs_last_error(), gs.lib().gs_last_error()
+
+
+def test_adamw_nothing_to_do():
+    assert _adamw(count=0, tensors=False) == gs.GS_OK
+    assert _adamw(n=0, param=None, grad=None, m=None, v=None) == gs.GS_OK
+    gs.gs_adamw([], [], [], [], 1, 1e-3)
+
+
+@pytest.mark.parametrize("kw,word", [
+    (dict(n=-1), b"n ="), (dict(moment=0), b"moment"), (dict(moment=3), b"moment"), (dict(typ=3), b"type"),
+    (dict(codes=None), b"codes"), (dict(scales=None), b"scales"), (dict(scales=P(18)), b"scales"),
+    (dict(values=None), b"values"), (dict(values=P(17)), b"values"),
+])
+def test_adamw_moment_refused(kw, word):
+    a = dict(codes=P(16), scales=P(16), n=4, moment=1, typ=0, values=P(16)) | kw
+    assert gs.lib().gs_adamw_moment(a["codes"], a["scales"], a["n"], a["moment"], a["typ"], a["values"],
+                                    None) == gs.GS_ERR_INVALID_ARG
+    assert word in gs.lib().gs_last_error()
+
+
+U1 = torch.uint8
+
+
+@pytest.mark.parametrize("call,match", [
+    (lambda: gs.gs_adamw([_t(4)], [_t(4)], [_t(4)], [], 1, 1e-3), "lists"),
+    (lambda: gs.gs_adamw([_t(4, dtype=torch.bfloat16)], [_t(4)], [_t(4)], [_t(4)], 1, 1e-3), "parameter 0"),
+    (lambda: gs.gs_adamw([_t(4, 4).t()[1:]], [_t(12)], [_t(12)], [_t(12)], 1, 1e-3), "contiguous"),
+    (lambda: gs.gs_adamw([_t(4)], [_t(5)], [_t(4)], [_t(4)], 1, 1e-3), "gradient 0"),
+    (lambda: gs.gs_adamw([_t(4)], [_t(4, dtype=torch.float64)], [_t(4)], [_t(4)], 1, 1e-3), "gradient 0"),
+    (lambda: gs.gs_adamw([_t(4)], [_t(4)], [_t(4, dtype=U1)], [_t(4)], 1, 1e-3), "m of"),
+    (lambda: gs.gs_adamw([_t(4)], [_t(4)], [_t(4, dtype=U1)], [_t(4, dtype=U1)], 1, 1e-3, m_scales=[_t(1)]), "scale"),
+    (lambda: gs.gs_adamw([_t(300)], [_t(300)], [_t(300, dtype=U1)], [_t(300, dtype=U1)], 1, 1e-3, m_scales=[_t(1)],
+                         v_scales=[_t(2)]), "scales"),
+    (lambda: gs.gs_adamw([_t(4)], [_t(4)], [_t(4)], [_t(4)], 1, 1e-3, copies=[_t(3)]), "copy"),
+    (lambda: gs.gs_adamw([_t(4)], [_t(4)], [_t(4)], [_t(4)], _t(1), 1e-3), "step"),
+    (lambda: gs.gs_adamw([_t(4)], [_t(4)], [_t(4)], [_t(4)], 1, 1e-3, grad_scale=_t(2)), "grad_scale"),
+    (lambda: gs.gs_adamw([_t(4)], [_t(4)], [_t(4)], [_t(4)], 1, 1e-3), "GPU tensor"),
+    (lambda: gs.gs_adamw_moment(_t(4), _t(1), 1), "codes"), (lambda: gs.gs_adamw_moment(_t(4, dtype=U1), _t(2), 1), "scales"),
+    (lambda: gs.gs_adamw_moment(_t(4, dtype=U1), _t(1), 1, torch.int32), "int32"),
+    (lambda: gs.gs_adamw_moment(_t(4, dtype=U1), _t(1), 1), "GPU tensor"),
+    (lambda: gs.AdamW([]), "no parameters"), (lambda: gs.AdamW([_t(4)], bits=16), "bits"),
+    (lambda: gs.AdamW([_t(4)], copies=[None, None]), "copies"),
+    (lambda: gs.AdamW([_t(4)]).step([]), "gradients"), (lambda: gs.AdamW([_t(4)]).step([_t(4)]), "GPU tensor"),
+])
+def test_adamw_binding_refuses(call, match):
+    with pytest.raises(ValueError, match=match):
+        call()
