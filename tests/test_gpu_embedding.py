@@ -160,8 +160,15 @@ def _check_bwd(gs, dy, ids, table_rows, scale=1.0, dtable=None, sort=None, **kw)
     flat = ids.reshape(-1).long()
     there = (flat >= 0) & (flat < table_rows)
     at, d = flat[there], dy.double()[there]
-    want = torch.zeros(table_rows, dy.shape[1], dtype=torch.float64, device="cuda").index_add_(0, at, d)
-    size = torch.zeros_like(want).index_add_(0, at, d.abs())
+    want = torch.zeros(table_rows, dy.shape[1], dtype=torch.float64, device="cuda")
+    size = torch.zeros_like(want)
+    found = at.unique()
+    if found.numel() <= 8:      # a great many atomic additions to one row take seconds
+        for v in found.tolist():
+            want[v], size[v] = d[at == v].sum(0), d[at == v].abs().sum(0)
+    else:
+        want.index_add_(0, at, d)
+        size.index_add_(0, at, d.abs())
     terms = torch.bincount(at, minlength=table_rows).double()[:, None]
     s = float(torch.tensor(scale))
     t = got.dtype
