@@ -20,10 +20,10 @@ __device__ __forceinline__ int64_t id_at(const void* __restrict__ ids, int id_by
 }
 
 // L lanes a row.
-template <typename T, int L>
+template <typename T, int L, bool kNarrow>
 __global__ __launch_bounds__(kThreads) void k_lookup(EmbedArgs a) {
   constexpr int K = kChunk<T>;
-  const Row<T> row(a.width);
+  const Row<T, kNarrow> row(a.width);
   constexpr int kRows = kThreads / L;
   for (int64_t r = int64_t(blockIdx.x) * kRows + threadIdx.x / L; r < a.rows; r += int64_t(gridDim.x) * kRows) {
     const int64_t id = id_at(a.ids, a.id_bytes, r);
@@ -55,11 +55,11 @@ __global__ __launch_bounds__(kThreads) void k_lookup(EmbedArgs a) {
 
 constexpr int kLongest = 128;      // positions of a stretch
 constexpr int kSpan = 32;          // an id over more stretches than that is joined by a whole workgroup
-constexpr int kJoinThreads = 1024;
 constexpr int kZeroRows = 8;       // table rows that L lanes look at
 
 struct Stretches {
   float* part;
+  int32_t* goes_on;         // the id that begins in a stretch and goes on behind it, or -1
   int64_t count;
   int32_t len, slices;      // slices: of 64 C chunks, across the row
 };
@@ -80,12 +80,12 @@ __device__ __forceinline__ int64_t positions(const EmbedArgs& a) {
   return n < 0 ? 0 : (n < a.rows ? n : a.rows);
 }
 
-template <typename T, typename O, int L, int C>
+template <typename T, typename O, int L, int C, bool kNarrow>
 __global__ __launch_bounds__(kThreads) void k_sum(EmbedArgs a, Stretches s, int64_t sum_groups) {
   constexpr int K = kChunk<T>, kGroups = kThreads / L, kAhead = 8 / C < 2 ? 2 : 8 / C;
   __shared__ int32_t s_row[kGroups * kLongest];
   __shared__ int32_t s_key[kGroups * kLongest + 2];      // one position more on either side
-  const Row<T> row(a.width);
+  const Row<T, kNarrow> row(a.width);
   const int l = threadIdx.x % L, g = threadIdx.x / L;
   if (int64_t(blockIdx.x) >= sum_groups) {
     // rows of no id
@@ -143,12 +143,11 @@ __global__ __launch_bounds__(kThreads) void k_sum(EmbedArgs a, Stretches s, int6
     Chunk<T> x[kAhead][C];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int32_t r = p + u < end ? s_row[p + u] : -1;
+      // past the end, and of no row: any row, whose sum is not used
+      const int32_t r = std::max(s_row[std::min(p + u, end - 1)], 0);
 #pragma unroll
-      for (int j = 0; j < C; ++j) {
-        x[u][j] = Chunk<T>{};
-        if (r >= 0 && c[j] < row.chunks) x[u][j] = row.load(static_cast<const T*>(a.dy) + r * a.lddy, c[j]);
-      }
+      for (int j = 0; j < C; ++j)
+        x[u][j] = row.load(static_cast<const T*>(a.dy) + r * a.lddy, std::min(c[j], row.chunks - 1));
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
@@ -166,28 +165,32 @@ __global__ __launch_bounds__(kThreads) void k_sum(EmbedArgs a, Stretches s, int6
     }
   }
   const bool on = s_key[end + 1] == key;
+  if (slice == 0 && l == 0) s.goes_on[block * kGroups + g] = on && !head ? key : -1;
   flush(head || on, head ? 0 : 1);
 }
 
 // Partial rows to table rows.  The first workgroups: L lanes for each stretch
 // whose last id begins there and goes on over at most kSpan further ones.  The
-// others: a workgroup for every kSpan stretches and 64 columns; the one id that
-// reaches over their end, if it is longer than that and begins there.
-template <typename O, int L>
-__global__ __launch_bounds__(kJoinThreads) void k_join(EmbedArgs a, Stretches s, int64_t short_groups) {
-  constexpr int kGroups = kJoinThreads / L;
-  __shared__ float box[kJoinThreads / 64][64];
-  const Row<float> row(a.width);
+// others: a workgroup for every kSpan stretches and 64 columns; of the ids that
+// begin in them only the last can be longer than that.
+template <typename O, int L, bool kNarrow>
+__global__ __launch_bounds__(kThreads) void k_join(EmbedArgs a, Stretches s, int64_t short_groups) {
+  constexpr int kGroups = kThreads / L, kWaves = kThreads / 64;
+  __shared__ float box[kWaves][64];
+  const Row<float, kNarrow> row(a.width);
   const int64_t n = positions(a), used = (n + s.len - 1) / s.len;
+  // the last stretch of an id that goes on behind stretch st
+  auto last_of = [&](int32_t key, int64_t st) {
+    const int64_t end = std::min(a.offsets[key + 1], n);
+    return std::max(st, (std::max<int64_t>(end, 1) - 1) / s.len);
+  };
   if (int64_t(blockIdx.x) < short_groups) {
     const int64_t st = int64_t(blockIdx.x) * kGroups + threadIdx.x / L;
-    const int64_t p0 = st * s.len, p1 = p0 + s.len;
-    if (p1 >= n) return;
-    const int32_t k0 = key_at(a, row_at(a, p0)), k1 = key_at(a, row_at(a, p1 - 1)), k2 = key_at(a, row_at(a, p1));
-    const int32_t before = p0 > 0 ? key_at(a, row_at(a, p0 - 1)) : -2;
-    if (k1 < 0 || k1 != k2 || (k0 == k1 && before == k1)) return;
-    const int64_t last = std::min<int64_t>((std::max<int64_t>(a.offsets[k1 + 1], p1 + 1) - 1) / s.len, used - 1);
+    const int32_t key = st < used ? s.goes_on[st] : -1;
+    if (key < 0) return;
+    const int64_t last = last_of(key, st);
     if (last - st > kSpan) return;
+    O* const dst = static_cast<O*>(a.dtable) + key * a.lddt;
     for (int c = threadIdx.x % L; c < row.chunks; c += L) {
       Chunk<float> x = row.load(s.part + (st * 2 + 1) * a.width, c);
       float sum[4];
@@ -199,47 +202,42 @@ __global__ __launch_bounds__(kJoinThreads) void k_join(EmbedArgs a, Stretches s,
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum[i] += x.v[i];
       }
-      O* const dst = static_cast<O*>(a.dtable) + k1 * a.lddt;
-      if (a.width >= 4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dst[row.at(c) + i] = O(sum[i] * a.scale);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (i < a.width) dst[i] = O(sum[i] * a.scale);
-      }
+      for (int i = 0; i < 4; ++i)
+        if (row.at(c) + i < a.width) dst[row.at(c) + i] = O(sum[i] * a.scale);
     }
     return;
   }
-  const int across = (a.width + 63) / 64;
+  const int across = (a.width + 63) / 64, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t block = (int64_t(blockIdx.x) - short_groups) / across;
-  const int col = int((int64_t(blockIdx.x) - short_groups) - block * across) * 64 + (threadIdx.x & 63);
-  const int w = threadIdx.x >> 6;
-  const int64_t p = (block + 1) * kSpan * s.len;
-  if (p >= n) return;      // the whole workgroup, as below
-  const int32_t k = key_at(a, row_at(a, p));
-  if (k < 0 || k != key_at(a, row_at(a, p - 1))) return;
-  const int64_t begin = std::max<int64_t>(a.offsets[k], 0) / s.len;
-  const int64_t last = std::min<int64_t>((std::max<int64_t>(a.offsets[k + 1], 1) - 1) / s.len, used - 1);
-  if (last - begin <= kSpan || begin < block * kSpan || begin >= (block + 1) * kSpan) return;
+  const int col = int((int64_t(blockIdx.x) - short_groups) - block * across) * 64 + lane;
+  const int64_t mine = block * kSpan + lane;
+  const int32_t id = lane < kSpan && mine < used ? s.goes_on[mine] : -1;
+  const uint64_t begins = __ballot(id >= 0);
+  if (begins == 0) return;      // the whole workgroup, as below
+  const int top = 63 - __builtin_clzll(begins);
+  const int64_t st = block * kSpan + top;
+  const int32_t key = __shfl(id, top, 64);
+  const int64_t last = last_of(key, st);
+  if (last - st <= kSpan) return;
   float sum = 0.0f;
   if (col < a.width) {
-    if (w == 0) sum = s.part[(begin * 2 + 1) * a.width + col];
+    if (w == 0) sum = s.part[(st * 2 + 1) * a.width + col];
 #pragma unroll 16
-    for (int64_t q = begin + 1 + w; q <= last; q += kJoinThreads / 64) sum += s.part[q * 2 * a.width + col];
+    for (int64_t q = st + 1 + w; q <= last; q += kWaves) sum += s.part[q * 2 * a.width + col];
   }
-  box[w][threadIdx.x & 63] = sum;
+  box[w][lane] = sum;
   __syncthreads();
   if (w != 0 || col >= a.width) return;
   sum = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kJoinThreads / 64; ++i) sum += box[i][threadIdx.x];
-  static_cast<O*>(a.dtable)[k * a.lddt + col] = O(sum * a.scale);
+  for (int i = 0; i < kWaves; ++i) sum += box[i][lane];
+  static_cast<O*>(a.dtable)[key * a.lddt + col] = O(sum * a.scale);
 }
 
-template <typename T, int L>
+template <typename T, int L, bool kNarrow = false>
 hipError_t go_fwd(const EmbedArgs& a, hipStream_t st) {
-  k_lookup<T, L><<<grid_of((a.rows + kThreads / L - 1) / (kThreads / L)), kThreads, 0, st>>>(a);
+  k_lookup<T, L, kNarrow><<<grid_of((a.rows + kThreads / L - 1) / (kThreads / L)), kThreads, 0, st>>>(a);
   return hipGetLastError();
 }
 
@@ -260,30 +258,38 @@ Stretches stretches_of(int type, int64_t rows, int32_t width, void* ws) {
   const Shape f = shape_of((width + chunk - 1) / chunk);
   int32_t len = 8;
   while (len < kLongest && rows * f.slices * f.lanes > int64_t(len) * 64 * 8192) len *= 2;
-  return {static_cast<float*>(ws), (rows + len - 1) / len, len, f.slices};
+  Stretches s{nullptr, nullptr, (rows + len - 1) / len, len, f.slices};
+  s.goes_on = static_cast<int32_t*>(ws);
+  s.part = reinterpret_cast<float*>(static_cast<char*>(ws) + align_up(size_t(s.count) * 4, 256));
+  return s;
+}
+size_t stretches_bytes(const Stretches& s, int32_t width) {
+  return align_up(size_t(s.count) * 4, 256) + size_t(s.count) * 2 * size_t(width) * sizeof(float);
 }
 
-template <typename T, typename O, int L, int C>
+template <typename T, typename O, int L, int C, bool kNarrow = false>
 void go_sum(const EmbedArgs& a, const Stretches& s, hipStream_t st) {
   constexpr int kGroups = kThreads / L;
   const int64_t sums = (s.count + kGroups - 1) / kGroups * s.slices;
   const int64_t zeros = (a.num_rows + kGroups * kZeroRows - 1) / (kGroups * kZeroRows);
-  k_sum<T, O, L, C><<<unsigned(sums + zeros), kThreads, 0, st>>>(a, s, sums);
+  k_sum<T, O, L, C, kNarrow><<<unsigned(sums + zeros), kThreads, 0, st>>>(a, s, sums);
 }
 
-template <typename O, int L>
+template <typename O, int L, bool kNarrow = false>
 void go_join(const EmbedArgs& a, const Stretches& s, hipStream_t st) {
   if (s.count < 2) return;
-  const int64_t spans = (s.count + kJoinThreads / L - 1) / (kJoinThreads / L);
+  const int64_t spans = (s.count + kThreads / L - 1) / (kThreads / L);
   const int64_t longs = s.count > kSpan ? (s.count + kSpan - 1) / kSpan * ((a.width + 63) / 64) : 0;
-  k_join<O, L><<<unsigned(spans + longs), kJoinThreads, 0, st>>>(a, s, spans);
+  k_join<O, L, kNarrow><<<unsigned(spans + longs), kThreads, 0, st>>>(a, s, spans);
 }
 
 template <typename T, typename O>
 hipError_t embed_bwd(int type, const EmbedArgs& a, void* ws, hipStream_t st) {
   const Shape f = shape_of((a.width + kChunk<T> - 1) / kChunk<T>);
   const Stretches s = stretches_of(type, a.rows, a.width, ws);
-  if (f.lanes == 8)
+  if (a.width < kChunk<T>)
+    go_sum<T, O, 8, 1, true>(a, s, st);
+  else if (f.lanes == 8)
     go_sum<T, O, 8, 1>(a, s, st);
   else if (f.lanes == 16)
     go_sum<T, O, 16, 1>(a, s, st);
@@ -297,7 +303,9 @@ hipError_t embed_bwd(int type, const EmbedArgs& a, void* ws, hipStream_t st) {
     go_sum<T, O, 64, 3>(a, s, st);
   else
     go_sum<T, O, 64, 4>(a, s, st);
-  if (a.width <= 64)
+  if (a.width < 4)
+    go_join<O, 16, true>(a, s, st);
+  else if (a.width <= 64)
     go_join<O, 16>(a, s, st);
   else
     go_join<O, 64>(a, s, st);
@@ -306,6 +314,7 @@ hipError_t embed_bwd(int type, const EmbedArgs& a, void* ws, hipStream_t st) {
 
 template <typename T>
 hipError_t embed_fwd(const EmbedArgs& a, hipStream_t st) {
+  if (a.width < kChunk<T>) return go_fwd<T, 8, true>(a, st);
   switch (row_lanes((a.width + kChunk<T> - 1) / kChunk<T>)) {
     case 8: return go_fwd<T, 8>(a, st);
     case 16: return go_fwd<T, 16>(a, st);
@@ -318,7 +327,7 @@ hipError_t embed_fwd(const EmbedArgs& a, hipStream_t st) {
 }  // namespace net
 
 size_t embedding_bwd_ws_bytes(int type, int64_t rows, int64_t, int32_t width) {
-  return size_t(net::stretches_of(type, rows, width, nullptr).count) * 2 * size_t(width) * sizeof(float);
+  return net::stretches_bytes(net::stretches_of(type, rows, width, nullptr), width);
 }
 
 hipError_t launch_embedding_fwd(int type, const EmbedArgs& a, hipStream_t st) {

@@ -48,9 +48,9 @@ __device__ __forceinline__ int64_t next_item() {
   return int64_t(gridDim.x) * (kThreads / L);
 }
 
-template <typename T, int L, int KM>
+template <typename T, int L, int KM, bool kNarrow>
 __global__ __launch_bounds__(kThreads) void k_dispatch(RouteArgs a, int slices) {
-  const Row<T> row(a.width);
+  const Row<T, kNarrow> row(a.width);
   T* const xs = static_cast<T*>(a.y);
   for (int64_t item = first_item<L>(); item < int64_t(a.rows) * slices; item += next_item<L>()) {
     const int64_t r = item / slices;
@@ -65,10 +65,10 @@ __global__ __launch_bounds__(kThreads) void k_dispatch(RouteArgs a, int slices) 
   }
 }
 
-template <typename T, int L, int KM>
+template <typename T, int L, int KM, bool kNarrow>
 __global__ __launch_bounds__(kThreads) void k_combine(RouteArgs a, int slices) {
   constexpr int K = kChunk<T>;
-  const Row<T> row(a.width);
+  const Row<T, kNarrow> row(a.width);
   const T* const ys = static_cast<const T*>(a.x);
   for (int64_t item = first_item<L>(); item < int64_t(a.rows) * slices; item += next_item<L>()) {
     const int64_t r = item / slices;
@@ -101,10 +101,10 @@ __global__ __launch_bounds__(kThreads) void k_combine(RouteArgs a, int slices) {
 }
 
 // L lanes a row, which they walk: the products' sums stay in registers.
-template <typename T, int L, int KM>
+template <typename T, int L, int KM, bool kNarrow>
 __global__ __launch_bounds__(kThreads) void k_combine_bwd(RouteArgs a) {
   constexpr int K = kChunk<T>;
-  const Row<T> row(a.width);
+  const Row<T, kNarrow> row(a.width);
   const int l = threadIdx.x % L;
   // all lanes of a row together
   for (int64_t r = first_item<L>(); r < a.rows; r += next_item<L>()) {
@@ -149,30 +149,31 @@ __global__ __launch_bounds__(kThreads) void k_combine_bwd(RouteArgs a) {
 
 enum Way { kDispatch, kCombine, kCombineBwd };
 
-template <typename T, int L, int KM>
+template <typename T, int L, int KM, bool kNarrow>
 hipError_t go(Way way, const RouteArgs& a, hipStream_t st) {
   const int64_t slices = way == kCombineBwd ? 1 : ((a.width + kChunk<T> - 1) / kChunk<T> + L - 1) / L;
   const unsigned grid = grid_of((a.rows * slices + kThreads / L - 1) / (kThreads / L));
   if (way == kDispatch)
-    k_dispatch<T, L, KM><<<grid, kThreads, 0, st>>>(a, int(slices));
+    k_dispatch<T, L, KM, kNarrow><<<grid, kThreads, 0, st>>>(a, int(slices));
   else if (way == kCombine)
-    k_combine<T, L, KM><<<grid, kThreads, 0, st>>>(a, int(slices));
+    k_combine<T, L, KM, kNarrow><<<grid, kThreads, 0, st>>>(a, int(slices));
   else
-    k_combine_bwd<T, L, KM><<<grid, kThreads, 0, st>>>(a);
+    k_combine_bwd<T, L, KM, kNarrow><<<grid, kThreads, 0, st>>>(a);
   return hipGetLastError();
 }
 
-template <typename T, int L>
+template <typename T, int L, bool kNarrow = false>
 hipError_t by_choices(Way way, const RouteArgs& a, hipStream_t st) {
-  if (a.k <= 1) return go<T, L, 1>(way, a, st);
-  if (a.k <= 2) return go<T, L, 2>(way, a, st);
-  if (a.k <= 4) return go<T, L, 4>(way, a, st);
-  if (a.k <= 8) return go<T, L, 8>(way, a, st);
-  return go<T, L, kMaxChoices>(way, a, st);
+  if (a.k <= 1) return go<T, L, 1, kNarrow>(way, a, st);
+  if (a.k <= 2) return go<T, L, 2, kNarrow>(way, a, st);
+  if (a.k <= 4) return go<T, L, 4, kNarrow>(way, a, st);
+  if (a.k <= 8) return go<T, L, 8, kNarrow>(way, a, st);
+  return go<T, L, kMaxChoices, kNarrow>(way, a, st);
 }
 
 template <typename T>
 hipError_t by_width(Way way, const RouteArgs& a, hipStream_t st) {
+  if (a.width < kChunk<T>) return by_choices<T, 8, true>(way, a, st);
   switch (row_lanes((a.width + kChunk<T> - 1) / kChunk<T>)) {
     case 8: return by_choices<T, 8>(way, a, st);
     case 16: return by_choices<T, 16>(way, a, st);

@@ -2,6 +2,8 @@
 // rows (embedding.hip, route.hip).
 #pragma once
 
+#include <algorithm>
+
 #include "net_common.hpp"
 
 namespace gs {
@@ -10,57 +12,53 @@ namespace net {
 // A row of at least one chunk's width is covered by whole chunks, the last
 // one moved back onto the row's end, so that no width takes a slower path:
 // what two chunks share is read twice and written twice with the same values.
-// A narrower row is one part of a chunk.
-template <typename T>
+// kNarrow: a row of less than a chunk, its one chunk in part.  That is a
+// template's choice and not a branch, because a load behind a branch is waited
+// for before the next one is asked for.
+template <typename T, bool kNarrow>
 struct Row {
   static constexpr int K = kChunk<T>;
   int width, chunks;
-  __device__ __forceinline__ explicit Row(int w) : width(w), chunks((w + K - 1) / K) {}
+  __device__ __forceinline__ explicit Row(int w) : width(w), chunks(kNarrow ? 1 : (w + K - 1) / K) {}
   __device__ __forceinline__ int at(int c) const {     // first column of chunk c
-    return width < K ? 0 : (c * K + K <= width ? c * K : width - K);
+    return kNarrow ? 0 : std::min(c * K, width - K);
   }
   __device__ __forceinline__ int again(int c) const {  // its columns that the chunk before has too
     return c * K - at(c);
   }
   __device__ __forceinline__ Chunk<T> load(const T* __restrict__ row, int c) const {
-    return width >= K ? load_chunk(row + at(c)) : load_chunk_n(row, width);
+    if constexpr (kNarrow)
+      return load_chunk_n(row, width);
+    else
+      return load_chunk(row + at(c));
+  }
+  __device__ __forceinline__ void copy(T* __restrict__ row, int c, const Chunk<T>& v) const {
+    if constexpr (kNarrow)
+      store_chunk_n(row, v, width);
+    else
+      store_chunk(row + at(c), v);
   }
   template <typename O>      // O of T's size, or fp32 for 16-bit T
   __device__ __forceinline__ void store(O* __restrict__ row, int c, const float (&v)[K]) const {
-    if constexpr (sizeof(O) == sizeof(T)) {
-      Chunk<O> o;
+    if constexpr (kNarrow) {
 #pragma unroll
-      for (int i = 0; i < K; ++i) o.v[i] = O(v[i]);
-      if (width >= K)
-        store_chunk(row + at(c), o);
-      else
-        store_chunk_n(row, o, width);
+      for (int i = 0; i < K; ++i)
+        if (i < width) row[i] = O(v[i]);
     } else {
-      if (width >= K) {
+      constexpr int kPart = kChunk<O>;
 #pragma unroll
-        for (int h = 0; h < K; h += 4) {
-          Chunk<float> o;
+      for (int h = 0; h < K; h += kPart) {
+        Chunk<O> o;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o.v[i] = v[h + i];
-          store_chunk(row + at(c) + h, o);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < K; ++i)
-          if (i < width) row[i] = v[i];
+        for (int i = 0; i < kPart; ++i) o.v[i] = O(v[h + i]);
+        store_chunk(row + at(c) + h, o);
       }
     }
-  }
-  __device__ __forceinline__ void copy(T* __restrict__ row, int c, const Chunk<T>& v) const {
-    if (width >= K)
-      store_chunk(row + at(c), v);
-    else
-      store_chunk_n(row, v, width);
   }
   // Without the columns that the chunk before has too: what rows that are
   // read and written in place need.
   __device__ __forceinline__ void store_rest(T* __restrict__ row, int c, const float (&v)[K]) const {
-    if (width < K || again(c) == 0) {
+    if (kNarrow || again(c) == 0) {
       store(row, c, v);
       return;
     }
