@@ -19,26 +19,46 @@ __device__ __forceinline__ int64_t id_at(const void* __restrict__ ids, int id_by
   return id_bytes == 8 ? static_cast<const int64_t*>(ids)[i] : int64_t(static_cast<const int32_t*>(ids)[i]);
 }
 
-// L lanes a row.
-template <typename T, int L, bool kNarrow>
-__global__ __launch_bounds__(kThreads) void k_lookup(EmbedArgs a) {
+// Chunk c of N rows from r0 on.  Nothing here is behind a branch, so that the
+// ids, and then the chunks, are in flight together.
+template <typename T, typename I, int N, bool kNarrow>
+__device__ __forceinline__ void look_up(const EmbedArgs& a, const Row<T, kNarrow>& row, int64_t r0, int c) {
   constexpr int K = kChunk<T>;
-  const Row<T, kNarrow> row(a.width);
-  constexpr int kRows = kThreads / L;
-  for (int64_t r = int64_t(blockIdx.x) * kRows + threadIdx.x / L; r < a.rows; r += int64_t(gridDim.x) * kRows) {
-    const int64_t id = id_at(a.ids, a.id_bytes, r);
-    const bool there = id >= 0 && id < a.num_rows;
-    const T* __restrict__ src = static_cast<const T*>(a.table) + (there ? id : 0) * a.ldt;
-    T* __restrict__ dst = static_cast<T*>(a.y) + r * a.ldy;
-    for (int c = threadIdx.x % L; c < row.chunks; c += L) {
-      float v[K] = {};
-      if (there) {
-        const Chunk<T> x = row.load(src, c);
+  int64_t id[N];
 #pragma unroll
-        for (int i = 0; i < K; ++i) v[i] = float(x.v[i]) * a.scale;
-      }
-      row.store(dst, c, v);
-    }
+  for (int u = 0; u < N; ++u) id[u] = static_cast<const I*>(a.ids)[r0 + u];
+  Chunk<T> x[N];
+  bool there[N];
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    there[u] = id[u] >= 0 && id[u] < a.num_rows;
+    x[u] = row.load(static_cast<const T*>(a.table) + (there[u] ? id[u] : 0) * a.ldt, c);
+  }
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    float v[K];
+#pragma unroll
+    for (int i = 0; i < K; ++i) v[i] = there[u] ? float(x[u].v[i]) * a.scale : 0.0f;
+    row.store(static_cast<T*>(a.y) + (r0 + u) * a.ldy, c, v);
+  }
+}
+
+// Items are slices of kRows rows: L lanes, a chunk of each row for each lane.
+// A row alone waits for its id and then for its chunk, and as many waves as
+// fit do not make up for that: several rows at a time where there are many.
+template <typename T, typename I, int L, int kRows, bool kNarrow>
+__global__ __launch_bounds__(kThreads) void k_lookup(EmbedArgs a, int slices, int64_t items) {
+  constexpr int kGroups = kThreads / L;
+  const Row<T, kNarrow> row(a.width);
+  for (int64_t item = int64_t(blockIdx.x) * kGroups + threadIdx.x / L; item < items;
+       item += int64_t(gridDim.x) * kGroups) {
+    const int64_t part = item / slices, r0 = part * kRows;
+    const int c = int(item - part * slices) * L + threadIdx.x % L;
+    if (c >= row.chunks) continue;
+    if (kRows == 1 || r0 + kRows <= a.rows)
+      look_up<T, I, kRows>(a, row, r0, c);
+    else
+      for (int64_t r = r0; r < a.rows; ++r) look_up<T, I, 1>(a, row, r, c);
   }
 }
 
@@ -235,9 +255,18 @@ __global__ __launch_bounds__(kThreads) void k_join(EmbedArgs a, Stretches s, int
   static_cast<O*>(a.dtable)[key * a.lddt + col] = O(sum * a.scale);
 }
 
-template <typename T, int L, bool kNarrow = false>
+template <typename T, typename I, int L, bool kNarrow = false>
 hipError_t go_fwd(const EmbedArgs& a, hipStream_t st) {
-  k_lookup<T, L, kNarrow><<<grid_of((a.rows + kThreads / L - 1) / (kThreads / L)), kThreads, 0, st>>>(a);
+  constexpr int kGroups = kThreads / L, kRows = 4;
+  const int slices = ((a.width + kChunk<T> - 1) / kChunk<T> + L - 1) / L;
+  // several rows where that leaves 16 waves for each SIMD
+  const int64_t items = (a.rows + kRows - 1) / kRows * slices;
+  if (items * L >= 64 * 16384) {
+    k_lookup<T, I, L, kRows, kNarrow><<<grid_of((items + kGroups - 1) / kGroups), kThreads, 0, st>>>(a, slices, items);
+  } else {
+    const int64_t ones = a.rows * slices;
+    k_lookup<T, I, L, 1, kNarrow><<<grid_of((ones + kGroups - 1) / kGroups), kThreads, 0, st>>>(a, slices, ones);
+  }
   return hipGetLastError();
 }
 
@@ -312,14 +341,14 @@ hipError_t embed_bwd(int type, const EmbedArgs& a, void* ws, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <typename T>
+template <typename T, typename I>
 hipError_t embed_fwd(const EmbedArgs& a, hipStream_t st) {
-  if (a.width < kChunk<T>) return go_fwd<T, 8, true>(a, st);
+  if (a.width < kChunk<T>) return go_fwd<T, I, 8, true>(a, st);
   switch (row_lanes((a.width + kChunk<T> - 1) / kChunk<T>)) {
-    case 8: return go_fwd<T, 8>(a, st);
-    case 16: return go_fwd<T, 16>(a, st);
-    case 32: return go_fwd<T, 32>(a, st);
-    default: return go_fwd<T, 64>(a, st);
+    case 8: return go_fwd<T, I, 8>(a, st);
+    case 16: return go_fwd<T, I, 16>(a, st);
+    case 32: return go_fwd<T, I, 32>(a, st);
+    default: return go_fwd<T, I, 64>(a, st);
   }
 }
 
@@ -330,10 +359,15 @@ size_t embedding_bwd_ws_bytes(int type, int64_t rows, int64_t, int32_t width) {
   return net::stretches_bytes(net::stretches_of(type, rows, width, nullptr), width);
 }
 
+template <typename I>
+static hipError_t embed_fwd_of(int type, const EmbedArgs& a, hipStream_t st) {
+  if (type == kTypeBF16) return net::embed_fwd<net::bf16, I>(a, st);
+  if (type == kTypeF16) return net::embed_fwd<net::f16, I>(a, st);
+  return net::embed_fwd<float, I>(a, st);
+}
+
 hipError_t launch_embedding_fwd(int type, const EmbedArgs& a, hipStream_t st) {
-  if (type == kTypeBF16) return net::embed_fwd<net::bf16>(a, st);
-  if (type == kTypeF16) return net::embed_fwd<net::f16>(a, st);
-  return net::embed_fwd<float>(a, st);
+  return a.id_bytes == 4 ? embed_fwd_of<int32_t>(type, a, st) : embed_fwd_of<int64_t>(type, a, st);
 }
 
 hipError_t launch_embedding_bwd(int type, const EmbedArgs& a, void* ws, hipStream_t st) {

@@ -11,7 +11,9 @@
 // A row lies in the registers of L lanes, read once.  A logit becomes an
 // unsigned number that orders as it does, with its column below it, so that a
 // maximum of numbers is the choice: 32 bits for 16-bit logits, 64 for fp32.
-// Bound by the bytes of the logits.
+// The gradient's few chosen entries go through LDS to the lanes that hold
+// their columns.  Bound by the bytes of the logits, with the vector unit about
+// as busy: the instructions of the loops over the logits count.
 #include <algorithm>
 
 #include "row_chunks.hpp"
@@ -22,84 +24,150 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Orders as x does: NaN above all, -0 as 0; never 0.
-__device__ __forceinline__ uint32_t rank_of(float x) {
-  x += 0.0f;
-  if (x != x) return 0xFFFFFFFFu;
-  const uint32_t b = __builtin_bit_cast(uint32_t, x);
-  return (b >> 31) != 0 ? ~b : b | 0x80000000u;
-}
-__device__ __forceinline__ float value_of(uint32_t rank) {
-  return __builtin_bit_cast(float, (rank >> 31) != 0 ? rank & 0x7FFFFFFFu : ~rank);
-}
-constexpr uint32_t kMinusInf = 0x007FFFFFu;      // rank_of(-inf)
+// A logit's bits as a number: its magnitude, negated under a sign, plus that of
+// infinity, without sign.  Minus infinity becomes 0, zeros of either sign the
+// same; NaN of either sign comes out above infinity (a negative one by wrapping
+// around).  16-bit logits two at a time.
+typedef int16_t s16x2 __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
-// The numbers compared: rank, then the lower column.  0: no logit.
+// What is compared: the number, then the lower column.  Below kOne: minus
+// infinity, or (0) no logit.
 template <typename T>
 struct Pick {      // fp32
   using U = uint64_t;
-  static __device__ __forceinline__ U make(T x, int col) { return U(rank_of(x)) << 32 | (0xFFFFu - col); }
-  static __device__ __forceinline__ float value(U u) { return value_of(uint32_t(u >> 32)); }
-  static __device__ __forceinline__ bool none(U u) { return uint32_t(u >> 32) <= kMinusInf; }
-  static __device__ __forceinline__ int column(U u) { return 0xFFFF - int(uint32_t(u) & 0xFFFFu); }
+  static constexpr U kOne = U(1) << 32;
+  static constexpr int32_t kInf = 0x7F800000;
+  static __device__ __forceinline__ void make(const Chunk<float>& v, int col, U (&u)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int32_t b = __builtin_bit_cast(int32_t, v.v[i]);
+      const uint32_t m = uint32_t(b >> 31);
+      u[i] = U(((uint32_t(b) & 0x7FFFFFFFu) ^ m) - m + uint32_t(kInf)) << 32 | uint32_t(0xFFFF - col - i);
+    }
+  }
+  static __device__ __forceinline__ float value(U u) {
+    const uint32_t s = uint32_t(u >> 32) - uint32_t(kInf), m = uint32_t(int32_t(s) >> 31);
+    return __builtin_bit_cast(float, ((s ^ m) - m) | (s & 0x80000000u));
+  }
 };
-
-template <typename T>
+template <typename T, uint16_t kInf>
 struct Pick16 {
   using U = uint32_t;
-  static __device__ __forceinline__ U make(T x, int col) {
-    uint32_t b = __builtin_bit_cast(uint16_t, x);
-    const float f = float(x);
-    b = f == 0.0f ? 0x8000u : (b >> 15) != 0 ? b ^ 0xFFFFu : b | 0x8000u;
-    return (f != f ? 0xFFFFu : b) << 16 | (0xFFFFu - col);
+  static constexpr U kOne = 0x10000u;
+  static __device__ __forceinline__ void make(const Chunk<T>& v, int col, U (&u)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      u16x2 b;
+      __builtin_memcpy(&b, &v.v[i], 4);
+      const u16x2 m = __builtin_bit_cast(u16x2, __builtin_bit_cast(s16x2, b) >> s16x2{15, 15});
+      const u16x2 n = ((b & u16x2{0x7FFF, 0x7FFF}) ^ m) - m + u16x2{kInf, kInf};
+      uint32_t both;
+      __builtin_memcpy(&both, &n, 4);
+      u[i] = both << 16 | uint32_t(0xFFFF - col - i);
+      u[i + 1] = (both & 0xFFFF0000u) | uint32_t(0xFFFF - col - i - 1);
+    }
   }
-  static __device__ __forceinline__ T stored(U u) {
-    const uint32_t b = u >> 16;
-    return __builtin_bit_cast(T, uint16_t((b >> 15) != 0 ? b & 0x7FFFu : ~b));
+  // the logit's bits as the upper half of a word
+  static __device__ __forceinline__ uint32_t bits(U u) {
+    const uint32_t s = (u & 0xFFFF0000u) - (uint32_t(kInf) << 16), m = uint32_t(int32_t(s) >> 31);
+    return ((s ^ m) - m) | (s & 0x80000000u);
   }
-  static __device__ __forceinline__ float value(U u) { return float(stored(u)); }
-  static __device__ __forceinline__ bool none(U u) { return u == 0 || value(u) == -__builtin_inff(); }
-  static __device__ __forceinline__ int column(U u) { return 0xFFFF - int(u & 0xFFFFu); }
 };
 template <>
-struct Pick<bf16> : Pick16<bf16> {};
+struct Pick<bf16> : Pick16<bf16, 0x7F80> {
+  static __device__ __forceinline__ float value(U u) { return __builtin_bit_cast(float, bits(u)); }
+};
 template <>
-struct Pick<f16> : Pick16<f16> {};
+struct Pick<f16> : Pick16<f16, 0x7C00> {
+  static __device__ __forceinline__ float value(U u) {
+    return float(__builtin_bit_cast(f16, uint16_t(bits(u) >> 16)));
+  }
+};
+__device__ __forceinline__ int column_of(uint64_t u) { return 0xFFFF - int(uint32_t(u) & 0xFFFFu); }
 
 template <typename U>
-__device__ __forceinline__ U larger(U a, U b) { return a > b ? a : b; }
+__device__ __forceinline__ U larger(U a, U b) {
+  return a > b ? a : b;
+}
 
-template <int L>
-__device__ __forceinline__ uint32_t row_max(uint32_t v) {
-#pragma unroll
-  for (int d = 1; d < L; d <<= 1) v = larger(v, uint32_t(__shfl_xor(int(v), d, 64)));
-  return v;
+// v of a lane whose number differs in one bit (d: 1, 2, 16, 32) or, for 4 and
+// 8, of one in the other 4 or 8 lanes, which is as good for a maximum or sum.
+template <int d>
+__device__ __forceinline__ uint32_t from_other(uint32_t v) {
+  if constexpr (d == 1) return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0xB1, 0xF, 0xF, false));
+  if constexpr (d == 2) return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x4E, 0xF, 0xF, false));
+  if constexpr (d == 4) return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x141, 0xF, 0xF, false));   // mirror of 8
+  if constexpr (d == 8) return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x140, 0xF, 0xF, false));   // of 16
+  return uint32_t(__shfl_xor(int(v), d, 64));
 }
-template <int L>
-__device__ __forceinline__ uint64_t row_max(uint64_t v) {
-#pragma unroll
-  for (int d = 1; d < L; d <<= 1) {
-    const uint64_t o = uint64_t(uint32_t(__shfl_xor(int(v >> 32), d, 64))) << 32 |
-                       uint32_t(__shfl_xor(int(v), d, 64));
-    v = larger(v, o);
+template <int d>
+__device__ __forceinline__ uint64_t from_other(uint64_t v) {
+  return uint64_t(from_other<d>(uint32_t(v >> 32))) << 32 | from_other<d>(uint32_t(v));
+}
+template <int d>
+__device__ __forceinline__ float from_other(float v) {
+  return __builtin_bit_cast(float, from_other<d>(__builtin_bit_cast(uint32_t, v)));
+}
+template <int L, int d = 1, typename U>
+__device__ __forceinline__ U row_max(U v) {
+  if constexpr (d < L)
+    return row_max<L, 2 * d>(larger(v, from_other<d>(v)));
+  else
+    return v;
+}
+template <int L, int d = 1>
+__device__ __forceinline__ float row_sum(float v) {
+  if constexpr (d < L)
+    return row_sum<L, 2 * d>(v + from_other<d>(v));
+  else
+    return v;
+}
+
+// e^x, x <= 0 or NaN: the native exp2 of the rounded product with log2 e, and
+// what that rounding left out (2^-22 of the result in all).
+__device__ __forceinline__ float exp_of(float x) {
+  const float y = x * 1.44269504088896340736f;
+  const float rest = fmaf(x, 1.92596299112661746887e-8f, fmaf(x, 1.44269504088896340736f, -y));
+  const float e = __builtin_amdgcn_exp2f(y);
+  return y < -200.0f ? 0.0f : fmaf(e, rest * 0.69314718055994530942f, e);
+}
+
+// Which chunks a lane holds.  kExact: every lane's lie inside the row.  Else
+// one past the row's end is moved back onto it, and what another chunk has is
+// masked; kNarrow: a row of less than a chunk.
+enum Fit { kExact, kMoved, kNarrow };
+
+// Lane l's chunks of a row, all asked for before the first is waited for.
+template <typename T, int L, int C, Fit F>
+struct Held {
+  Chunk<T> v[C];
+  __device__ __forceinline__ static int first(int l, int j) { return (l + L * j) * kChunk<T>; }
+  __device__ __forceinline__ static int at(int l, int j, int groups) {
+    return F == kNarrow ? 0 : F == kExact ? first(l, j) : std::min(first(l, j), groups - kChunk<T>);
   }
-  return v;
-}
+  __device__ __forceinline__ void load(const GateArgs& a, int64_t r, int l) {
+    const T* __restrict__ x = static_cast<const T*>(a.logits) + r * a.ld;
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+      v[j] = F == kNarrow ? load_chunk_n(x, a.groups) : load_whole(x + at(l, j, a.groups));
+  }
+};
 
 // L lanes a row, C chunks a lane; KM: choices, rounded up.
-template <typename T, int L, int C, int KM>
-__device__ __forceinline__ void gate_row(const GateArgs& a, int64_t r, int l) {
+template <typename T, int L, int C, int KM, Fit F>
+__device__ __forceinline__ void gate_row(const GateArgs& a, int64_t r, int l, const Held<T, L, C, F>& x) {
   constexpr int K = kChunk<T>;
   using P = Pick<T>;
   using U = typename P::U;
-  const T* __restrict__ x = static_cast<const T*>(a.logits) + r * a.ld;
   U u[C][K];
 #pragma unroll
   for (int j = 0; j < C; ++j) {
-    const int c0 = (l + L * j) * K, n = std::min(K, std::max(0, a.groups - c0));
-    const Chunk<T> v = load_chunk_n(x + (n > 0 ? c0 : 0), n);
+    const int at = x.at(l, j, a.groups);
+    P::make(x.v[j], at, u[j]);
+    if constexpr (F != kExact)
 #pragma unroll
-    for (int i = 0; i < K; ++i) u[j][i] = i < n ? P::make(v.v[i], c0 + i) : U(0);
+      for (int i = 0; i < K; ++i) u[j][i] = at + i < x.first(l, j) || at + i >= a.groups ? U(0) : u[j][i];
   }
   float e[KM];
   int32_t id[KM];
@@ -112,120 +180,166 @@ __device__ __forceinline__ void gate_row(const GateArgs& a, int64_t r, int l) {
 #pragma unroll
       for (int i = 0; i < K; ++i) best = larger(best, u[j][i]);
     best = row_max<L>(best);
-    const bool none = P::none(best);
+    const bool none = best < P::kOne;
+    const float value = P::value(best);
     if (q == 0) {
-      top = none ? 0.0f : P::value(best);
+      top = value;
       if (a.renorm == 0) {
 #pragma unroll
         for (int j = 0; j < C; ++j)
 #pragma unroll
-          for (int i = 0; i < K; ++i) total += P::none(u[j][i]) ? 0.0f : expf(P::value(u[j][i]) - top);
-#pragma unroll
-        for (int d = 1; d < L; d <<= 1) total += __shfl_xor(total, d, 64);
+          for (int i = 0; i < K; ++i) total += u[j][i] < P::kOne ? 0.0f : exp_of(P::value(u[j][i]) - top);
+        total = row_sum<L>(total);
       }
     }
-    id[q] = none ? -1 : P::column(best);
-    e[q] = none ? 0.0f : expf(P::value(best) - top);
+    id[q] = none ? -1 : column_of(best);
+    // the first is e^0, or NaN of an infinite top
+    e[q] = none ? 0.0f : q == 0 ? 1.0f + (value - top) : exp_of(value - top);
     if (a.renorm != 0 && q < a.k) total += e[q];
-    // columns are distinct, so one element is the choice
+    if (q + 1 < KM)      // columns are distinct, so one element is the choice
 #pragma unroll
-    for (int j = 0; j < C; ++j)
+      for (int j = 0; j < C; ++j)
 #pragma unroll
-      for (int i = 0; i < K; ++i) u[j][i] = u[j][i] == best ? U(0) : u[j][i];
+        for (int i = 0; i < K; ++i) u[j][i] = u[j][i] == best ? U(0) : u[j][i];
   }
-  const bool dead = id[0] < 0;
+  // 1 / total, total of at least 1: the reciprocal and one step of Newton's
+  float share = __builtin_amdgcn_rcpf(total);
+  share = fmaf(fmaf(-total, share, 1.0f), share, share);
+  // choice q from lane q
 #pragma unroll
-  for (int q = 0; q < KM; ++q)
-    if (q < a.k && (q & (L - 1)) == l) {
-      a.ids[r * a.k + q] = id[q];
-      a.weights[r * a.k + q] = dead || id[q] < 0 ? 0.0f : e[q] / total;
+  for (int q0 = 0; q0 < KM; q0 += L) {
+    int32_t mine = id[q0];
+    float weight = e[q0];
+#pragma unroll
+    for (int q = q0 + 1; q < KM && q < q0 + L; ++q) {
+      mine = l == q - q0 ? id[q] : mine;
+      weight = l == q - q0 ? e[q] : weight;
     }
+    if (q0 + l < a.k && l < KM) {
+      a.ids[r * a.k + q0 + l] = mine;
+      a.weights[r * a.k + q0 + l] = mine < 0 ? 0.0f : weight * share;
+    }
+  }
 }
 
-template <typename T, int L, int C, int KM>
-__device__ __forceinline__ void gate_row_bwd(const GateArgs& a, int64_t r, int l) {
-  constexpr int K = kChunk<T>;
-  const T* __restrict__ x = static_cast<const T*>(a.logits) + r * a.ld;
+template <typename T, int L, int C, int KM, Fit F>
+__device__ __forceinline__ void gate_row_bwd(const GateArgs& a, int64_t r, int l, const Held<T, L, C, F>& x,
+                                             float* __restrict__ box) {
+  constexpr int K = kChunk<T>, Q = (KM + L - 1) / L;      // choices of a lane
   T* __restrict__ dl = static_cast<T*>(a.dlogits) + r * a.lddl;
-  int32_t id[KM];
-  float part[KM], w[KM], s = 0.0f;
+  int32_t id[Q];
+  float part[Q], w[Q], s = 0.0f;
 #pragma unroll
-  for (int q = 0; q < KM; ++q) {
-    id[q] = q < a.k ? a.ids[r * a.k + q] : -1;
+  for (int q = 0; q < Q; ++q) {
+    const int c = l + q * L;
+    id[q] = c < a.k ? a.ids[r * a.k + c] : -1;
     if (uint32_t(id[q]) >= uint32_t(a.groups)) id[q] = -1;
-    w[q] = id[q] < 0 ? 0.0f : a.weights[r * a.k + q];
-    part[q] = id[q] < 0 ? 0.0f : w[q] * a.dweights[r * a.k + q];
+    w[q] = id[q] < 0 ? 0.0f : a.weights[r * a.k + c];
+    part[q] = id[q] < 0 ? 0.0f : w[q] * a.dweights[r * a.k + c];
     s += part[q];
   }
-  float first = 0.0f;
-  if (a.renorm != 0) {
+  // the row's part of the box, 0 but for the choices
+  float* const mine = box + (threadIdx.x / L) * (L * C * K);
 #pragma unroll
-    for (int q = 0; q < KM; ++q) part[q] -= w[q] * s;
-  } else if (id[0] >= 0) {
-    first = float(x[id[0]]);
+  for (int j = 0; j < C; ++j)
+#pragma unroll
+    for (int i = 0; i < K; i += 4)
+      *reinterpret_cast<f32x4*>(mine + x.first(l, j) + i) = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  wave_sync();
+  s = row_sum<L>(s);
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+    if (id[q] >= 0) atomicAdd(mine + id[q], a.renorm != 0 ? part[q] - w[q] * s : part[q]);
+  const int base = threadIdx.x & 63 & ~(L - 1);
+  float first = 0.0f, scale = 0.0f;
+  if (a.renorm == 0) {
+    const int32_t id0 = __shfl(id[0], base, 64);
+    if (id0 >= 0) {
+      first = float(static_cast<const T*>(a.logits)[r * a.ld + id0]);
+      scale = -__shfl(w[0], base, 64) * s;
+    }
   }
+  wave_sync();
 #pragma unroll
   for (int j = 0; j < C; ++j) {
-    const int c0 = (l + L * j) * K, n = std::min(K, std::max(0, a.groups - c0));
-    if (n == 0) continue;
-    float g[K] = {};
-    if (a.renorm == 0 && id[0] >= 0) {
-      const Chunk<T> v = load_chunk_n(x + c0, n);
-#pragma unroll
-      for (int i = 0; i < K; ++i) g[i] = -(w[0] * expf(float(v.v[i]) - first)) * s;
-    }
-#pragma unroll
-    for (int q = 0; q < KM; ++q)
-#pragma unroll
-      for (int i = 0; i < K; ++i) g[i] += id[q] == c0 + i ? part[q] : 0.0f;
+    const int at = x.at(l, j, a.groups);
     Chunk<T> o;
 #pragma unroll
-    for (int i = 0; i < K; ++i) o.v[i] = T(g[i]);
-    store_chunk_n(dl + c0, o, n);
+    for (int i = 0; i < K; ++i) {
+      float g = mine[at + i];
+      if (a.renorm == 0) g = fmaf(scale, exp_of(float(x.v[j].v[i]) - first), g);
+      o.v[i] = T(g);
+    }
+    // a chunk that was moved back writes what others write too
+    if constexpr (F == kNarrow) {
+      if (l == 0) store_chunk_n(dl, o, a.groups);
+    } else if (x.first(l, j) < a.groups) {
+      store_chunk(dl + at, o);
+    }
   }
+  wave_sync();      // the next row's zeros
 }
 
-template <typename T, int L, int C, int KM, bool kFwd>
+// Rows are walked with the next one's logits on their way: a row's work is
+// longer than its loads, but a wave that starts with a load only waits.
+template <typename T, int L, int C, int KM, Fit F, bool kFwd>
 __global__ __launch_bounds__(kThreads) void k_gate(GateArgs a) {
   constexpr int kRows = kThreads / L;
+  __shared__ __align__(16) float box[kFwd ? 4 : kThreads * C * kChunk<T>];
+  const int l = threadIdx.x % L;
+  const bool reads = kFwd || a.renorm == 0;
+  Held<T, L, C, F> next;
+  int64_t r = int64_t(blockIdx.x) * kRows + threadIdx.x / L;
+  if (r >= a.rows) return;
+  if (reads) next.load(a, r, l);
   // all lanes of a row together
-  for (int64_t r = int64_t(blockIdx.x) * kRows + threadIdx.x / L; r < a.rows; r += int64_t(gridDim.x) * kRows) {
+  for (; r < a.rows; r += int64_t(gridDim.x) * kRows) {
+    const Held<T, L, C, F> x = next;
+    if (reads) next.load(a, std::min<int64_t>(r + int64_t(gridDim.x) * kRows, a.rows - 1), l);
     if constexpr (kFwd)
-      gate_row<T, L, C, KM>(a, r, threadIdx.x % L);
+      gate_row<T, L, C, KM, F>(a, r, l, x);
     else
-      gate_row_bwd<T, L, C, KM>(a, r, threadIdx.x % L);
+      gate_row_bwd<T, L, C, KM, F>(a, r, l, x, box);
   }
 }
 
-template <typename T, int L, int C, int KM>
+template <typename T, int L, int C, int KM, Fit F>
 hipError_t go(bool fwd, const GateArgs& a, hipStream_t st) {
-  const unsigned grid = grid_of((int64_t(a.rows) + kThreads / L - 1) / (kThreads / L));
+  // as many workgroups as are there at a time
+  const int64_t blocks = std::min<int64_t>((int64_t(a.rows) + kThreads / L - 1) / (kThreads / L), 2048);
   if (fwd)
-    k_gate<T, L, C, KM, true><<<grid, kThreads, 0, st>>>(a);
+    k_gate<T, L, C, KM, F, true><<<unsigned(blocks), kThreads, 0, st>>>(a);
   else
-    k_gate<T, L, C, KM, false><<<grid, kThreads, 0, st>>>(a);
+    k_gate<T, L, C, KM, F, false><<<unsigned(blocks), kThreads, 0, st>>>(a);
   return hipGetLastError();
 }
 
-template <typename T, int L, int C>
+template <typename T, int L, int C, Fit F>
 hipError_t by_choices(bool fwd, const GateArgs& a, hipStream_t st) {
-  if (a.k <= 1) return go<T, L, C, 1>(fwd, a, st);
-  if (a.k <= 2) return go<T, L, C, 2>(fwd, a, st);
-  if (a.k <= 4) return go<T, L, C, 4>(fwd, a, st);
-  if (a.k <= 8) return go<T, L, C, 8>(fwd, a, st);
-  return go<T, L, C, kMaxChoices>(fwd, a, st);
+  if (a.k <= 1) return go<T, L, C, 1, F>(fwd, a, st);
+  if (a.k <= 2) return go<T, L, C, 2, F>(fwd, a, st);
+  if (a.k <= 4) return go<T, L, C, 4, F>(fwd, a, st);
+  if (a.k <= 8) return go<T, L, C, 8, F>(fwd, a, st);
+  return go<T, L, C, kMaxChoices, F>(fwd, a, st);
+}
+
+template <typename T, int L, int C>
+hipError_t by_fit(bool fwd, const GateArgs& a, hipStream_t st) {
+  if (a.groups == L * C * kChunk<T>) return by_choices<T, L, C, kExact>(fwd, a, st);
+  return by_choices<T, L, C, kMoved>(fwd, a, st);
 }
 
 template <typename T>
 hipError_t by_width(bool fwd, const GateArgs& a, hipStream_t st) {
   const int chunks = (a.groups + kChunk<T> - 1) / kChunk<T>;
-  if (chunks <= 8) return by_choices<T, 8, 1>(fwd, a, st);
-  if (chunks <= 16) return by_choices<T, 16, 1>(fwd, a, st);
-  if (chunks <= 32) return by_choices<T, 32, 1>(fwd, a, st);
-  if (chunks <= 64) return by_choices<T, 64, 1>(fwd, a, st);
+  if (a.groups < kChunk<T>) return by_choices<T, 8, 1, kNarrow>(fwd, a, st);
+  if (chunks <= 8) return by_fit<T, 8, 1>(fwd, a, st);
+  if (chunks <= 16) return by_fit<T, 16, 1>(fwd, a, st);
+  if (chunks <= 32) return by_fit<T, 32, 1>(fwd, a, st);
+  if (chunks <= 64) return by_fit<T, 64, 1>(fwd, a, st);
   if constexpr (sizeof(T) == 4)
-    if (chunks > 128) return by_choices<T, 64, 4>(fwd, a, st);
-  return by_choices<T, 64, 2>(fwd, a, st);
+    if (chunks > 128) return by_fit<T, 64, 4>(fwd, a, st);
+  return by_fit<T, 64, 2>(fwd, a, st);
 }
 
 hipError_t by_type(int type, bool fwd, const GateArgs& a, hipStream_t st) {

@@ -9,6 +9,16 @@
 namespace gs {
 namespace net {
 
+// A chunk as one vector: its elements one by one would be taken for loads of
+// their own, and one of them put behind a branch.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+template <typename T>
+__device__ __forceinline__ Chunk<T> load_whole(const T* __restrict__ p) {
+  u32x4 w;
+  __builtin_memcpy(&w, p, 16);
+  return __builtin_bit_cast(Chunk<T>, w);
+}
+
 // A row of at least one chunk's width is covered by whole chunks, the last
 // one moved back onto the row's end, so that no width takes a slower path:
 // what two chunks share is read twice and written twice with the same values.
@@ -30,7 +40,7 @@ struct Row {
     if constexpr (kNarrow)
       return load_chunk_n(row, width);
     else
-      return load_chunk(row + at(c));
+      return load_whole(row + at(c));
   }
   __device__ __forceinline__ void copy(T* __restrict__ row, int c, const Chunk<T>& v) const {
     if constexpr (kNarrow)
