@@ -21,7 +21,7 @@ __device__ __forceinline__ int64_t id_at(const void* __restrict__ ids, int id_by
 
 // Chunk c of N rows from r0 on.  Nothing here is behind a branch, so that the
 // ids, and then the chunks, are in flight together.
-template <typename T, typename I, int N, bool kNarrow>
+template <typename T, typename I, int N, bool kFar, bool kNarrow>
 __device__ __forceinline__ void look_up(const EmbedArgs& a, const Row<T, kNarrow>& row, int64_t r0, int c) {
   constexpr int K = kChunk<T>;
   int64_t id[N];
@@ -39,14 +39,14 @@ __device__ __forceinline__ void look_up(const EmbedArgs& a, const Row<T, kNarrow
     float v[K];
 #pragma unroll
     for (int i = 0; i < K; ++i) v[i] = there[u] ? float(x[u].v[i]) * a.scale : 0.0f;
-    row.store(static_cast<T*>(a.y) + (r0 + u) * a.ldy, c, v);
+    row.template store<kFar>(static_cast<T*>(a.y) + (r0 + u) * a.ldy, c, v);
   }
 }
 
 // Items are slices of kRows rows: L lanes, a chunk of each row for each lane.
 // A row alone waits for its id and then for its chunk, and as many waves as
 // fit do not make up for that: several rows at a time where there are many.
-template <typename T, typename I, int L, int kRows, bool kNarrow>
+template <typename T, typename I, int L, int kRows, bool kFar, bool kNarrow>
 __global__ __launch_bounds__(kThreads) void k_lookup(EmbedArgs a, int slices, int64_t items) {
   constexpr int kGroups = kThreads / L;
   const Row<T, kNarrow> row(a.width);
@@ -56,9 +56,9 @@ __global__ __launch_bounds__(kThreads) void k_lookup(EmbedArgs a, int slices, in
     const int c = int(item - part * slices) * L + threadIdx.x % L;
     if (c >= row.chunks) continue;
     if (kRows == 1 || r0 + kRows <= a.rows)
-      look_up<T, I, kRows>(a, row, r0, c);
+      look_up<T, I, kRows, kFar>(a, row, r0, c);
     else
-      for (int64_t r = r0; r < a.rows; ++r) look_up<T, I, 1>(a, row, r, c);
+      for (int64_t r = r0; r < a.rows; ++r) look_up<T, I, 1, kFar>(a, row, r, c);
   }
 }
 
@@ -260,13 +260,15 @@ hipError_t go_fwd(const EmbedArgs& a, hipStream_t st) {
   constexpr int kGroups = kThreads / L, kRows = 4;
   const int slices = ((a.width + kChunk<T> - 1) / kChunk<T> + L - 1) / L;
   // several rows where that leaves 16 waves for each SIMD
-  const int64_t items = (a.rows + kRows - 1) / kRows * slices;
-  if (items * L >= 64 * 16384) {
-    k_lookup<T, I, L, kRows, kNarrow><<<grid_of((items + kGroups - 1) / kGroups), kThreads, 0, st>>>(a, slices, items);
-  } else {
-    const int64_t ones = a.rows * slices;
-    k_lookup<T, I, L, 1, kNarrow><<<grid_of((ones + kGroups - 1) / kGroups), kThreads, 0, st>>>(a, slices, ones);
-  }
+  const int64_t items = (a.rows + kRows - 1) / kRows * slices, ones = a.rows * slices;
+  if (items * L < 64 * 16384)
+    k_lookup<T, I, L, 1, false, kNarrow><<<grid_of((ones + kGroups - 1) / kGroups), kThreads, 0, st>>>(a, slices, ones);
+  else if (is_far(a.y, a.ldy, a.rows, sizeof(T)))
+    k_lookup<T, I, L, kRows, true, kNarrow>
+        <<<grid_of((items + kGroups - 1) / kGroups), kThreads, 0, st>>>(a, slices, items);
+  else
+    k_lookup<T, I, L, kRows, false, kNarrow>
+        <<<grid_of((items + kGroups - 1) / kGroups), kThreads, 0, st>>>(a, slices, items);
   return hipGetLastError();
 }
 
@@ -280,13 +282,15 @@ Shape shape_of(int chunks) {
   return {64, each, (chunks + 64 * each - 1) / (64 * each)};
 }
 
-// Stretches are as long as 8192 waves (8 for each SIMD) leave them, 8 to
-// kLongest positions: longer ones leave fewer partial rows.
+// Stretches are as long as 4096 waves (4 for each SIMD) leave them, 8 to
+// kLongest positions: longer ones leave fewer partial rows, but 8,191 rows are
+// too few for them (1,000,000 x 256 bf16 with 128 positions 200 us, 64 208, 32 212,
+// 16 233; 8,191 x 515 fp32 with 8 44 us, 32 50, 128 94).
 Stretches stretches_of(int type, int64_t rows, int32_t width, void* ws) {
   const int chunk = type == kTypeF32 ? 4 : 8;
   const Shape f = shape_of((width + chunk - 1) / chunk);
   int32_t len = 8;
-  while (len < kLongest && rows * f.slices * f.lanes > int64_t(len) * 64 * 8192) len *= 2;
+  while (len < kLongest && rows * f.slices * f.lanes > int64_t(len) * 64 * 4096) len *= 2;
   Stretches s{nullptr, nullptr, (rows + len - 1) / len, len, f.slices};
   s.goes_on = static_cast<int32_t*>(ws);
   s.part = reinterpret_cast<float*>(static_cast<char*>(ws) + align_up(size_t(s.count) * 4, 256));

@@ -328,10 +328,13 @@ __global__ __launch_bounds__(kT) void k_place(Pass p) {
 
 // offsets[g] = the first position whose key is at least g.  A workgroup's
 // bounds lie between those of its first and its last group, which two of its
-// waves find with 64 keys a step; then each thread, with 3.
+// waves find with 64 keys a step.  Each thread goes on in LDS, or, where an id
+// of very many entries is among them, in memory with 3 keys a step.
 __global__ __launch_bounds__(256) void k_bounds(const uint32_t* __restrict__ keys, int64_t n, int64_t groups,
                                                 int64_t* __restrict__ offsets) {
+  constexpr int kHeld = 4096;
   __shared__ int64_t s_ends[2];
+  __shared__ uint32_t s_key[kHeld];
   const int64_t g0 = int64_t(blockIdx.x) * 256, g = g0 + threadIdx.x;
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
   if (w < 2) {
@@ -348,8 +351,23 @@ __global__ __launch_bounds__(256) void k_bounds(const uint32_t* __restrict__ key
     if (lane == 0) s_ends[w] = lo;
   }
   __syncthreads();
-  if (g > groups) return;
   int64_t lo = s_ends[0], hi = s_ends[1];
+  if (hi - lo <= kHeld) {
+    const int n_held = int(hi - lo);
+#pragma unroll 8
+    for (int i = threadIdx.x; i < n_held; i += 256) s_key[i] = keys[lo + i];
+    __syncthreads();
+    int a = 0, b = n_held;
+    while (a < b) {
+      const int mid = (a + b) >> 1;
+      const bool below = int64_t(s_key[mid]) < g;
+      a = below ? mid + 1 : a;
+      b = below ? b : mid;
+    }
+    if (g <= groups) offsets[g] = lo + a;
+    return;
+  }
+  if (g > groups) return;
   while (lo < hi) {
     const int64_t q = (hi - lo) >> 2, a = lo + q, b = a + q, c = b + q;      // lo <= a <= b <= c < hi
     const bool sa = int64_t(keys[a]) < g, sb = int64_t(keys[b]) < g, sc = int64_t(keys[c]) < g;

@@ -48,7 +48,7 @@ __device__ __forceinline__ int64_t next_item() {
   return int64_t(gridDim.x) * (kThreads / L);
 }
 
-template <typename T, int L, int KM, bool kNarrow>
+template <typename T, int L, int KM, bool kFar, bool kNarrow>
 __global__ __launch_bounds__(kThreads) void k_dispatch(RouteArgs a, int slices) {
   const Row<T, kNarrow> row(a.width);
   T* const xs = static_cast<T*>(a.y);
@@ -61,7 +61,7 @@ __global__ __launch_bounds__(kThreads) void k_dispatch(RouteArgs a, int slices) 
     load_places<KM>(a, r, at);
 #pragma unroll
     for (int j = 0; j < KM; ++j)
-      if (at[j] >= 0) row.copy(xs + at[j] * a.ldy, c, x);
+      if (at[j] >= 0) row.template copy<kFar>(xs + at[j] * a.ldy, c, x);
   }
 }
 
@@ -153,8 +153,10 @@ template <typename T, int L, int KM, bool kNarrow>
 hipError_t go(Way way, const RouteArgs& a, hipStream_t st) {
   const int64_t slices = way == kCombineBwd ? 1 : ((a.width + kChunk<T> - 1) / kChunk<T> + L - 1) / L;
   const unsigned grid = grid_of((a.rows * slices + kThreads / L - 1) / (kThreads / L));
-  if (way == kDispatch)
-    k_dispatch<T, L, KM, kNarrow><<<grid, kThreads, 0, st>>>(a, int(slices));
+  if (way == kDispatch && is_far(a.y, a.ldy, int64_t(a.rows) * a.k, sizeof(T)))
+    k_dispatch<T, L, KM, true, kNarrow><<<grid, kThreads, 0, st>>>(a, int(slices));
+  else if (way == kDispatch)
+    k_dispatch<T, L, KM, false, kNarrow><<<grid, kThreads, 0, st>>>(a, int(slices));
   else if (way == kCombine)
     k_combine<T, L, KM, kNarrow><<<grid, kThreads, 0, st>>>(a, int(slices));
   else
