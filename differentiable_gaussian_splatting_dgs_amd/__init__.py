@@ -33,7 +33,7 @@ GS_MAX_NET_GROUPS = 1024
 GS_MAX_SORT_GROUPS = 1 << 30
 GS_MAX_CHOICES = 16
 GS_ADAMW_BLOCK = 256
-GS_MAX_ADAMW_SIZE = 1 << 35
+GS_MAX_ADAMW_SIZE = 1 << 33
 GS_PROJ_WORDS = 16
 GS_GRAD2D_WORDS = 12
 GS_MAX_FUSED_VIEWS = 16

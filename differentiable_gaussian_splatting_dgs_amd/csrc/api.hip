@@ -1218,7 +1218,7 @@ gs_status gs_adamw(const gs_adamw_tensor* tensors, int32_t count, double lr, dou
     const uintptr_t at = reinterpret_cast<uintptr_t>(p);
     ranges[written++] = {at, at + uintptr_t(bytes)};
   };
-  bool any[2] = {false, false};
+  bool any[2][3] = {};      // moments in 8 bits, type of the gradients
   for (int32_t i = 0; i < count; ++i) {
     const gs_adamw_tensor& t = tensors[i];
     REQUIRE(t.n >= 0 && t.n <= GS_MAX_ADAMW_SIZE, "tensor %d: n = %lld out of range", int(i), (long long)t.n);
@@ -1248,23 +1248,26 @@ gs_status gs_adamw(const gs_adamw_tensor* tensors, int32_t count, double lr, dou
       writes(t.m_scale, blocks * 4);
       writes(t.v_scale, blocks * 4);
     }
-    any[eight] = true;
+    any[eight][t.grad_type] = true;
   }
   std::sort(ranges, ranges + written);
   for (size_t i = 1; i < written; ++i) REQUIRE(ranges[i].first >= ranges[i - 1].second, "written ranges overlap");
   const gs::AdamwHyper h{lr, beta1, beta2, eps, weight_decay, step, step_dev, grad_scale};
-  for (int eight = 0; eight < 2; ++eight) {
-    if (!any[eight]) continue;
+  for (int kind = 0; kind < 6; ++kind) {
+    const bool eight = kind >= 3;
+    const int type = kind % 3;
+    if (!any[eight][type]) continue;
     gs::AdamwTensor batch[gs::kAdamwTensors];
     int held = 0;
     uint32_t workgroups = 0;
     for (int32_t i = 0; i <= count; ++i) {
-      const bool take = i < count && tensors[i].n > 0 && (tensors[i].m_scale != nullptr) == (eight != 0);
+      const bool take = i < count && tensors[i].n > 0 && (tensors[i].m_scale != nullptr) == eight &&
+                        tensors[i].grad_type == type;
       const uint32_t mine = take ? gs::adamw_workgroups(tensors[i].n) : 0;
       // a launch ends with its room for tensors, or where its threads would pass 2^32 - 1
       if (held > 0 && (i == count || (take && (held == gs::kAdamwTensors || workgroups + mine >= (1u << 24))))) {
         const hipError_t e =
-            gs::launch_adamw(batch, held, eight != 0, workgroups, h, static_cast<hipStream_t>(stream));
+            gs::launch_adamw(batch, held, eight, type, workgroups, h, static_cast<hipStream_t>(stream));
         if (e != hipSuccess) return hip_status(e, "gs_adamw");
         held = 0;
         workgroups = 0;
@@ -1272,7 +1275,7 @@ gs_status gs_adamw(const gs_adamw_tensor* tensors, int32_t count, double lr, dou
       if (!take) continue;
       const gs_adamw_tensor& t = tensors[i];
       batch[held++] = {t.param, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.copy, t.n, workgroups,
-                       gs::adamw_key(seed, uint32_t(i)), int16_t(t.grad_type), int16_t(t.copy_type), 0};
+                       gs::adamw_key(seed, uint32_t(i)), t.copy_type};
       workgroups += mine;
     }
   }

@@ -278,7 +278,7 @@ hipError_t launch_combine_bwd(int type, const RouteArgs& a, hipStream_t st);
 
 // --- AdamW over many tensors (adamw.hip) ------------------------------------------
 constexpr int kAdamwBlock = 256;
-constexpr int64_t kMaxAdamwSize = int64_t(1) << 35;
+constexpr int64_t kMaxAdamwSize = int64_t(1) << 33;
 struct AdamwTensor {
   float* param;
   const void* grad;
@@ -288,8 +288,7 @@ struct AdamwTensor {
   int64_t n;
   uint32_t first;               // the launch's workgroup with its first element
   uint32_t key;                 // of its random numbers
-  int16_t grad_type, copy_type;
-  int32_t pad;
+  int32_t copy_type;
 };
 struct AdamwHyper {
   double lr, beta1, beta2, eps, weight_decay;
@@ -298,11 +297,12 @@ struct AdamwHyper {
   const float* grad_scale;      // or NULL
 };
 uint32_t adamw_key(uint64_t seed, uint32_t place);
-// Tensors of one kind of moments, in launches of at most kAdamwTensors.
+// Tensors of one kind of moments and type of gradients, in launches of at most
+// kAdamwTensors.
 constexpr int kAdamwTensors = 40;
 uint32_t adamw_workgroups(int64_t n);
-hipError_t launch_adamw(const AdamwTensor* tensors, int count, bool eight, uint32_t workgroups, const AdamwHyper& h,
-                        hipStream_t st);
+hipError_t launch_adamw(const AdamwTensor* tensors, int count, bool eight, int grad_type, uint32_t workgroups,
+                        const AdamwHyper& h, hipStream_t st);
 hipError_t launch_adamw_moment(const uint8_t* codes, const float* scales, int64_t n, int moment, int type,
                                void* values, hipStream_t st);
 

@@ -937,7 +937,7 @@ typedef struct gs_adamw_tensor {
 
 /* values that share a scale, and most elements of a tensor */
 #define GS_ADAMW_BLOCK 256
-#define GS_MAX_ADAMW_SIZE ((int64_t)1 << 35)
+#define GS_MAX_ADAMW_SIZE ((int64_t)1 << 33)
 
 /* One AdamW step over many tensors, with t the step's number (from 1 on) and
  * g = grad * *grad_scale:

@@ -259,7 +259,8 @@ def test_adamw_zero_gradients(gs):
 
 
 def test_adamw_codes(gs):
-    """Every code of both moments stands for its value, in every type."""
+    """Every code of both moments stands for its value, in every type and at
+    every distance from the end."""
     codes = torch.arange(256, dtype=torch.uint8, device="cuda").repeat(3)[: 2 * 256 + 200]
     scales = torch.tensor([1.0, 2.0 ** -126, 2.0 ** 96], device="cuda")
     for moment, signed in ((1, True), (2, False)):
@@ -270,6 +271,15 @@ def test_adamw_codes(gs):
         got = gs.gs_adamw_moment(codes[:256], scales[:1] * 2.0 ** -20, moment, torch.float16)
         want = (_decode(codes[:256], scales[:1], signed) * 2.0 ** -20).half()
         assert torch.equal(got.nan_to_num(7.0), want.nan_to_num(7.0))
+    for n in (1, 2, 3, 4, 5, 255, 1027, 4095, 4096, 4097, 8190, 8192, 8193, 100_001):
+        codes = torch.arange(n, device="cuda").mul_(7).remainder_(256).to(torch.uint8)
+        scales = 2.0 ** -(torch.arange(-(-n // 256), device="cuda") % 20).float()
+        for moment, signed in ((1, True), (2, False)):
+            want = _decode(codes, scales, signed)
+            for t in TYPES.values():
+                got = gs.gs_adamw_moment(codes, scales, moment, t)
+                assert torch.equal(got.nan_to_num(7.0, 1e4, -1e4), want.to(t).nan_to_num(7.0, 1e4, -1e4)), (n, moment, t)
+    codes, scales = torch.arange(256, device="cuda").to(torch.uint8), torch.ones(1, device="cuda")
     # as e4m3fn times 2^9 scale
     m = codes[:256].view(torch.float8_e4m3fn).float() * 512
     assert torch.equal(m.nan_to_num(7.0), gs.gs_adamw_moment(codes[:256], scales[:1], 1).nan_to_num(7.0))

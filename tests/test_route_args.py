@@ -208,7 +208,7 @@ NAN = float("nan")
     (dict(wd=float("inf")), b"weight_decay"), (dict(b1=1.0), b"beta"), (dict(b1=-0.1), b"beta"), (dict(b2=NAN), b"beta"),
     (dict(eps=0.0), b"eps"), (dict(eps=1e-60), b"eps"), (dict(eps=NAN), b"eps"), (dict(eps=1e60), b"eps"),
     (dict(step=0), b"step"), (dict(step_dev=P(12)), b"step_dev"), (dict(scale=P(6)), b"grad_scale"),
-    (dict(n=-1), b"n ="), (dict(n=(1 << 35) + 1), b"n ="), (dict(n=4, grad_type=3), b"grad_type"),
+    (dict(n=-1), b"n ="), (dict(n=(1 << 33) + 1), b"n ="), (dict(n=4, grad_type=3), b"grad_type"),
     (dict(n=4, param=None), b"param"), (dict(n=4, param=2), b"param"), (dict(n=4, grad=None), b"grad"),
     (dict(n=4, grad=6), b"grad"), (dict(n=4, m=None), b"m or v"), (dict(n=4, v=10), b"m or v"),
     (dict(n=4, m_scale=64), b"scale"), (dict(n=4, v_scale=64), b"scale"), (dict(n=4, m_scale=66, v_scale=128), b"scale"),
