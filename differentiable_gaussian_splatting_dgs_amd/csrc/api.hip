@@ -977,7 +977,7 @@ gs_status gs_group_sort_workspace_size(int64_t n, int64_t num_groups, size_t* by
   REQUIRE(bytes != nullptr, "bytes is NULL");
   *bytes = 0;
   CHECK(check_sort_sizes(n, num_groups));
-  *bytes = std::max<size_t>(256, gs::group_sort_ws_bytes(n, num_groups));
+  *bytes = gs::group_sort_ws_bytes(n, num_groups);
   return ok();
 }
 
@@ -988,8 +988,8 @@ gs_status gs_group_sort(const void* ids, int32_t id_bytes, int64_t n, int64_t nu
   REQUIRE(offsets != nullptr && aligned(offsets, 8), "offsets NULL or not 8-byte aligned");
   CHECK(check_vector("order", order));
   CHECK(check_vector("place", place));
-  REQUIRE(workspace != nullptr && aligned(workspace, 256), "workspace NULL or not 256-byte aligned");
   const size_t need = gs::group_sort_ws_bytes(n, num_groups);
+  REQUIRE((workspace != nullptr || need == 0) && aligned(workspace, 256), "workspace NULL or not 256-byte aligned");
   REQUIRE(workspace_bytes >= need, "workspace_bytes = %zu < %zu needed", workspace_bytes, need);
   const gs::SortArgs a{ids, id_bytes, n, num_groups, offsets, order, place};
   return hip_status(gs::launch_group_sort(a, workspace, static_cast<hipStream_t>(stream)), "gs_group_sort");

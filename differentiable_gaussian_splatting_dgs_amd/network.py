@@ -29,7 +29,7 @@ _byref, _size_t = C.byref, C.c_size_t
 # the stream's handle without a Stream object, where this torch has it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda device: torch.cuda.current_stream(device).cuda_stream)
-_current_device = torch.cuda.current_device
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _type(x, name="x"):
@@ -127,6 +127,8 @@ def _scratch(ws, like):
 
 
 def _workspace(ws, need, device):
+    if ws is None and need == 0:
+        return None, 0
     if ws is None:
         return _empty(need, dtype=_U8, device=device), need
     return ws, ws.numel() * ws.element_size()
@@ -351,7 +353,7 @@ def _group_sort(s, ids, num_groups, offsets, order, place, want_order, want_plac
         place = _whole(place, _I32, ids.shape, device, "place")
     ws, nbytes = _workspace(workspace, need, device)
     st = lib().gs_group_sort(at, id_bytes, n, num_groups, offsets.data_ptr(), _optional(order), _optional(place),
-                             ws.data_ptr(), nbytes, s)
+                             _optional(ws), nbytes, s)
     if st:
         _check(st, "gs_group_sort")
     return offsets, order, place

@@ -10,12 +10,16 @@ in the same pass.  Errors as in the network operators: ``ValueError`` or
 """
 from __future__ import annotations
 
-import ctypes as C
+import array
 
 import torch
 
-from . import GS_ADAMW_BLOCK, _check, gs_adamw_tensor, lib
+from . import GS_ADAMW_BLOCK, _check, lib
 from .network import _F32, _I64, _TYPES, _U8, _launch, _on_gpu
+
+# a gs_adamw_tensor as 64-bit words: param, grad, m, v, m_scale, v_scale, copy,
+# n, grad_type below copy_type
+_WORDS, _GRAD, _COUNT, _KINDS = 9, 1, 7, 8
 
 
 def _blocks(n):
@@ -31,31 +35,40 @@ def _tensor(t, dtypes, n, device, name):
     return t.data_ptr()
 
 
-def _entry(e, device, i, param, m, v, m_scale, v_scale, copy):
+def _entry(table, i, device, param, m, v, m_scale, v_scale, copy):
+    """Appends tensor i without a gradient; returns its copy's type as the upper
+    half of the last word."""
     n = param.numel()
-    e.param = _tensor(param, (_F32,), n, device, f"parameter {i}")
     if (m_scale is None) != (v_scale is None):
         raise ValueError(f"parameter {i}: one scale of two")
     kinds = (_F32,) if m_scale is None else (_U8,)
-    e.m = _tensor(m, kinds, n, device, f"m of parameter {i}")
-    e.v = _tensor(v, kinds, n, device, f"v of parameter {i}")
-    e.m_scale = e.v_scale = e.copy = None
-    if m_scale is not None:
-        e.m_scale = _tensor(m_scale, (_F32,), _blocks(n), device, f"m's scales of parameter {i}")
-        e.v_scale = _tensor(v_scale, (_F32,), _blocks(n), device, f"v's scales of parameter {i}")
-    if copy is not None:
-        e.copy = _tensor(copy, tuple(_TYPES), n, device, f"copy of parameter {i}")
-        e.copy_type = _TYPES[copy.dtype]
+    table.append(_tensor(param, (_F32,), n, device, f"parameter {i}"))
+    table.append(0)
+    table.append(_tensor(m, kinds, n, device, f"m of parameter {i}"))
+    table.append(_tensor(v, kinds, n, device, f"v of parameter {i}"))
+    for name, scale in (("m", m_scale), ("v", v_scale)):
+        table.append(0 if scale is None else
+                     _tensor(scale, (_F32,), _blocks(n), device, f"{name}'s scales of parameter {i}"))
+    table.append(0 if copy is None else _tensor(copy, tuple(_TYPES), n, device, f"copy of parameter {i}"))
+    kind = 0 if copy is None else _TYPES[copy.dtype] << 32
+    table.extend((0, kind))
+    return kind
 
 
-def _grad(e, device, i, param, grad):
-    """Fills in a gradient; None: nothing is done for this tensor."""
-    if grad is None:
-        e.n = 0
-        return
-    e.grad = _tensor(grad, tuple(_TYPES), param.numel(), device, f"gradient {i}")
-    e.grad_type = _TYPES[grad.dtype]
-    e.n = param.numel()
+def _grads(table, device, sizes, kinds, grads):
+    """Fills in the gradients; None: nothing is done for that tensor."""
+    at, index = 0, device.index
+    for i, g in enumerate(grads):
+        if g is None:
+            table[at + _COUNT] = 0
+        else:
+            n, t = sizes[i], _TYPES.get(g.dtype)
+            if t is None or g.numel() != n or g.get_device() != index or not g.is_contiguous():
+                _tensor(g, tuple(_TYPES), n, device, f"gradient {i}")       # says what is wrong, if it is
+            table[at + _GRAD] = g.data_ptr()
+            table[at + _COUNT] = n
+            table[at + _KINDS] = kinds[i] + t
+        at += _WORDS
 
 
 def _scalar(t, dtype, device, name):
@@ -67,7 +80,8 @@ def _call(s, first, table, count, numbers, step, grad_scale, seed):
     step_at = _scalar(step, _I64, device, "step") if isinstance(step, torch.Tensor) else None
     scale_at = _scalar(grad_scale, _F32, device, "grad_scale")
     _on_gpu(first, "parameter 0")
-    st = lib().gs_adamw(table, count, *numbers, 0 if step_at is not None else step, step_at, scale_at, seed, s)
+    st = lib().gs_adamw(table.buffer_info()[0], count, *numbers, 0 if step_at is not None else step, step_at, scale_at,
+                        seed, s)
     if st:
         _check(st, "gs_adamw")
 
@@ -89,11 +103,9 @@ def gs_adamw(params, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, we
         raise ValueError(f"{count} parameters with lists of {[len(x) for x in lists]}")
     if count == 0:
         return
-    table = (gs_adamw_tensor * count)()
-    device = params[0].device
-    for i, (p, g, *rest) in enumerate(zip(params, *lists)):
-        _entry(table[i], device, i, p, *rest)
-        _grad(table[i], device, i, p, g)
+    table, device = array.array("Q"), params[0].device
+    kinds = [_entry(table, i, device, *row) for i, row in enumerate(zip(params, *lists[1:]))]
+    _grads(table, device, [p.numel() for p in params], kinds, grads)
     _launch(_call, params[0], stream, table, count, (lr, beta1, beta2, eps, weight_decay), step, grad_scale, seed)
 
 
@@ -155,12 +167,9 @@ class AdamW:
             raise ValueError(f"{count} parameters, {len(self.copies)} copies, {len(self.state)} states")
         self.steps = step
         self.step_dev = torch.tensor([step], dtype=_I64, device=device) if capturable else None
-        self._table, self._held = None, None
-
-    def _tensors(self):
-        for p, c, s in zip(self.params, self.copies, self.state):
-            yield p
-            yield from (x for x in (c, *s) if x is not None)
+        rows = zip(self.params, self.copies, self.state)
+        self._pointers = [t.data_ptr for p, c, s in rows for t in (p, c, *s) if t is not None]
+        self._table, self._held, self._sizes, self._kinds = None, None, None, None
 
     def step(self, grads=None, grad_scale=None, stream=None):
         """One step with ``grads`` (default: each parameter's .grad; None leaves
@@ -170,14 +179,13 @@ class AdamW:
         if len(grads) != count:
             raise ValueError(f"{len(grads)} gradients of {count} parameters")
         # the addresses as they are now: a tensor's storage may have been replaced
-        held = [t.data_ptr() for t in self._tensors()]
+        held = [address() for address in self._pointers]
         if held != self._held:
-            table = (gs_adamw_tensor * count)()
-            for i, (p, c, (m, v, ms, vs)) in enumerate(zip(self.params, self.copies, self.state)):
-                _entry(table[i], device, i, p, m, v, ms, vs, c)
-            self._table, self._held = table, held
-        for i, g in enumerate(grads):
-            _grad(self._table[i], device, i, self.params[i], g)
+            table = array.array("Q")
+            self._kinds = [_entry(table, i, device, p, *s, c)
+                           for i, (p, s, c) in enumerate(zip(self.params, self.state, self.copies))]
+            self._table, self._held, self._sizes = table, held, [p.numel() for p in self.params]
+        _grads(self._table, device, self._sizes, self._kinds, grads)
         numbers = (self.lr, *self.betas, self.eps, self.weight_decay)
         _launch(self._enqueue, self.params[0], stream, numbers, grad_scale)
         self.steps += 1

@@ -805,7 +805,8 @@ gs_status gs_grouped_linear_bwd(const void* x, int64_t ldx, const void* w, int64
 gs_status gs_group_sort(const void* ids, int32_t id_bytes, int64_t n, int64_t num_groups, int64_t* offsets,
                         int32_t* order, int32_t* place, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace bytes of gs_group_sort (host, no device work). */
+/* Workspace bytes of gs_group_sort (host, no device work); 0 for few ids of few
+ * groups, where workspace may be NULL. */
 gs_status gs_group_sort_workspace_size(int64_t n, int64_t num_groups, size_t* bytes);
 
 /* Rows of a table: y[i] = scale table[ids[i]], rounded once; a row of zeros

@@ -32,7 +32,7 @@ def _embed_bwd(dy=P(16), lddy=64, ids=P(16), id_bytes=8, offsets=P(16), order=P(
     (_sort, dict(ids=None), b"ids"), (_sort, dict(ids=P(18)), b"ids"), (_sort, dict(ids=P(20), id_bytes=8), b"ids"),
     (_sort, dict(offsets=None), b"offsets"), (_sort, dict(offsets=P(12)), b"offsets"),
     (_sort, dict(order=P(18)), b"order"), (_sort, dict(place=P(17)), b"place"),
-    (_sort, dict(ws=None), b"workspace"), (_sort, dict(ws=P(128)), b"workspace"),
+    (_sort, dict(n=100_000, ws=None), b"workspace"), (_sort, dict(ws=P(128)), b"workspace"),
     (_sort, dict(n=100_000, ws_bytes=256), b"workspace_bytes"),
     (_embed, dict(typ=3), b"type"), (_embed, dict(rows=-1), b"rows"), (_embed, dict(rows=1 << 31), b"rows"),
     (_embed, dict(num_rows=0), b"num_rows"), (_embed, dict(num_rows=(1 << 30) + 1), b"num_rows"),
@@ -61,7 +61,8 @@ def test_nothing_to_do():
 def test_workspace_sizes():
     for n in (0, 1, 2048, 1_000_000):
         for groups in (1, 1000, 100_000):
-            assert gs.gs_group_sort_workspace_size(n, groups) >= 256
+            assert gs.gs_group_sort_workspace_size(n, groups) >= (4 * n if groups > 10_000 else 0)
+    assert gs.gs_group_sort_workspace_size(100, 64) == 0
     assert gs.gs_embedding_workspace_size(0, 1, 1, 0) >= 256
     with pytest.raises(gs.GSError, match="num_groups"):
         gs.gs_group_sort_workspace_size(4, 0)
