@@ -265,6 +265,33 @@ def test_routed_rows_past_32_bits(gs):
     assert dw[0].tolist() == [9.0 * width] * 2 and dw[-1].tolist() == [25.0 * width] * 2
 
 
+def test_combine_gradient_against_differences(gs):
+    """combine is linear in ys and in the weights each, so that a difference over
+    any step is the derivative, but for the roundings of y (fp32, (k + 3) 2^-24 of
+    the absolute terms on either side) over twice the step."""
+    rows, k, width = 30, 3, 50
+    g = gen(11)
+    place = gs.gs_group_sort(_picks(1, rows, k, 8), 8)[2]
+    ys, w, dy = rand(g, rows * k, width), torch.rand(rows, k, generator=g, device="cuda"), rand(g, rows, width)
+    dys = torch.zeros_like(ys)
+    _, dw = gs.gs_combine_bwd(dy, ys, place, w, dys=dys)
+    for d, h in ((rand(g, rows, k), 0.5), (rand(g, rows * k, width), 0.25)):
+        if d.shape == w.shape:
+            up, down, want = gs.gs_combine_fwd(ys, place, w + h * d), gs.gs_combine_fwd(ys, place, w - h * d), dw
+        else:
+            up, down, want = gs.gs_combine_fwd(ys + h * d, place, w), gs.gs_combine_fwd(ys - h * d, place, w), dys
+        got = ((up.double() - down.double()) * dy.double()).sum() / (2 * h)
+        want = (want.double() * d.double()).sum()
+        there = place >= 0
+        size = ((w.abs() + h * d.abs() if d.shape == w.shape else w)[:, :, None] *
+                torch.where(there[:, :, None], ys.abs()[place.clamp_min(0).long()] + (0 if d.shape == w.shape else
+                            h * d.abs()[place.clamp_min(0).long()]), 0.0)).sum(1)
+        tol = 2 * ((k + 5) * EPS32 * size.double() * dy.double().abs()).sum() / (2 * h)
+        # dw and dys themselves: sums of `width` products, and products
+        tol += (width + 4) * EPS32 * float((size.double() * dy.double().abs()).sum()) * float(d.abs().max())
+        assert abs(float(got - want)) <= float(tol)
+
+
 def test_a_layer_of_routed_heads(gs):
     """Gate, sort, dispatch, grouped linear, combine, and the way back, as a
     user runs them, against autograd in 64 bits through the same choices;
