@@ -8,8 +8,8 @@
 // Up to kSmall keys: one workgroup, all passes in LDS, one launch (and one for
 // the bounds of many groups), so that a few hundred routed rows cost a launch.
 // More keys: a pass is three launches, the digit counts of every block of
-// keys, a scan of each digit's counts over the blocks, and the keys to their
-// places.  A block's keys are brought into the digits' order in LDS first and
+// keys, a scan of each digit's counts over the blocks (left out for few
+// blocks), and the keys to their places.  A block's keys are brought into the digits' order in LDS first and
 // leave as runs of one digit, key and entry as one 8-byte word, instead of
 // one by one.  Up to 1023 groups that is one pass, whose digits are the
 // groups and whose counts are the bounds; more groups take the bounds from
@@ -150,6 +150,7 @@ constexpr int kW = kT / 64;
 constexpr int kItems = 8;            // keys of a thread
 constexpr int kBlockKeys = kT * kItems;
 constexpr int kMaxBits = 10;         // of a digit
+constexpr int kFewBlocks = 32;       // so many blocks' counts are read by each instead of scanned by a launch
 
 struct Pass {
   const void* src;               // ids in the first pass, then keys and entries as words
@@ -159,7 +160,7 @@ struct Pass {
   int32_t* place;                // last pass, or NULL
   int64_t* offsets;              // the only pass: written here; else NULL
   uint32_t* counts;              // [block][digit]
-  uint32_t* totals;
+  uint32_t* totals;              // NULL: few blocks, whose counts are not scanned
   int64_t n;
   uint32_t groups;
   int32_t shift, bits, nb;
@@ -269,12 +270,22 @@ __global__ __launch_bounds__(kT) void k_place(Pass p) {
   }
   __syncthreads();
   // thread t: kPer neighbouring digits
-  uint32_t tot[kPer], in_block[kPer], tot_sum = 0, block_sum = 0;
+  uint32_t tot[kPer], before[kPer], in_block[kPer], tot_sum = 0, block_sum = 0;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int b = t * kPer + j;
-    tot[j] = b < bins ? p.totals[b] : 0u;
-    in_block[j] = 0;
+    tot[j] = before[j] = in_block[j] = 0;
+    if (b < bins && p.totals != nullptr) {
+      tot[j] = p.totals[b];
+      before[j] = p.counts[(size_t(blockIdx.x) << p.bits) + b];
+    } else if (b < bins) {
+#pragma unroll 8
+      for (int k = 0; k < p.nb; ++k) {
+        const uint32_t c = p.counts[(size_t(k) << p.bits) + b];
+        tot[j] += c;
+        before[j] += k < int(blockIdx.x) ? c : 0u;
+      }
+    }
     if (b < bins)
 #pragma unroll
       for (int k = 0; k < kW; ++k) in_block[j] += s_cnt[k][b];
@@ -289,7 +300,7 @@ __global__ __launch_bounds__(kT) void k_place(Pass p) {
     const int b = t * kPer + j;
     if (b < bins) {
       if (p.offsets != nullptr && blockIdx.x == 0 && uint32_t(b) <= p.groups) p.offsets[b] = start;
-      s_to[b] = start + p.counts[(size_t(blockIdx.x) << p.bits) + b] - local;
+      s_to[b] = start + before[j] - local;
       uint32_t at = local;
 #pragma unroll
       for (int k = 0; k < kW; ++k) {
@@ -412,7 +423,7 @@ SortSpace sort_space(void* ws, int64_t n, int64_t groups) {
 template <typename I, bool kFirst>
 void pass(const Pass& p, hipStream_t st) {
   k_count<I, kFirst><<<p.nb, kT, 0, st>>>(p);
-  k_scan<<<((1 << p.bits) + 63) / 64, 1024, 0, st>>>(p.counts, p.bits, p.nb, p.totals);
+  if (p.totals != nullptr) k_scan<<<((1 << p.bits) + 63) / 64, 1024, 0, st>>>(p.counts, p.bits, p.nb, p.totals);
   k_place<I, kFirst><<<p.nb, kT, 0, st>>>(p);
 }
 
@@ -440,7 +451,7 @@ hipError_t sort(const SortArgs& a, void* ws, hipStream_t st) {
   p.bits = (bits + passes - 1) / passes;
   p.nb = int((a.n + kBlockKeys - 1) / kBlockKeys);
   p.counts = s.counts;
-  p.totals = s.totals;
+  p.totals = p.nb <= kFewBlocks ? nullptr : s.totals;
   for (int k = 0; k < passes; ++k) {
     const bool last = k == passes - 1;
     p.shift = k * p.bits;

@@ -100,12 +100,15 @@ __global__ __launch_bounds__(kThreads) void k_combine(RouteArgs a, int slices) {
   }
 }
 
-// L lanes a row, which they walk: the products' sums stay in registers.
-template <typename T, int L, int KM, bool kNarrow>
+// L lanes a row, which they walk C chunks a lane at a time: the products' sums
+// stay in registers.
+template <typename T, int L, int C, int KM, bool kNarrow>
 __global__ __launch_bounds__(kThreads) void k_combine_bwd(RouteArgs a) {
   constexpr int K = kChunk<T>;
   const Row<T, kNarrow> row(a.width);
   const int l = threadIdx.x % L;
+  const T* const ys = static_cast<const T*>(a.x);
+  T* const dys = static_cast<T*>(a.y);
   // all lanes of a row together
   for (int64_t r = first_item<L>(); r < a.rows; r += next_item<L>()) {
     int32_t at[KM];
@@ -113,29 +116,41 @@ __global__ __launch_bounds__(kThreads) void k_combine_bwd(RouteArgs a) {
     load_places<KM>(a, r, at);
     load_weights<KM>(a, r, w);
     const T* const dy = static_cast<const T*>(a.dy) + r * a.lddy;
-    const T* const ys = static_cast<const T*>(a.x);
-    T* const dys = static_cast<T*>(a.y);
-    for (int c = l; c < row.chunks; c += L) {
-      const Chunk<T> g = row.load(dy, c);
+    for (int c0 = l; c0 < row.chunks; c0 += L * C) {
+      int c[C];      // past the row's end: its last chunk, which does not count
+      Chunk<T> g[C];
+#pragma unroll
+      for (int q = 0; q < C; ++q) {
+        c[q] = std::min(c0 + q * L, row.chunks - 1);
+        g[q] = row.load(dy, c[q]);
+      }
       if (a.dweights != nullptr) {
-        Chunk<T> v[KM];
+        Chunk<T> v[C][KM];
 #pragma unroll
-        for (int j = 0; j < KM; ++j) v[j] = row.load(ys + (at[j] < 0 ? 0 : at[j]) * a.ldx, c);
-        const int again = row.again(c);
+        for (int q = 0; q < C; ++q)
 #pragma unroll
-        for (int j = 0; j < KM; ++j)
+          for (int j = 0; j < KM; ++j) v[q][j] = row.load(ys + (at[j] < 0 ? 0 : at[j]) * a.ldx, c[q]);
 #pragma unroll
-          for (int i = 0; i < K; ++i) dot[j] = i < again ? dot[j] : fmaf(float(g.v[i]), float(v[j].v[i]), dot[j]);
+        for (int q = 0; q < C; ++q) {
+          const int skip = c0 + q * L < row.chunks ? row.again(c[q]) : K;
+#pragma unroll
+          for (int j = 0; j < KM; ++j)
+#pragma unroll
+            for (int i = 0; i < K; ++i)
+              dot[j] = i < skip ? dot[j] : fmaf(float(g[q].v[i]), float(v[q][j].v[i]), dot[j]);
+        }
       }
       if (dys != nullptr)
 #pragma unroll
-        for (int j = 0; j < KM; ++j)
-          if (at[j] >= 0) {
-            float o[K];
+        for (int q = 0; q < C; ++q)
 #pragma unroll
-            for (int i = 0; i < K; ++i) o[i] = w[j] * float(g.v[i]);
-            row.store(dys + at[j] * a.ldy, c, o);
-          }
+          for (int j = 0; j < KM; ++j)
+            if (at[j] >= 0 && c0 + q * L < row.chunks) {
+              float o[K];
+#pragma unroll
+              for (int i = 0; i < K; ++i) o[i] = w[j] * float(g[q].v[i]);
+              row.store(dys + at[j] * a.ldy, c[q], o);
+            }
     }
     if (a.dweights == nullptr) continue;
 #pragma unroll
@@ -151,6 +166,8 @@ enum Way { kDispatch, kCombine, kCombineBwd };
 
 template <typename T, int L, int KM, bool kNarrow>
 hipError_t go(Way way, const RouteArgs& a, hipStream_t st) {
+  // rows of several chunks a lane: as many in flight as registers allow
+  constexpr int kAhead = L != 64 ? 1 : KM <= 2 ? 3 : KM <= 4 ? 2 : 1;
   const int64_t slices = way == kCombineBwd ? 1 : ((a.width + kChunk<T> - 1) / kChunk<T> + L - 1) / L;
   const unsigned grid = grid_of((a.rows * slices + kThreads / L - 1) / (kThreads / L));
   if (way == kDispatch && is_far(a.y, a.ldy, int64_t(a.rows) * a.k, sizeof(T)))
@@ -159,8 +176,10 @@ hipError_t go(Way way, const RouteArgs& a, hipStream_t st) {
     k_dispatch<T, L, KM, false, kNarrow><<<grid, kThreads, 0, st>>>(a, int(slices));
   else if (way == kCombine)
     k_combine<T, L, KM, kNarrow><<<grid, kThreads, 0, st>>>(a, int(slices));
+  else if (kAhead > 1 && a.width > 64 * kChunk<T>)
+    k_combine_bwd<T, L, kAhead, KM, kNarrow><<<grid, kThreads, 0, st>>>(a);
   else
-    k_combine_bwd<T, L, KM, kNarrow><<<grid, kThreads, 0, st>>>(a);
+    k_combine_bwd<T, L, 1, KM, kNarrow><<<grid, kThreads, 0, st>>>(a);
   return hipGetLastError();
 }
 
