@@ -1204,12 +1204,12 @@ gs_status gs_adamw(const gs_adamw_tensor* tensors, int32_t count, double lr, dou
   REQUIRE(step_dev != nullptr || step >= 1, "step = %lld: 1 or more expected", (long long)step);
   REQUIRE(aligned(step_dev, 8) && aligned(grad_scale, 4), "step_dev or grad_scale misaligned");
   // written ranges, as (first byte, one past the last), sorted to find overlaps
-  constexpr int kFew = 64 * 5;
-  std::pair<uintptr_t, uintptr_t> few[kFew];
+  constexpr int kFew = 64, kRanges = 6;      // tensors; param, m, v, both scales, copy
+  std::pair<uintptr_t, uintptr_t> few[kFew * kRanges];
   std::unique_ptr<std::pair<uintptr_t, uintptr_t>[]> more;
   std::pair<uintptr_t, uintptr_t>* ranges = few;
-  if (count > kFew / 5) {
-    more.reset(new (std::nothrow) std::pair<uintptr_t, uintptr_t>[size_t(count) * 6]);
+  if (count > kFew) {
+    more.reset(new (std::nothrow) std::pair<uintptr_t, uintptr_t>[size_t(count) * kRanges]);
     if (more == nullptr) return fail(GS_ERR_INVALID_ARG, "no host memory for %d tensors", int(count));
     ranges = more.get();
   }

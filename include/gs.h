@@ -843,8 +843,9 @@ gs_status gs_embedding_bwd(const void* dy, int64_t lddy, const void* ids, int32_
 /* Workspace bytes of gs_embedding_bwd (host, no device work). */
 gs_status gs_embedding_workspace_size(int64_t rows, int64_t num_rows, int32_t width, int32_t type, size_t* bytes);
 
-/* The gate: the k largest logits of each row, in descending order (ties: the
- * lower index first; NaN counts as the largest), and their weights
+/* The gate: the k largest logits of each row, in descending order (ties, also
+ * of 0 and -0: the lower index first; NaN above infinity, several in any fixed
+ * order), and their weights
  *   renorm != 0   e^l / sum of e^l over the row's chosen logits
  *   renorm == 0   e^l / sum of e^l over all of the row's logits
  * A logit of minus infinity is never chosen: where fewer than k others are

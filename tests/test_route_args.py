@@ -223,6 +223,22 @@ def test_adamw_refused(kw, word):
     assert word in gs.lib().gs_last_error(), gs.lib().gs_last_error()
 
 
+@pytest.mark.parametrize("count", [1, 2, 63, 64, 65, 200])
+def test_adamw_overlap_among_many(count):
+    """All six written ranges of every tensor are looked at: only the last
+    tensor's copy lies where the first one's parameter is."""
+    size = 1 << 12
+    t = (gs.gs_adamw_tensor * count)()
+    for i in range(count):
+        at = (1 << 30) + i * 8 * size
+        for k, name in enumerate(("param", "m", "v", "m_scale", "v_scale", "copy", "grad")):
+            setattr(t[i], name, at + k * size)
+        t[i].n, t[i].grad_type, t[i].copy_type = 256, 2, 0
+    t[count - 1].copy = 1 << 30
+    assert gs.lib().gs_adamw(t, count, 1e-3, 0.9, 0.999, 1e-8, 0.0, 1, None, None, 0, None) == gs.GS_ERR_INVALID_ARG
+    assert b"overlap" in gs.lib().gs_last_error()
+
+
 def test_adamw_nothing_to_do():
     assert _adamw(count=0, tensors=False) == gs.GS_OK
     assert _adamw(n=0, param=None, grad=None, m=None, v=None) == gs.GS_OK
