@@ -210,11 +210,17 @@ __global__ __launch_bounds__(1024) void k_scan(uint32_t* __restrict__ counts, in
   __shared__ uint32_t sh[16][64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, d = blockIdx.x * 64 + lane;
   const bool live = d < (1 << bits);
+  constexpr int kHeld = 16;
   const int each = (nb + 15) / 16, b0 = std::min(w * each, nb), b1 = std::min(b0 + each, nb);
-  uint32_t sum = 0;
+  uint32_t sum = 0, held[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    held[i] = live && b0 + i < b1 ? counts[(size_t(b0 + i) << bits) + d] : 0u;
+    sum += held[i];
+  }
   if (live)
 #pragma unroll 8
-    for (int b = b0; b < b1; ++b) sum += counts[(size_t(b) << bits) + d];
+    for (int b = b0 + kHeld; b < b1; ++b) sum += counts[(size_t(b) << bits) + d];
   sh[w][lane] = sum;
   __syncthreads();
   uint32_t at = 0, all = 0;
@@ -226,8 +232,13 @@ __global__ __launch_bounds__(1024) void k_scan(uint32_t* __restrict__ counts, in
   }
   if (!live) return;
   if (w == 0) totals[d] = all;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    if (b0 + i < b1) counts[(size_t(b0 + i) << bits) + d] = at;
+    at += held[i];
+  }
 #pragma unroll 8
-  for (int b = b0; b < b1; ++b) {
+  for (int b = b0 + kHeld; b < b1; ++b) {
     uint32_t* const c = counts + (size_t(b) << bits) + d;
     const uint32_t mine = *c;
     *c = at;
@@ -254,6 +265,25 @@ __global__ __launch_bounds__(kT) void k_place(Pass p) {
     const int i = first + it * 64;
     word[it] = i < n ? load_word<I, kFirst>(p.src, block + i, p.groups) : 0u;
   }
+  // thread t: what it has to know of kPer neighbouring digits, on its way while
+  // the keys are ranked
+  uint32_t tot[kPer], before[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int b = t * kPer + j;
+    tot[j] = before[j] = 0;
+    if (b < bins && p.totals != nullptr) {
+      tot[j] = p.totals[b];
+      before[j] = p.counts[(size_t(blockIdx.x) << p.bits) + b];
+    } else if (b < bins) {
+#pragma unroll 8
+      for (int k = 0; k < p.nb; ++k) {
+        const uint32_t c = p.counts[(size_t(k) << p.bits) + b];
+        tot[j] += c;
+        before[j] += k < int(blockIdx.x) ? c : 0u;
+      }
+    }
+  }
   for (int b = lane; b < bins; b += 64) s_cnt[w][b] = 0;
   __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -270,22 +300,11 @@ __global__ __launch_bounds__(kT) void k_place(Pass p) {
   }
   __syncthreads();
   // thread t: kPer neighbouring digits
-  uint32_t tot[kPer], before[kPer], in_block[kPer], tot_sum = 0, block_sum = 0;
+  uint32_t in_block[kPer], tot_sum = 0, block_sum = 0;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int b = t * kPer + j;
-    tot[j] = before[j] = in_block[j] = 0;
-    if (b < bins && p.totals != nullptr) {
-      tot[j] = p.totals[b];
-      before[j] = p.counts[(size_t(blockIdx.x) << p.bits) + b];
-    } else if (b < bins) {
-#pragma unroll 8
-      for (int k = 0; k < p.nb; ++k) {
-        const uint32_t c = p.counts[(size_t(k) << p.bits) + b];
-        tot[j] += c;
-        before[j] += k < int(blockIdx.x) ? c : 0u;
-      }
-    }
+    in_block[j] = 0;
     if (b < bins)
 #pragma unroll
       for (int k = 0; k < kW; ++k) in_block[j] += s_cnt[k][b];
@@ -338,28 +357,33 @@ __global__ __launch_bounds__(kT) void k_place(Pass p) {
 }
 
 // offsets[g] = the first position whose key is at least g.  A workgroup's
-// bounds lie between those of its first and its last group, which two of its
-// waves find with 64 keys a step.  Each thread goes on in LDS, or, where an id
+// bounds lie between those of its first and its last group, which its first and
+// its last two waves find with 128 keys a step.  Each thread goes on in LDS, or, where an id
 // of very many entries is among them, in memory with 3 keys a step.
 __global__ __launch_bounds__(256) void k_bounds(const uint32_t* __restrict__ keys, int64_t n, int64_t groups,
                                                 int64_t* __restrict__ offsets) {
   constexpr int kHeld = 4096;
+  __shared__ int s_smaller[2][4];
   __shared__ int64_t s_ends[2];
   __shared__ uint32_t s_key[kHeld];
   const int64_t g0 = int64_t(blockIdx.x) * 256, g = g0 + threadIdx.x;
-  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  if (w < 2) {
+  {
     // keys before lo are smaller, keys from hi on are not
-    const int64_t want = g0 + w * 256;
+    const int w = threadIdx.x >> 6, i = threadIdx.x & 127;
+    const int64_t want = g0 + (w >> 1) * 256;
     int64_t lo = 0, hi = n;
-    while (lo < hi) {
-      const int64_t step = (hi - lo + 63) / 64, at = lo + lane * step;
-      const uint64_t smaller = ballot(at < hi && int64_t(keys[at < hi ? at : lo]) < want);
-      const int k = __popcll(smaller);      // ascending keys: the first k of them
-      hi = std::min(hi, lo + k * step);
-      lo = k == 0 ? hi : lo + (k - 1) * step + 1;
+    for (int64_t left = n, turn = 0; left > 0; left = (left + 127) / 128 - 1, ++turn) {      // as long for both
+      const int64_t step = (hi - lo + 127) / 128, at = lo + i * step;
+      const uint64_t smaller = ballot(lo < hi && at < hi && int64_t(keys[at < hi ? at : lo]) < want);
+      if ((threadIdx.x & 63) == 0) s_smaller[turn & 1][w] = __popcll(smaller);
+      __syncthreads();
+      const int k = s_smaller[turn & 1][w & 2] + s_smaller[turn & 1][w | 1];      // ascending keys: the first k
+      if (lo < hi) {
+        hi = std::min(hi, lo + k * step);
+        lo = k == 0 ? hi : lo + (k - 1) * step + 1;
+      }
     }
-    if (lane == 0) s_ends[w] = lo;
+    if ((threadIdx.x & 127) == 0) s_ends[w >> 1] = lo;
   }
   __syncthreads();
   int64_t lo = s_ends[0], hi = s_ends[1];
