@@ -269,7 +269,11 @@ gs_status check_route(const gs::RouteArgs& a, int64_t rows, int32_t type) {
   if (rows == 0) return GS_OK;
   REQUIRE(a.place != nullptr && aligned(a.place, 4), "place NULL or not 4-byte aligned");
   CHECK(check_vector("weights", a.weights));
-  if (a.residual != nullptr) CHECK(check_matrix("residual", a.residual, a.ldr, a.width, gs::type_bytes(type)));
+  if (a.residual != nullptr) {
+    CHECK(check_matrix("residual", a.residual, a.ldr, a.width, gs::type_bytes(type)));
+    REQUIRE(a.residual != a.y || a.ldr == a.ldy, "in place with leading dimensions %lld and %lld", (long long)a.ldr,
+            (long long)a.ldy);
+  }
   return GS_OK;
 }
 

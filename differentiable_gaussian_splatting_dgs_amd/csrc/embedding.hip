@@ -113,15 +113,17 @@ __global__ __launch_bounds__(kThreads) void k_sum(EmbedArgs a, Stretches s, int6
   const int l = threadIdx.x % L, g = threadIdx.x / L;
   if (int64_t(blockIdx.x) >= sum_groups) {
     // rows of no id
-    const int64_t v0 = ((int64_t(blockIdx.x) - sum_groups) * kGroups + g) * kZeroRows;
-    int64_t ends[kZeroRows + 1];
-#pragma unroll
-    for (int k = 0; k <= kZeroRows; ++k) ends[k] = a.offsets[std::min<int64_t>(v0 + k, a.num_rows)];
     const float none[K] = {};
+    for (int64_t v0 = ((int64_t(blockIdx.x) - sum_groups) * kGroups + g) * kZeroRows; v0 < a.num_rows;
+         v0 += (int64_t(gridDim.x) - sum_groups) * kGroups * kZeroRows) {
+      int64_t ends[kZeroRows + 1];
 #pragma unroll
-    for (int k = 0; k < kZeroRows; ++k)
-      if (v0 + k < a.num_rows && ends[k] == ends[k + 1])
-        for (int c = l; c < row.chunks; c += L) row.store(static_cast<O*>(a.dtable) + (v0 + k) * a.lddt, c, none);
+      for (int k = 0; k <= kZeroRows; ++k) ends[k] = a.offsets[std::min<int64_t>(v0 + k, a.num_rows)];
+#pragma unroll
+      for (int k = 0; k < kZeroRows; ++k)
+        if (v0 + k < a.num_rows && ends[k] == ends[k + 1])
+          for (int c = l; c < row.chunks; c += L) row.store(static_cast<O*>(a.dtable) + (v0 + k) * a.lddt, c, none);
+    }
     return;
   }
   const int64_t n = positions(a), block = blockIdx.x / s.slices;
@@ -308,7 +310,7 @@ template <typename T, typename O, int L, int C, bool kNarrow = false>
 void go_sum(const EmbedArgs& a, const Stretches& s, hipStream_t st) {
   constexpr int kGroups = kThreads / L;
   const int64_t sums = (s.count + kGroups - 1) / kGroups * s.slices;
-  const int64_t zeros = (a.num_rows + kGroups * kZeroRows - 1) / (kGroups * kZeroRows);
+  const int64_t zeros = grid_of((a.num_rows + kGroups * kZeroRows - 1) / (kGroups * kZeroRows));
   k_sum<T, O, L, C, kNarrow><<<unsigned(sums + zeros), kThreads, 0, st>>>(a, s, sums);
 }
 

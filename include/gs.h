@@ -890,7 +890,8 @@ gs_status gs_dispatch_fwd(const void* x, int64_t ldx, const int32_t* place, int6
 /* Its backward pass: dx[i] = sum over j of dxs[place[i][j]] (+ dres[i]), in
  * fp32, j ascending.  The sum has no term for a place that was left out.
  *   dres         device, [rows][ldr] (the gradient that reaches x past the
- *                heads), or NULL; dx may be dres itself
+ *                heads), or NULL; dx may be dres itself, with the same leading
+ *                dimension
  *   dx           device out, [rows][lddx]
  * Errors: as the forward pass. */
 gs_status gs_dispatch_bwd(const void* dxs, int64_t lddxs, const int32_t* place, int64_t rows, int32_t k,
@@ -902,7 +903,8 @@ gs_status gs_dispatch_bwd(const void* dxs, int64_t lddxs, const int32_t* place, 
  * not matter; a place that was left out adds nothing, whatever its weight.
  *   ys           device, [rows k][ldys]
  *   weights      device, [rows][k] fp32, or NULL: 1
- *   residual     device, [rows][ldr], or NULL; y may be residual itself
+ *   residual     device, [rows][ldr], or NULL; y may be residual itself, with
+ *                the same leading dimension
  *   y            device out, [rows][ldy]
  * Errors: as gs_dispatch_fwd. */
 gs_status gs_combine_fwd(const void* ys, int64_t ldys, const int32_t* place, const float* weights,

@@ -380,6 +380,39 @@ def test_adamw_class(gs, bits):
         gs.AdamW(twins, bits=40 - bits).load_state_dict(opt.state_dict())
 
 
+def test_adamw_past_32_bits(gs):
+    """A tensor of over 2^32 elements, in 8 bits: its first and last elements.
+    Random numbers past 2^32: the upper half of the element's number, times
+    0x9E3779B9, is mixed in."""
+    n, seed, step = 2 ** 32 + 1000, 5, 3
+    t = [torch.zeros(n, device="cuda"), torch.zeros(n, dtype=torch.bfloat16, device="cuda"),
+         torch.zeros(n, dtype=torch.uint8, device="cuda"), torch.zeros(n, dtype=torch.uint8, device="cuda"),
+         torch.zeros(-(-n // 256), device="cuda"), torch.zeros(-(-n // 256), device="cuda")]
+    parts = [(0, 2560), (2 ** 32 - 512, n)]
+    rows = []
+    for a, b in parts:
+        part = _make(a % 1000 + 1, b - a, 8, "bf16")
+        for x, y in zip(t[:4], part):
+            x[a:b] = y
+        for x, y in zip(t[4:], part[4:]):
+            x[a // 256:-(-b // 256)] = y
+        rows.append(part)
+    _step(gs, [t], step, seed=seed)
+    key = _mix((_mix((_mix(seed) + 0) % 2 ** 32) + step) % 2 ** 32)
+    for (a, b), part in zip(parts, rows):
+        want = _oracle([part], step)[0]
+        close(t[0][a:b], want[0], want[1], "p")
+        e = torch.arange(a, b, device="cuda")
+        h = _mix((e % 2 ** 32) ^ (e // 2 ** 32 * 0x9E3779B9 % 2 ** 32) ^ key)
+        g = part[1].double()
+        m1 = 0.9 * _decode(part[2], part[4], True) + (1 - 0.9) * g
+        v1 = 0.999 * _decode(part[3], part[5], False) + (1 - 0.999) * g * g
+        for got, scales, x, u, signed in ((t[2], t[4], m1, h % 65536, True), (t[3], t[5], v1, h // 65536, False)):
+            codes, units = _encode(x, ((u + 0.5) / 65536).double(), signed)
+            assert torch.equal(got[a:b], codes) and torch.equal(scales[a // 256:-(-b // 256)], units)
+    assert not bool(t[0][2560:10 ** 6].any())
+
+
 def test_adamw_overlap_is_refused(gs):
     buf = torch.zeros(400, device="cuda")
     p, m, v = buf[:100], buf[100:200], buf[200:300]

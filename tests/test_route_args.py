@@ -147,6 +147,7 @@ def _combine_bwd(dy=P(16), lddy=64, ys=P(16), ldys=64, place=P(16), weights=P(16
     (_dispatch_bwd, dict(dres=P(16), ldr=1), b"residual"), (_dispatch_bwd, dict(lddx=2), b"dx"),
     (_combine, dict(ys=None), b"ys"), (_combine, dict(y=None), b"y"), (_combine, dict(weights=P(18)), b"weights"),
     (_combine, dict(res=P(17), ldr=64), b"residual"), (_combine, dict(ldy=63), b"y"),
+    (_combine, dict(res=P(16), ldr=65), b"in place"), (_dispatch_bwd, dict(dres=P(16), ldr=66), b"in place"),
     (_combine_bwd, dict(dy=None), b"dy"), (_combine_bwd, dict(ys=None), b"ys"), (_combine_bwd, dict(lddys=1), b"dys"),
     (_combine_bwd, dict(dw=P(18)), b"dweights"), (_combine_bwd, dict(place=None), b"place"),
 ])
