@@ -97,10 +97,10 @@ __device__ __forceinline__ U larger(U a, U b) {
 // 8, of one in the other 4 or 8 lanes, which is as good for a maximum or sum.
 template <int d>
 __device__ __forceinline__ uint32_t from_other(uint32_t v) {
-  if constexpr (d == 1) return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0xB1, 0xF, 0xF, false));
-  if constexpr (d == 2) return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x4E, 0xF, 0xF, false));
-  if constexpr (d == 4) return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x141, 0xF, 0xF, false));   // mirror of 8
-  if constexpr (d == 8) return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x140, 0xF, 0xF, false));   // of 16
+  if constexpr (d == 1) return uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0xB1, 0xF, 0xF, true));
+  if constexpr (d == 2) return uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x4E, 0xF, 0xF, true));
+  if constexpr (d == 4) return uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x141, 0xF, 0xF, true));   // mirror of 8
+  if constexpr (d == 8) return uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x140, 0xF, 0xF, true));   // of 16
   return uint32_t(__shfl_xor(int(v), d, 64));
 }
 template <int d>
@@ -124,6 +124,28 @@ __device__ __forceinline__ float row_sum(float v) {
     return row_sum<L, 2 * d>(v + from_other<d>(v));
   else
     return v;
+}
+
+// 4 or 8 numbers in descending order: pairs, halves, and their merge (Batcher's
+// odd-even network).
+template <int N, typename U>
+__device__ __forceinline__ void sort_down(U (&v)[N]) {
+  auto order = [&](int i, int j) {
+    const U a = larger(v[i], v[j]);
+    v[j] = v[i] < v[j] ? v[i] : v[j];
+    v[i] = a;
+  };
+#pragma unroll
+  for (int h = 0; h < N; h += 4) {
+    order(h, h + 1), order(h + 2, h + 3);
+    order(h, h + 2), order(h + 1, h + 3);
+    order(h + 1, h + 2);
+  }
+  if constexpr (N == 8) {
+    order(0, 4), order(1, 5), order(2, 6), order(3, 7);
+    order(2, 4), order(3, 5);
+    order(1, 2), order(3, 4), order(5, 6);
+  }
 }
 
 // e^x, x <= 0 or NaN: the native exp2 of the rounded product with log2 e, and
@@ -162,66 +184,68 @@ __device__ __forceinline__ void gate_row(const GateArgs& a, int64_t r, int l, co
   constexpr int K = kChunk<T>;
   using P = Pick<T>;
   using U = typename P::U;
-  U u[C][K];
+  constexpr int N = C * K;
+  U mine[N];
 #pragma unroll
   for (int j = 0; j < C; ++j) {
     const int at = x.at(l, j, a.groups);
-    P::make(x.v[j], at, u[j]);
-    if constexpr (F != kExact)
+    U u[K];
+    P::make(x.v[j], at, u);
 #pragma unroll
-      for (int i = 0; i < K; ++i) u[j][i] = at + i < x.first(l, j) || at + i >= a.groups ? U(0) : u[j][i];
+    for (int i = 0; i < K; ++i)
+      mine[j * K + i] = F != kExact && (at + i < x.first(l, j) || at + i >= a.groups) ? U(0) : u[i];
   }
-  float e[KM];
-  int32_t id[KM];
+  // In descending order a lane's next choice is its first number, and a choice
+  // moves the others up; otherwise a choice is looked for and taken out among
+  // all of them, which is less for few choices of many.
+  constexpr bool kSorted = N <= 8 && KM >= (sizeof(U) == 8 ? 4 : 8);
+  if constexpr (kSorted) sort_down<N>(mine);
+  // choice q is lane q's, modulo L, to weigh and to write
+  constexpr int Q = (KM + L - 1) / L;
+  U pick[Q] = {};
   float top = 0.0f, total = 0.0f;
 #pragma unroll
   for (int q = 0; q < KM; ++q) {
-    U best = 0;
+    U best = mine[0];
+    if constexpr (!kSorted)
 #pragma unroll
-    for (int j = 0; j < C; ++j)
-#pragma unroll
-      for (int i = 0; i < K; ++i) best = larger(best, u[j][i]);
+      for (int i = 1; i < N; ++i) best = larger(best, mine[i]);
     best = row_max<L>(best);
-    const bool none = best < P::kOne;
-    const float value = P::value(best);
     if (q == 0) {
-      top = value;
-      if (a.renorm == 0) {
+      top = P::value(best);
+      if (a.renorm == 0)
 #pragma unroll
-        for (int j = 0; j < C; ++j)
-#pragma unroll
-          for (int i = 0; i < K; ++i) total += u[j][i] < P::kOne ? 0.0f : exp_of(P::value(u[j][i]) - top);
-        total = row_sum<L>(total);
-      }
+        for (int i = 0; i < N; ++i) total += mine[i] < P::kOne ? 0.0f : exp_of(P::value(mine[i]) - top);
     }
-    id[q] = none ? -1 : column_of(best);
-    // the first is e^0, or NaN of an infinite top
-    e[q] = none ? 0.0f : q == 0 ? 1.0f + (value - top) : exp_of(value - top);
-    if (a.renorm != 0 && q < a.k) total += e[q];
-    if (q + 1 < KM)      // columns are distinct, so one element is the choice
+    pick[q / L] = q < a.k && l == q % L ? best : pick[q / L];
+    // columns are distinct, so one number is the choice
+    const bool chosen = mine[0] == best;
 #pragma unroll
-      for (int j = 0; j < C; ++j)
-#pragma unroll
-        for (int i = 0; i < K; ++i) u[j][i] = u[j][i] == best ? U(0) : u[j][i];
+    for (int i = 0; i < N; ++i) {
+      if (q + 1 == KM) continue;
+      if constexpr (kSorted)
+        mine[i] = chosen ? (i + 1 < N ? mine[i + 1 < N ? i + 1 : i] : U(0)) : mine[i];
+      else
+        mine[i] = mine[i] == best ? U(0) : mine[i];
+    }
   }
+  float e[Q];
+#pragma unroll
+  for (int j = 0; j < Q; ++j) {
+    e[j] = pick[j] < P::kOne ? 0.0f : exp_of(P::value(pick[j]) - top);
+    if (a.renorm != 0) total += e[j];
+  }
+  total = row_sum<L>(total);
   // 1 / total, total of at least 1: the reciprocal and one step of Newton's
   float share = __builtin_amdgcn_rcpf(total);
   share = fmaf(fmaf(-total, share, 1.0f), share, share);
-  // choice q from lane q
 #pragma unroll
-  for (int q0 = 0; q0 < KM; q0 += L) {
-    int32_t mine = id[q0];
-    float weight = e[q0];
-#pragma unroll
-    for (int q = q0 + 1; q < KM && q < q0 + L; ++q) {
-      mine = l == q - q0 ? id[q] : mine;
-      weight = l == q - q0 ? e[q] : weight;
+  for (int j = 0; j < Q; ++j)
+    if (j * L + l < a.k) {
+      const bool none = pick[j] < P::kOne;
+      a.ids[r * a.k + j * L + l] = none ? -1 : column_of(pick[j]);
+      a.weights[r * a.k + j * L + l] = none ? 0.0f : e[j] * share;
     }
-    if (q0 + l < a.k && l < KM) {
-      a.ids[r * a.k + q0 + l] = mine;
-      a.weights[r * a.k + q0 + l] = mine < 0 ? 0.0f : weight * share;
-    }
-  }
 }
 
 template <typename T, int L, int C, int KM, Fit F>
@@ -274,7 +298,7 @@ __device__ __forceinline__ void gate_row_bwd(const GateArgs& a, int64_t r, int l
     }
     // a chunk that was moved back writes what others write too
     if constexpr (F == kNarrow) {
-      if (l == 0) store_chunk_n(dl, o, a.groups);
+      store_chunk_n(dl, o, a.groups);
     } else if (x.first(l, j) < a.groups) {
       store_chunk(dl + at, o);
     }
@@ -334,7 +358,11 @@ hipError_t by_fit(bool fwd, const GateArgs& a, hipStream_t st) {
 template <typename T>
 hipError_t by_width(bool fwd, const GateArgs& a, hipStream_t st) {
   const int chunks = (a.groups + kChunk<T> - 1) / kChunk<T>;
-  if (a.groups < kChunk<T>) return by_choices<T, 8, 1, kNarrow>(fwd, a, st);
+  // as many lanes as chunks: with 8 lanes for 16 bf16 logits six would be idle
+  if (a.groups < kChunk<T>) return by_choices<T, 1, 1, kNarrow>(fwd, a, st);
+  if (chunks <= 1) return by_fit<T, 1, 1>(fwd, a, st);
+  if (chunks <= 2) return by_fit<T, 2, 1>(fwd, a, st);
+  if (chunks <= 4) return by_fit<T, 4, 1>(fwd, a, st);
   if (chunks <= 8) return by_fit<T, 8, 1>(fwd, a, st);
   if (chunks <= 16) return by_fit<T, 16, 1>(fwd, a, st);
   if (chunks <= 32) return by_fit<T, 32, 1>(fwd, a, st);
