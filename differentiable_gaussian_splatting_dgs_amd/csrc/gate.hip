@@ -93,37 +93,48 @@ __device__ __forceinline__ U larger(U a, U b) {
   return a > b ? a : b;
 }
 
-// v of a lane whose number differs in one bit (d: 1, 2, 16, 32) or, for 4 and
-// 8, of one in the other 4 or 8 lanes, which is as good for a maximum or sum.
-template <int d>
-__device__ __forceinline__ uint32_t from_other(uint32_t v) {
-  if constexpr (d == 1) return uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0xB1, 0xF, 0xF, true));
-  if constexpr (d == 2) return uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x4E, 0xF, 0xF, true));
-  if constexpr (d == 4) return uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x141, 0xF, 0xF, true));   // mirror of 8
-  if constexpr (d == 8) return uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x140, 0xF, 0xF, true));   // of 16
-  return uint32_t(__shfl_xor(int(v), d, 64));
+// op(v, w) with w that of a lane whose number differs in one bit (d: 1, 2, 16,
+// 32) or, for 4 and 8, of one in the other 4 or 8 lanes, which is as good for a
+// maximum or sum of lanes that agree so far.  All in the vector unit: within 16
+// lanes by their rows' patterns, beyond by exchanging rows of two copies.
+template <int d, typename Op>
+__device__ __forceinline__ uint32_t with_other(uint32_t v, Op op) {
+  if constexpr (d == 1) return op(v, uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0xB1, 0xF, 0xF, true)));
+  if constexpr (d == 2) return op(v, uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x4E, 0xF, 0xF, true)));
+  if constexpr (d == 4) return op(v, uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x141, 0xF, 0xF, true)));   // mirror of 8
+  if constexpr (d == 8) return op(v, uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x140, 0xF, 0xF, true)));   // of 16
+  if constexpr (d == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return op(uint32_t(r[0]), uint32_t(r[1]));
+  }
+  if constexpr (d == 32) {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return op(uint32_t(r[0]), uint32_t(r[1]));
+  }
 }
-template <int d>
-__device__ __forceinline__ uint64_t from_other(uint64_t v) {
-  return uint64_t(from_other<d>(uint32_t(v >> 32))) << 32 | from_other<d>(uint32_t(v));
-}
-template <int d>
-__device__ __forceinline__ float from_other(float v) {
-  return __builtin_bit_cast(float, from_other<d>(__builtin_bit_cast(uint32_t, v)));
-}
-template <int L, int d = 1, typename U>
-__device__ __forceinline__ U row_max(U v) {
+template <int L, int d = 1, typename Op>
+__device__ __forceinline__ uint32_t row_all(uint32_t v, Op op) {
   if constexpr (d < L)
-    return row_max<L, 2 * d>(larger(v, from_other<d>(v)));
+    return row_all<L, 2 * d>(with_other<d>(v, op), op);
   else
     return v;
 }
-template <int L, int d = 1>
+template <int L>
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+  return row_all<L>(v, larger<uint32_t>);
+}
+// The upper halves' maximum, then that of the lower halves that go with it.
+template <int L>
+__device__ __forceinline__ uint64_t row_max(uint64_t v) {
+  const uint32_t upper = row_max<L>(uint32_t(v >> 32));
+  return uint64_t(upper) << 32 | row_max<L>(uint32_t(v >> 32) == upper ? uint32_t(v) : 0u);
+}
+template <int L>
 __device__ __forceinline__ float row_sum(float v) {
-  if constexpr (d < L)
-    return row_sum<L, 2 * d>(v + from_other<d>(v));
-  else
-    return v;
+  return __builtin_bit_cast(float, row_all<L>(__builtin_bit_cast(uint32_t, v), [](uint32_t a, uint32_t b) {
+                              return __builtin_bit_cast(
+                                  uint32_t, __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b));
+                            }));
 }
 
 // 4 or 8 numbers in descending order: pairs, halves, and their merge (Batcher's
