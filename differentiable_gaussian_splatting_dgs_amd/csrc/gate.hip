@@ -123,10 +123,16 @@ template <int L>
 __device__ __forceinline__ uint32_t row_max(uint32_t v) {
   return row_all<L>(v, larger<uint32_t>);
 }
-// The upper halves' maximum, then that of the lower halves that go with it.
+// The upper halves' maximum, then that of the lower halves that go with it; of
+// a whole wave usually one lane's.
 template <int L>
 __device__ __forceinline__ uint64_t row_max(uint64_t v) {
   const uint32_t upper = row_max<L>(uint32_t(v >> 32));
+  if constexpr (L == 64) {
+    const uint64_t has = __builtin_amdgcn_ballot_w64(uint32_t(v >> 32) == upper);
+    if ((has & (has - 1)) == 0)
+      return uint64_t(upper) << 32 | uint32_t(__builtin_amdgcn_readlane(int(v), __builtin_ctzll(has)));
+  }
   return uint64_t(upper) << 32 | row_max<L>(uint32_t(v >> 32) == upper ? uint32_t(v) : 0u);
 }
 template <int L>
