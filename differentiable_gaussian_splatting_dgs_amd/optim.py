@@ -110,17 +110,21 @@ def gs_adamw(params, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, we
 
 
 def _moment(s, codes, scales, moment, dtype, values):
-    n, device = codes.numel(), codes.device
-    at = _tensor(codes, (_U8,), n, device, "codes")
-    scales_at = _tensor(scales, (_F32,), _blocks(n), device, "scales")
-    if dtype not in _TYPES:
+    n, t, index = codes.numel(), _TYPES.get(dtype), codes.get_device()
+    if t is None:
         raise ValueError(f"values of {dtype}: bfloat16, float16 or float32 expected")
-    _on_gpu(codes, "codes")
+    if codes.dtype is not _U8 or not codes.is_contiguous():
+        _tensor(codes, (_U8,), n, codes.device, "codes")
+    if (scales.dtype is not _F32 or scales.numel() != -(-n // GS_ADAMW_BLOCK) or scales.get_device() != index
+            or not scales.is_contiguous()):
+        _tensor(scales, (_F32,), _blocks(n), codes.device, "scales")
+    if index < 0:
+        _on_gpu(codes, "codes")
     if values is None:
-        values = torch.empty(codes.shape, dtype=dtype, device=device)
+        values = torch.empty_like(codes, dtype=dtype)
     else:
-        _tensor(values, (dtype,), n, device, "values")
-    st = lib().gs_adamw_moment(at, scales_at, n, moment, _TYPES[dtype], values.data_ptr(), s)
+        _tensor(values, (dtype,), n, codes.device, "values")
+    st = lib().gs_adamw_moment(codes.data_ptr(), scales.data_ptr(), n, moment, t, values.data_ptr(), s)
     if st:
         _check(st, "gs_adamw_moment")
     return values
@@ -139,7 +143,7 @@ class AdamW:
     in 8 bits (2 bytes a parameter instead of 8); ``copies[i]`` (or None) is
     written with parameter i's new values.  ``capturable`` keeps the step's
     number on the device, so that a captured ``step`` counts on with each
-    replay.  ``state``: (m, v, m_scale, v_scale) of each tensor to go on from,
+    replay (``steps``, on the host, does not; without it a capture is refused).  ``state``: (m, v, m_scale, v_scale) of each tensor to go on from,
     taken as they are (scales None for moments in 32 bits), ``step`` the number
     of steps done."""
 
@@ -191,10 +195,13 @@ class AdamW:
         self.steps += 1
 
     def _enqueue(self, s, first, numbers, grad_scale):
-        step = self.steps + 1
+        _on_gpu(first, "parameter 0")
         if self.step_dev is not None:
-            _on_gpu(first, "parameter 0")
             step = self.step_dev.add_(1)
+        elif torch.cuda.is_current_stream_capturing():
+            raise ValueError("a captured step would stay the same step in every replay: make the AdamW capturable")
+        else:
+            step = self.steps + 1
         _call(s, first, self._table, len(self.params), numbers, step, grad_scale, self.seed)
 
     def state_dict(self):

@@ -335,6 +335,17 @@ def test_adamw_device_step_scale_and_graph(gs):
         torch.cuda.synchronize()
         _compare(tensors, want, f"replay {k}")
     assert opt.state_dict()["steps"] == 45
+    # a step whose number is the host's is not captured
+    fixed = gs.AdamW([torch.ones(8, device="cuda")])
+    g8 = torch.ones(8, device="cuda")
+    fixed.step([g8])
+    kept = fixed.params[0].clone()
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        with pytest.raises(ValueError, match="capturable"):
+            fixed.step([g8])
+        torch.zeros(1, device="cuda")
+    torch.cuda.synchronize()
+    assert fixed.steps == 1 and torch.equal(fixed.params[0], kept)
     step.fill_(-3)        # counts as the first
     want = _oracle(tensors, 1)
     _step(gs, tensors, step)
