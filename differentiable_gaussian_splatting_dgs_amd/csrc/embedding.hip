@@ -353,8 +353,12 @@ hipError_t embed_bwd(int type, const EmbedArgs& a, void* ws, hipStream_t st) {
 
 template <typename T, typename I>
 hipError_t embed_fwd(const EmbedArgs& a, hipStream_t st) {
-  if (a.width < kChunk<T>) return go_fwd<T, I, 8, true>(a, st);
-  switch (row_lanes((a.width + kChunk<T> - 1) / kChunk<T>)) {
+  if (a.width < kChunk<T>) return go_fwd<T, I, 2, true>(a, st);
+  const int chunks = (a.width + kChunk<T> - 1) / kChunk<T>;
+  // 1,000,000 x 16 bf16 with 8 lanes 16 us, with 2 12
+  if (chunks <= 2) return go_fwd<T, I, 2>(a, st);
+  if (chunks <= 4) return go_fwd<T, I, 4>(a, st);
+  switch (row_lanes(chunks)) {
     case 8: return go_fwd<T, I, 8>(a, st);
     case 16: return go_fwd<T, I, 16>(a, st);
     case 32: return go_fwd<T, I, 32>(a, st);

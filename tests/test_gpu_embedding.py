@@ -128,6 +128,29 @@ def test_embedding_forward(gs, name, width):
             assert rows == 1 or bool((padding(y) == 7.0).all())
 
 
+@pytest.mark.parametrize("rows,width,name", [
+    (4_200_003, 3, "bf16"), (2_100_002, 16, "fp16"), (1_100_001, 20, "bf16"), (1_050_003, 12, "fp32"), (600_003, 40, "bf16"),
+    (70_001, 515, "fp32"), (300_002, 255, "fp16"), (600_001, 128, "fp32"), (270_001, 1024, "bf16")])
+def test_embedding_forward_of_many_rows(gs, rows, width, name):
+    """Several rows at a time, with some left at the end, and outputs beyond the
+    caches' size; with a scale of a power of two every value is exact."""
+    t = TYPES[name]
+    table = rand(gen(width), 5000, width, dtype=t)
+    ids = _ids(rows, rows, 5000, torch.int32 if rows % 2 else torch.int64)
+    there = (ids >= 0) & (ids < 5000)
+    want = torch.where(there[:, None], table[torch.where(there, ids, 0).long()] * 2.0, torch.zeros((), dtype=t, device="cuda"))
+    assert torch.equal(gs.gs_embedding_fwd(table, ids, 2.0), want)
+    y = strided(torch.full((rows, width), 5.0, dtype=t, device="cuda"), 5, 1, fill=7.0)
+    gs.gs_embedding_fwd(table, ids, 2.0, y=y)
+    assert torch.equal(y, want) and bool((padding(y) == 7.0).all())
+
+
+@pytest.mark.parametrize("name", list(TYPES))
+@pytest.mark.parametrize("width", [4, 5, 12, 16, 17, 24, 31, 32, 33])
+def test_embedding_forward_of_few_chunks(gs, name, width):
+    test_embedding_forward(gs, name, width)
+
+
 def test_embedding_forward_no_rows(gs):
     table = torch.ones(4, 8, device="cuda")
     assert gs.gs_embedding_fwd(table, torch.empty(0, dtype=torch.int64, device="cuda")).shape == (0, 8)

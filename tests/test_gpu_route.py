@@ -223,6 +223,31 @@ def test_routed_rows(gs, name, width):
         _check_routes(gs, x, place, None, None, shift=1)
 
 
+@pytest.mark.parametrize("rows,k,width,name", [
+    (3001, 1, 258, "fp32"), (1500, 2, 261, "fp32"), (700, 2, 520, "bf16"), (2003, 1, 1000, "fp16"), (801, 2, 1025, "bf16"),
+    (901, 4, 515, "fp32"), (5000, 2, 512, "bf16")])
+def test_routed_rows_of_more_than_a_wave(gs, rows, k, width, name):
+    g = gen(rows)
+    x, residual = rand(g, rows, width, dtype=TYPES[name]), rand(g, rows, width, dtype=TYPES[name])
+    w = torch.rand(rows, k, generator=g, device="cuda")
+    place = gs.gs_group_sort(_picks(rows, rows, k, 24), 24)[2]
+    _check_routes(gs, x, place, w, residual)
+    _check_routes(gs, x, place, w, residual, shift=1)
+
+
+def test_dispatch_beyond_the_caches(gs):
+    """An output of over 2^28 bytes, whose stores go past the caches."""
+    for rows, k, width, t in ((140_001, 2, 512, torch.bfloat16), (70_003, 3, 516, torch.float32)):
+        x = rand(gen(k), rows, width, dtype=t)
+        place = gs.gs_group_sort(_picks(1, rows, k, 16), 16)[2]
+        there = place >= 0
+        xs = torch.full((rows * k, width), 5.0, dtype=t, device="cuda")
+        gs.gs_dispatch_fwd(x, place, xs=xs)
+        want = torch.full_like(xs, 5.0)
+        want[place[there].long()] = x[there.nonzero()[:, 0]]
+        assert torch.equal(xs, want)
+
+
 def test_routed_rows_all_dropped_and_no_rows(gs):
     x = rand(gen(1), 6, 40)
     place = torch.full((6, 2), -1, dtype=torch.int32, device="cuda")
