@@ -16,7 +16,7 @@
 // as busy: the instructions of the loops over the logits count.  1,000,000 x 64
 // bf16, 2 choices: 32 us (144 MB at 4.5 TB/s); gradient of 70,001 x 250 fp32, 8
 // choices, of all logits: 32 us (147 MB at 4.5 TB/s).  With 8 choices the vector
-// unit bounds it: bf16 x 64 47 us, x 256 207, fp32 x 64 105, x 256 490.
+// unit bounds it: bf16 x 64 39 us, x 256 130, fp32 x 64 72, x 256 264.
 #include <algorithm>
 
 #include "row_chunks.hpp"
@@ -188,6 +188,10 @@ struct Held {
   __device__ __forceinline__ static int at(int l, int j, int groups) {
     return F == kNarrow ? 0 : F == kExact ? first(l, j) : std::min(first(l, j), groups - kChunk<T>);
   }
+  // whether no other chunk has the i-th of chunk j, and the row does
+  __device__ __forceinline__ static bool own(int l, int j, int i, int groups) {
+    return F == kNarrow ? i < groups : i >= first(l, j) - at(l, j, groups);
+  }
   __device__ __forceinline__ void load(const GateArgs& a, int64_t r, int l) {
     const T* __restrict__ x = static_cast<const T*>(a.logits) + r * a.ld;
 #pragma unroll
@@ -196,14 +200,21 @@ struct Held {
   }
 };
 
+// Choices (rounded up) for which a lane sorts its numbers: from 4 where that
+// saves looking through several chunks, or 64-bit numbers (1,000,000 x 256 bf16,
+// k 4, four chunks a lane 109 us sorted; one chunk unsorted 167).
+template <typename T>
+constexpr bool many_choices(int chunks, int km) {
+  return km >= (sizeof(T) == 4 || chunks > 1 ? 4 : 8);
+}
+
 // L lanes a row, C chunks a lane; KM: choices, rounded up.
 template <typename T, int L, int C, int KM, Fit F>
 __device__ __forceinline__ void gate_row(const GateArgs& a, int64_t r, int l, const Held<T, L, C, F>& x) {
   constexpr int K = kChunk<T>;
   using P = Pick<T>;
   using U = typename P::U;
-  constexpr int N = C * K;
-  U mine[N];
+  U mine[C][K];
 #pragma unroll
   for (int j = 0; j < C; ++j) {
     const int at = x.at(l, j, a.groups);
@@ -211,40 +222,51 @@ __device__ __forceinline__ void gate_row(const GateArgs& a, int64_t r, int l, co
     P::make(x.v[j], at, u);
 #pragma unroll
     for (int i = 0; i < K; ++i)
-      mine[j * K + i] = F != kExact && (at + i < x.first(l, j) || at + i >= a.groups) ? U(0) : u[i];
+      mine[j][i] = F != kExact && !x.own(l, j, i, a.groups) ? U(0) : u[i];
   }
-  // In descending order a lane's next choice is its first number, and a choice
-  // moves the others up; otherwise a choice is looked for and taken out among
-  // all of them, which is less for few choices of many.
-  constexpr bool kSorted = N <= 8 && KM >= (sizeof(U) == 8 ? 4 : 8);
-  if constexpr (kSorted) sort_down<N>(mine);
+  // With its chunks in descending order a lane's next choice is one of their
+  // first numbers, and a choice moves that chunk's others up; otherwise a choice
+  // is looked for and taken out among all of them, which is less for few choices.
+  constexpr bool kSorted = many_choices<T>(C, KM);
+  if constexpr (kSorted)
+#pragma unroll
+    for (int j = 0; j < C; ++j) sort_down<K>(mine[j]);
   // choice q is lane q's, modulo L, to weigh and to write
   constexpr int Q = (KM + L - 1) / L;
   U pick[Q] = {};
   float top = 0.0f, total = 0.0f;
 #pragma unroll
   for (int q = 0; q < KM; ++q) {
-    U best = mine[0];
-    if constexpr (!kSorted)
+    U best = mine[0][0];
 #pragma unroll
-      for (int i = 1; i < N; ++i) best = larger(best, mine[i]);
+    for (int j = 0; j < C; ++j)
+#pragma unroll
+      for (int i = 0; i < (kSorted ? 1 : K); ++i) best = larger(best, mine[j][i]);
     best = row_max<L>(best);
     if (q == 0) {
       top = P::value(best);
       if (a.renorm == 0)
 #pragma unroll
-        for (int i = 0; i < N; ++i) total += mine[i] < P::kOne ? 0.0f : exp_of(P::value(mine[i]) - top);
+        for (int j = 0; j < C; ++j)
+#pragma unroll
+          for (int i = 0; i < K; ++i) {
+            const float e = exp_of(float(x.v[j].v[i]) - top);
+            total += F != kExact && !x.own(l, j, i, a.groups) ? 0.0f : e;
+          }
     }
     pick[q / L] = q < a.k && l == q % L ? best : pick[q / L];
     // columns are distinct, so one number is the choice
-    const bool chosen = mine[0] == best;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (q + 1 == KM) continue;
-      if constexpr (kSorted)
-        mine[i] = chosen ? (i + 1 < N ? mine[i + 1 < N ? i + 1 : i] : U(0)) : mine[i];
-      else
-        mine[i] = mine[i] == best ? U(0) : mine[i];
+    for (int j = 0; j < C; ++j) {
+      const bool chosen = mine[j][0] == best;
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        if (q + 1 == KM) continue;
+        if constexpr (kSorted)
+          mine[j][i] = chosen ? (i + 1 < K ? mine[j][i + 1 < K ? i + 1 : i] : U(0)) : mine[j][i];
+        else
+          mine[j][i] = mine[j][i] == best ? U(0) : mine[j][i];
+      }
     }
   }
   float e[Q];
@@ -347,53 +369,71 @@ __global__ __launch_bounds__(kThreads) void k_gate(GateArgs a) {
   }
 }
 
-template <typename T, int L, int C, int KM, Fit F>
-hipError_t go(bool fwd, const GateArgs& a, hipStream_t st) {
+template <typename T, int L, int C, int KM, Fit F, bool kFwd>
+hipError_t go(const GateArgs& a, hipStream_t st) {
   // as many workgroups as are there at a time
   const int64_t blocks = std::min<int64_t>((int64_t(a.rows) + kThreads / L - 1) / (kThreads / L), 2048);
-  if (fwd)
-    k_gate<T, L, C, KM, F, true><<<unsigned(blocks), kThreads, 0, st>>>(a);
-  else
-    k_gate<T, L, C, KM, F, false><<<unsigned(blocks), kThreads, 0, st>>>(a);
+  k_gate<T, L, C, KM, F, kFwd><<<unsigned(blocks), kThreads, 0, st>>>(a);
   return hipGetLastError();
 }
 
-template <typename T, int L, int C, Fit F>
-hipError_t by_choices(bool fwd, const GateArgs& a, hipStream_t st) {
-  if (a.k <= 1) return go<T, L, C, 1, F>(fwd, a, st);
-  if (a.k <= 2) return go<T, L, C, 2, F>(fwd, a, st);
-  if (a.k <= 4) return go<T, L, C, 4, F>(fwd, a, st);
-  if (a.k <= 8) return go<T, L, C, 8, F>(fwd, a, st);
-  return go<T, L, C, kMaxChoices, F>(fwd, a, st);
+template <typename T, int L, int C, Fit F, bool kFwd>
+hipError_t by_choices(const GateArgs& a, hipStream_t st) {
+  if (a.k <= 1) return go<T, L, C, 1, F, kFwd>(a, st);
+  if (a.k <= 2) return go<T, L, C, 2, F, kFwd>(a, st);
+  if (a.k <= 4) return go<T, L, C, 4, F, kFwd>(a, st);
+  if constexpr (C == 4 && 4 * L < kMaxChoices)      // at most four choices a lane, as below
+    return go<T, L, C, 8, F, kFwd>(a, st);
+  else
+    return a.k <= 8 ? go<T, L, C, 8, F, kFwd>(a, st) : go<T, L, C, kMaxChoices, F, kFwd>(a, st);
 }
 
-template <typename T, int L, int C>
-hipError_t by_fit(bool fwd, const GateArgs& a, hipStream_t st) {
-  if (a.groups == L * C * kChunk<T>) return by_choices<T, L, C, kExact>(fwd, a, st);
-  return by_choices<T, L, C, kMoved>(fwd, a, st);
+template <typename T, int L, int C, bool kFwd>
+hipError_t by_fit(const GateArgs& a, hipStream_t st) {
+  if (a.groups == L * C * kChunk<T>) return by_choices<T, L, C, kExact, kFwd>(a, st);
+  return by_choices<T, L, C, kMoved, kFwd>(a, st);
+}
+
+// The forward pass: with four chunks a lane instead of one, four times as many
+// rows share the exchanges between lanes (k 8, bf16 1,000,000 x 64 45 -> 39 us, x 256 206
+// -> 129, fp32 x 64 103 -> 70, x 256 490 -> 262; k 2, bf16 x 64 30 -> 25, x 256 126 ->
+// 101).  Not so where that leaves a SIMD less than four waves (20,000 x 256 bf16, k 16,
+// 9 us with one chunk, 11 with four), a lane more than four choices to weigh
+// (1,000,000 x 64 bf16, k 16, 71 us with 8 lanes, 85 with 2), or one lane alone (x 16
+// fp32, k 8, 29 and 46).
+template <typename T, int L, int C, bool kFwd>
+hipError_t by_lanes(const GateArgs& a, int chunks, hipStream_t st) {
+  if constexpr (kFwd && L * C >= 8)
+    if (int64_t(a.rows) * chunks >= 4 * 64 * 4096 && a.k <= L * C) return by_fit<T, L * C / 4, 4, true>(a, st);
+  return by_fit<T, L, C, kFwd>(a, st);
+}
+
+template <typename T, bool kFwd>
+hipError_t by_width(const GateArgs& a, hipStream_t st) {
+  const int chunks = (a.groups + kChunk<T> - 1) / kChunk<T>;
+  // as many lanes as chunks: with 8 lanes for 16 bf16 logits six would be idle
+  if (a.groups < kChunk<T>) return by_choices<T, 1, 1, kNarrow, kFwd>(a, st);
+  if (chunks <= 1) return by_lanes<T, 1, 1, kFwd>(a, chunks, st);
+  if (chunks <= 2) return by_lanes<T, 2, 1, kFwd>(a, chunks, st);
+  if (chunks <= 4) return by_lanes<T, 4, 1, kFwd>(a, chunks, st);
+  if (chunks <= 8) return by_lanes<T, 8, 1, kFwd>(a, chunks, st);
+  if (chunks <= 16) return by_lanes<T, 16, 1, kFwd>(a, chunks, st);
+  if (chunks <= 32) return by_lanes<T, 32, 1, kFwd>(a, chunks, st);
+  if (chunks <= 64) return by_lanes<T, 64, 1, kFwd>(a, chunks, st);
+  if constexpr (sizeof(T) == 4)
+    if (chunks > 128) return by_fit<T, 64, 4, kFwd>(a, st);
+  return by_lanes<T, 64, 2, kFwd>(a, chunks, st);
 }
 
 template <typename T>
-hipError_t by_width(bool fwd, const GateArgs& a, hipStream_t st) {
-  const int chunks = (a.groups + kChunk<T> - 1) / kChunk<T>;
-  // as many lanes as chunks: with 8 lanes for 16 bf16 logits six would be idle
-  if (a.groups < kChunk<T>) return by_choices<T, 1, 1, kNarrow>(fwd, a, st);
-  if (chunks <= 1) return by_fit<T, 1, 1>(fwd, a, st);
-  if (chunks <= 2) return by_fit<T, 2, 1>(fwd, a, st);
-  if (chunks <= 4) return by_fit<T, 4, 1>(fwd, a, st);
-  if (chunks <= 8) return by_fit<T, 8, 1>(fwd, a, st);
-  if (chunks <= 16) return by_fit<T, 16, 1>(fwd, a, st);
-  if (chunks <= 32) return by_fit<T, 32, 1>(fwd, a, st);
-  if (chunks <= 64) return by_fit<T, 64, 1>(fwd, a, st);
-  if constexpr (sizeof(T) == 4)
-    if (chunks > 128) return by_fit<T, 64, 4>(fwd, a, st);
-  return by_fit<T, 64, 2>(fwd, a, st);
+hipError_t either(bool fwd, const GateArgs& a, hipStream_t st) {
+  return fwd ? by_width<T, true>(a, st) : by_width<T, false>(a, st);
 }
 
 hipError_t by_type(int type, bool fwd, const GateArgs& a, hipStream_t st) {
-  if (type == kTypeBF16) return by_width<bf16>(fwd, a, st);
-  if (type == kTypeF16) return by_width<f16>(fwd, a, st);
-  return by_width<float>(fwd, a, st);
+  if (type == kTypeBF16) return either<bf16>(fwd, a, st);
+  if (type == kTypeF16) return either<f16>(fwd, a, st);
+  return either<float>(fwd, a, st);
 }
 
 }  // namespace

@@ -83,6 +83,19 @@ def test_gate(gs, name, groups):
             _check_gate_bwd(gs, x, ids, w, renorm)
 
 
+@pytest.mark.parametrize("name", list(TYPES))
+@pytest.mark.parametrize("groups,rows", [(20, 300_000), (32, 270_001), (33, 230_001), (40, 212_000), (64, 150_001), (65, 120_000),
+                                         (128, 70_003), (250, 40_003), (256, 34_001), (500, 20_000), (512, 18_001),
+                                         (700, 12_007), (1024, 9_001)])
+def test_gate_of_many_rows(gs, name, groups, rows):
+    """Rows enough for four waves for each SIMD: a row's lanes hold more of it then."""
+    rows *= 1 if name == "fp32" else 2
+    x = _logits(groups, rows, groups, TYPES[name])
+    for k, renorm in ((1, True), (2, False), (4, True), (8, False), (8, True), (16, False), (13, True)):
+        _check_gate(gs, x, k, renorm)
+    _check_gate(gs, strided(x, 3, 1), 7, False)
+
+
 def _check_gate_bwd(gs, x, ids, w, renorm, **kw):
     rows, k = ids.shape
     dw = rand(gen(rows), rows, k)
