@@ -14,7 +14,7 @@
 // The gradient's few chosen entries go through LDS to the lanes that hold
 // their columns.  Bound by the bytes of the logits, with the vector unit about
 // as busy: the instructions of the loops over the logits count.  1,000,000 x 64
-// bf16, 2 choices: 32 us (144 MB at 4.5 TB/s); gradient of 70,001 x 250 fp32, 8
+// bf16, 2 choices: 29 us (144 MB at 5.0 TB/s); gradient of 70,001 x 250 fp32, 8
 // choices, of all logits: 32 us (147 MB at 4.5 TB/s).  With 8 choices the vector
 // unit bounds it: bf16 x 64 39 us, x 256 130, fp32 x 64 72, x 256 264.
 #include <algorithm>
