@@ -170,7 +170,8 @@ class AdamW:
         if len(self.copies) != count or len(self.state) != count:
             raise ValueError(f"{count} parameters, {len(self.copies)} copies, {len(self.state)} states")
         self.steps = step
-        self.step_dev = torch.tensor([step], dtype=_I64, device=device) if capturable else None
+        # the next step's number: counted on behind a call that was taken
+        self.step_dev = torch.tensor([step + 1], dtype=_I64, device=device) if capturable else None
         rows = zip(self.params, self.copies, self.state)
         self._pointers = [t.data_ptr for p, c, s in rows for t in (p, c, *s) if t is not None]
         self._table, self._held, self._sizes, self._kinds = None, None, None, None
@@ -196,17 +197,16 @@ class AdamW:
 
     def _enqueue(self, s, first, numbers, grad_scale):
         _on_gpu(first, "parameter 0")
-        if self.step_dev is not None:
-            step = self.step_dev.add_(1)
-        elif torch.cuda.is_current_stream_capturing():
+        if self.step_dev is None and torch.cuda.is_current_stream_capturing():
             raise ValueError("a captured step would stay the same step in every replay: make the AdamW capturable")
-        else:
-            step = self.steps + 1
+        step = self.steps + 1 if self.step_dev is None else self.step_dev
         _call(s, first, self._table, len(self.params), numbers, step, grad_scale, self.seed)
+        if self.step_dev is not None:
+            self.step_dev.add_(1)
 
     def state_dict(self):
         """The moments, as they are held, and the number of steps done."""
-        steps = self.steps if self.step_dev is None else int(self.step_dev)
+        steps = self.steps if self.step_dev is None else int(self.step_dev) - 1
         return {"state": [tuple(None if x is None else x.clone() for x in s) for s in self.state], "steps": steps}
 
     def load_state_dict(self, d):
@@ -222,4 +222,4 @@ class AdamW:
                     a.copy_(b)
         self.steps = int(d["steps"])
         if self.step_dev is not None:
-            self.step_dev.fill_(self.steps)
+            self.step_dev.fill_(self.steps + 1)

@@ -436,3 +436,33 @@ def test_adamw_overlap_is_refused(gs):
         gs.gs_adamw([p], [g], [m], [m], 1, 1e-3)
     with pytest.raises(gs.GSError, match="overlap"):
         gs.gs_adamw([p], [g], [m], [v], 1, 1e-3, copies=[p])
+
+
+def test_adamw_refused_steps_do_not_count(gs):
+    """A call that is refused leaves the number of a capturable optimiser's steps,
+    on the device too, and all tensors: the next step is the one it would have been."""
+    tensors = [_make(3, 700, 8), _make(4, 301, 32)]
+    opt = gs.AdamW([t[0] for t in tensors], lr=HYPER["lr"], weight_decay=0.02, capturable=True, seed=9, step=6,
+                   state=[t[2:] for t in tensors])
+    grads = [t[1] for t in tensors]
+    want, before = _oracle(tensors, 7, seed=9), [_clone(t) for t in tensors]
+    for scale in (torch.ones(1), torch.ones(1, dtype=F64, device="cuda"), torch.ones(2, device="cuda")):
+        with pytest.raises(ValueError, match="grad_scale"):
+            opt.step(grads, grad_scale=scale)
+    for name, bad in (("lr", math.nan), ("eps", 0.0), ("weight_decay", math.inf)):
+        good = getattr(opt, name)
+        setattr(opt, name, bad)
+        with pytest.raises(gs.GSError, match=name):
+            opt.step(grads)
+        setattr(opt, name, good)
+    with pytest.raises(ValueError, match="gradient 1"):
+        opt.step([grads[0], grads[0]])
+    assert opt.steps == 6 and opt.state_dict()["steps"] == 6
+    assert all(a is None or torch.equal(a, b) for s, t in zip(tensors, before) for a, b in zip(s, t))
+    opt.step(grads)
+    _compare(tensors, want)
+    assert opt.steps == 7 and opt.state_dict()["steps"] == 7
+    opt.load_state_dict(opt.state_dict())
+    want = _oracle(tensors, 8, seed=9)
+    opt.step(grads)
+    _compare(tensors, want)
