@@ -11,6 +11,7 @@ in the same pass.  Errors as in the network operators: ``ValueError`` or
 from __future__ import annotations
 
 import array
+from operator import attrgetter
 
 import torch
 
@@ -20,6 +21,8 @@ from .network import _F32, _I64, _TYPES, _U8, _launch, _on_gpu
 # a gs_adamw_tensor as 64-bit words: param, grad, m, v, m_scale, v_scale, copy,
 # n, grad_type below copy_type
 _WORDS, _GRAD, _COUNT, _KINDS = 9, 1, 7, 8
+_address, _dense = torch.Tensor.data_ptr, torch.Tensor.is_contiguous
+_nbytes, _dtype = attrgetter("nbytes"), attrgetter("dtype")
 
 
 def _blocks(n):
@@ -143,20 +146,23 @@ class AdamW:
     in 8 bits (2 bytes a parameter instead of 8); ``copies[i]`` (or None) is
     written with parameter i's new values.  ``capturable`` keeps the step's
     number on the device, so that a captured ``step`` counts on with each
-    replay (``steps``, on the host, does not; without it a capture is refused).  ``state``: (m, v, m_scale, v_scale) of each tensor to go on from,
-    taken as they are (scales None for moments in 32 bits), ``step`` the number
-    of steps done."""
+    replay (``steps``, on the host, does not; without it a capture is refused).
+    ``state``: (m, v, m_scale, v_scale) of each tensor to go on from, taken as
+    they are (scales None for moments in 32 bits), ``step`` the number of steps
+    done.  ``params``, ``copies`` and ``state`` stay the tensors that they are
+    from then on; a tensor's storage may be replaced (its ``.data``), and each
+    step looks at all of them again."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, bits=32, min_8bit=4096,
                  copies=None, seed=0, capturable=False, state=None, step=0):
-        self.params = list(params)
-        if not self.params:
+        self._params = tuple(params)
+        if not self._params:
             raise ValueError("no parameters")
         if bits not in (8, 32):
             raise ValueError(f"bits = {bits}: 8 or 32 expected")
         self.lr, self.betas, self.eps, self.weight_decay, self.seed = lr, betas, eps, weight_decay, seed
         count, device = len(self.params), self.params[0].device
-        self.copies = list(copies) if copies is not None else [None] * count
+        self._copies = (None,) * count if copies is None else tuple(copies)
         if state is None:
             state = []
             for p in self.params:
@@ -166,15 +172,20 @@ class AdamW:
                                  + tuple(torch.zeros(_blocks(n), device=device) for _ in range(2)))
                 else:
                     state.append((torch.zeros(n, device=device), torch.zeros(n, device=device), None, None))
-        self.state = [tuple(s) for s in state]
+        self._state = tuple(tuple(s) for s in state)
         if len(self.copies) != count or len(self.state) != count:
             raise ValueError(f"{count} parameters, {len(self.copies)} copies, {len(self.state)} states")
         self.steps = step
         # the next step's number: counted on behind a call that was taken
         self.step_dev = torch.tensor([step + 1], dtype=_I64, device=device) if capturable else None
         rows = zip(self.params, self.copies, self.state)
-        self._pointers = [t.data_ptr for p, c, s in rows for t in (p, c, *s) if t is not None]
+        self._tensors = [t for p, c, s in rows for t in (p, c, *s) if t is not None]
+        self._typed = [c for c in self.copies if c is not None]
         self._table, self._held, self._sizes, self._kinds = None, None, None, None
+
+    params = property(attrgetter("_params"))
+    copies = property(attrgetter("_copies"))
+    state = property(attrgetter("_state"))
 
     def step(self, grads=None, grad_scale=None, stream=None):
         """One step with ``grads`` (default: each parameter's .grad; None leaves
@@ -183,8 +194,10 @@ class AdamW:
         count, device = len(self.params), self.params[0].device
         if len(grads) != count:
             raise ValueError(f"{len(grads)} gradients of {count} parameters")
-        # the addresses as they are now: a tensor's storage may have been replaced
-        held = [address() for address in self._pointers]
+        # the tensors as they are now: storage or layout may have been replaced
+        # (float32 and codes go by their bytes alone, a copy by its type too)
+        held = [*map(_address, self._tensors), *map(_nbytes, self._tensors), *map(_dense, self._tensors),
+                *map(_dtype, self._typed)]
         if held != self._held:
             table = array.array("Q")
             self._kinds = [_entry(table, i, device, p, *s, c)

@@ -466,3 +466,28 @@ def test_adamw_refused_steps_do_not_count(gs):
     want = _oracle(tensors, 8, seed=9)
     opt.step(grads)
     _compare(tensors, want)
+
+
+def test_adamw_storage_that_changes(gs):
+    """Parameters, copies and moments whose storage is replaced between steps
+    are followed; one that is transposed where it is, is refused."""
+    p, m, v = rand(gen(1), 40, 40), rand(gen(2), 1600, scale=0.1), rand(gen(3), 1600, scale=0.1) ** 2
+    c = torch.empty(40, 40, dtype=torch.bfloat16, device="cuda")
+    g = rand(gen(4), 40, 40)
+    opt = gs.AdamW([p], lr=HYPER["lr"], weight_decay=0.02, copies=[c], state=[(m, v, None, None)])
+    for k, t in enumerate((None, p, c, m, v)):
+        if t is not None:
+            old = t.data
+            t.data = old.clone()
+            old.fill_(7)
+        want = _oracle([[p, g, m, v, None, None]], k + 1)
+        opt.step([g])
+        _compare([[p, g, m, v, None, None]], want, f"step {k}")
+        assert torch.equal(c, p.bfloat16())
+    kept = p.clone()
+    p.data = p.data.t()
+    with pytest.raises(ValueError, match="contiguous"):
+        opt.step([g])
+    assert opt.steps == 5 and torch.equal(p.data.t(), kept)
+    p.data = p.data.t()
+    opt.step([g])

@@ -285,3 +285,42 @@ U1 = torch.uint8
 def test_adamw_binding_refuses(call, match):
     with pytest.raises(ValueError, match=match):
         call()
+
+
+@pytest.mark.parametrize("change,match", [
+    (lambda p, c, s: setattr(p, "data", p.data.t()), "contiguous"),
+    (lambda p, c, s: setattr(p, "data", p.data[:2]), "m of parameter 0"),
+    (lambda p, c, s: setattr(p, "data", p.data.bfloat16()), "bfloat16"),
+    (lambda p, c, s: setattr(c, "data", c.data.t()), "copy of parameter 0 has to be contiguous"),
+    (lambda p, c, s: setattr(c, "data", c.data[:1]), "copy of parameter 0"),
+    (lambda p, c, s: setattr(c, "data", c.data.view(torch.int16)), "copy of parameter 0 is torch.int16"),
+    (lambda p, c, s: setattr(s, "data", s.data[::2]), "m of parameter 0"),
+    (lambda p, c, s: setattr(s, "data", s.data[:7]), "m of parameter 0"),
+])
+def test_adamw_layouts_are_looked_at_again(change, match):
+    """A tensor that becomes another layout, size or type at the same address
+    is refused as it would have been at first (without a GPU a good call ends
+    with the refusal of CPU tensors)."""
+    p, c, g = _t(4, 4), _t(4, 4, dtype=torch.bfloat16), _t(4, 4)
+    m = _t(16)
+    opt = gs.AdamW([p], copies=[c], state=[(m, _t(16), None, None)])
+    with pytest.raises(ValueError, match="GPU tensor"):
+        opt.step([g])
+    change(p, c, m)
+    with pytest.raises(ValueError, match=match):
+        opt.step([g])
+
+
+def test_adamw_lists_are_fixed():
+    """What the step works on is chosen once: neither the lists nor an entry of
+    theirs can be replaced behind its back."""
+    params, copies = [_t(4), _t(3)], [None, _t(3)]
+    opt = gs.AdamW(params, copies=copies, bits=8, min_8bit=4)
+    params[0], copies[1] = _t(5), None
+    assert opt.params[0].numel() == 4 and opt.copies[1].numel() == 3
+    assert [s[2] is None for s in opt.state] == [False, True]
+    for name in ("params", "copies", "state"):
+        with pytest.raises(TypeError):
+            getattr(opt, name)[0] = None
+        with pytest.raises(AttributeError):
+            setattr(opt, name, [])
