@@ -24,7 +24,8 @@
 // and NaN) is behind branches that a whole wave takes or not: every instruction
 // for each value counts, the vector unit is about as long as the memory.
 // p's square root and reciprocal are the hardware's (about 1 ulp each, far
-// below the rounding that p's own sum makes of a small update).
+// below the rounding that p's own sum makes of a small update), which take
+// subnormal numbers as 0: where eps is that small, the update scales them.
 #include <algorithm>
 #include <cmath>
 
@@ -218,9 +219,24 @@ __device__ __forceinline__ int tensor_of(const AdamwBatch& b) {
   return lo;
 }
 
+// The root of a subnormal number is under 2^-63: taken as 0 it is at most half
+// a step of an eps from 2^-39 on.  A smaller eps (the same branch for all):
+// where the root is under k^-1 = 2^-32, root and eps are taken k times and,
+// so that its product with the rate is no subnormal, a small m is too.  eps is
+// at least 2^-126 and at most 2^125, so that no reciprocal leaves fp32.
+constexpr float kPlainEps = 0x1p-39f;
 __device__ __forceinline__ float update(float p, float m, float v, const AdamwNumbers& h, const StepNumbers& s) {
-  const float d = __builtin_amdgcn_sqrtf(v * s.inv_c2) + h.eps;
-  return fmaf(p, h.decay, -(s.rate * m * __builtin_amdgcn_rcpf(d)));
+  const float x = v * s.inv_c2;
+  float step;
+  if (h.eps >= kPlainEps) {
+    step = s.rate * m * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(x) + h.eps);
+  } else {
+    const float k = x < 0x1p-64f ? 0x1p32f : 1.0f;
+    const float r = __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(x * k * k) + h.eps * k);
+    const bool small = fabsf(m) < 0x1p-32f;
+    step = s.rate * (small ? m * k : m) * (small ? r : r * k);
+  }
+  return fmaf(p, h.decay, -step);
 }
 
 // G: the gradients' type.

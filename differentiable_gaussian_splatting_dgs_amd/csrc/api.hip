@@ -1204,7 +1204,10 @@ gs_status gs_adamw(const gs_adamw_tensor* tensors, int32_t count, double lr, dou
   REQUIRE(count >= 0 && (count == 0 || tensors != nullptr), "count = %d, or tensors NULL", int(count));
   REQUIRE(std::isfinite(lr) && std::isfinite(weight_decay), "lr or weight_decay not finite");
   REQUIRE(beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0, "a beta outside [0, 1)");
-  REQUIRE(std::isfinite(eps) && float(eps) > 0.0f && std::isfinite(float(eps)), "eps not above 0");
+  // the update's fp32 factors; the hardware's reciprocal takes subnormal numbers as 0
+  REQUIRE(float(eps) >= 0x1p-126f && float(eps) <= 0x1p125f, "eps = %g outside [2^-126, 2^125]", eps);
+  REQUIRE(std::isfinite(float(lr / (1.0 - beta1))), "lr = %g: too large for fp32 over 1 - beta1", lr);
+  REQUIRE(std::isfinite(float(1.0 - lr * weight_decay)), "lr weight_decay = %g too large for fp32", lr * weight_decay);
   REQUIRE(step_dev != nullptr || step >= 1, "step = %lld: 1 or more expected", (long long)step);
   REQUIRE(aligned(step_dev, 8) && aligned(grad_scale, 4), "step_dev or grad_scale misaligned");
   // written ranges, as (first byte, one past the last), sorted to find overlaps

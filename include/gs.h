@@ -968,9 +968,10 @@ typedef struct gs_adamw_tensor {
  *                1), for a captured call whose replays are further steps
  *   grad_scale   device, fp32 scalar, or NULL: 1
  * Errors: GS_ERR_INVALID_ARG for a negative count, n outside [0,
- * GS_MAX_ADAMW_SIZE], step below 1, an unknown type, lr, eps or weight_decay
- * not finite, a beta outside [0, 1), eps (as fp32) not above 0, scales that do
- * not match, a NULL or misaligned array, or written ranges that overlap. */
+ * GS_MAX_ADAMW_SIZE], step below 1, an unknown type, lr or weight_decay not
+ * finite, a beta outside [0, 1), eps (as fp32) outside [2^-126, 2^125], lr / (1 -
+ * beta1) or lr weight_decay past fp32, scales that do not match, a NULL or
+ * misaligned array, or written ranges that overlap. */
 gs_status gs_adamw(const gs_adamw_tensor* tensors, int32_t count, double lr, double beta1, double beta2, double eps,
                    double weight_decay, int64_t step, const int64_t* step_dev, const float* grad_scale,
                    uint64_t seed, void* stream);

@@ -491,3 +491,47 @@ def test_adamw_storage_that_changes(gs):
     assert opt.steps == 5 and torch.equal(p.data.t(), kept)
     p.data = p.data.t()
     opt.step([g])
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("eps", [2.0 ** -126, 1e-37, 1e-30, 1e-22, 1e-19, 1e-15, 1e-12, 1e-8, 1e20, 2.0 ** 125])
+@pytest.mark.parametrize("scale", [1e-36, 1e-30, 1e-22, 1e-19, 1e-17, 1.0])
+def test_adamw_small_and_large_eps(gs, bits, eps, scale):
+    """Every eps that is taken, with second moments from 0 and subnormal numbers
+    up.  The moments are off as above and by 2^-149 (a subnormal's half steps: two
+    products' and the sum's); v over the correction by as much once more; the
+    update lies between those ends and is off by 12 e of itself.  A product of
+    fp32 that is subnormal (rate times m where v is not small) is off by 2^-150,
+    under a reciprocal of at most 2^32."""
+    n, step = 4000, 2
+    t = _make(21, n, bits, scale=scale)
+    t[1][::3] = 0.0
+    if bits == 32:
+        t[2][::3], t[3][::6] = 0.0, 0.0
+    else:
+        t[2][:512], t[3][:512] = 0, 0      # two blocks with moments of 0
+    for start in (1.0, 0.0):
+        t[0].mul_(start)
+        rows = [_clone(t)]
+        p, g, m, v, ms, vs = (None if x is None else x.double() for x in t)
+        if bits == 8:
+            m, v = _decode(t[2], t[4], True), _decode(t[3], t[5], False)
+        e = float(torch.tensor(eps))      # what the call rounds it to
+        c1, c2, lr, decay = 1 - 0.9 ** step, 1 - 0.999 ** step, HYPER["lr"], 1 - HYPER["lr"] * 0.02
+        m1, v1 = 0.9 * m + (1 - 0.9) * g, 0.999 * v + (1 - 0.999) * g * g
+        off_m = 6 * EPS32 * (0.9 * m.abs() + (1 - 0.9) * g.abs()) + 2.0 ** -149
+        off_v = 6 * EPS32 * v1 + 2.0 ** -148
+        most = ((v1 + off_v) / c2 + 2.0 ** -149).sqrt() + e
+        least = ((v1 - off_v).clamp_min(0) / c2 - 2.0 ** -149).clamp_min(0).sqrt() + e
+        # nothing in both: exactly nothing
+        nothing = (g == 0) & (m == 0)
+        ends = [lr / c1 * (m1 + a * off_m) / d for a in (-1, 1) for d in (most, least)]
+        low, high = torch.stack(ends).amin(0), torch.stack(ends).amax(0)
+        slack = 12 * EPS32 * torch.maximum(low.abs(), high.abs()) + 2 * EPS32 * p.abs() + 2.0 ** -117
+        _step(gs, rows, step, eps=eps)
+        got = rows[0][0].double()
+        assert bool(got.isfinite().all())
+        fine = torch.where(nothing, (got - p * decay).abs() <= 2 * EPS32 * p.abs(),
+                           (got >= p * decay - high - slack) & (got <= p * decay - low + slack))
+        bad = (~fine).nonzero()[:, 0]
+        assert bad.numel() == 0, (bad.numel(), int(bad[0]), [float(x[bad[0]]) for x in (got, p, g, m1, v1, low, high)])

@@ -324,3 +324,21 @@ def test_adamw_lists_are_fixed():
             getattr(opt, name)[0] = None
         with pytest.raises(AttributeError):
             setattr(opt, name, [])
+
+
+@pytest.mark.parametrize("kw,word", [
+    (dict(eps=1.17e-38), b"eps"), (dict(eps=1e-40), b"eps"), (dict(eps=5e37), b"eps"),
+    (dict(lr=1e38), b"lr"), (dict(lr=-1e38), b"lr"), (dict(lr=1e39), b"lr"),
+    (dict(lr=1e20, wd=1e20), b"weight_decay"), (dict(lr=1e30, b1=1 - 2.0 ** -53), b"lr"),
+])
+def test_adamw_numbers_that_fp32_cannot_hold(kw, word):
+    """The update works in fp32: a reciprocal of eps, lr over the first step's
+    1 - beta1 and the decay's factor have to be normal numbers there."""
+    assert _adamw(**kw) == gs.GS_ERR_INVALID_ARG
+    assert word in gs.lib().gs_last_error(), gs.lib().gs_last_error()
+
+
+@pytest.mark.parametrize("kw", [dict(eps=2.0 ** -126), dict(eps=1e-15), dict(eps=1e30), dict(eps=2.0 ** 125), dict(lr=1e30),
+                                dict(lr=-1.0), dict(lr=0.0), dict(lr=1e-300), dict(b1=0.0, b2=0.0)])
+def test_adamw_numbers_that_are_taken(kw):
+    assert _adamw(**kw) == gs.GS_OK
