@@ -6,7 +6,8 @@
 //             (renorm) or over all
 //   backward  renorm: dl = w (dw - s) where chosen, s = sum w dw; else
 //             dl = [chosen] w dw - p s, p = w_0 e^(l - l_0), 0 the first choice:
-//             the row's maximum and sum are not worked out again
+//             the row's maximum and sum are not worked out again (but for a row
+//             without its first choice)
 //
 // A row lies in the registers of L lanes, read once.  A logit becomes an
 // unsigned number that orders as it does, with its column below it, so that a
@@ -135,6 +136,13 @@ __device__ __forceinline__ uint64_t row_max(uint64_t v) {
       return uint64_t(upper) << 32 | uint32_t(__builtin_amdgcn_readlane(int(v), __builtin_ctzll(has)));
   }
   return uint64_t(upper) << 32 | row_max<L>(uint32_t(v >> 32) == upper ? uint32_t(v) : 0u);
+}
+template <int L>
+__device__ __forceinline__ float row_max_of(float v) {
+  return __builtin_bit_cast(float, row_all<L>(__builtin_bit_cast(uint32_t, v), [](uint32_t a, uint32_t b) {
+                              return __builtin_bit_cast(
+                                  uint32_t, fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)));
+                            }));
 }
 template <int L>
 __device__ __forceinline__ float row_sum(float v) {
@@ -323,6 +331,24 @@ __device__ __forceinline__ void gate_row_bwd(const GateArgs& a, int64_t r, int l
     if (id0 >= 0) {
       first = float(static_cast<const T*>(a.logits)[r * a.ld + id0]);
       scale = -__shfl(w[0], base, 64) * s;
+    } else {
+      // no first choice: nothing was left to choose, or it was dropped since
+      float most = -__builtin_inff(), total = 0.0f;
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+          if (F == kExact || x.own(l, j, i, a.groups)) most = fmaxf(most, float(x.v[j].v[i]));
+      most = row_max_of<L>(most);
+      if (most > -__builtin_inff()) {
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+#pragma unroll
+          for (int i = 0; i < K; ++i)
+            if (F == kExact || x.own(l, j, i, a.groups)) total += exp_of(float(x.v[j].v[i]) - most);
+        first = most;
+        scale = -s / row_sum<L>(total);
+      }
     }
   }
   wave_sync();

@@ -493,7 +493,8 @@ def _gate_bwd(s, logits, ids, weights, dweights, renorm, dlogits):
 
 def gs_gate_bwd(logits, ids, weights, dweights, renorm=True, dlogits=None, stream=None):
     """dlogits of gs_gate_fwd, whose ``ids`` and ``weights`` it reads, for the
-    gradient ``dweights`` of the weights."""
+    gradient ``dweights`` of the weights.  A choice that is left out afterwards
+    loses its place (-1), not its id: gs_combine_bwd's dweight for it is 0."""
     return _launch(_gate_bwd, logits, stream, ids, weights, dweights, renorm, dlogits)
 
 

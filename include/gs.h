@@ -863,9 +863,14 @@ gs_status gs_gate_fwd(const void* logits, int64_t ld, int64_t rows, int32_t grou
 /* Its backward pass, with s = sum over the row's choices of weight dweight:
  *   renorm != 0   dlogits = weight (dweight - s) where chosen, else 0
  *   renorm == 0   dlogits = [chosen] weight dweight - p s, p = e^l / sum e^l,
- *                 as weights[0] e^(l - logit of the first choice)
- *   ids, weights   device, as the forward pass wrote them; an id outside
- *                [0, groups) is no choice
+ *                 as weights[0] e^(l - logit of the first choice) where that is
+ *                 there
+ *   ids, weights   device, as the forward pass wrote them.  An id outside
+ *                [0, groups) is no choice: s has no term for it.  A choice that
+ *                the caller leaves out afterwards (its head is full) keeps its id
+ *                and weight here and loses its place alone, so that
+ *                gs_combine_bwd's dweight is 0: with renorm its logit has a
+ *                gradient still
  *   dweights     device, [rows][k] fp32
  *   dlogits      device out, [rows][lddl]
  * Errors: as the forward pass. */

@@ -384,3 +384,27 @@ def test_a_layer_of_routed_heads(gs):
         other = layer()
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(other, layer()))
+
+
+@pytest.mark.parametrize("name", list(TYPES))
+@pytest.mark.parametrize("groups", [3, 8, 12, 31, 64, 100, 250, 512, 700, 1024])
+def test_gate_gradient_without_some_choices(gs, name, groups):
+    """An id outside the groups is no choice, the first one or another: s is the
+    sum over those that are left, and p stays the softmax of all logits, which
+    may be far from 0 (fp16's largest is 65504, and what is left may be far
+    below the row's largest).  Tolerances as above, with the sum over the row worked
+    out again, which the n terms of the weight's bound hold as well."""
+    t = TYPES[name]
+    for shift, rows in ((0.0, 67), (300.0, 40), (-300.0, 41)):
+        k = min(4, groups - 1)
+        x = _logits(groups, rows, groups, torch.float32) + shift
+        x = x.to(t)
+        for renorm in (True, False):
+            ids, w = gs.gs_gate_fwd(x, k, renorm)
+            for drop in ([0], [0, 1], [k - 1], list(range(k)), [0, k - 1]):
+                some, w_some = ids.clone(), w.clone()
+                some[::2, drop] = -1
+                w_some[::2, drop] = float("nan")      # of no choice: not read
+                got, dw = _check_gate_bwd(gs, x, some, w_some, renorm)
+                some[::4, drop] = groups + 5
+                assert torch.equal(gs.gs_gate_bwd(x, some, w_some, dw, renorm), got)
