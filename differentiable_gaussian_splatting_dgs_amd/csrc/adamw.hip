@@ -159,8 +159,9 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   return uint32_t(__builtin_amdgcn_readlane(int(v), 63));
 }
 
-// Exponent of the scale under which `most` is at most 14 steps of the last
-// octave (of kOctaves; 15 with a carry would be NaN's code).
+// Exponent of the scale under which `most` is below 14 steps of the last octave
+// (of kOctaves): from 14 and a part of one on it may be rounded to 15, NaN's
+// code, and the word's cut off half does not tell 14 from that.
 template <int kOctaves>
 __device__ __forceinline__ int unit_of(uint32_t most) {
   const int e = int(most >> 20) - 1023 + ((most & 0xFFFFFu) >= 0xC0000u ? 1 : 0);

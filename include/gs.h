@@ -963,9 +963,11 @@ typedef struct gs_adamw_tensor {
  * rounded up or down at random, so that a moment that a step changes by less
  * than half of an eighth still follows its mean.  The random numbers are a
  * function of seed, t, the tensor's place in the list and the element's: the
- * same call gives the same bits.  The scale is the smallest that holds the
- * largest finite magnitude of the 256 and at least 2^-126; a v over 0 is never
- * rounded to 0.  A moment that is infinite or NaN becomes NaN, that one alone.
+ * same call gives the same bits.  The scale is the smallest under which the
+ * largest finite magnitude of the 256 is below 14 steps of the last octave (m:
+ * 14 scale 2^14, v: 14 scale 2^30; from there on it may be rounded up to NaN's
+ * code), and at least 2^-126; a v over 0 is never rounded to 0.  A moment that
+ * is infinite or NaN becomes NaN, that one alone.
  *   tensors      host, [count]; read during the call.  Moments in 8 and in 32
  *                bits may be mixed.
  *   step         t, or ignored where

@@ -535,3 +535,41 @@ def test_adamw_small_and_large_eps(gs, bits, eps, scale):
                            (got >= p * decay - high - slack) & (got <= p * decay - low + slack))
         bad = (~fine).nonzero()[:, 0]
         assert bad.numel() == 0, (bad.numel(), int(bad[0]), [float(x[bad[0]]) for x in (got, p, g, m1, v1, low, high)])
+
+
+def test_adamw_scale_at_its_border(gs):
+    """The scale is the smallest under which a block's largest magnitude is below
+    14 steps of the last octave: at 14 exactly it is twice that, since what is
+    rounded up from there on would be NaN's code."""
+    for e in (-90, -20, 0, 3, 60):
+        border = 1.75 * 2.0 ** e
+        sizes = [border * (1 - 2.0 ** -24), border, border * (1 + 2.0 ** -23), 2.0 ** (e + 1), 1.5 * 2.0 ** e]
+        want = [e, e + 1, e + 1, e + 1, e]
+        # beta1 = 0: m is the gradient
+        g = torch.zeros(len(sizes), 256, device="cuda")
+        g[:, 77] = torch.tensor(sizes, dtype=F64).float().cuda()
+        g[1, 77] *= -1
+        g[:, 78] = g[:, 77] / 3
+        t = [torch.zeros(g.numel(), device="cuda"), g.view(-1), torch.zeros(g.numel(), dtype=torch.uint8, device="cuda"),
+             torch.zeros(g.numel(), dtype=torch.uint8, device="cuda"), torch.zeros(len(sizes), device="cuda"),
+             torch.zeros(len(sizes), device="cuda")]
+        _step(gs, [t], 1, beta1=0.0)
+        assert t[4].tolist() == [2.0 ** (w - 3 - 14) for w in want]
+        m = gs.gs_adamw_moment(t[2], t[4], 1).view(len(sizes), 256)
+        assert bool(m.isfinite().all())
+        # rounded by less than a step of the largest value's octave, 2^(e - 3)
+        assert bool(((m - g).abs() < 2.0 ** (e - 2)).all())
+        assert m[1, 77] == -border and m[3, 77] == 2.0 ** (e + 1)
+        # beta2 = 1/2 and no gradient: v is half of what it was
+        half = torch.full((256,), 0.5, dtype=F64, device="cuda")
+        for k, unit in ((14, e + 1), (13, e), (15, e + 1)):
+            v0 = torch.zeros(256, dtype=F64, device="cuda")
+            v0[9] = 2.0 * k * 2.0 ** (e - 3)
+            codes, scales = _encode(v0, half, False)
+            assert _decode(codes, scales, False)[9] == v0[9]
+            t = [torch.zeros(256, device="cuda"), torch.zeros(256, device="cuda"),
+                 torch.zeros(256, dtype=torch.uint8, device="cuda"), codes, torch.zeros(1, device="cuda"), scales]
+            _step(gs, [t], 2, beta2=0.5)
+            got = gs.gs_adamw_moment(t[3], t[5], 2)
+            assert float(t[5]) == 2.0 ** (unit - 3 - 30)
+            assert float(got[9]) == k * 2.0 ** (e - 3)
