@@ -297,3 +297,29 @@ def test_sort_and_embedding_on_streams_and_in_graphs(gs):
         assert all(torch.equal(a, b) for a, b in zip((offsets, order, place), want))
         assert torch.equal(y, gs.gs_embedding_fwd(table, ids, 2.0))
         assert torch.equal(dt, _check_bwd(gs, dy, ids, table_rows, 2.0))
+
+
+@pytest.mark.parametrize("rows,width,name,length", [
+    (200_003, 256, "bf16", 32), (100_001, 515, "fp32", 32), (150_001, 512, "fp16", 64), (300_001, 256, "bf16", 64),
+    (60_001, 4100, "bf16", 64), (1_000_003, 256, "bf16", 128), (2_100_001, 8, "bf16", 128), (700_001, 130, "fp32", 128)])
+def test_embedding_backward_of_long_stretches(gs, rows, width, name, length):
+    """Stretches of the sorted order that are longer than for few rows, and ids
+    whose rows end at, begin at, reach over and fill them, up to and past the
+    number of stretches that are joined in one go."""
+    runs, left = [], rows - rows // 50      # the rest: rows of no id
+    kinds = [length, 1, length - 1, length + 1, 2, 3 * length, 7, 32 * length, 33 * length + 5, 34 * length - 1, 5, 5,
+             length // 2, 40 * length, 0, 3, 0]
+    while left > 0:
+        runs.append(min(left, kinds[len(runs) % len(kinds)]))
+        left -= runs[-1]
+    counts = torch.tensor(runs, device="cuda")
+    ids = torch.arange(counts.numel(), device="cuda").repeat_interleave(counts)
+    ids = torch.cat([ids, torch.full((rows - ids.numel(),), -1, device="cuda")])
+    ids = ids[torch.randperm(rows, generator=gen(rows), device="cuda")]
+    dy = rand(gen(width), rows, width, dtype=TYPES[name])
+    first = _check_bwd(gs, dy, ids, counts.numel(), 0.5)
+    ws = torch.full((gs.gs_embedding_workspace_size(rows, counts.numel(), width, list(TYPES).index(name)),), 255,
+                    dtype=torch.uint8, device="cuda")
+    assert torch.equal(_check_bwd(gs, dy, ids, counts.numel(), 0.5, workspace=ws), first)
+    # ids as a scene has them: few with thousands of rows, many with a few
+    _check_bwd(gs, dy, _ids(rows, rows, rows // 10 + 1, torch.int32), rows // 10 + 1)

@@ -408,3 +408,78 @@ def test_gate_gradient_without_some_choices(gs, name, groups):
                 got, dw = _check_gate_bwd(gs, x, some, w_some, renorm)
                 some[::4, drop] = groups + 5
                 assert torch.equal(gs.gs_gate_bwd(x, some, w_some, dw, renorm), got)
+
+
+def _check_weights(gs, x, k, renorm):
+    """The weights within a bound that goes by how far each logit is from the
+    largest.  (u = 2^-24, D the distance.)  The difference is off by u D, which
+    makes e^ of it off by as much of itself, beside the function's 4 u; a sum's
+    terms are off by 4 u and u times their distance, whose mean with the softmax's
+    weights is at most ln n; at most 38 additions follow on each other (32 of a
+    lane, 6 between lanes); the reciprocal's 2 u and the product's u.  Powers under
+    2^-126 may become 0."""
+    ids, w = gs.gs_gate_fwd(x, k, renorm)
+    want_ids, want = _gate_plain(x, k, renorm)
+    assert torch.equal(ids.long(), want_ids)
+    xd = x.double()
+    far = torch.where(want_ids >= 0, xd.amax(1, keepdim=True) - xd.gather(1, want_ids.clamp_min(0)), 0.0)
+    n = k if renorm else x.shape[1]
+    tol = (far + torch.tensor(float(n)).log() + 4 + 4 + 38 + 3) * EPS32 * want + 2.0 ** -126
+    close(w, want, tol, "weights")
+    return ids, w
+
+
+@pytest.mark.parametrize("name", list(TYPES))
+@pytest.mark.parametrize("spread", [0.1, 2.0, 20.0, 100.0, 1000.0])
+@pytest.mark.parametrize("groups", [5, 16, 64, 100, 250, 256, 512, 1024])
+def test_gate_of_far_logits(gs, name, spread, groups):
+    """Logits up to thousands apart: powers of e that are subnormal, that are 0,
+    and that still count; few rows, and rows that share lanes' registers."""
+    t = TYPES[name]
+    for rows in (201, 8 * 2 ** 20 // groups + 3):
+        x = rand(gen(rows + groups), rows, groups, scale=spread).to(t)
+        # next to where e^-D ends, 87.3 (the smallest normal) and 103.97 (0)
+        x[3] = -torch.linspace(80.0, 110.0, groups, device="cuda").to(t)
+        x[3, groups // 2] = 0.0
+        for k, renorm in ((1, False), (min(2, groups), True), (min(5, groups), False), (min(8, groups), True)):
+            ids, w = _check_weights(gs, x, k, renorm)
+            if rows < 1000:
+                _check_gate_bwd_far(gs, x, ids, w, renorm)
+
+
+def _check_gate_bwd_far(gs, x, ids, w, renorm):
+    """_check_gate_bwd with the distances counted: p = w0 e^(l - l0) is off by u
+    times the distance and, with the weight's own bound, by under (110 + ln n + 60) u
+    where it is above 2^-126."""
+    rows, k = ids.shape
+    dw = rand(gen(rows), rows, k)
+    got = gs.gs_gate_bwd(x, ids, w, dw, renorm)
+    xd, wd = x.double(), w.double()
+    part = wd * dw.double()
+    s, size = part.sum(1, keepdim=True), part.abs().sum(1, keepdim=True)
+    p = torch.zeros_like(xd) if renorm else torch.softmax(xd, 1)
+    mine = part - wd * s if renorm else part
+    at = ids.long()
+    want = (-p * s).scatter_add(1, at, mine)
+    terms = (p * size).scatter_add(1, at, part.abs() + wd * size)
+    tol = (half_step(x.dtype) + EPS32) * want.abs() + (110 + 7 + 60 + k + 6) * EPS32 * terms + tiny(x.dtype)
+    # a power that became 0, and a weight that did
+    close(got, want, tol + 2.0 ** -125 * (1 + size), "dlogits")
+
+
+@pytest.mark.parametrize("name,rows,groups", [
+    ("fp32", 20_003, 250), ("bf16", 20_003, 500), ("fp16", 20_003, 700), ("fp32", 20_003, 1024), ("bf16", 9_001, 1024),
+    ("fp32", 40_003, 100), ("bf16", 70_001, 100), ("fp32", 140_003, 20), ("fp16", 140_001, 30), ("bf16", 300_001, 16), ("fp32", 300_001, 8),
+    ("fp16", 600_001, 8), ("fp32", 600_001, 3), ("bf16", 600_001, 5)])
+def test_gate_backward_of_many_rows(gs, name, rows, groups):
+    """More rows than there are groups of lanes at a time, with a remainder: the
+    rows that follow in the same lanes and the same part of LDS."""
+    t = TYPES[name]
+    x = _logits(rows, rows, groups, t)
+    for k, renorm in ((min(2, groups), True), (min(8, groups), False), (min(16, groups), True), (1, False)):
+        ids, w = gs.gs_gate_fwd(x, k, renorm)
+        _check_gate_bwd(gs, x, ids, w, renorm)
+    out = strided(torch.full((rows, groups), 3.0, dtype=t, device="cuda"), 3, 1, fill=7.0)
+    ids, w = gs.gs_gate_fwd(x, min(3, groups), False)
+    _check_gate_bwd(gs, strided(x, 5, 1, fill=INF), ids, w, False, dlogits=out)
+    assert bool((padding(out) == 7.0).all())
