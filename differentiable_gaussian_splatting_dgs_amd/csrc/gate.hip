@@ -403,21 +403,23 @@ hipError_t go(const GateArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <typename T, int L, int C, Fit F, bool kFwd>
+// Choices in powers of two, up to those that such a row can have: no more than
+// its columns, and with four chunks four a lane, as below.
+template <typename T, int L, int C, Fit F, bool kFwd, int KM = 1>
 hipError_t by_choices(const GateArgs& a, hipStream_t st) {
-  if (a.k <= 1) return go<T, L, C, 1, F, kFwd>(a, st);
-  if (a.k <= 2) return go<T, L, C, 2, F, kFwd>(a, st);
-  if (a.k <= 4) return go<T, L, C, 4, F, kFwd>(a, st);
-  if constexpr (C == 4 && 4 * L < kMaxChoices)      // at most four choices a lane, as below
-    return go<T, L, C, 8, F, kFwd>(a, st);
+  constexpr int kColumns = F == kNarrow ? kChunk<T> - 1 : L * C * kChunk<T>;
+  constexpr int kMost = std::min({int(kMaxChoices), kColumns, C == 4 ? 4 * L : int(kMaxChoices)});
+  if constexpr (KM >= kMost)
+    return go<T, L, C, KM, F, kFwd>(a, st);
   else
-    return a.k <= 8 ? go<T, L, C, 8, F, kFwd>(a, st) : go<T, L, C, kMaxChoices, F, kFwd>(a, st);
+    return a.k <= KM ? go<T, L, C, KM, F, kFwd>(a, st) : by_choices<T, L, C, F, kFwd, 2 * KM>(a, st);
 }
 
 template <typename T, int L, int C, bool kFwd>
 hipError_t by_fit(const GateArgs& a, hipStream_t st) {
-  if (a.groups == L * C * kChunk<T>) return by_choices<T, L, C, kExact, kFwd>(a, st);
-  return by_choices<T, L, C, kMoved, kFwd>(a, st);
+  if constexpr (L * C > 1)      // a row of one chunk, and not less, is exact
+    if (a.groups != L * C * kChunk<T>) return by_choices<T, L, C, kMoved, kFwd>(a, st);
+  return by_choices<T, L, C, kExact, kFwd>(a, st);
 }
 
 // The forward pass: with four chunks a lane instead of one, four times as many
