@@ -323,3 +323,47 @@ def test_embedding_backward_of_long_stretches(gs, rows, width, name, length):
     assert torch.equal(_check_bwd(gs, dy, ids, counts.numel(), 0.5, workspace=ws), first)
     # ids as a scene has them: few with thousands of rows, many with a few
     _check_bwd(gs, dy, _ids(rows, rows, rows // 10 + 1, torch.int32), rows // 10 + 1)
+
+
+@pytest.mark.parametrize("n,groups", [(5, 2 ** 30), (5000, 2 ** 25 - 1), (8192, 2 ** 30 - 1), (20_000, 2 ** 30 - 1), (300_001, 2 ** 30)])
+def test_group_sort_of_the_most_groups(gs, n, groups):
+    """Keys of 25 to 31 bits: four digits for few ids, three or four for many.
+    The bounds (8 GB of them) against the sorted keys, a part at a time."""
+    ids = _ids(n, n, groups)
+    ids[:2] = torch.tensor([groups - 1, groups], device="cuda")
+    offsets, order, place = gs.gs_group_sort(ids, groups)
+    key = torch.where((ids < 0) | (ids >= groups), groups, ids)
+    keys, want = torch.sort(key, stable=True)
+    assert torch.equal(order.long(), want)
+    at = torch.empty_like(want)
+    at[want] = torch.arange(n, device="cuda")
+    assert torch.equal(place.long(), torch.where(key < groups, at, -1))
+    step = 2 ** 26
+    for a in range(0, groups + 1, step):
+        part = torch.arange(a, min(a + step, groups + 1), device="cuda")
+        assert torch.equal(offsets[a:a + step], torch.searchsorted(keys, part))
+
+
+def test_embedding_of_the_most_rows(gs):
+    """A table of 2^30 rows, and 2^31 - 1 ids."""
+    rows = 2 ** 30
+    table = torch.zeros(rows, 1, dtype=torch.bfloat16, device="cuda")
+    picks = [0, 5, 2 ** 29 + 1, rows - 1]
+    for k, r in enumerate(picks):
+        table[r] = k + 1
+    ids = torch.tensor([rows - 1, 5, -1, rows, 2 ** 29 + 1, 0, rows - 1, 5], device="cuda")
+    assert gs.gs_embedding_fwd(table, ids)[:, 0].tolist() == [4, 2, 0, 0, 3, 1, 4, 2]
+    offsets, order, _ = gs.gs_group_sort(ids, rows, want_place=False)
+    dy = torch.arange(1.0, 9.0, device="cuda")[:, None].bfloat16()
+    table.fill_(9)
+    gs.gs_embedding_bwd(dy, ids, offsets, order, dtable=table)
+    assert [float(table[r]) for r in picks] == [6, 10, 5, 8]
+    assert sum(int((table[a:a + 2 ** 28] != 0).sum()) for a in range(0, rows, 2 ** 28)) == 4
+    del table, offsets, order
+    n = 2 ** 31 - 1
+    ids = torch.full((n,), 2, dtype=torch.int32, device="cuda")
+    ids[0], ids[-1], ids[2 ** 30] = 0, 1, 7
+    y = gs.gs_embedding_fwd(torch.tensor([[1.0], [3.0], [5.0]], dtype=torch.bfloat16, device="cuda"), ids)
+    assert [float(y[i]) for i in (0, 1, 2 ** 30, n - 2, n - 1)] == [1, 5, 0, 5, 3]
+    step = 2 ** 28
+    assert sum(int((y[a:a + step] == 5).sum()) for a in range(0, n, step)) == n - 3

@@ -483,3 +483,25 @@ def test_gate_backward_of_many_rows(gs, name, rows, groups):
     ids, w = gs.gs_gate_fwd(x, min(3, groups), False)
     _check_gate_bwd(gs, strided(x, 5, 1, fill=INF), ids, w, False, dlogits=out)
     assert bool((padding(out) == 7.0).all())
+
+
+def test_routing_of_the_most_rows(gs):
+    """2^31 - 1 rows through the gate, and as many places."""
+    n, step = 2 ** 31 - 1, 2 ** 28
+    x = torch.zeros(n, 1, dtype=torch.bfloat16, device="cuda")
+    x[0], x[2 ** 30], x[-1] = -INF, -INF, 3.0
+    ids, w = gs.gs_gate_fwd(x, 1)
+    assert [int(ids[i]) for i in (0, 1, 2 ** 30, n - 1)] == [-1, 0, -1, 0] and float(w[-1]) == 1
+    assert sum(int((ids[a:a + step] == 0).sum()) for a in range(0, n, step)) == n - 2
+    assert sum(int((w[a:a + step] == 1).sum()) for a in range(0, n, step)) == n - 2
+    del w
+    # every row one place on, the last one to the front
+    place = ids
+    for a in range(0, n, step):
+        m = min(step, n - a)
+        place[a:a + m, 0] = torch.arange(a + 1, a + m + 1, device="cuda", dtype=torch.int64).remainder_(n).int()
+        x[a:a + m, 0] = (torch.arange(a, a + m, device="cuda") % 251).bfloat16()
+    xs = gs.gs_dispatch_fwd(x, place)
+    back = gs.gs_combine_fwd(xs, place)
+    assert torch.equal(xs[1:2 ** 30], x[:2 ** 30 - 1]) and torch.equal(xs[2 ** 30:], x[2 ** 30 - 1:-1])
+    assert torch.equal(xs[0], x[-1]) and torch.equal(back[:2 ** 30], x[:2 ** 30]) and torch.equal(back[2 ** 30:], x[2 ** 30:])
