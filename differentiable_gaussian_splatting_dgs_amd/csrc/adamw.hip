@@ -4,9 +4,11 @@
 //   p = p (1 - lr wd) - lr (m / c1) / (sqrt(v / c2) + eps),  c = 1 - b^t
 //
 // Bound by the bytes: p, m and v in and out, g in, the copy out.  The nine
-// tensors of a decoder with 500,003 x 64 features, fp32: 172 us (963 MB at 5.6
-// TB/s); 1,000,003 x 64, bf16 gradients, moments in 8 bits: 190 to 204 us (1.04 GB
-// at 5.1 TB/s, 69 vector instructions a value).  The tensors'
+// tensors of a decoder with 500,003 x 64 features, fp32: 176 us (963 MB at 5.5
+// TB/s); 1,000,003 x 64, bf16 gradients, moments in 8 bits: 192 to 215 us (1.04 GB
+// at 4.8 to 5.4 TB/s, 70 vector instructions a value).  A step whose number is on
+// the device works out its corrections in every thread: 8 and 18 us more with
+// the launch that counts.  The tensors'
 // addresses travel as the launch's arguments; a workgroup finds its tensor by
 // bisection of their first workgroups and works on kGroup of its elements.
 //
@@ -37,8 +39,8 @@ namespace {
 
 constexpr int kThreads = 256;
 // Elements of a workgroup: four a thread, so that a wave's registers leave room
-// for more waves (500,003 x 64 fp32: 179 us, with 8 a thread 183, 16 186; 8 bits:
-// 328, 339, 349).
+// for more waves (calls in a row as it was chosen, 500,003 x 64 fp32: 179 us, with
+// 8 a thread 183, 16 186; 8 bits with the moments read out: 328, 339, 349).
 constexpr int kGroup = kThreads * 4;
 
 struct AdamwBatch {

@@ -17,7 +17,10 @@
 // as busy: the instructions of the loops over the logits count.  1,000,000 x 64
 // bf16, 2 choices: 29 us (144 MB at 5.0 TB/s); gradient of 70,001 x 250 fp32, 8
 // choices, of all logits: 32 us (147 MB at 4.5 TB/s).  With 8 choices the vector
-// unit bounds it: bf16 x 64 39 us, x 256 130, fp32 x 64 72, x 256 264.
+// unit bounds it: bf16 x 64 39 us, x 256 130, fp32 x 64 72, x 256 264.  The gradient
+// over the chosen reads no logits and is bound by LDS: 1,000,000 x 64 bf16, 2
+// choices, 51 us, of which LDS is busy 42, most of it conflicts of banks (152 MB
+// take 30); over all logits 68 us.
 #include <algorithm>
 
 #include "row_chunks.hpp"

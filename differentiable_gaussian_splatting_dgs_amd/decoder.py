@@ -138,7 +138,7 @@ class AttributeDecoder:
 
 class RoutedDecoder(AttributeDecoder):
     """Features of ``rows`` anchors, looked up by ``anchors`` ([n]; -1: a
-    Gaussian without features, whose attributes are the layers' biases), and
+    Gaussian without features, for which a row of zeros is decoded), and
     ``heads`` heads, ``choices`` of them for each Gaussian by the gate.  The
     masters have "gate" beside AttributeDecoder's."""
 

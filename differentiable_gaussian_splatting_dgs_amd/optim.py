@@ -146,7 +146,9 @@ class AdamW:
     in 8 bits (2 bytes a parameter instead of 8); ``copies[i]`` (or None) is
     written with parameter i's new values.  ``capturable`` keeps the step's
     number on the device, so that a captured ``step`` counts on with each
-    replay (``steps``, on the host, does not; without it a capture is refused).
+    replay (``steps``, on the host, does not; without it a capture is refused);
+    ``lr`` and the other numbers, which may be set between steps, stay those of
+    the capture.
     ``state``: (m, v, m_scale, v_scale) of each tensor to go on from, taken as
     they are (scales None for moments in 32 bits), ``step`` the number of steps
     done.  ``params``, ``copies`` and ``state`` stay the tensors that they are
