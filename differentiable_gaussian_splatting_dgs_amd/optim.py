@@ -183,7 +183,7 @@ class AdamW:
         rows = zip(self.params, self.copies, self.state)
         self._tensors = [t for p, c, s in rows for t in (p, c, *s) if t is not None]
         self._typed = [c for c in self.copies if c is not None]
-        self._table, self._held, self._sizes, self._kinds = None, None, None, None
+        self._table, self._held, self._sizes, self._kinds, self._given = None, None, None, None, None
 
     params = property(attrgetter("_params"))
     copies = property(attrgetter("_copies"))
@@ -205,7 +205,17 @@ class AdamW:
             self._kinds = [_entry(table, i, device, p, *s, c)
                            for i, (p, s, c) in enumerate(zip(self.params, self.state, self.copies))]
             self._table, self._held, self._sizes = table, held, [p.numel() for p in self.params]
-        _grads(self._table, device, self._sizes, self._kinds, grads)
+            self._given = None
+        # gradients that are filled where they were have their entries (an address
+        # is of one device)
+        try:
+            given = [*map(_address, grads), *map(_nbytes, grads), *map(_dense, grads), *map(_dtype, grads)]
+        except TypeError:       # None among them
+            given = None
+        if given is None or given != self._given:
+            self._given = None
+            _grads(self._table, device, self._sizes, self._kinds, grads)
+            self._given = given
         numbers = (self.lr, *self.betas, self.eps, self.weight_decay)
         _launch(self._enqueue, self.params[0], stream, numbers, grad_scale)
         self.steps += 1

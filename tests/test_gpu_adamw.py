@@ -573,3 +573,30 @@ def test_adamw_scale_at_its_border(gs):
             got = gs.gs_adamw_moment(t[3], t[5], 2)
             assert float(t[5]) == 2.0 ** (unit - 3 - 30)
             assert float(got[9]) == k * 2.0 ** (e - 3)
+
+
+def test_adamw_gradients_that_change(gs):
+    """Gradients in place, at new addresses, of other types, left out and back,
+    and of a size, layout or device that is refused, one after the other."""
+    params = [rand(gen(1), 30, 20), rand(gen(2), 77)]
+    opt = gs.AdamW(params, lr=HYPER["lr"], weight_decay=0.02)
+    g0, g1 = rand(gen(3), 30, 20), rand(gen(4), 77)
+    half = g0.bfloat16()
+    k = 0
+    for grads in ([g0, g1], [g0, g1], [g0.clone(), g1], [half, g1], [half, g1], [None, g1], [half, None], [g0, g1], [g0, g1]):
+        rows = [[p, torch.zeros_like(p) if g is None else g, *s] for p, g, s in zip(params, grads, opt.state)]
+        k += 1
+        want, kept = _oracle(rows, k), [p.clone() for p in params]
+        opt.step(grads)
+        for i, g in enumerate(grads):
+            if g is None:
+                assert torch.equal(params[i], kept[i])
+            else:
+                _compare([rows[i]], [want[i]], f"step {k} of {i}")
+        for bad in ([g0, g1[:76]], [g0.t(), g1], [g0, g1.cpu()], [g0, g1.double()], [g0.view(torch.int32), g1],
+                    [g0.view(torch.bfloat16), g1]):
+            kept = [p.clone() for p in params]
+            with pytest.raises(ValueError, match="gradient"):
+                opt.step(bad)
+            assert opt.steps == k and all(torch.equal(a, b) for a, b in zip(params, kept))
+        g0.mul_(1.5)
